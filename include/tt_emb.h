@@ -394,6 +394,157 @@ typedef enum {
 
 int tt_emb_debug_inject(tt_emb_t h, int32_t what, int32_t spin_limit);
 
+/* =====================================================================================
+ * Dense tables and the AdamW step.  A model keeps dense tables beside its TT-compressed
+ * ones (its token table, and tables too small to compress), and trains all of them.  The
+ * conventions at the top of this file hold here too.  The pages have no counterpart.
+ * ===================================================================================== */
+
+/* Element types of dense tables, their activations and gradients, and of AdamW's tensors. */
+typedef enum { TT_F32 = 0, TT_BF16 = 1, TT_F16 = 2 } tt_dtype;
+
+typedef struct tt_emb_dense_handle* tt_emb_dense_t;
+
+/*
+ * Creates a handle for one dense table of num_rows rows of dim values (host call; allocates
+ * the handle and its 256-byte device status block on the current device).
+ *   num_rows     1 .. 2^31 - 2
+ *   dim          1 .. 2^20
+ *   table_type   tt_dtype of the table
+ *   scale        factor of every row looked up, and of its gradient
+ *   padding_row  a row that receives no gradient, or -1 for none (it is looked up like any other)
+ *   out          host: receives the handle
+ * Returns TT_OK, TT_ERR_ARG (a null pointer, an unknown type), TT_ERR_SHAPE (sizes or padding_row
+ * outside these ranges) or TT_ERR_CUDA.  Every call below that enqueues work wants the device of
+ * this call to be current, and returns TT_ERR_STATE otherwise.
+ */
+int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float scale, int64_t padding_row,
+                        tt_emb_dense_t* out);
+
+/*
+ * Registers the table and, for training, the buffer of its gradient, by borrowing device
+ * pointers: row-major [num_rows][dim], each aligned to its element.  grad may be NULL for
+ * inference; grad_type is its tt_dtype.  Returns TT_OK or TT_ERR_ARG.
+ */
+int tt_emb_dense_set_table(tt_emb_dense_t h, const void* table, void* grad, int32_t grad_type);
+
+/*
+ * Device workspace that tt_emb_dense_backward needs for at most max_tokens tokens (host call);
+ * the forward needs none.  Returns TT_OK or TT_ERR_ARG (max_tokens outside 0 .. 2^31 - 2).
+ */
+int tt_emb_dense_workspace_size(tt_emb_dense_t h, int64_t max_tokens, size_t* bytes);
+
+/*
+ * Registers caller-owned device workspace (256-byte aligned).  Nothing in it lives from one
+ * call to the next; two calls that overlap on the GPU must not share it.  Returns TT_OK,
+ * TT_ERR_ARG or TT_ERR_WORKSPACE (bytes below the size asked).
+ */
+int tt_emb_dense_set_workspace(tt_emb_dense_t h, void* workspace, size_t bytes, int64_t max_tokens);
+
+/*
+ * Lookup: out[i][c] = scale * table[tokens[i]][c], computed in fp32 and rounded once.
+ *   tokens       device int32 or int64 (token_bytes 4 or 8) [num_tokens], each in [0, num_rows)
+ *   out          device, tt_dtype out_type; row i begins out_stride (>= dim) elements after row i - 1;
+ *                values between rows are left as they were
+ * Host errors: TT_ERR_ARG, TT_ERR_STATE (no table, another device), TT_ERR_CUDA; a token outside
+ * the table surfaces as TT_ERR_INDEX_RANGE at tt_emb_dense_sync, and until then the later kernels
+ * of the handle do nothing.
+ */
+int tt_emb_dense_forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t num_tokens, void* out,
+                         int32_t out_type, int64_t out_stride, tt_stream_t stream);
+
+/*
+ * Gradient of the table for the given tokens: for every row v,
+ *   grad[v][c] = (accumulate ? grad[v][c] : 0) + scale * sum over i with tokens[i] = v of grad_out[i][c]
+ * where tokens equal to padding_row are left out.  The tokens are sorted by row (stable), sums
+ * are formed in fp32 in an order that depends only on the tokens, and rounded once to grad_type;
+ * the same call gives the same bits.  Without accumulate every row of grad is written.
+ *   grad_out     device, tt_dtype grad_out_type; row i begins grad_out_stride (>= 0; 0 repeats one
+ *                row) elements after row i - 1
+ * It needs no preceding forward.  Errors as above, TT_ERR_STATE without a gradient buffer, and
+ * TT_ERR_WORKSPACE (no workspace, or num_tokens above its max_tokens).
+ */
+int tt_emb_dense_backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t num_tokens,
+                          const void* grad_out, int32_t grad_out_type, int64_t grad_out_stride, int32_t accumulate,
+                          tt_stream_t stream);
+
+/* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy. */
+int tt_emb_dense_sync(tt_emb_dense_t h);
+int tt_emb_dense_last_error(tt_emb_dense_t h);
+void tt_emb_dense_destroy(tt_emb_dense_t h);
+
+/* Device address of the handle's status word: not zero while a device error waits for the next
+ * sync.  NULL for a null handle.  (The guard of tt_emb_adamw_tensor.) */
+const int32_t* tt_emb_status_word(tt_emb_t h);
+const int32_t* tt_emb_dense_status_word(tt_emb_dense_t h);
+
+/*
+ * One tensor of an AdamW step: size contiguous values of param and grad, each aligned to its
+ * element; exp_avg (m) and exp_avg_sq (v) float32 [size].  With 8-bit moments, m and v are
+ * [size] bytes in the e4m3 format (m as it is; v as its square root), each block of
+ * TT_ADAMW_BLOCK values with one float32 scale in m_scale and v_scale [ceil(size / block)].
+ * All pointers are borrowed; those of a tensor of size 0 may be NULL.
+ *   guard        device, may be NULL: the tensor is left as it is while *guard is not 0 (the
+ *                status word of the handle that computed grad, so that no update follows a
+ *                failed backward)
+ */
+#define TT_ADAMW_BLOCK 256
+typedef struct {
+    void* param;
+    const void* grad;
+    void* exp_avg;
+    void* exp_avg_sq;
+    float* m_scale;
+    float* v_scale;
+    const int32_t* guard;
+    int64_t size;
+    int32_t param_type;      /* tt_dtype */
+    int32_t grad_type;       /* tt_dtype */
+    double weight_decay;     /* decoupled, >= 0 */
+} tt_emb_adamw_tensor;
+
+typedef struct {
+    double beta1, beta2;     /* in [0, 1) */
+    double eps;              /* > 0, also when rounded to float32 */
+    int32_t state_bits;      /* 32 or 8 */
+    int32_t reserved;        /* must be zero */
+    uint64_t seed;           /* of the 8-bit moments' rounding */
+} tt_emb_adamw_options;
+
+typedef struct tt_emb_adamw_handle* tt_emb_adamw_t;
+
+/*
+ * Creates an AdamW optimiser over count tensors (host call; allocates the handle and a
+ * 256-byte device block on the current device).
+ *   tensors      host [count]
+ *   steps        device int64 [1], 8-byte aligned, borrowed: the number of steps taken
+ * Returns TT_OK, TT_ERR_ARG (a null or misaligned pointer, an unknown type, an option outside
+ * its range) or TT_ERR_CUDA.
+ */
+int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const tt_emb_adamw_options* opt,
+                        int64_t* steps, tt_emb_adamw_t* out);
+
+/*
+ * One step of every tensor, t = *steps + 1, in fp32:
+ *   m <- beta1 m + (1 - beta1) g,   v <- beta2 v + (1 - beta2) g^2
+ *   p <- (1 - lr weight_decay) p - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * and *steps <- t.  p is rounded once to its type.  8-bit moments are read as code x scale and
+ * written anew for each block: the scale is the largest finite magnitude / 448 (0, with all
+ * codes 0, where that magnitude is below 2^-100), m goes to the nearest code, and sqrt(v) up or
+ * down at random, so that steps smaller than the code's are not lost on average; a v above zero
+ * keeps the least code at least, and values that are not finite become NaN.  The random bits are
+ * the outputs of SplitMix64 started from (seed, t): four values in a row, counted over all tensors
+ * with each rounded up to whole blocks, take the four 16-bit parts of one output.
+ *   lr           host; or lr_device (device float32 [1], may be NULL) in its place, so that a
+ *                captured graph follows a schedule
+ * Enqueues on stream.  Returns TT_OK, TT_ERR_ARG, TT_ERR_STATE (another device than the
+ * handle's is current) or TT_ERR_CUDA.
+ */
+int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_stream_t stream);
+
+/* Destroys the handle (host + its device block).  NULL is ignored. */
+void tt_emb_adamw_destroy(tt_emb_adamw_t h);
+
 /* ABI version of the loaded library (TT_EMB_ABI_VERSION). */
 int tt_emb_abi_version(void);
 

@@ -24,7 +24,9 @@ TT_SCHED_STATIC, TT_SCHED_STEAL, TT_SCHED_STEAL_L2 = 0, 1, 2
 TT_GROUP_PREFIX, TT_GROUP_UNIQUE_ONLY = 0, 1
 TT_PREC_FP32, TT_PREC_BF16_TC, TT_PREC_FP32_SPLIT_TC = 0, 1, 2
 TT_INJECT_NONE, TT_INJECT_POOL_WAIT, TT_INJECT_MMA_WAIT_FWD, TT_INJECT_MMA_WAIT_BWD = 0, 1, 2, 3
+TT_F32, TT_BF16, TT_F16 = 0, 1, 2
 MAX_TABLES, MAX_CORES = 64, 4
+ADAMW_BLOCK = 256      # values that share one scale of an 8-bit moment
 
 
 class TTEmbError(RuntimeError):
@@ -47,6 +49,18 @@ class SegView(ctypes.Structure):
                 ("perm", ctypes.c_void_p), ("uniq_keys", ctypes.c_void_p),
                 ("uniq_start", ctypes.c_void_p), ("grp_start", ctypes.c_void_p),
                 ("bag_sorted", ctypes.c_void_p)]
+
+
+class AdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("guard", ctypes.c_void_p), ("size", ctypes.c_int64), ("param_type", ctypes.c_int32),
+                ("grad_type", ctypes.c_int32), ("weight_decay", ctypes.c_double)]
+
+
+class AdamWOptions(ctypes.Structure):
+    _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32), ("seed", ctypes.c_uint64)]
 
 
 _LIB = None
@@ -80,6 +94,26 @@ _SIGS = {
     "tt_emb_set_probe": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32], ctypes.c_int),
     "tt_emb_debug_inject": ([ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32], ctypes.c_int),
     "tt_emb_destroy": ([ctypes.c_void_p], None),
+    "tt_emb_dense_create": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_int64,
+                             ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+    "tt_emb_dense_set_table": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32], ctypes.c_int),
+    "tt_emb_dense_workspace_size": ([ctypes.c_void_p, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)],
+                                    ctypes.c_int),
+    "tt_emb_dense_set_workspace": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64],
+                                   ctypes.c_int),
+    "tt_emb_dense_forward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                              ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                               ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_sync": ([ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_last_error": ([ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_destroy": ([ctypes.c_void_p], None),
+    "tt_emb_status_word": ([ctypes.c_void_p], ctypes.c_void_p),
+    "tt_emb_dense_status_word": ([ctypes.c_void_p], ctypes.c_void_p),
+    "tt_emb_adamw_create": ([ctypes.c_int32, ctypes.POINTER(AdamWTensor), ctypes.POINTER(AdamWOptions),
+                             ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+    "tt_emb_adamw_step": ([ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_adamw_destroy": ([ctypes.c_void_p], None),
 }
 
 NOALLOC_MAX_LOOKUPS = 262144
@@ -283,3 +317,138 @@ def tt_emb_debug_inject(h, what: int, spin_limit: int = 0):
 def tt_emb_destroy(h):
     if h is not None and h.value:
         lib().tt_emb_destroy(h)
+
+
+# ---------------------------------------------------------------------------
+# Dense tables
+# ---------------------------------------------------------------------------
+def dtype_code(dtype) -> int:
+    """TT_F32, TT_BF16 or TT_F16 of a torch dtype."""
+    import torch
+    codes = {torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16}
+    if dtype not in codes:
+        raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+    return codes[dtype]
+
+
+def _tokens(t):
+    """(pointer, bytes of a token, tokens) of an integer CUDA tensor of any shape."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("tokens must be a CUDA tensor")
+    if t.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"tokens must be int32 or int64, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tokens must be contiguous")
+    return t.data_ptr(), t.element_size(), t.numel()
+
+
+def _rows(t, n: int, dim: int, name: str):
+    """(pointer, type, row stride) of n rows of dim values: contiguous of any shape, or [n][dim] with
+    neighbouring values in a row and any distance between rows."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    code = dtype_code(t.dtype)
+    if t.numel() != n * dim or t.shape[-1:] != (dim,):
+        raise ValueError(f"{name} must hold {n} rows of {dim} values, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), code, dim
+    if t.dim() != 2 or (dim > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    return t.data_ptr(), code, t.stride(0)
+
+
+def tt_emb_dense_create(num_rows: int, dim: int, dtype, scale: float = 1.0, padding_row: int = -1):
+    h = ctypes.c_void_p()
+    _check(lib().tt_emb_dense_create(int(num_rows), int(dim), dtype_code(dtype), float(scale), int(padding_row),
+                                     ctypes.byref(h)), "tt_emb_dense_create")
+    return h
+
+
+def tt_emb_dense_set_table(h, table, grad=None):
+    import torch
+    for t, name in ((table, "table"), (grad, "grad")):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
+            raise TypeError(f"{name} must be a contiguous CUDA tensor")
+    _check(lib().tt_emb_dense_set_table(h, table.data_ptr(), None if grad is None else grad.data_ptr(),
+                                        dtype_code(table.dtype if grad is None else grad.dtype)),
+           "tt_emb_dense_set_table")
+
+
+def tt_emb_dense_workspace_size(h, max_tokens: int) -> int:
+    out = ctypes.c_size_t()
+    _check(lib().tt_emb_dense_workspace_size(h, int(max_tokens), ctypes.byref(out)), "tt_emb_dense_workspace_size")
+    return int(out.value)
+
+
+def tt_emb_dense_set_workspace(h, workspace, max_tokens: int):
+    import torch
+    ptr = _dev_ptr(workspace, torch.uint8, "workspace")
+    _check(lib().tt_emb_dense_set_workspace(h, ptr, workspace.numel(), int(max_tokens)),
+           "tt_emb_dense_set_workspace")
+
+
+def tt_emb_dense_forward(h, tokens, out, dim: int, stream=None):
+    ptr, nbytes, n = _tokens(tokens)
+    optr, otype, stride = _rows(out, n, dim, "out")
+    _check(lib().tt_emb_dense_forward(h, ptr, nbytes, n, optr, otype, stride, _stream(stream)),
+           "tt_emb_dense_forward")
+
+
+def tt_emb_dense_backward(h, tokens, grad_out, dim: int, accumulate: bool = False, stream=None):
+    ptr, nbytes, n = _tokens(tokens)
+    gptr, gtype, stride = _rows(grad_out, n, dim, "grad_out")
+    _check(lib().tt_emb_dense_backward(h, ptr, nbytes, n, gptr, gtype, stride, 1 if accumulate else 0,
+                                       _stream(stream)), "tt_emb_dense_backward")
+
+
+def tt_emb_dense_sync(h):
+    _check(lib().tt_emb_dense_sync(h), "tt_emb_dense_sync")
+
+
+def tt_emb_dense_last_error(h) -> int:
+    return int(lib().tt_emb_dense_last_error(h))
+
+
+def tt_emb_dense_destroy(h):
+    if h is not None and h.value:
+        lib().tt_emb_dense_destroy(h)
+
+
+def tt_emb_status_word(h) -> int:
+    """Device address of a TT handle's status word (0 for a null handle)."""
+    return lib().tt_emb_status_word(h) or 0
+
+
+def tt_emb_dense_status_word(h) -> int:
+    return lib().tt_emb_dense_status_word(h) or 0
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+def tt_emb_adamw_create(tensors, options: AdamWOptions, steps):
+    """tensors: a list of AdamWTensor; steps: a CUDA int64 tensor of one value."""
+    import torch
+    arr = (AdamWTensor * len(tensors))(*tensors)
+    h = ctypes.c_void_p()
+    _check(lib().tt_emb_adamw_create(len(tensors), arr, ctypes.byref(options),
+                                     _dev_ptr(steps, torch.int64, "steps"), ctypes.byref(h)), "tt_emb_adamw_create")
+    return h
+
+
+def tt_emb_adamw_step(h, lr, stream=None):
+    """lr: a number, or a CUDA float32 tensor of one value that the device reads."""
+    import torch
+    at = None
+    if isinstance(lr, torch.Tensor):
+        if lr.numel() != 1:
+            raise ValueError("lr must have one value")
+        at, lr = _dev_ptr(lr, torch.float32, "lr"), 0.0
+    _check(lib().tt_emb_adamw_step(h, float(lr), at, _stream(stream)), "tt_emb_adamw_step")
+
+
+def tt_emb_adamw_destroy(h):
+    if h is not None and h.value:
+        lib().tt_emb_adamw_destroy(h)

@@ -1025,6 +1025,8 @@ int tt_emb_last_error(tt_emb_t h)
     return rc;
 }
 
+const int32_t* tt_emb_status_word(tt_emb_t h) { return h ? h->d_status : nullptr; }
+
 int tt_emb_set_probe(tt_emb_t h, uint64_t* records, int32_t max_blocks)
 {
     if (!h || max_blocks < 0 || (records && max_blocks == 0)) return note(h, TT_ERR_ARG);

@@ -1,0 +1,108 @@
+"""DenseEmbedding: one dense table, its scaled lookup and its gradient.
+
+The tables that are not worth compressing (a model's token table, small categorical
+ones) live beside the TT tables: same library, same streams, same errors.  As in
+``embedding.py``, PyTorch supplies device memory and the current stream only.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import abi
+
+
+def on_device(device: torch.device):
+    """Makes `device` current for the library's calls where another one is."""
+    return torch.cuda.device(device)
+
+
+class DenseEmbedding:
+    """A table of num_rows rows of dim values (float32, bfloat16 or float16).
+
+    ``forward`` returns scale * table[tokens]; ``backward`` the gradient of the table for an
+    upstream gradient of those rows.  padding_idx: a row that receives no gradient.
+    """
+
+    def __init__(self, num_rows: int, dim: int, dtype: torch.dtype = torch.float32, scale: float = 1.0,
+                 padding_idx: int | None = None, device="cuda"):
+        if padding_idx is not None and not 0 <= padding_idx < num_rows:
+            raise ValueError(f"padding_idx must be in [0, {num_rows}), got {padding_idx}")
+        self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        with on_device(self.device):
+            self.handle = abi.tt_emb_dense_create(num_rows, dim, dtype, scale,
+                                                  -1 if padding_idx is None else padding_idx)
+        self.num_rows, self.dim, self.dtype = int(num_rows), int(dim), dtype
+        self.table = None
+        self.grad = None
+        self._ws = None
+        self._ws_tokens = -1
+
+    def _check(self, t, name: str, dtype=None):
+        if not isinstance(t, torch.Tensor) or t.device != self.device:
+            raise TypeError(f"{name} must be a tensor on {self.device}")
+        if dtype is not None and t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+
+    def set_table(self, table: torch.Tensor, grad: torch.Tensor | None = None, with_grad: bool = True):
+        """table: contiguous [num_rows, dim] (borrowed).  grad: a buffer for its gradient of the same
+        shape, of any of the three types; allocated in the table's type if not given."""
+        self._check(table, "table", self.dtype)
+        if tuple(table.shape) != (self.num_rows, self.dim):
+            raise ValueError(f"table has shape {tuple(table.shape)}")
+        if grad is not None:
+            self._check(grad, "grad")
+            if tuple(grad.shape) != tuple(table.shape):
+                raise ValueError(f"grad has shape {tuple(grad.shape)}")
+        elif with_grad:
+            grad = torch.empty_like(table)
+        abi.tt_emb_dense_set_table(self.handle, table, grad)
+        self.table, self.grad = table, grad
+
+    def reserve(self, max_tokens: int):
+        """Allocates (or grows) the backward's workspace for up to this many tokens."""
+        if max_tokens <= self._ws_tokens:
+            return
+        nbytes = abi.tt_emb_dense_workspace_size(self.handle, max_tokens)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        abi.tt_emb_dense_set_workspace(self.handle, ws, max_tokens)
+        self._ws, self._ws_tokens = ws, max_tokens
+
+    def forward(self, tokens: torch.Tensor, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                stream=None) -> torch.Tensor:
+        """scale * table[tokens], in out's type, or out_dtype, or the table's.
+
+        out: contiguous, or [n, dim] with rows any distance of at least dim values apart."""
+        self._check(tokens, "tokens")
+        with on_device(self.device):
+            if out is None:
+                out = torch.empty(*tokens.shape, self.dim, dtype=out_dtype or self.dtype, device=self.device)
+            else:
+                self._check(out, "out", out_dtype)
+            abi.tt_emb_dense_forward(self.handle, tokens, out, self.dim, stream)
+        return out
+
+    def backward(self, tokens: torch.Tensor, grad_out: torch.Tensor, accumulate: bool = False,
+                 stream=None) -> torch.Tensor:
+        """The table's gradient for these tokens, written to (or added to) ``self.grad``."""
+        self._check(tokens, "tokens")
+        self._check(grad_out, "grad_out")
+        with on_device(self.device):
+            self.reserve(tokens.numel())
+            abi.tt_emb_dense_backward(self.handle, tokens, grad_out, self.dim, accumulate, stream)
+        return self.grad
+
+    def sync(self):
+        abi.tt_emb_dense_sync(self.handle)
+
+    def close(self):
+        if getattr(self, "handle", None) is not None:
+            abi.tt_emb_dense_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
