@@ -505,7 +505,7 @@ typedef struct {
 
 typedef struct {
     double beta1, beta2;     /* in [0, 1) */
-    double eps;              /* > 0, also when rounded to float32 */
+    double eps;              /* a normal float32 at least (1.2e-38) */
     int32_t state_bits;      /* 32 or 8 */
     int32_t reserved;        /* must be zero */
     uint64_t seed;           /* of the 8-bit moments' rounding */
@@ -532,9 +532,13 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
  * written anew for each block: the scale is the largest finite magnitude / 448 (0, with all
  * codes 0, where that magnitude is below 2^-100), m goes to the nearest code, and sqrt(v) up or
  * down at random, so that steps smaller than the code's are not lost on average; a v above zero
- * keeps the least code at least, and values that are not finite become NaN.  The random bits are
- * the outputs of SplitMix64 started from (seed, t): four values in a row, counted over all tensors
- * with each rounded up to whole blocks, take the four 16-bit parts of one output.
+ * (1.2e-38 at least) keeps the least code at least, and values that are not finite become NaN.
+ * The random bits are the outputs of SplitMix64 from the state mix(seed + t * 0x9E3779B97F4A7C15):
+ * four values in a row, counted over all tensors with each rounded up to whole blocks, take the
+ * four 16-bit parts of one output, and the code is that of the scaled root with 16 random bits
+ * added below the bits kept.  For them every product, sum, root and reciprocal (values are scaled
+ * by 448 x (1 / magnitude)) is rounded to nearest on its own, so that a step's codes and scales can
+ * be computed bit for bit elsewhere, of a v of 2^-102 at least.
  *   lr           host; or lr_device (device float32 [1], may be NULL) in its place, so that a
  *                captured graph follows a schedule
  * Enqueues on stream.  Returns TT_OK, TT_ERR_ARG, TT_ERR_STATE (another device than the

@@ -2,12 +2,16 @@
 // block of 256 values.
 //
 // Every value is read and written once: 28 bytes a value in fp32, 10 with 16-bit weights and
-// gradients and 8-bit moments, for about 15 operations, so memory bounds it.  A warp takes one
-// block of 256 values, eight in a row per lane: 16-byte loads of every operand, all issued
-// before the first use, and a block's largest magnitude is one warp reduction, so an 8-bit
-// block is read, updated, scaled and written without leaving registers.
+// gradients and 8-bit moments.  A warp takes one block of 256 values, eight per lane: all loads
+// are issued before the first use, and a block's largest magnitude is one warp reduction, so an
+// 8-bit block is read, updated, scaled and written without leaving registers.  In 32 bits memory
+// bounds it; at 10 bytes a value the card's memory delivers a value every 55 issue slots, so
+// there the arithmetic is packed in pairs and kept short, and a warp's next blocks travel to
+// shared memory while it computes.
+#include <float.h>
 #include <math.h>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "types.cuh"
@@ -19,6 +23,7 @@ namespace {
 constexpr int kBlk = TT_ADAMW_BLOCK;
 constexpr int kPerLane = kBlk / 32;
 constexpr int kWarps = 8;
+constexpr int kPerWarp = 16;          // blocks of a warp in a tile at most (half a warp of scales)
 constexpr int kLaunchTensors = 128;   // tensors of one launch; their records travel as its parameters
 constexpr uint64_t kGamma = 0x9E3779B97F4A7C15ull;
 
@@ -31,17 +36,20 @@ struct Rec {
     float* vs;
     const int32_t* guard;
     int64_t size;
-    int64_t blk0;      // first block of the tensor, counted over the launch
+    int64_t tile0;     // first tile of the tensor, counted over the launch
     uint64_t quad0;    // first group of four values, counted over all tensors of the optimiser
-    double decay;
+    float decay;
+    int32_t wide;      // every buffer begins at a place that vector loads can take
 };
 
 struct List {
     int32_t count;
     int32_t last;      // the step's last launch: it advances the step count
-    int64_t blocks;
+    int32_t per_warp;  // a tile is up to kWarps * per_warp blocks of one tensor
+    int32_t pad;
+    int64_t tiles;
     double log_b1, log_b2;
-    float b1, b2, c1, c2, eps;   // c = 1 - b, rounded from 64 bits
+    float b1, b2, c1, c2, eps, one;   // c = 1 - b, rounded from 64 bits
     uint64_t seed;
     int64_t* steps;
     uint32_t* ticket;
@@ -56,189 +64,523 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z)
     return z ^ (z >> 31);
 }
 
-// largest finite magnitude of a block of 256 (zero below 2^-100, where 448 / a could overflow)
-__device__ __forceinline__ float block_max(const float (&x)[kPerLane])
+// Pairs of fp32 values in one register pair: one instruction for both.  The moments' products and
+// sums are each rounded on their own, as the header says: a sum of two products is written
+// a * one + b with a factor the compiler cannot see, since it fuses packed products and sums, .rn
+// or not.
+struct F2 { float x, y; };
+__device__ __forceinline__ uint64_t bits2(F2 a) { uint64_t r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y)); return r; }
+__device__ __forceinline__ F2 pair(uint64_t r) { F2 a; asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r)); return a; }
+__device__ __forceinline__ F2 both(float x) { return {x, x}; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair(r);
+}
+// 1 / x (normal x) and the root of x within an ulp: of the update only, not of what an 8-bit code depends on
+__device__ __forceinline__ float rcp(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float root(float x)
+{
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Two roots to nearest, in eight instructions and without a branch.  With r near 1 / sqrt(x), s = x r is
+// near the root and e = x - s^2, which the fused multiply-add gives exactly, is what its square is off;
+// Heron's step s + e / (2 s) = s + e r / 2 then rounds once.  Equal to sqrtf for every mantissa and both
+// parities of the exponent from 2^-102 on; below that e loses places.  0 gives 0, values below the
+// least normal number a root that is too small, infinity NaN.
+__device__ __forceinline__ F2 root2(F2 x)
+{
+    F2 r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(x.x, FLT_MIN)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(x.y, FLT_MIN)));
+    const F2 s = mul2(x, r);
+    return fma2(fma2({-s.x, -s.y}, s, x), mul2(r, both(0.5f)), s);
+}
+
+// 1 / x to nearest, without a branch, by a Newton step on an approximation r: 1 - x r is exact in a fused
+// multiply-add, and r + r (1 - x r) rounds once
+__device__ __forceinline__ float inverse(float x)
+{
+    const float r = rcp(x);
+    return __fmaf_rn(__fmaf_rn(-x, r, 1.f), r, r);
+}
+
+constexpr int kPairs = kPerLane / 2;
+
+// largest magnitude of a block's values, NaN if one of them is; the same in every lane
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float block_max(const F2 (&x)[kPairs])
 {
     float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        const float y = fabsf(x[i]);
-        a = y < INFINITY ? fmaxf(a, y) : a;
-    }
-    // magnitudes order like their bits, so one integer reduction does
-    a = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
-    return a < 0x1p-100f ? 0.f : a;
+    for (int i = 0; i < kPairs; ++i) a = max3(a, x[i].x, x[i].y);
+    // magnitudes order like their bits, NaN above infinity
+    return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
 }
 
-__device__ __forceinline__ float decode8(uint32_t code)   // e4m3 to fp32, exact
+// the same of the finite values only (blocks that hold others take this second look)
+__device__ __noinline__ float finite_max(F2 a, F2 b, F2 c, F2 d)
 {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)code, __NV_E4M3);
-    return __half2float(__half(h));
+    F2 x[kPairs] = {a, b, c, d};
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        if (!(fabsf(x[i].x) < INFINITY)) x[i].x = 0.f;
+        if (!(fabsf(x[i].y) < INFINITY)) x[i].y = 0.f;
+    }
+    return block_max(x);
+}
+
+// four codes, NaN's in the place of those whose values are not finite
+__device__ __noinline__ uint32_t without_infinities(uint32_t codes, F2 a, F2 b)
+{
+    const float x[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (!(fabsf(x[i]) < INFINITY)) codes = (codes & ~(255u << (8 * i))) | 0x7fu << (8 * i);
+    return codes;
+}
+
+__device__ __forceinline__ F2 decode8(uint32_t codes)   // two e4m3 codes (low 16 bits) to fp32, exact
+{
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return {f.x, f.y};
+}
+
+// A lane's eight values are kGroups runs of kRun neighbours, kRun * 32 apart: loads of 16 bytes a
+// lane and 512 a warp in fp32, and of 16-bit values where no operand is wider than that.
+template <typename P, typename G, bool k8> struct Shape {
+    static constexpr int run = k8 && sizeof(P) == 2 && sizeof(G) == 2 ? 8 : 4;
+    static constexpr int groups = kPerLane / run;
+};
+
+template <int run, typename T>
+__device__ __forceinline__ void widen(const Pack<T, run>& q, F2* x)
+{
+#pragma unroll
+    for (int i = 0; i < run / 2; ++i) x[i] = {to_f32(q.v[2 * i]), to_f32(q.v[2 * i + 1])};
+}
+template <int run, typename T>
+__device__ __forceinline__ Pack<T, run> narrow(const F2* x)
+{
+    Pack<T, run> q;
+#pragma unroll
+    for (int i = 0; i < run / 2; ++i) {
+        q.v[2 * i] = from_f32<T>(x[i].x);
+        q.v[2 * i + 1] = from_f32<T>(x[i].y);
+    }
+    return q;
+}
+struct Factors {
+    F2 one, b1, c1, b2, c2, eps, inv_root2, keep, minus_lr;
+    uint64_t start;
+};
+
+// A tile, and a warp's share of it: `count` blocks in a row.
+struct Tile {
+    int64_t first;
+    int count;
+    int whole;         // those of them that are full and at places that vector loads can take
+    __device__ __forceinline__ Tile(const Rec& r, const List& L, int64_t tile)
+    {
+        const int64_t from = (tile - r.tile0) * (L.per_warp * kWarps), blocks = ceil_div(r.size, kBlk);
+        const int here = (int)min64(L.per_warp * kWarps, blocks - from), each = (here + kWarps - 1) / kWarps;
+        const int skip = (int)(threadIdx.x >> 5) * each;
+        first = from + skip;
+        count = max(0, min(each, here - skip));
+        whole = r.wide ? (int)max((int64_t)0, min64(count, r.size / kBlk - first)) : 0;
+    }
+};
+__device__ __forceinline__ const Rec& tensor_of(const List& L, int64_t tile)
+{
+    int lo = 0, hi = L.count;   // r[lo].tile0 <= tile < r[hi].tile0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (L.r[mid].tile0 <= tile) lo = mid; else hi = mid;
+    }
+    return L.r[lo];
+}
+
+// One lane's part of a block as it lies in memory.
+template <typename P, typename G, bool k8> struct Raw {
+    static constexpr int run = Shape<P, G, k8>::run, groups = Shape<P, G, k8>::groups;
+    using M = std::conditional_t<k8, uint8_t, float>;
+    using Moment = std::conditional_t<k8, std::conditional_t<run == 8, uint2, uint32_t>, Pack<float, run>>;
+    Pack<P, run> p[groups];
+    Pack<G, run> g[groups];
+    Moment m[groups], v[groups];
+    float ms, vs;
+    __device__ __forceinline__ uint32_t codes(const Moment (&c)[groups], int w) const   // four codes of the lane's eight
+    {
+        if constexpr (run == 8) return w ? c[0].y : c[0].x;
+        else return c[w];
+    }
+    __device__ __forceinline__ void set_codes(Moment (&c)[groups], int w, uint32_t x)
+    {
+        if constexpr (run == 8) (w ? c[0].y : c[0].x) = x;
+        else c[w] = x;
+    }
+};
+
+// The lane's values in memory, moving from one of the warp's blocks to the next.
+template <typename P, typename G, bool k8> struct Place {
+    using R = Raw<P, G, k8>;
+    static constexpr int run = R::run, step = kBlk;
+    P* p;
+    const G* g;
+    typename R::M *m, *v;
+    __device__ __forceinline__ Place(const Rec& r, int64_t blk, int lane)
+    {
+        const int64_t e = blk * kBlk + lane * run;
+        p = (P*)r.param + e;
+        g = (const G*)r.grad + e;
+        m = (typename R::M*)r.m + e;
+        v = (typename R::M*)r.v + e;
+    }
+    __device__ __forceinline__ void next(int blocks)
+    {
+        p += blocks * step;
+        g += blocks * step;
+        m += blocks * step;
+        v += blocks * step;
+    }
+};
+
+// n values at p (none of the others is touched) into or out of a vector of N
+template <int N, typename Q, typename T>
+__device__ __forceinline__ Q some_in(const T* p, int n)
+{
+    Q q;
+    memset(&q, 0, sizeof(q));
+    T x[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < n ? p[i] : T(0);
+    memcpy(&q, x, sizeof(q));
+    return q;
+}
+template <int N, typename Q, typename T>
+__device__ __forceinline__ void some_out(T* p, const Q& q, int n)
+{
+    T x[N];
+    memcpy(x, &q, sizeof(q));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (i < n) p[i] = x[i];
 }
 
 template <typename P, typename G, bool k8>
-__global__ void __launch_bounds__(kWarps * 32) k_adamw(const __grid_constant__ List L, float lr,
-                                                       const float* __restrict__ lr_device)
+__device__ __forceinline__ void store_block(const Place<P, G, k8>& at, int from, const Raw<P, G, k8>& x, bool whole, int64_t left)
 {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    using R = Raw<P, G, k8>;
+#pragma unroll
+    for (int k = 0; k < R::groups; ++k) {
+        const int o = from + k * 32 * R::run;
+        if (whole) {
+            *(Pack<P, R::run>*)(at.p + o) = x.p[k];
+            *(typename R::Moment*)(at.m + o) = x.m[k];
+            *(typename R::Moment*)(at.v + o) = x.v[k];
+        } else {
+            const int n = (int)max((int64_t)0, min64(R::run, left - k * 32 * R::run));
+            some_out<R::run>(at.p + o, x.p[k], n);
+            some_out<R::run>(at.m + o, x.m[k], n);
+            some_out<R::run>(at.v + o, x.v[k], n);
+        }
+    }
+}
+
+// `random`: the lane's place in the stream of random words
+template <typename P, typename G, bool k8>
+__device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const Factors& f)
+{
+    constexpr int run = Shape<P, G, k8>::run, groups = Shape<P, G, k8>::groups;
+    F2 p[kPairs], g[kPairs], m[kPairs], v[kPairs], u[kPairs];
+#pragma unroll
+    for (int k = 0; k < groups; ++k) {
+        widen<run>(b.p[k], p + k * run / 2);
+        widen<run>(b.g[k], g + k * run / 2);
+        if constexpr (!k8) {
+            widen<run>(b.m[k], m + k * run / 2);
+            widen<run>(b.v[k], v + k * run / 2);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        if constexpr (k8) {
+            m[i] = mul2(decode8(b.codes(b.m, i / 2) >> (16 * (i & 1)) & 0xffffu), both(b.ms));
+            u[i] = mul2(decode8(b.codes(b.v, i / 2) >> (16 * (i & 1)) & 0xffffu), both(b.vs));
+            v[i] = mul2(u[i], u[i]);
+        }
+        m[i] = fma2(mul2(m[i], f.b1), f.one, mul2(g[i], f.c1));
+        v[i] = fma2(mul2(v[i], f.b2), f.one, mul2(mul2(g[i], g[i]), f.c2));
+        if constexpr (k8) u[i] = root2(v[i]);
+        else u[i] = {root(v[i].x), root(v[i].y)};
+    }
+    float am = 0.f, au = 0.f;
+    bool odd = false;                                // a value of the block is not finite
+    if constexpr (k8) {
+        am = block_max(m);
+        au = block_max(u);
+        odd = !(am < INFINITY && au < INFINITY);
+        if (odd) {
+#pragma unroll
+            for (int i = 0; i < kPairs; ++i) {
+                if (v[i].x == INFINITY) u[i].x = INFINITY;
+                if (v[i].y == INFINITY) u[i].y = INFINITY;
+            }
+            am = finite_max(m[0], m[1], m[2], m[3]);
+            au = finite_max(u[0], u[1], u[2], u[3]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+        const F2 den = fma2(u[i], f.inv_root2, f.eps);
+        p[i] = fma2(mul2(m[i], f.minus_lr), {rcp(den.x), rcp(den.y)}, mul2(p[i], f.keep));
+    }
+    if constexpr (k8) {
+        if (am < 0x1p-100f) am = 0.f;
+        if (au < 0x1p-100f) au = 0.f;
+        b.ms = am * (1.f / 448.f);
+        b.vs = au * (1.f / 448.f);
+        const F2 im = both(am > 0.f ? __fmul_rn(448.f, inverse(am)) : 0.f), iu = both(au > 0.f ? __fmul_rn(448.f, inverse(au)) : 0.f);
+#pragma unroll
+        for (int w = 0; w < kPairs / 2; ++w) {       // four neighbours: one word of random bits
+            const uint64_t word = mix64(random + (run == 8 ? w : w * 32) * kGamma);
+            uint32_t code[4], mc[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 2 * w + h;
+                const F2 x = mul2(m[i], im);
+                mc[h] = __nv_cvt_float2_to_fp8x2(make_float2(x.x, x.y), __NV_SATFINITE, __NV_E4M3);
+                // times 2^-120 the format's exponents are those of fp32 (its subnormals fp32's), so that
+                // the code is the top bits; 16 random ones below them round up or down.  All are
+                // shifted by 4, which makes the code the top byte.  A product a few ulps above 448 still
+                // gives 448's code, as the random bits end 4 places above the lowest.
+                const F2 y = mul2(mul2(u[i], iu), both(0x1p-120f));
+                const uint32_t part = (uint32_t)(word >> (32 * h));
+                code[2 * h] = (__float_as_uint(y.x) << 4) + ((part & 0xffffu) << 8);
+                code[2 * h + 1] = (__float_as_uint(y.y) << 4) + (part >> 16 << 8);
+                // a root above zero (its bits are above 2^24) keeps the least code at least
+                code[2 * h] = max(code[2 * h], min(__float_as_uint(u[i].x), 1u << 24));
+                code[2 * h + 1] = max(code[2 * h + 1], min(__float_as_uint(u[i].y), 1u << 24));
+            }
+            b.set_codes(b.m, w, mc[0] | mc[1] << 16);
+            b.set_codes(b.v, w, __byte_perm(__byte_perm(code[0], code[1], 0x0073), __byte_perm(code[2], code[3], 0x0073), 0x5410));
+        }
+        if (odd) {   // the format has no infinity, and conversion saturates
+#pragma unroll
+            for (int w = 0; w < kPairs / 2; ++w) {
+                b.set_codes(b.m, w, without_infinities(b.codes(b.m, w), m[2 * w], m[2 * w + 1]));
+                b.set_codes(b.v, w, without_infinities(b.codes(b.v, w), u[2 * w], u[2 * w + 1]));
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < groups; ++k) {
+        b.p[k] = narrow<run, P>(p + k * run / 2);
+        if constexpr (!k8) {
+            b.m[k] = narrow<run, float>(m + k * run / 2);
+            b.v[k] = narrow<run, float>(v + k * run / 2);
+        }
+    }
+}
+
+__device__ __forceinline__ Factors factors(const List& L, int64_t t, float lr)
+{
+    Factors f;
+    // 1 - beta^t without cancellation: the product is formed in 64 bits, the rest in 32
+    f.minus_lr = both(lr / expm1f((float)((double)t * L.log_b1)));
+    f.inv_root2 = both(1.f / sqrtf(-expm1f((float)((double)t * L.log_b2))));
+    f.one = both(L.one);
+    f.b1 = both(L.b1);
+    f.c1 = both(L.c1);
+    f.b2 = both(L.b2);
+    f.c2 = both(L.c2);
+    f.eps = both(L.eps);
+    f.start = mix64((uint64_t)t * kGamma + L.seed);
+    return f;
+}
+
+// The block that is last to get here (all have read the count by then) advances it.
+__device__ __forceinline__ void count_step(const List& L, int64_t t)
+{
+    if (!L.last) return;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(L.ticket, 1u) == gridDim.x - 1) {
+            *L.ticket = 0;
+            *L.steps = t;
+        }
+    }
+}
+
+template <typename P, typename G>
+__global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constant__ List L, float lr,
+                                                          const float* __restrict__ lr_device)
+{
+    using R = Raw<P, G, false>;
+    const int lane = threadIdx.x & 31;
     const int64_t t = *L.steps + 1;
     if (lr_device) lr = *lr_device;
-    // 1 - beta^t without cancellation: the product is formed in 64 bits, the rest in 32
-    const float fix1 = -expm1f((float)((double)t * L.log_b1));
-    const float root2 = sqrtf(-expm1f((float)((double)t * L.log_b2)));
-    const float lr1 = lr / fix1;
-    const uint64_t start = k8 ? mix64((uint64_t)t * kGamma + L.seed) : 0;
-
-    for (int64_t b = (int64_t)blockIdx.x * kWarps + wid; b < L.blocks; b += (int64_t)gridDim.x * kWarps) {
-        int lo = 0, hi = L.count;   // r[lo].blk0 <= b < r[hi].blk0
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (L.r[mid].blk0 <= b) lo = mid; else hi = mid;
-        }
-        const Rec& r = L.r[lo];
+    Factors f = factors(L, t, lr);
+    for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
+        const Rec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
-        const int64_t blk = b - r.blk0;
-        const int64_t e0 = blk * kBlk + lane * kPerLane;
-        const int n = (int)max((int64_t)0, min64(kPerLane, r.size - e0));   // this lane's values
-        P* p_at = (P*)r.param + e0;
-        const G* g_at = (const G*)r.grad + e0;
-        const uintptr_t where = (uintptr_t)p_at | (uintptr_t)g_at | (k8 ? 0 : (uintptr_t)r.m | (uintptr_t)r.v);
-        const bool wide = n == kPerLane && (where & 15) == 0 &&
-                          (!k8 || (((uintptr_t)r.m | (uintptr_t)r.v) & 7) == 0);
-
-        float p[kPerLane], g[kPerLane], m[kPerLane], v[kPerLane];
-        uint32_t mc[kPerLane], vc[kPerLane];
-        float ms = 0.f, vs = 0.f;
-        if (k8) {
-            ms = r.ms[blk];
-            vs = r.vs[blk];
-        }
-        if (wide) {
-            load_pack(p_at, p);
-            load_pack(g_at, g);
-            if (k8) {
-                const uint2 a = *(const uint2*)((const uint8_t*)r.m + e0), c = *(const uint2*)((const uint8_t*)r.v + e0);
+        f.keep = both(fmaf(-lr, r.decay, 1.f));
+        const int64_t blk = (b - r.tile0) * kWarps + (threadIdx.x >> 5);
+        const int64_t left = r.size - (blk * kBlk + lane * R::run);
+        if (blk * kBlk >= r.size) continue;
+        const bool whole = r.wide && (blk + 1) * kBlk <= r.size;
+        const Place<P, G, false> at(r, blk, lane);
+        R x;
 #pragma unroll
-                for (int i = 0; i < kPerLane; ++i) {
-                    mc[i] = ((i < 4 ? a.x : a.y) >> (8 * (i & 3))) & 255u;
-                    vc[i] = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 255u;
-                }
+        for (int k = 0; k < R::groups; ++k) {
+            const int o = k * 32 * R::run;
+            if (whole) {
+                x.p[k] = *(const Pack<P, R::run>*)(at.p + o);
+                x.g[k] = *(const Pack<G, R::run>*)(at.g + o);
+                x.m[k] = *(const typename R::Moment*)(at.m + o);
+                x.v[k] = *(const typename R::Moment*)(at.v + o);
             } else {
-                load_pack((const float*)r.m + e0, m);
-                load_pack((const float*)r.v + e0, v);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                const bool in = i < n;
-                p[i] = in ? to_f32(p_at[i]) : 0.f;
-                g[i] = in ? to_f32(g_at[i]) : 0.f;
-                if (k8) {
-                    mc[i] = in ? ((const uint8_t*)r.m)[e0 + i] : 0u;
-                    vc[i] = in ? ((const uint8_t*)r.v)[e0 + i] : 0u;
-                } else {
-                    m[i] = in ? ((const float*)r.m)[e0 + i] : 0.f;
-                    v[i] = in ? ((const float*)r.v)[e0 + i] : 0.f;
-                }
+                const int n = (int)max((int64_t)0, min64(R::run, left - o));
+                x.p[k] = some_in<R::run, Pack<P, R::run>>(at.p + o, n);
+                x.g[k] = some_in<R::run, Pack<G, R::run>>(at.g + o, n);
+                x.m[k] = some_in<R::run, typename R::Moment>(at.m + o, n);
+                x.v[k] = some_in<R::run, typename R::Moment>(at.v + o, n);
             }
         }
-        const float keep = (float)(1.0 - (double)lr * r.decay);
-        float u[kPerLane];
-#pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            if (k8) {
-                m[i] = __fmul_rn(decode8(mc[i]), ms);
-                u[i] = __fmul_rn(decode8(vc[i]), vs);
-                v[i] = __fmul_rn(u[i], u[i]);
-            }
-            // each operation rounded on its own (no fused multiply-add), and the root to nearest, so
-            // that an 8-bit code is a function of the formula and not of the instructions chosen
-            m[i] = __fadd_rn(__fmul_rn(m[i], L.b1), __fmul_rn(g[i], L.c1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], L.b2), __fmul_rn(__fmul_rn(g[i], g[i]), L.c2));
-            u[i] = __fsqrt_rn(v[i]);
-            p[i] = p[i] * keep - lr1 * m[i] / (u[i] / root2 + L.eps);
-        }
-        if (k8) {
-            const float am = block_max(m), au = block_max(u);
-            const float im = am > 0.f ? 448.f / am : 0.f, iu = au > 0.f ? 448.f / au : 0.f;
-            uint64_t word[2];
-            const uint64_t q = r.quad0 + (uint64_t)(e0 >> 2);
-            word[0] = mix64(start + (q + 1) * kGamma);
-            word[1] = mix64(start + (q + 2) * kGamma);
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i) {
-                // an infinite moment is NaN in 8 bits, which has no infinity; conversion saturates
-                const float x = fabsf(m[i]) < INFINITY ? __fmul_rn(m[i], im) : NAN;
-                mc[i] = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-                // times 2^-120 the format's exponents are those of fp32 (its subnormals fp32's), so
-                // that the code is the top bits; 16 random ones below them round up or down
-                const float y = __fmul_rn(fminf(__fmul_rn(u[i], iu), 448.f), 0x1p-120f);
-                const uint32_t part = (uint32_t)(word[i >> 2] >> (16 * (i & 3))) & 0xffffu;
-                const uint32_t c = (__float_as_uint(y) + (part << 4)) >> 20;
-                vc[i] = u[i] < INFINITY ? (u[i] > 0.f ? max(c, 1u) : 0u) : 0x7fu;
-            }
-            if (lane == 0) {
-                r.ms[blk] = am * (1.f / 448.f);
-                r.vs[blk] = au * (1.f / 448.f);
-            }
-        }
-        if (wide) {
-            store_pack(p_at, p);
-            if (k8) {
-                uint2 a = {0, 0}, c = {0, 0};
-#pragma unroll
-                for (int i = 0; i < kPerLane; ++i) {
-                    (i < 4 ? a.x : a.y) |= mc[i] << (8 * (i & 3));
-                    (i < 4 ? c.x : c.y) |= vc[i] << (8 * (i & 3));
-                }
-                *(uint2*)((uint8_t*)r.m + e0) = a;
-                *(uint2*)((uint8_t*)r.v + e0) = c;
-            } else {
-                store_pack((float*)r.m + e0, m);
-                store_pack((float*)r.v + e0, v);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kPerLane; ++i)
-                if (i < n) {
-                    p_at[i] = from_f32<P>(p[i]);
-                    if (k8) {
-                        ((uint8_t*)r.m)[e0 + i] = (uint8_t)mc[i];
-                        ((uint8_t*)r.v)[e0 + i] = (uint8_t)vc[i];
-                    } else {
-                        ((float*)r.m)[e0 + i] = m[i];
-                        ((float*)r.v)[e0 + i] = v[i];
-                    }
-                }
-        }
+        update<P, G, false>(x, 0, f);
+        store_block<P, G, false>(at, 0, x, whole, left);
     }
-
-    // The block that is last to get here (all have read the count by then) advances it.
-    if (L.last) {
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            __threadfence();
-            if (atomicAdd(L.ticket, 1u) == gridDim.x - 1) {
-                *L.ticket = 0;
-                *L.steps = t;
-            }
-        }
-    }
+    count_step(L, t);
 }
 
-template <typename P, typename G, bool k8>
-cudaError_t launch(const List& L, int sms, float lr, const float* lr_device, cudaStream_t s)
+template <int N>
+__device__ __forceinline__ void copy_async(void* to, const void* from)
 {
-    static int per_sm = 0;   // resident blocks of this kernel on an SM; a race writes the same value
-    if (per_sm == 0) {
-        int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_adamw<P, G, k8>, kWarps * 32, 0);
-        if (e != cudaSuccess) return e;
-        per_sm = n > 0 ? n : 1;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(N) : "memory");
+}
+
+constexpr int kFit8 = 3;     // blocks of threads on an SM: 80 registers; 64 would spill (740 against 779 us for 403 M values)
+constexpr int kStages = 2;   // blocks of a warp: one being computed, the next on its way
+
+// Each thread copies its own values to its own place in shared memory and reads them back, so the
+// copies need no barrier, only their own completion.
+template <typename P, typename G> struct Stage {
+    using R = Raw<P, G, true>;
+    Pack<P, R::run> p[R::groups][kWarps * 32];
+    Pack<G, R::run> g[R::groups][kWarps * 32];
+    typename R::Moment m[R::groups][kWarps * 32], v[R::groups][kWarps * 32];
+};
+
+template <typename P, typename G>
+__global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_constant__ List L, float lr,
+                                                          const float* __restrict__ lr_device)
+{
+    using R = Raw<P, G, true>;
+    __shared__ Stage<P, G> st[kStages];
+    const int lane = threadIdx.x & 31, me = threadIdx.x;
+    const int64_t t = *L.steps + 1;
+    if (lr_device) lr = *lr_device;
+    Factors f = factors(L, t, lr);
+    for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
+        const Rec& r = tensor_of(L, b);
+        if (r.guard && has_error(r.guard)) continue;
+        f.keep = both(fmaf(-lr, r.decay, 1.f));
+        const Tile w(r, L, b);
+        Place<P, G, true> at(r, w.first, lane);
+        // lane j < 16 holds the scale of m of the warp's block j, lane 16 + j that of v
+        float* const at_scale = (lane < 16 ? r.ms : r.vs) + w.first + (lane & 15);
+        const bool has_scale = (lane & 15) < w.count;
+        float scale = has_scale ? *at_scale : 0.f;
+        uint64_t random = f.start + (r.quad0 + (uint64_t)((w.first * kBlk + lane * R::run) / 4) + 1) * kGamma;
+        auto left = [&](int j) { return r.size - ((w.first + j) * kBlk + lane * R::run); };
+        // block j, which is `ahead` blocks behind where `at` stands, to a stage
+        auto fetch = [&](int j, int ahead, Stage<P, G>& s) {
+            const int far = ahead * Place<P, G, true>::step;
+            if (j < w.whole) {
+#pragma unroll
+                for (int k = 0; k < R::groups; ++k) {
+                    const int o = far + k * 32 * R::run;
+                    copy_async<sizeof(s.p[0][0])>(&s.p[k][me], at.p + o);
+                    copy_async<sizeof(s.g[0][0])>(&s.g[k][me], at.g + o);
+                    copy_async<sizeof(s.m[0][0])>(&s.m[k][me], at.m + o);
+                    copy_async<sizeof(s.v[0][0])>(&s.v[k][me], at.v + o);
+                }
+            } else if (j < w.count) {
+#pragma unroll
+                for (int k = 0; k < R::groups; ++k) {
+                    const int o = far + k * 32 * R::run;
+                    const int n = (int)max((int64_t)0, min64(R::run, left(j) - k * 32 * R::run));
+                    s.p[k][me] = some_in<R::run, Pack<P, R::run>>(at.p + o, n);
+                    s.g[k][me] = some_in<R::run, Pack<G, R::run>>(at.g + o, n);
+                    s.m[k][me] = some_in<R::run, typename R::Moment>(at.m + o, n);
+                    s.v[k][me] = some_in<R::run, typename R::Moment>(at.v + o, n);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) fetch(k, k, st[k]);
+        for (int j0 = 0; j0 < w.count; j0 += kStages) {
+#pragma unroll
+            for (int u = 0; u < kStages; ++u) {   // unrolled over the stages, so that their places are constants
+                const int j = j0 + u;
+                if (j >= w.count) break;
+                fetch(j + kStages - 1, u + kStages - 1, st[(u + kStages - 1) % kStages]);
+                asm volatile("cp.async.wait_group %0;" :: "n"(kStages - 1) : "memory");
+                const Stage<P, G>& s = st[u];
+                R x;
+#pragma unroll
+                for (int k = 0; k < R::groups; ++k) {
+                    x.p[k] = s.p[k][me];
+                    x.g[k] = s.g[k][me];
+                    x.m[k] = s.m[k][me];
+                    x.v[k] = s.v[k][me];
+                }
+                x.ms = __shfl_sync(kFull, scale, j);
+                x.vs = __shfl_sync(kFull, scale, 16 + j);
+                update<P, G, true>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f);
+                store_block<P, G, true>(at, u * Place<P, G, true>::step, x, j < w.whole, left(j));
+                if ((lane & 15) == j) scale = lane < 16 ? x.ms : x.vs;
+            }
+            at.next(kStages);
+            random += (uint64_t)(kStages * kBlk / 4) * kGamma;
+        }
+        if (has_scale) *at_scale = scale;
     }
-    int64_t grid = min64(ceil_div(L.blocks, kWarps), (int64_t)sms * per_sm);
+    count_step(L, t);
+}
+
+template <typename P, typename G>
+cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* lr_device, cudaStream_t s)
+{
+    // Blocks that stay and take tile after tile.  Two on an SM keep enough 32-bit loads on their way, and
+    // more of them spread the card's reads: 311 us for the rank-64 cores with three, 285 with two.
+    // In 8 bits as many as its launch bounds let fit.
+    int64_t grid = min64(L.tiles, (int64_t)sms * (k8 ? kFit8 : 2));
     if (grid < 1) grid = 1;
-    k_adamw<P, G, k8><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
+    if (k8) k_adamw8<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
+    else k_adamw32<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
     return cudaGetLastError();
 }
 
@@ -261,7 +603,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
     *out = nullptr;
     if (!tensors || !opt || !steps || ((uintptr_t)steps & 7) || count < 1) return TT_ERR_ARG;
     if (!(opt->beta1 >= 0.0 && opt->beta1 < 1.0 && opt->beta2 >= 0.0 && opt->beta2 < 1.0)) return TT_ERR_ARG;
-    if (!((float)opt->eps > 0.f && (float)opt->eps < INFINITY) || opt->reserved != 0) return TT_ERR_ARG;
+    if (!((float)opt->eps >= FLT_MIN && (float)opt->eps < INFINITY) || opt->reserved != 0) return TT_ERR_ARG;
     if (opt->state_bits != 32 && opt->state_bits != 8) return TT_ERR_ARG;
     const bool k8 = opt->state_bits == 8;
     const int sb = k8 ? 1 : 4;
@@ -300,9 +642,19 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         base.c1 = (float)(1.0 - opt->beta1);
         base.c2 = (float)(1.0 - opt->beta2);
         base.eps = (float)opt->eps;
+        base.one = 1.f;
         base.seed = opt->seed;
         base.steps = steps;
         base.ticket = h->ticket;
+        // In 8 bits, where instructions bound, a warp takes up to 16 blocks of a tensor at a time, which
+        // spreads what it does once a tile (869 us for 403 M values against 1003 with 4); fewer where
+        // the list has not that many for every warp that fits on the card.  In 32 bits, where memory
+        // bounds, it takes one, so that the whole card reads neighbouring places (284 us for the 55 M
+        // values of the rank-64 cores against 299 with 4 and 303 with 16).
+        int64_t all = 0;
+        for (int32_t i = 0; i < count; ++i) all += ceil_div(tensors[i].size, kBlk);
+        const int64_t warps = (int64_t)h->sms * kFit8 * kWarps;
+        base.per_warp = (int32_t)(!k8 || all / warps < 1 ? 1 : all / warps > kPerWarp ? kPerWarp : all / warps);
         uint64_t quad = 0;
         for (int32_t i = 0; i < count; ++i) {
             const tt_emb_adamw_tensor& x = tensors[i];
@@ -316,9 +668,11 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
                     part = &h->parts.back();
                 }
                 List& L = part->list;
-                L.r[L.count++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.m_scale, x.v_scale, x.guard,
-                                  x.size, L.blocks, quad, x.weight_decay};
-                L.blocks += blocks;
+                const uintptr_t at = (uintptr_t)x.param | (uintptr_t)x.grad | (k8 ? 0 : (uintptr_t)x.exp_avg | (uintptr_t)x.exp_avg_sq);
+                const uintptr_t at8 = k8 ? (uintptr_t)x.exp_avg | (uintptr_t)x.exp_avg_sq : 0;
+                L.r[L.count++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.m_scale, x.v_scale, x.guard, x.size,
+                                  L.tiles, quad, (float)x.weight_decay, (at & 15) == 0 && (at8 & 7) == 0};
+                L.tiles += ceil_div(blocks, L.per_warp * kWarps);
             }
             quad += (uint64_t)blocks * (kBlk / 4);
         }
@@ -346,8 +700,7 @@ int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_str
             return by_type(part.gtype, [&](auto g) {
                 using P = decltype(p);
                 using G = decltype(g);
-                return h->k8 ? launch<P, G, true>(part.list, h->sms, lr, lr_device, s)
-                             : launch<P, G, false>(part.list, h->sms, lr, lr_device, s);
+                return launch_step<P, G>(h->k8, part.list, h->sms, lr, lr_device, s);
             });
         });
         if (e != cudaSuccess) return TT_ERR_CUDA;

@@ -125,7 +125,7 @@ def _rule8(p, g, mc, vc, ms, vs, first, t, lr, wd, seed):
             return np.where(a < f(2.0 ** -100), f(0), a)
 
         am, au = top(m), top(u)
-        im, iu = (np.where(a > 0, f(448) / np.where(a > 0, a, f(1)), f(0)).astype(f) for a in (am, au))
+        im, iu = (np.where(a > 0, f(448) * (f(1) / np.where(a > 0, a, f(1))), f(0)).astype(f) for a in (am, au))
         x = np.where(np.isfinite(m), np.clip(m * np.repeat(im, 256), -448, 448), np.nan).astype(f)
         mcode = torch.from_numpy(x).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
         gamma = np.uint64(0x9E3779B97F4A7C15)
