@@ -156,6 +156,14 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _stream_on(stream, device: int) -> int:
+    """The given stream, or the current one of device number `device`."""
+    import torch
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _dev_ptr(t, dtype, name):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -322,13 +330,18 @@ def tt_emb_destroy(h):
 # ---------------------------------------------------------------------------
 # Dense tables
 # ---------------------------------------------------------------------------
+_CODES = {}
+
+
 def dtype_code(dtype) -> int:
     """TT_F32, TT_BF16 or TT_F16 of a torch dtype."""
-    import torch
-    codes = {torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16}
-    if dtype not in codes:
+    if not _CODES:
+        import torch
+        _CODES.update({torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16})
+    code = _CODES.get(dtype)
+    if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
-    return codes[dtype]
+    return code
 
 
 def _tokens(t):
@@ -336,11 +349,12 @@ def _tokens(t):
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("tokens must be a CUDA tensor")
-    if t.dtype not in (torch.int32, torch.int64):
+    nbytes = 8 if t.dtype is torch.int64 else 4 if t.dtype is torch.int32 else 0
+    if not nbytes:
         raise TypeError(f"tokens must be int32 or int64, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError("tokens must be contiguous")
-    return t.data_ptr(), t.element_size(), t.numel()
+    return t.data_ptr(), nbytes, t.numel()
 
 
 def _rows(t, n: int, dim: int, name: str):
@@ -350,7 +364,7 @@ def _rows(t, n: int, dim: int, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     code = dtype_code(t.dtype)
-    if t.numel() != n * dim or t.shape[-1:] != (dim,):
+    if t.numel() != n * dim or t.dim() == 0 or t.size(-1) != dim:
         raise ValueError(f"{name} must hold {n} rows of {dim} values, got {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), code, dim
@@ -392,15 +406,18 @@ def tt_emb_dense_set_workspace(h, workspace, max_tokens: int):
 def tt_emb_dense_forward(h, tokens, out, dim: int, stream=None):
     ptr, nbytes, n = _tokens(tokens)
     optr, otype, stride = _rows(out, n, dim, "out")
-    _check(lib().tt_emb_dense_forward(h, ptr, nbytes, n, optr, otype, stride, _stream(stream)),
-           "tt_emb_dense_forward")
+    rc = lib().tt_emb_dense_forward(h, ptr, nbytes, n, optr, otype, stride, _stream_on(stream, tokens.get_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_forward")
 
 
 def tt_emb_dense_backward(h, tokens, grad_out, dim: int, accumulate: bool = False, stream=None):
     ptr, nbytes, n = _tokens(tokens)
     gptr, gtype, stride = _rows(grad_out, n, dim, "grad_out")
-    _check(lib().tt_emb_dense_backward(h, ptr, nbytes, n, gptr, gtype, stride, 1 if accumulate else 0,
-                                       _stream(stream)), "tt_emb_dense_backward")
+    rc = lib().tt_emb_dense_backward(h, ptr, nbytes, n, gptr, gtype, stride, 1 if accumulate else 0,
+                                     _stream_on(stream, tokens.get_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_backward")
 
 
 def tt_emb_dense_sync(h):
@@ -446,7 +463,9 @@ def tt_emb_adamw_step(h, lr, stream=None):
         if lr.numel() != 1:
             raise ValueError("lr must have one value")
         at, lr = _dev_ptr(lr, torch.float32, "lr"), 0.0
-    _check(lib().tt_emb_adamw_step(h, float(lr), at, _stream(stream)), "tt_emb_adamw_step")
+    rc = lib().tt_emb_adamw_step(h, float(lr), at, _stream_on(stream, torch.cuda.current_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_adamw_step")
 
 
 def tt_emb_adamw_destroy(h):

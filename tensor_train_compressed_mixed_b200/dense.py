@@ -6,14 +6,18 @@ ones) live beside the TT tables: same library, same streams, same errors.  As in
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
 from . import abi
 
+_HERE = contextlib.nullcontext()
+
 
 def on_device(device: torch.device):
     """Makes `device` current for the library's calls where another one is."""
-    return torch.cuda.device(device)
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 class DenseEmbedding:
@@ -40,7 +44,7 @@ class DenseEmbedding:
         self._ws_tokens = -1
 
     def _check(self, t, name: str, dtype=None):
-        if not isinstance(t, torch.Tensor) or t.device != self.device:
+        if not isinstance(t, torch.Tensor) or t.get_device() != self.device.index:   # -1 on the CPU
             raise TypeError(f"{name} must be a tensor on {self.device}")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
