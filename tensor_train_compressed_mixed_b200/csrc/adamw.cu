@@ -64,26 +64,6 @@ __device__ __forceinline__ uint64_t mix64(uint64_t z)
     return z ^ (z >> 31);
 }
 
-// Pairs of fp32 values in one register pair: one instruction for both.  The moments' products and
-// sums are each rounded on their own, as the header says: a sum of two products is written
-// a * one + b with a factor the compiler cannot see, since it fuses packed products and sums, .rn
-// or not.
-struct F2 { float x, y; };
-__device__ __forceinline__ uint64_t bits2(F2 a) { uint64_t r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y)); return r; }
-__device__ __forceinline__ F2 pair(uint64_t r) { F2 a; asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r)); return a; }
-__device__ __forceinline__ F2 both(float x) { return {x, x}; }
-__device__ __forceinline__ F2 mul2(F2 a, F2 b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return pair(r);
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return pair(r);
-}
 // 1 / x (normal x) and the root of x within an ulp: of the update only, not of what an 8-bit code depends on
 __device__ __forceinline__ float rcp(float x)
 {

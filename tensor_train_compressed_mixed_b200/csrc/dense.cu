@@ -1,3 +1,21 @@
+#ifndef WT
+#define WT 24
+#endif
+#ifndef SW
+#define SW 8
+#endif
+#ifndef CW4
+#define CW4 1
+#endif
+#ifndef CW8
+#define CW8 1
+#endif
+#ifndef SA
+#define SA 8
+#endif
+#ifndef CA
+#define CA 2
+#endif
 // Dense tables: scaled lookup of rows, and the table's gradient by sorted tokens.
 //
 // Both move rows and do one or two operations a value, so memory bounds them.
@@ -14,6 +32,7 @@
 // no sum depends on the order in which blocks run.
 #include <cooperative_groups.h>
 #include <new>
+#include <type_traits>
 
 #include "types.cuh"
 
@@ -36,66 +55,55 @@ struct LookupArgs {
     int64_t n, rows, out_stride;
     int token_bytes, dim;
     float scale;
-    int per_unit;        // tokens of a unit, 1 .. 32
     int lanes;           // lanes that share a row, a power of two
-    int slabs;           // units of the same tokens, 32 vectors (times kCols) of a row each
+    int slabs;           // units of the same tokens, 32 * kCols vectors of a row each
     int32_t* status;
 };
 
-// A warp takes a unit: up to 32 tokens, one a lane, and a slab of their rows.  A step moves 32 / lanes
-// rows; the loads of kSteps steps are on their way while the kSteps before them are stored.  No
-// load hangs on a condition, so that none waits for another: places behind the last token read
-// the last one's row, tokens outside the table row 0.
+// A warp takes a unit: some tokens and a slab of their rows.  A step moves 32 / lanes rows; the loads
+// of all kSteps steps are issued before the first store.  No load hangs on a condition, so that
+// none waits for another: places behind the last token read the last one's row, tokens outside the
+// table row 0.
 template <typename T, typename O, int V, int kCols, int kSteps>
 __global__ void __launch_bounds__(kThreads) k_lookup(LookupArgs a, const T* __restrict__ table, O* __restrict__ out)
 {
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), group = unit / a.slabs;
-    const int64_t i0 = group * a.per_unit;
+    const int rows = 32 / a.lanes;
+    const int64_t i0 = group * (rows * kSteps < 32 ? rows * kSteps : 32);
     if (i0 >= a.n) return;
-    const int cnt = (int)min64(a.per_unit, a.n - i0);
+    const int cnt = (int)min64(min(32, rows * kSteps), a.n - i0);
     int64_t token = token_at(a.tokens, a.token_bytes, i0 + min(lane, cnt - 1));
-    if (has_error(a.status)) return;
+    const bool stop = has_error(a.status);
     const bool bad = token < 0 || token >= a.rows;
+    if (bad) token = 0;
+    const int sub = lane & (a.lanes - 1), own = lane / a.lanes;
+    const int c0 = ((int)(unit - group * a.slabs) * kCols * 32 + sub) * V;
+    Pack<T, V> x[kSteps][kCols];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+        const int64_t row = __shfl_sync(kFull, token, min(s * rows + own, cnt - 1));
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+            const int c = c0 + k * 32 * V;
+            x[s][k] = *reinterpret_cast<const Pack<T, V>*>(table + row * a.dim + (c < a.dim ? c : 0));
+        }
+    }
+    if (stop) return;
     if (bad && lane < cnt) raise_error(a.status, TT_ERR_INDEX_RANGE, (int)min64(i0 + lane, INT32_MAX));
     const unsigned good = __ballot_sync(kFull, !bad);
-    if (bad) token = 0;
-    const int sub = lane & (a.lanes - 1), own = lane / a.lanes, rows = 32 / a.lanes, steps = (cnt + rows - 1) / rows;
-    const int c0 = ((int)(unit - group * a.slabs) * kCols * 32 + sub) * V;
-    Pack<T, V> x[2][kSteps][kCols];
-    auto load = [&](Pack<T, V> (&to)[kSteps][kCols], int s0) {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int64_t row = __shfl_sync(kFull, token, min((s0 + s) * rows + own, cnt - 1));
+    for (int s = 0; s < kSteps; ++s) {
+        const int i = s * rows + own;
+        if (i >= cnt || !(good >> i & 1u)) continue;
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                const int c = c0 + k * 32 * V;
-                to[s][k] = *reinterpret_cast<const Pack<T, V>*>(table + row * a.dim + (c < a.dim ? c : 0));
-            }
+        for (int k = 0; k < kCols; ++k) {
+            const int c = c0 + k * 32 * V;
+            float y[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) y[j] = to_f32(x[s][k].v[j]) * a.scale;
+            if (c < a.dim) store_pack(out + (i0 + i) * a.out_stride + c, y);
         }
-    };
-    auto store = [&](const Pack<T, V> (&from)[kSteps][kCols], int s0) {
-#pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-            const int i = (s0 + s) * rows + own;
-            if (i >= cnt || !(good >> i & 1u)) continue;
-#pragma unroll
-            for (int k = 0; k < kCols; ++k) {
-                const int c = c0 + k * 32 * V;
-                float y[V];
-#pragma unroll
-                for (int j = 0; j < V; ++j) y[j] = to_f32(from[s][k].v[j]) * a.scale;
-                if (c < a.dim) store_pack(out + (i0 + i) * a.out_stride + c, y);
-            }
-        }
-    };
-    load(x[0], 0);
-    for (int s0 = 0; s0 < steps; s0 += 2 * kSteps) {
-        load(x[1], s0 + kSteps);
-        store(x[0], s0);
-        if (s0 + kSteps >= steps) break;
-        load(x[0], s0 + 2 * kSteps);
-        store(x[1], s0 + kSteps);
     }
 }
 
@@ -145,12 +153,13 @@ constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int64_t kClusterTokens = (int64_t)kCluster * kSortThreads * 8;
 
 template <int kItems> struct SortShared {
-    uint32_t key[kSortThreads * kItems];
-    int32_t val[kSortThreads * kItems];
+    uint2 come[kSortThreads * kItems];      // (key, position) from all blocks: this block's share of a pass's result
+    uint2 mine[kSortThreads * kItems];      // this block's keys in the order of their digits
     uint16_t before[kSortWarps][kDigits];   // keys of a digit in the warps before, of this block
     uint32_t count[kDigits];                // keys of a digit in this block
-    uint32_t first[kDigits];                // place of this block's first key of a digit
-    uint32_t scan[kSortWarps];
+    uint32_t here[kDigits];                 // place in `mine` of its first key of a digit
+    uint32_t there[kDigits];                // place among all keys of that one
+    uint32_t scan[2][kSortWarps];
 };
 
 template <int kItems>
@@ -169,108 +178,141 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_token_sort(TokenArgs a, int
         for (int64_t i = (int64_t)me * kSortThreads + tid; i < touched_words; i += (int64_t)blocks * kSortThreads) a.touched[i] = 0;
         cluster.sync();
     }
-    uint32_t key[kItems];
-    int32_t val[kItems];
-    bool in[kItems];
+    const int first = wid * 32 * kItems + lane;             // the thread's keys: first, first + 32, ..
+    const int cnt = (int)max((int64_t)0, min64(kChunk, a.n - (int64_t)me * kChunk));
+    uint2 key[kItems];
     {
         int64_t t[kItems];
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {
-            val[j] = me * kChunk + wid * 32 * kItems + j * 32 + lane;
-            in[j] = val[j] < a.n;
-            t[j] = token_at(a.tokens, a.token_bytes, in[j] ? val[j] : 0);
+            const int e = first + j * 32;
+            t[j] = token_at(a.tokens, a.token_bytes, e < cnt ? (int64_t)me * kChunk + e : 0);
         }
 #pragma unroll
-        for (int j = 0; j < kItems; ++j) key[j] = in[j] ? token_key(a, val[j], t[j]) : 0u;
+        for (int j = 0; j < kItems; ++j) {
+            const int e = first + j * 32;
+            const int64_t i = (int64_t)me * kChunk + e;
+            key[j] = make_uint2(e < cnt ? token_key(a, i, t[j]) : 0u, (uint32_t)i);
+        }
     }
     const int passes = (bits + kDigitBits - 1) / kDigitBits, width = (bits + passes - 1) / passes, digits = 1 << width;
     for (int pass = 0; pass < passes; ++pass) {
         const int shift = pass * width;
         for (int i = tid; i < kSortWarps * kDigits / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(s.before)[i] = 0;
         __syncthreads();
+        // lanes with the same digit: a vote for each of its bits (those above the width are zero)
         uint32_t rank[kItems];
-        int digit[kItems];
+        unsigned same[kItems];
+#pragma unroll
+        for (int j = 0; j < kItems; ++j) same[j] = __ballot_sync(kFull, first + j * 32 < cnt);
+#pragma unroll
+        for (int b = 0; b < kDigitBits; ++b)
+#pragma unroll
+            for (int j = 0; j < kItems; ++j) {
+                const bool one = b < width && (key[j].x >> (shift + b) & 1u);
+                const unsigned ones = __ballot_sync(kFull, one);
+                same[j] &= one ? ones : ~ones;
+            }
 #pragma unroll
         for (int j = 0; j < kItems; ++j) {
-            digit[j] = (int)((key[j] >> shift) & (digits - 1));
-            // lanes with the same digit, a vote for each of its bits (a match instruction takes three times as long)
-            unsigned same = __ballot_sync(kFull, in[j]);
-            for (int b = 0; b < width; ++b) {
-                const bool one = digit[j] >> b & 1;
-                const unsigned ones = __ballot_sync(kFull, one);
-                same &= one ? ones : ~ones;
-            }
-            const uint32_t seen = in[j] ? s.before[wid][digit[j]] : 0u;
-            rank[j] = seen + __popc(same & lt);
+            const int d = (int)((key[j].x >> shift) & (digits - 1));
+            const uint32_t seen = s.before[wid][d];
+            rank[j] = seen + __popc(same[j] & lt);
             __syncwarp();
-            if (in[j] && (same & lt) == 0) s.before[wid][digit[j]] = (uint16_t)(seen + __popc(same));
+            if (first + j * 32 < cnt && (same[j] & lt) == 0) s.before[wid][d] = (uint16_t)(seen + __popc(same[j]));
             __syncwarp();
         }
         __syncthreads();
         // counts of the warps before, and of the block: two threads for a digit, half of the warps each
         {
+            constexpr int kHalf = kSortWarps / 2;
             const int d = tid >> 1, half = tid & 1;
-            uint32_t run = 0;
+            uint32_t c[kHalf], run = 0;
             if (d < digits)
-                for (int w = half * (kSortWarps / 2); w < (half + 1) * (kSortWarps / 2); ++w) {
-                    const uint32_t c = s.before[w][d];
-                    s.before[w][d] = (uint16_t)run;
-                    run += c;
-                }
+#pragma unroll
+                for (int w = 0; w < kHalf; ++w) c[w] = s.before[half * kHalf + w][d];
+            else
+#pragma unroll
+                for (int w = 0; w < kHalf; ++w) c[w] = 0;
+#pragma unroll
+            for (int w = 0; w < kHalf; ++w) run += c[w];
             const uint32_t other = __shfl_xor_sync(kFull, run, 1);
-            if (d < digits && half)
-                for (int w = kSortWarps / 2; w < kSortWarps; ++w) s.before[w][d] += (uint16_t)other;
-            if (d < digits && !half) s.count[d] = run + other;
+            if (d < digits) {
+                uint32_t sum = half ? other : 0u;
+#pragma unroll
+                for (int w = 0; w < kHalf; ++w) {
+                    s.before[half * kHalf + w][d] = (uint16_t)sum;
+                    sum += c[w];
+                }
+                if (half) s.count[d] = sum;
+            }
         }
         cluster.sync();
-        // a digit's keys in the blocks before and in all; their places by a scan over the digits
+        // places of a digit's first key in this block and among all: scans over the digits
         {
-            uint32_t earlier = 0, all = 0;
+            uint32_t own = 0, earlier = 0, all = 0;
             if (tid < digits) {
                 uint32_t x[kCluster];
 #pragma unroll
                 for (int c = 0; c < kCluster; ++c) x[c] = c < blocks ? *cluster.map_shared_rank(&s.count[tid], c) : 0u;
 #pragma unroll
                 for (int c = 0; c < kCluster; ++c) {
+                    if (c == me) own = x[c];
                     earlier += c < me ? x[c] : 0u;
                     all += x[c];
                 }
             }
-            uint32_t x = all;
+            uint32_t x = own, y = all;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o) x += y;
+                const uint32_t u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
+                if (lane >= o) {
+                    x += u;
+                    y += v;
+                }
             }
-            if (lane == 31) s.scan[wid] = x;
+            if (lane == 31) {
+                s.scan[0][wid] = x;
+                s.scan[1][wid] = y;
+            }
             __syncthreads();
-            uint32_t sum = 0;
-            for (int w = 0; w < wid; ++w) sum += s.scan[w];
-            if (tid < digits) s.first[tid] = sum + x - all + earlier;
+            const uint32_t sx = __reduce_add_sync(kFull, lane < wid ? s.scan[0][lane] : 0u);
+            const uint32_t sy = __reduce_add_sync(kFull, lane < wid ? s.scan[1][lane] : 0u);
+            if (tid < digits) {
+                s.here[tid] = sx + x - own;
+                s.there[tid] = sy + y - all + earlier;
+            }
         }
+        __syncthreads();
+        // into the order of their digits here first, so that neighbours then go to neighbouring places
+#pragma unroll
+        for (int j = 0; j < kItems; ++j)
+            if (first + j * 32 < cnt) {
+                const int d = (int)((key[j].x >> shift) & (digits - 1));
+                s.mine[s.here[d] + s.before[wid][d] + rank[j]] = key[j];
+            }
         __syncthreads();
         const bool last = pass + 1 == passes;
 #pragma unroll
-        for (int j = 0; j < kItems; ++j)
-            if (in[j]) {
-                const uint32_t to = s.first[digit[j]] + s.before[wid][digit[j]] + rank[j];
+        for (int j = 0; j < kItems; ++j) {
+            const int e = j * kSortThreads + tid;
+            if (e < cnt) {
+                const uint2 k = s.mine[e];
+                const int d = (int)((k.x >> shift) & (digits - 1));
+                const uint32_t to = s.there[d] + (e - s.here[d]);
                 if (last) {
-                    keys_out[to] = key[j];
-                    vals_out[to] = val[j];
+                    keys_out[to] = k.x;
+                    vals_out[to] = (int32_t)k.y;
                 } else {
-                    SortShared<kItems>* there = cluster.map_shared_rank(&s, to / kChunk);
-                    there->key[to % kChunk] = key[j];
-                    there->val[to % kChunk] = val[j];
+                    cluster.map_shared_rank(s.come, to / kChunk)[to % kChunk] = k;
                 }
             }
+        }
         cluster.sync();   // also keeps every block's counts in place until they are read
         if (!last) {
 #pragma unroll
             for (int j = 0; j < kItems; ++j)
-                if (in[j]) {
-                    key[j] = s.key[wid * 32 * kItems + j * 32 + lane];
-                    val[j] = s.val[wid * 32 * kItems + j * 32 + lane];
-                }
+                if (first + j * 32 < cnt) key[j] = s.come[first + j * 32];
         }
     }
 }
@@ -304,9 +346,16 @@ __device__ __forceinline__ void finish_row(W* at, const float (&x)[V], const Pac
     store_pack(at, y);
 }
 
+#ifndef UU
+#define UU 4
+#endif
+#ifndef UA
+#define UA 2
+#endif
 template <typename G, typename W, int V, bool kAdd>
 __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
 {
+    constexpr int kRows = kAdd ? UA : UU;                             // rows on their way at a time
     if (has_error(a.status)) return;
     const int lane = threadIdx.x & 31;
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -317,117 +366,151 @@ __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __re
     const int at_c = on ? c : 0;      // lanes behind the last column load the first ones
     const uint32_t none = (uint32_t)a.rows;
     const int64_t p0 = tile * a.tile, p1 = min64(p0 + a.tile, a.n);
-    uint32_t key = a.keys[p0];
-    bool began = p0 > 0 && a.keys[p0 - 1] == key;         // the current run began in an earlier tile
-    constexpr int U = 8;                                  // rows on their way at a time
-    float acc[V];
+    bool began = p0 > 0 && a.keys[p0 - 1] == a.keys[p0];  // the current run began in an earlier tile
+    F2 acc[(V + 1) / 2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    for (int j = 0; j < (V + 1) / 2; ++j) acc[j] = both(0.f);
     for (int64_t p = p0; p < p1; p += 32) {
-        // a lane holds one position; past the tile's end the key that follows, past the last one none
-        const uint32_t my_key = p + lane < a.n ? a.keys[p + lane] : none;
-        const int32_t my_val = p + lane < p1 ? a.vals[p + lane] : 0;
-        const uint32_t after = p + 32 < a.n ? a.keys[p + 32] : none;
-        const int cnt = (int)min64(32, p1 - p);
-        const uint32_t up1 = __shfl_down_sync(kFull, my_key, 1);
-        const uint32_t my_next = lane == 31 ? after : up1;
-        if (__shfl_sync(kFull, my_key, 0) >= none) break;  // what follows gets no gradient
+        // a lane holds one position, and whether its run ends there or at the tile's end
+        const bool in = p + lane < p1;
+        const uint32_t key = in ? a.keys[p + lane] : none;
+        const int32_t val = in ? a.vals[p + lane] : 0;
+        const uint32_t next = p + lane + 1 < a.n ? a.keys[p + lane + 1] : none;
+        const bool last = next != key;
+        const int cnt = __popc(__ballot_sync(kFull, key < none));   // the others, behind, get no gradient
+        const unsigned ends = __ballot_sync(kFull, last || p + lane + 1 == p1);
+        const unsigned whole = __ballot_sync(kFull, last);
 #pragma unroll 1
-        for (int q = 0; q < cnt; q += U) {
-            // No load hangs on a condition, so that all are on their way together.  Places without a sum
-            // read a row they do not use (position 0's, row 0); with kAdd each place loads its row of the
+        for (int q = 0; q < cnt; q += kRows) {
+            // No load hangs on a condition, so that none waits for another.  Places without a sum read a
+            // row they do not use (position 0's, row 0); with kAdd each place loads its row of the
             // gradient as it is, which equal neighbours find in the cache.
-            Pack<G, V> x[U];
-            Pack<W, V> old[U];
+            Pack<G, V> x[kRows];
+            Pack<W, V> old[kAdd ? kRows : 1];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t row = __shfl_sync(kFull, my_val, q + u);
+            for (int u = 0; u < kRows; ++u) {
+                const int64_t row = __shfl_sync(kFull, val, q + u);
                 x[u] = *reinterpret_cast<const Pack<G, V>*>(up + row * stride + at_c);
-                if (kAdd) {
-                    const uint32_t k = __shfl_sync(kFull, my_key, q + u);
+                if constexpr (kAdd) {
+                    const uint32_t k = __shfl_sync(kFull, key, q + u);
                     old[u] = *reinterpret_cast<const Pack<W, V>*>(grad + (int64_t)(k < none ? k : 0u) * a.dim + at_c);
-                } else {
-                    memset(&old[u], 0, sizeof(old[u]));
                 }
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t k = __shfl_sync(kFull, my_key, q + u), next = __shfl_sync(kFull, my_next, q + u);
-                if (q + u >= cnt || k >= none) break;
+            for (int u = 0; u < kRows; ++u) {
+                if (q + u >= cnt) break;
+                if constexpr (V > 1) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] += to_f32(x[u].v[j]);
-                const bool at_end = p + q + u + 1 == p1;
-                if (!at_end && next == k) continue;
+                    for (int j = 0; j < V / 2; ++j) acc[j] = add2(acc[j], {to_f32(x[u].v[2 * j]), to_f32(x[u].v[2 * j + 1])});
+                } else {
+                    acc[0].x += to_f32(x[u].v[0]);
+                }
+                if (!(ends >> (q + u) & 1u)) continue;
+                float sum[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum[j] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+                const bool here = whole >> (q + u) & 1u;
+                const uint32_t k = __shfl_sync(kFull, key, q + u);
                 if (on) {
-                    if (began) store_pack(a.head + tile * a.dim + c, acc);
-                    else if (next == k) store_pack(a.tail + tile * a.dim + c, acc);
-                    else finish_row(grad + (int64_t)k * a.dim + c, acc, old[u], a.scale);
+                    if (began) {
+                        store_pack(a.head + tile * a.dim + c, sum);
+                    } else if (!here) {
+                        store_pack(a.tail + tile * a.dim + c, sum);
+                    } else {
+                        if constexpr (!kAdd) memset(&old[0], 0, sizeof(old[0]));
+                        finish_row(grad + (int64_t)k * a.dim + c, sum, old[kAdd ? u : 0], a.scale);
+                    }
                 }
                 began = false;
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[j] = 0.f;
+                for (int j = 0; j < (V + 1) / 2; ++j) acc[j] = both(0.f);
+            }
+        }
+        if (cnt < 32) break;
+    }
+}
+
+// The first `joins` blocks: where a run begins in a tile and goes on, they add up its parts, a warp
+// for each of its slabs, in the order of the tiles.  The other blocks clear the rows that no token
+// names.
+constexpr int kClear = 16;        // vectors of 16 bytes a thread clears
+
+// What one block clears: vectors of 16 bytes of the buffer, whatever rows they lie in.  The values in
+// front of the buffer's first 16-byte place and behind its last are left to block 0.
+template <typename W> struct Clear {
+    static constexpr int N = 16 / sizeof(W);
+    int64_t values, vectors, at, row0;
+    int skip;
+    unsigned col0;
+    __device__ __forceinline__ Clear(const SumArgs& a, int64_t block, const W* grad)
+    {
+        values = a.rows * a.dim;
+        skip = (int)((16 - ((uintptr_t)grad & 15)) & 15) / (int)sizeof(W);
+        vectors = values > skip ? (values - skip) / N : 0;
+        at = block * (kThreads * kClear);
+        row0 = (at * N + skip) / a.dim;
+        col0 = (unsigned)(at * N + skip - row0 * a.dim);
+    }
+    // hit: whether a token names a row of this block's vectors; far: any row
+    template <typename Hit, typename Far>
+    __device__ __forceinline__ void run(const SumArgs& a, W* grad, Hit hit, Far far) const
+    {
+        if (at == 0) {
+            const int64_t e = threadIdx.x < skip ? threadIdx.x : skip + vectors * N + threadIdx.x - skip;
+            if (e < values && !far(e / a.dim)) grad[e] = W(0.f);
+        }
+        const unsigned dim = a.dim;
+        Pack<W, N> zero;
+        memset(&zero, 0, sizeof(zero));
+#pragma unroll 1
+        for (int i0 = 0; i0 < kClear; i0 += 4) {
+            unsigned col[4];
+            int64_t row[4];
+            bool named[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {     // all four are looked up first
+                const unsigned off = col0 + ((i0 + i) * kThreads + threadIdx.x) * N, more = off / dim;
+                col[i] = off - more * dim;
+                row[i] = row0 + more;
+                named[i] = hit(min64(row[i], a.rows - 1));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t v = at + (i0 + i) * kThreads + threadIdx.x;
+                if (v >= vectors) return;
+                W* const p = grad + skip + v * N;
+                if (col[i] + N <= dim) {
+                    if (!named[i]) *reinterpret_cast<Pack<W, N>*>(p) = zero;
+                } else {
+                    for (int j = 0; j < N; ++j)
+                        if (!hit(row[i] + (col[i] + j) / dim)) p[j] = W(0.f);
+                }
             }
         }
     }
-}
-
-// The first `joins` blocks, one for each unit: where a run begins in the unit's tile and goes on, they
-// add up its parts, each warp a row of tiles, then the warps' sums in order.  The other blocks
-// clear the rows that no token names.
-constexpr int kClear = 16;        // vectors of 16 bytes a thread clears
-
-template <typename W>
-__device__ __forceinline__ void clear_rows(const SumArgs& a, int64_t block, W* grad)
-{
-    constexpr int N = 16 / sizeof(W);
-    const int64_t values = a.rows * a.dim;
-    // vectors of the buffer, whatever rows they lie in; those in front of its first 16-byte place
-    // and behind its last are left to the first block
-    const int skip = (int)((16 - ((uintptr_t)grad & 15)) & 15) / (int)sizeof(W);
-    const int64_t vectors = values > skip ? (values - skip) / N : 0;
-    const int64_t at = block * (kThreads * kClear), first = at * N + skip, row0 = first / a.dim;
-    const unsigned col0 = (unsigned)(first - row0 * a.dim), dim = a.dim;
-    auto touched = [&](int64_t row) { return a.touched[row >> 5] >> (row & 31) & 1u; };
-    Pack<W, N> zero;
-    memset(&zero, 0, sizeof(zero));
-#pragma unroll 4
-    for (int i = 0; i < kClear; ++i) {
-        const int64_t v = at + i * kThreads + threadIdx.x;
-        if (v >= vectors) break;
-        const unsigned off = col0 + (i * kThreads + threadIdx.x) * N, more = off / dim, col = off - more * dim;
-        const int64_t row = row0 + more;
-        W* const p = grad + skip + v * N;
-        if (col + N <= dim) {
-            if (!touched(row)) *reinterpret_cast<Pack<W, N>*>(p) = zero;
-        } else {
-            for (int j = 0; j < N; ++j)
-                if (!touched(row + (col + j) / dim)) p[j] = W(0.f);
-        }
-    }
-    if (block == 0) {
-        const int64_t behind = skip + vectors * N;
-        const int64_t e = threadIdx.x < skip ? threadIdx.x : behind + threadIdx.x - skip;
-        if (e < values && (threadIdx.x < skip || e >= behind) && !touched(e / a.dim)) grad[e] = W(0.f);
-    }
-}
+};
 
 template <typename W, int V>
 __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t joins, W* __restrict__ grad)
 {
-    __shared__ float s_part[kWarps][32 * V];
-    if (has_error(a.status)) return;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int groups = (a.slabs + kWarps - 1) / kWarps;           // blocks of a tile
+    const int64_t tile = blockIdx.x / groups, p0 = tile * a.tile, p1 = p0 + a.tile;
+    const bool join = blockIdx.x < joins && p1 < a.n;
+    const uint32_t k = join ? a.keys[p1 - 1] : 0u, then = join ? a.keys[p1] : 0u, front = join && p0 > 0 ? a.keys[p0 - 1] : ~0u;
+    if (has_error(a.status)) return;
     if (blockIdx.x >= joins) {
-        clear_rows(a, blockIdx.x - joins, grad);
+        auto hit = [&](int64_t row) { return a.touched[row >> 5] >> (row & 31) & 1u; };
+        Clear<W>(a, blockIdx.x - joins, grad).run(a, grad, hit, hit);
         return;
     }
-    const int64_t tile = blockIdx.x / a.slabs;
-    const int64_t p0 = tile * a.tile, p1 = p0 + a.tile;
-    if (p1 >= a.n) return;
-    const uint32_t k = a.keys[p1 - 1];
-    if (k >= (uint32_t)a.rows || a.keys[p1] != k) return;         // nothing goes on
-    if (p0 > 0 && a.keys[p0 - 1] == k) return;                    // it began earlier
-    // the run's end: each step the lanes split what is left, (lo, hi], into 33
+    // nothing goes on, or it began earlier
+    if (!join || k >= (uint32_t)a.rows || then != k || front == k) return;
+    const int c = ((int)((blockIdx.x - tile * groups) * kWarps + wid) * 32 + lane) * V;
+    if (c - lane * V >= a.dim) return;
+    const bool on = c < a.dim;
+    const int at_c = on ? c : 0;
+    // the run's end: each step the lanes split what is left, (lo, hi), into 33
     int64_t lo = p1, hi = a.n;                                    // keys[lo] = k; keys[hi] is above k or past the end
     while (hi - lo > 1) {
         const int64_t step = (hi - lo + 32) / 33, at = lo + step * (lane + 1);
@@ -436,41 +519,171 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
         hi = min64(hi, lo + step * (m + 1));
         lo = lo + step * m;
     }
-    const int64_t last = lo / a.tile, parts = last - tile;        // heads of tiles tile + 1 .. last
-    const int c = ((int)(blockIdx.x - tile * a.slabs) * 32 + lane) * V;
+    const int64_t last = lo / a.tile;                             // heads of tiles tile + 1 .. last
+    W* const at = grad + (int64_t)k * a.dim + at_c;
+    Pack<W, V> old;
+    if (a.accumulate) old = *reinterpret_cast<const Pack<W, V>*>(at);
+    else memset(&old, 0, sizeof(old));
+    float acc[V];
+    load_pack(a.tail + tile * a.dim + at_c, acc);
+    constexpr int kParts = 8;                                     // parts on their way at a time
+    for (int64_t t = tile + 1; t <= last; t += kParts) {
+        Pack<float, V> x[kParts];
+#pragma unroll
+        for (int i = 0; i < kParts; ++i)
+            x[i] = *reinterpret_cast<const Pack<float, V>*>(a.head + min64(t + i, last) * a.dim + at_c);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            if (t + i > last) break;
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] += x[i].v[j];
+        }
+    }
+    if (on) finish_row(at, acc, old, a.scale);
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens: one launch.  A block of the first `slabs` sorts the tokens by itself (each key's place is
+// the number of keys in front of it, counted) and adds up one slab, each warp a part of the sorted
+// positions, whose ends are joined in shared memory.  The others clear rows; each looks
+// up the few tokens in the rows that it covers.
+// ---------------------------------------------------------------------------
+constexpr int kFew = 512;
+constexpr int kFewRows = kThreads * kClear * 8;   // rows that a block's vectors lie in at most
+
+template <typename G, typename W, int V, bool kAdd>
+__global__ void __launch_bounds__(kThreads) k_token_few(TokenArgs t, SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
+{
+    constexpr int kRows = 4;
+    __shared__ alignas(16) uint32_t s_key[kFew + 4];
+    __shared__ uint32_t s_bits[kFewRows / 32 + 1];
+    __shared__ uint32_t s_sorted[kFew + 1];
+    __shared__ int32_t s_place[kFew];
+    __shared__ float s_part[kWarps][32 * V];
+    const int n = (int)t.n, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const uint32_t none = (uint32_t)a.rows;
+    constexpr int kMine = kFew / kThreads;
+    int64_t token[kMine];
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) token[j] = token_at(t.tokens, t.token_bytes, min(tid + j * kThreads, n - 1));
+    bool bad = has_error(t.status);
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+        const int i = tid + j * kThreads;
+        if (i < n && (token[j] < 0 || token[j] >= a.rows)) {
+            raise_error(t.status, TT_ERR_INDEX_RANGE, i);
+            bad = true;
+        }
+        s_key[i] = i < n && token[j] != t.pad ? (uint32_t)token[j] : none;
+    }
+    if (tid < 4) s_key[kFew + tid] = none;
+    if (__syncthreads_or(bad)) return;
+    if ((int)blockIdx.x >= a.slabs) {
+        // the rows of this block's vectors that a token names, as bits
+        const Clear<W> clear(a, blockIdx.x - a.slabs, grad);
+        for (int i = tid; i < kFewRows / 32 + 1; i += kThreads) s_bits[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const int64_t r = (int64_t)s_key[i] - clear.row0;
+            if (s_key[i] < none && r >= 0 && r < kFewRows + 32) atomicOr(&s_bits[r >> 5], 1u << (r & 31));
+        }
+        __syncthreads();
+        auto hit = [&](int64_t row) { return s_bits[(row - clear.row0) >> 5] >> ((row - clear.row0) & 31) & 1u; };
+        auto far = [&](int64_t row) {
+            bool found = false;
+            for (int i = 0; i < n; ++i) found |= s_key[i] == (uint32_t)row;
+            return found;
+        };
+        clear.run(a, grad, hit, far);
+        return;
+    }
+    // places: keys below mine, and equal ones in front
+    {
+        uint32_t mine[kMine];
+        int place[kMine];
+#pragma unroll
+        for (int j = 0; j < kMine; ++j) {
+            mine[j] = s_key[tid + j * kThreads];
+            place[j] = 0;
+        }
+        for (int i = 0; i < n; i += 4) {
+            const uint4 q = *reinterpret_cast<const uint4*>(s_key + i);
+            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int j = 0; j < kMine; ++j)
+                    place[j] += i + e < n && (k[e] < mine[j] || (k[e] == mine[j] && i + e < tid + j * kThreads));
+        }
+#pragma unroll
+        for (int j = 0; j < kMine; ++j)
+            if (tid + j * kThreads < n) {
+                s_sorted[place[j]] = mine[j];
+                s_place[place[j]] = tid + j * kThreads;
+            }
+        if (tid == 0) s_sorted[n] = none;
+    }
+    __syncthreads();
+    const int c = ((int)blockIdx.x * 32 + lane) * V;
     const bool on = c < a.dim;
-    const int64_t each = (parts + kWarps - 1) / kWarps, from = tile + 1 + wid * each, to = min64(from + each, last + 1);
+    const int at_c = on ? c : 0;
+    const int each = (n + kWarps - 1) / kWarps, p0 = min(n, wid * each), p1 = min(n, p0 + each);
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    if (on)
-#pragma unroll 4
-        for (int64_t t = from; t < to; ++t) {
-            float x[V];
-            load_pack(a.head + t * a.dim + c, x);
+    auto row_of = [&](uint32_t k) { return grad + (int64_t)k * a.dim + at_c; };
+    // a run that goes over this part's end is left in acc, and what ends one that began before in s_part
+    bool began = p0 > 0 && p0 < n && s_sorted[p0 - 1] == s_sorted[p0];
+    uint32_t k = none;
+    for (int p = p0; p < p1; p += kRows) {
+        Pack<G, V> x[kRows];
+        Pack<W, V> old[kAdd ? kRows : 1];
+        memset(&old[0], 0, sizeof(old[0]));
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += x[j];
+        for (int u = 0; u < kRows; ++u) {
+            const int q = min(p + u, p1 - 1);
+            x[u] = *reinterpret_cast<const Pack<G, V>*>(up + (int64_t)s_place[q] * stride + at_c);
+            if constexpr (kAdd) old[u] = *reinterpret_cast<const Pack<W, V>*>(row_of(s_sorted[q] < none ? s_sorted[q] : 0u));
         }
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
-    __syncthreads();
-    if (wid > 0 || !on) return;
-    float sum[V];
-    load_pack(a.tail + tile * a.dim + c, sum);
-    for (int w = 0; w < kWarps; ++w)
+        for (int u = 0; u < kRows; ++u) {
+            if (p + u >= p1) break;
+            k = s_sorted[p + u];
+            if (k >= none) break;
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] += s_part[w][j * 32 + lane];
-    W* const at = grad + (int64_t)k * a.dim + c;
+            for (int j = 0; j < V; ++j) acc[j] += to_f32(x[u].v[j]);
+            if (s_sorted[p + u + 1] == k) continue;
+            if (began) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+                began = false;
+            } else if (on) {
+                finish_row(row_of(k), acc, old[kAdd ? u : 0], a.scale);
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[j] = 0.f;
+        }
+    }
+    // what is left in acc goes on behind this part, or is all of a part that a run covers
+    const bool goes_on = p1 > p0 && p1 < n && k < none && s_sorted[p1] == k;
+    if (goes_on && began)
+#pragma unroll
+        for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+    __syncthreads();
+    if (!goes_on || began) return;
+    for (int w = wid + 1; w < kWarps && w * each < n && s_sorted[w * each] == k; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] += s_part[w][j * 32 + lane];
     Pack<W, V> old;
     memset(&old, 0, sizeof(old));
-    if (a.accumulate) old = *reinterpret_cast<const Pack<W, V>*>(at);
-    finish_row(at, sum, old, a.scale);
+    if constexpr (kAdd) old = *reinterpret_cast<const Pack<W, V>*>(row_of(k));
+    if (on) finish_row(row_of(k), acc, old, a.scale);
 }
 
 // Positions a tile has: longer tiles cut fewer runs, shorter ones give every warp of the card a unit.
 int tile_of(int64_t n, int slabs, int sms)
 {
-    const int64_t units = ceil_div(n, 32) * slabs, want = (int64_t)sms * 24;
+    const int64_t units = ceil_div(n, 32) * slabs, want = (int64_t)sms * WT;
     return 32 * (int)(units <= want ? 1 : units / want >= 8 ? 8 : units / want);
 }
 
@@ -562,8 +775,8 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     h->used_stream = true;
     if (n == 0) return TT_OK;
     const bool wide = h->dim % 8 == 0 && wide_rows(h->table, h->dim, h->table_type) && wide_rows(out, out_stride, out_type);
-    // 16 bytes a lane of the wider type; where rows begin anywhere, single values, four to a lane
-    const int V = !wide ? 1 : h->table_type == TT_F32 || out_type == TT_F32 ? 4 : 8;
+    // 16 bytes a lane of the narrower type; where rows begin anywhere, single values, two to a lane
+    const int V = !wide ? 1 : h->table_type == TT_F32 && out_type == TT_F32 ? 4 : 8;
     const int64_t vectors = ceil_div(h->dim, V);
     LookupArgs a;
     a.tokens = tokens;
@@ -575,19 +788,21 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     a.scale = h->scale;
     a.status = h->d_status;
     for (a.lanes = 1; a.lanes < vectors && a.lanes < 32;) a.lanes *= 2;
-    a.slabs = (int)ceil_div(vectors, wide ? 32 : 32 * 4);
-    // as many tokens to a unit as leave every warp of the card a few
-    a.per_unit = 32;
-    while (a.per_unit > 1 && ceil_div(n, a.per_unit) * a.slabs < (int64_t)h->num_sms * 64) a.per_unit /= 2;
-    const unsigned grid = (unsigned)ceil_div(ceil_div(n, a.per_unit) * a.slabs, kWarps);
+    const int cols = wide ? V == 4 ? CW4 : CW8 : CA, rows = 32 / a.lanes;
+    a.slabs = (int)ceil_div(vectors, 32 * cols);
+    // as many steps to a unit as leave every warp of the card a unit or more
+    const bool many = ceil_div(n, rows * 4) * a.slabs >= (int64_t)h->num_sms * 16;
+    const int steps = many ? wide ? SW : SA : 1;
+    const unsigned grid = (unsigned)ceil_div(ceil_div(n, rows * steps < 32 ? rows * steps : 32) * a.slabs, kWarps);
     by_type(h->table_type, [&](auto t) {
         by_type(out_type, [&](auto o) {
             using T = decltype(t);
             using O = decltype(o);
             auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, (const T*)h->table, (O*)out); };
-            constexpr int kWide = sizeof(T) == 4 || sizeof(O) == 4 ? 4 : 8;
-            if (wide) go(k_lookup<T, O, kWide, 1, 4>);
-            else go(k_lookup<T, O, 1, 4, 2>);
+            constexpr bool f32 = sizeof(T) == 4 && sizeof(O) == 4;
+            constexpr int kWide = f32 ? 4 : 8, kCols = f32 ? CW4 : CW8;
+            if (wide) go(many ? k_lookup<T, O, kWide, kCols, SW> : k_lookup<T, O, kWide, kCols, 1>);
+            else go(many ? k_lookup<T, O, 1, CA, SA> : k_lookup<T, O, 1, CA, 1>);
         });
     });
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
@@ -667,8 +882,8 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     ta.touched = accumulate ? nullptr : (uint32_t*)(h->ws + y.touched);
     ta.status = h->d_status;
     const bool wide = h->dim % 8 == 0 && wide_rows(h->grad, h->dim, h->grad_type) && wide_rows(up, up_stride, up_type);
-    // 16 bytes a lane of the wider type
-    const int V = !wide ? 1 : h->grad_type == TT_F32 || up_type == TT_F32 ? 4 : 8;
+    // 16 bytes a lane of the narrower type
+    const int V = !wide ? 1 : h->grad_type == TT_F32 && up_type == TT_F32 ? 4 : 8;
     SumArgs a;
     a.n = n;
     a.rows = h->rows;
@@ -682,10 +897,25 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     a.tail = (float*)(h->ws + y.tail);
     a.touched = ta.touched;
     a.status = h->d_status;
-    const int64_t joins = a.tiles > 1 ? a.tiles * a.slabs : 0;
+    const int64_t joins = a.tiles > 1 ? a.tiles * ceil_div(a.slabs, kWarps) : 0;
     const int64_t clears = accumulate ? 0 : ceil_div(ceil_div(h->rows * h->dim, 16 / type_bytes(h->grad_type)), kThreads * kClear);
     const unsigned grid = (unsigned)ceil_div(a.tiles * a.slabs, kWarps);
     if (joins + clears > INT32_MAX) return TT_ERR_ARG;   // sizes that no device holds
+    if (n <= kFew) {
+        by_type(h->grad_type, [&](auto w) {
+            by_type(up_type, [&](auto g) {
+                using W = decltype(w);
+                using G = decltype(g);
+                auto go = [&](auto kernel) {
+                    kernel<<<(unsigned)(a.slabs + clears), kThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
+                };
+                constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
+                if (wide) go(accumulate ? k_token_few<G, W, kWide, true> : k_token_few<G, W, kWide, false>);
+                else go(accumulate ? k_token_few<G, W, 1, true> : k_token_few<G, W, 1, false>);
+            });
+        });
+        return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    }
     int bits = 1, which = 0;
     while (h->rows >> bits) ++bits;
     if (sort_tokens(h, ta, y, bits, &which, s) != cudaSuccess) return TT_ERR_CUDA;
@@ -696,15 +926,15 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
         by_type(up_type, [&](auto g) {
             using G = decltype(g);
             auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, (const G*)up, up_stride, (W*)h->grad); };
-            constexpr int kWide = sizeof(W) == 4 || sizeof(G) == 4 ? 4 : 8;
+            constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
             if (wide) go(accumulate ? k_token_sum<G, W, kWide, true> : k_token_sum<G, W, kWide, false>);
             else go(accumulate ? k_token_sum<G, W, 1, true> : k_token_sum<G, W, 1, false>);
         });
         if (joins + clears == 0) return;
         auto go = [&](auto kernel) { kernel<<<(unsigned)(joins + clears), kThreads, 0, s>>>(a, joins, (W*)h->grad); };
         if (V == 1) go(k_token_join<W, 1>);
-        else if (V == 4) go(k_token_join<W, 4>);
-        else if constexpr (sizeof(W) == 2) go(k_token_join<W, 8>);
+        else if (V == 8) go(k_token_join<W, 8>);
+        else if constexpr (sizeof(W) == 4) go(k_token_join<W, 4>);
     });
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }

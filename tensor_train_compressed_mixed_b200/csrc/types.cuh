@@ -44,6 +44,31 @@ __device__ __forceinline__ void store_pack(T* p, const float (&x)[N])
     *reinterpret_cast<Pack<T, N>*>(p) = q;
 }
 
+// Pairs of fp32 values in one register pair: one instruction for both.  The compiler fuses packed
+// products and sums, .rn or not; where each is to be rounded on its own, a sum of products is written
+// fma2(a, one, b) with a factor that it cannot see.
+struct F2 { float x, y; };
+__device__ __forceinline__ uint64_t bits2(F2 a) { uint64_t r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y)); return r; }
+__device__ __forceinline__ F2 pair(uint64_t r) { F2 a; asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r)); return a; }
+__device__ __forceinline__ F2 both(float x) { return {x, x}; }
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return pair(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return pair(r);
+}
 // f(T()) for the C++ type of a known tt_dtype
 template <typename F>
 auto by_type(int t, F&& f)

@@ -122,6 +122,23 @@ def test_gradient(law, n, rows, dim, up, out, extra, accumulate):
         assert torch.equal(first.view(torch.uint8), e.grad.view(torch.uint8))   # the same bits
 
 
+@pytest.mark.parametrize("n", [20, 512, 513, 4000, 70000])
+@pytest.mark.parametrize("rows,dim,shift", [(3, 1, 1), (50, 3, 1), (7, 24, 1), (1000, 8, 3), (33000, 1, 0), (4099, 20, 5), (2, 5000, 2)])
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_gradient_buffer_that_begins_anywhere(n, rows, dim, shift, out):
+    """Every value of the buffer is written, none beside it; rows of one value, blocks of many rows."""
+    g = torch.Generator().manual_seed(n)
+    buf = torch.full((shift + rows * dim + 9,), 5.0, dtype=out, device="cuda")
+    e = DenseEmbedding(rows, dim)
+    e.set_table(torch.zeros(rows, dim, device="cuda"), grad=buf[shift:shift + rows * dim].view(rows, dim))
+    tok = torch.randint(max(1, rows // 2), (n,), generator=g) * 2 % rows
+    u = torch.randn(n, dim, generator=g)
+    e.backward(tok.cuda(), u.cuda())
+    e.sync()
+    _check_grad(e, tok, u, None, 1.0, None, out)
+    assert (buf[:shift] == 5.0).all() and (buf[shift + rows * dim:] == 5.0).all()
+
+
 @pytest.mark.parametrize("n,rows,dim,pad", [(500, 40, 24, 3), (40000, 90, 8, 0), (3000, 1, 16, 0), (70, 33, 33, 32)])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_padding_gets_no_gradient(n, rows, dim, pad, accumulate):
