@@ -1,21 +1,3 @@
-#ifndef WT
-#define WT 24
-#endif
-#ifndef SW
-#define SW 8
-#endif
-#ifndef CW4
-#define CW4 1
-#endif
-#ifndef CW8
-#define CW8 1
-#endif
-#ifndef SA
-#define SA 8
-#endif
-#ifndef CA
-#define CA 2
-#endif
 // Dense tables: scaled lookup of rows, and the table's gradient by sorted tokens.
 //
 // Both move rows and do one or two operations a value, so memory bounds them.
@@ -55,57 +37,65 @@ struct LookupArgs {
     int64_t n, rows, out_stride;
     int token_bytes, dim;
     float scale;
-    int lanes;           // lanes that share a row, a power of two
-    int slabs;           // units of the same tokens, 32 * kCols vectors of a row each
+    int per_unit;        // tokens of a unit, 1 .. 32
+    int lane_bits;       // 2^lane_bits lanes share a row
+    unsigned slabs;      // units of the same tokens; a slab is 32 * kCols vectors of a row
     int32_t* status;
 };
 
-// A warp takes a unit: some tokens and a slab of their rows.  A step moves 32 / lanes rows; the loads
-// of all kSteps steps are issued before the first store.  No load hangs on a condition, so that
-// none waits for another: places behind the last token read the last one's row, tokens outside the
-// table row 0.
+// A warp takes a unit: up to 32 tokens, one a lane, and a slab of their rows.  A step moves 32 / lanes
+// rows; the loads of kSteps steps are issued before the first store.  No load hangs on a
+// condition, so that none waits for another: places behind the last token read the last one's row,
+// tokens outside the table row 0.
 template <typename T, typename O, int V, int kCols, int kSteps>
 __global__ void __launch_bounds__(kThreads) k_lookup(LookupArgs a, const T* __restrict__ table, O* __restrict__ out)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5), group = unit / a.slabs;
-    const int rows = 32 / a.lanes;
-    const int64_t i0 = group * (rows * kSteps < 32 ? rows * kSteps : 32);
+    const unsigned unit = blockIdx.x * kWarps + (threadIdx.x >> 5), group = unit / a.slabs, slab = unit - group * a.slabs;
+    const int64_t i0 = (int64_t)group * a.per_unit;
     if (i0 >= a.n) return;
-    const int cnt = (int)min64(min(32, rows * kSteps), a.n - i0);
+    const int cnt = (int)min64(a.per_unit, a.n - i0);
     int64_t token = token_at(a.tokens, a.token_bytes, i0 + min(lane, cnt - 1));
     const bool stop = has_error(a.status);
     const bool bad = token < 0 || token >= a.rows;
     if (bad) token = 0;
-    const int sub = lane & (a.lanes - 1), own = lane / a.lanes;
-    const int c0 = ((int)(unit - group * a.slabs) * kCols * 32 + sub) * V;
-    Pack<T, V> x[kSteps][kCols];
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int64_t row = __shfl_sync(kFull, token, min(s * rows + own, cnt - 1));
-#pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const int c = c0 + k * 32 * V;
-            x[s][k] = *reinterpret_cast<const Pack<T, V>*>(table + row * a.dim + (c < a.dim ? c : 0));
-        }
-    }
-    if (stop) return;
-    if (bad && lane < cnt) raise_error(a.status, TT_ERR_INDEX_RANGE, (int)min64(i0 + lane, INT32_MAX));
+    const int lanes = 1 << a.lane_bits, rows = 32 >> a.lane_bits, sub = lane & (lanes - 1), own = lane >> a.lane_bits;
+    const int steps = (cnt + rows - 1) >> (5 - a.lane_bits);
+    const int c0 = ((int)slab * kCols * 32 + sub) * V;
     const unsigned good = __ballot_sync(kFull, !bad);
+    for (int s0 = 0; s0 < steps; s0 += kSteps) {
+        Pack<T, V> x[kSteps][kCols];
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-        const int i = s * rows + own;
-        if (i >= cnt || !(good >> i & 1u)) continue;
+        for (int s = 0; s < kSteps; ++s) {
+            const int64_t row = __shfl_sync(kFull, token, min(((s0 + s) << (5 - a.lane_bits)) + own, cnt - 1));
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-            const int c = c0 + k * 32 * V;
-            float y[V];
+            for (int k = 0; k < kCols; ++k) {
+                const int c = c0 + k * 32 * V;
+                x[s][k] = *reinterpret_cast<const Pack<T, V>*>(table + row * a.dim + (c < a.dim ? c : 0));
+            }
+        }
+        if (stop) return;
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = to_f32(x[s][k].v[j]) * a.scale;
-            if (c < a.dim) store_pack(out + (i0 + i) * a.out_stride + c, y);
+        for (int s = 0; s < kSteps; ++s) {
+            const int i = ((s0 + s) << (5 - a.lane_bits)) + own;
+            if (i >= cnt || !(good >> i & 1u)) continue;
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) {
+                const int c = c0 + k * 32 * V;
+                float y[V];
+#pragma unroll
+                for (int j = 0; j < V; ++j) y[j] = to_f32(x[s][k].v[j]) * a.scale;
+                if (c < a.dim) store_pack(out + (i0 + i) * a.out_stride + c, y);
+            }
         }
     }
+    if (bad && lane < cnt) raise_error(a.status, TT_ERR_INDEX_RANGE, (int)min64(i0 + lane, INT32_MAX));
 }
+
+// The gradient's kernels are launched with leave to start while the one before still runs: each
+// waits here until that one has ended and its writes can be read, which hides the launch.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // Sorted tokens: keys ascending, each with its input position, equal keys in input order.  A key is
@@ -147,10 +137,11 @@ __global__ void __launch_bounds__(kThreads) k_token_keys(TokenArgs a, uint32_t* 
 // that is.  One launch instead of ten: 4 to 10 us instead of 30.
 // It goes on after an error: a cluster's blocks must all reach its barriers, and it writes
 // nothing but workspace.
-constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kCluster = 8;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kCluster = 16;     // needs leave for more than eight blocks, given once a device
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int64_t kClusterTokens = (int64_t)kCluster * kSortThreads * 8;
+static_assert(kDigits == kSortThreads, "a thread for each digit");
 
 template <int kItems> struct SortShared {
     uint2 come[kSortThreads * kItems];      // (key, position) from all blocks: this block's share of a pass's result
@@ -166,6 +157,7 @@ template <int kItems>
 __global__ void __launch_bounds__(kSortThreads, 1) k_token_sort(TokenArgs a, int bits, uint32_t* __restrict__ keys_out,
                                                                 int32_t* __restrict__ vals_out, int64_t touched_words)
 {
+    let_next_kernel_start();
     extern __shared__ __align__(16) char s_raw[];
     SortShared<kItems>& s = *reinterpret_cast<SortShared<kItems>*>(s_raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -223,29 +215,17 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_token_sort(TokenArgs a, int
             __syncwarp();
         }
         __syncthreads();
-        // counts of the warps before, and of the block: two threads for a digit, half of the warps each
+        // counts of the warps before, and of the block: a thread for each digit
         {
-            constexpr int kHalf = kSortWarps / 2;
-            const int d = tid >> 1, half = tid & 1;
-            uint32_t c[kHalf], run = 0;
-            if (d < digits)
+            uint32_t c[kSortWarps], sum = 0;
 #pragma unroll
-                for (int w = 0; w < kHalf; ++w) c[w] = s.before[half * kHalf + w][d];
-            else
+            for (int w = 0; w < kSortWarps; ++w) c[w] = s.before[w][tid];
 #pragma unroll
-                for (int w = 0; w < kHalf; ++w) c[w] = 0;
-#pragma unroll
-            for (int w = 0; w < kHalf; ++w) run += c[w];
-            const uint32_t other = __shfl_xor_sync(kFull, run, 1);
-            if (d < digits) {
-                uint32_t sum = half ? other : 0u;
-#pragma unroll
-                for (int w = 0; w < kHalf; ++w) {
-                    s.before[half * kHalf + w][d] = (uint16_t)sum;
-                    sum += c[w];
-                }
-                if (half) s.count[d] = sum;
+            for (int w = 0; w < kSortWarps; ++w) {
+                s.before[w][tid] = (uint16_t)sum;
+                sum += c[w];
             }
+            s.count[tid] = sum;
         }
         cluster.sync();
         // places of a digit's first key in this block and among all: scans over the digits
@@ -331,6 +311,8 @@ struct SumArgs {
     int tile;                 // positions per tile, a multiple of 32
     int64_t tiles;
     int slabs;                // units of a tile
+    int64_t sums;             // blocks of the first kernel that add up; its others clear rows,
+    int64_t first_clear;      // and the second kernel's go on from here
     float* head;              // [tiles][dim] part of a run that began in an earlier tile
     float* tail;              // [tiles][dim] part of a run that begins here and goes on
     const uint32_t* touched;  // a bit for every row that a token names (without accumulate)
@@ -346,18 +328,122 @@ __device__ __forceinline__ void finish_row(W* at, const float (&x)[V], const Pac
     store_pack(at, y);
 }
 
-#ifndef UU
-#define UU 4
-#endif
-#ifndef UA
-#define UA 2
-#endif
+// What one block clears: vectors of 16 bytes of the buffer, whatever rows they lie in.  The values in
+// front of the buffer's first 16-byte place and behind its last are left to block 0.
+constexpr int kClearVectors = 4096;   // of a block
+template <typename W, int kBlock> struct Clear {
+    static constexpr int N = 16 / sizeof(W), kEach = kClearVectors / kBlock;
+    static_assert(kEach % 4 == 0, "four at a time");
+    int64_t values, vectors, at, row0;
+    int skip;
+    unsigned col0;
+    __device__ __forceinline__ Clear(const SumArgs& a, int64_t block, const W* grad)
+    {
+        values = a.rows * a.dim;
+        skip = (int)((16 - ((uintptr_t)grad & 15)) & 15) / (int)sizeof(W);
+        vectors = values > skip ? (values - skip) / N : 0;
+        at = block * kClearVectors;
+        row0 = (at * N + skip) / a.dim;
+        col0 = (unsigned)(at * N + skip - row0 * a.dim);
+    }
+    // hit: whether a token names a row of this block's vectors; far: any row
+    template <typename Hit, typename Far>
+    __device__ __forceinline__ void run(const SumArgs& a, W* grad, Hit hit, Far far) const
+    {
+        if (at == 0) {
+            const int64_t e = threadIdx.x < skip ? threadIdx.x : skip + vectors * N + threadIdx.x - skip;
+            if (e < values && !far(e / a.dim)) grad[e] = W(0.f);
+        }
+        const unsigned dim = a.dim;
+        Pack<W, N> zero;
+        memset(&zero, 0, sizeof(zero));
+        // from one of the thread's vectors to the next
+        const unsigned ahead = kBlock * N / dim, aside = kBlock * N - ahead * dim;
+        const unsigned off = col0 + threadIdx.x * N, more = off / dim;
+        unsigned col = off - more * dim;
+        int64_t row = row0 + more;
+        int64_t v = at + threadIdx.x;
+        W* p = grad + skip + v * N;
+        if (skip == 0 && dim % N == 0) {          // no vector lies in two rows
+#pragma unroll 1
+            for (int i0 = 0; i0 < kEach; i0 += 4) {
+                bool named[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {     // all four are looked up first
+                    named[i] = hit(min64(row, a.rows - 1));
+                    row += ahead;
+                    col += aside;
+                    if (col >= dim) {
+                        col -= dim;
+                        ++row;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (v < vectors && !named[i]) *reinterpret_cast<Pack<W, N>*>(p) = zero;
+                    v += kBlock;
+                    p += kBlock * N;
+                }
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < kEach; i0 += 4) {
+            unsigned cols[4];
+            int64_t rows[4];
+            bool named[4], next[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                cols[i] = col;
+                rows[i] = row;
+                named[i] = hit(min64(row, a.rows - 1));
+                next[i] = col + N > dim && hit(min64(row + 1, a.rows - 1));
+                row += ahead;
+                col += aside;
+                if (col >= dim) {
+                    col -= dim;
+                    ++row;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (v < vectors) {
+                    if (dim >= N && !named[i] && !next[i]) {      // in one row, or in two that no token names
+                        *reinterpret_cast<Pack<W, N>*>(p) = zero;
+                    } else if (dim >= N) {
+                        for (unsigned j = 0; j < N; ++j)
+                            if (!(cols[i] + j < dim ? named[i] : next[i])) p[j] = W(0.f);
+                    } else {
+                        for (unsigned j = 0; j < N; ++j)
+                            if (!hit(rows[i] + (cols[i] + j) / dim)) p[j] = W(0.f);
+                    }
+                }
+                v += kBlock;
+                p += kBlock * N;
+            }
+        }
+    }
+};
+
+template <typename W>
+__device__ __forceinline__ void clear_block(const SumArgs& a, int64_t block, W* grad)
+{
+    auto hit = [&](int64_t row) { return a.touched[row >> 5] >> (row & 31) & 1u; };
+    Clear<W, kThreads>(a, block, grad).run(a, grad, hit, hit);
+}
+
 template <typename G, typename W, int V, bool kAdd>
 __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
 {
-    constexpr int kRows = kAdd ? UA : UU;                             // rows on their way at a time
+    constexpr int kRows = kAdd ? 2 : 4;   // rows on their way at a time
+    let_next_kernel_start();
+    wait_for_kernel_before();
     if (has_error(a.status)) return;
     const int lane = threadIdx.x & 31;
+    if (blockIdx.x >= a.sums) {
+        clear_block<W>(a, blockIdx.x - a.sums, grad);
+        return;
+    }
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int64_t tile = unit / a.slabs;
     if (tile >= a.tiles) return;
@@ -430,116 +516,72 @@ __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __re
     }
 }
 
-// The first `joins` blocks: where a run begins in a tile and goes on, they add up its parts, a warp
-// for each of its slabs, in the order of the tiles.  The other blocks clear the rows that no token
-// names.
-constexpr int kClear = 16;        // vectors of 16 bytes a thread clears
-
-// What one block clears: vectors of 16 bytes of the buffer, whatever rows they lie in.  The values in
-// front of the buffer's first 16-byte place and behind its last are left to block 0.
-template <typename W> struct Clear {
-    static constexpr int N = 16 / sizeof(W);
-    int64_t values, vectors, at, row0;
-    int skip;
-    unsigned col0;
-    __device__ __forceinline__ Clear(const SumArgs& a, int64_t block, const W* grad)
-    {
-        values = a.rows * a.dim;
-        skip = (int)((16 - ((uintptr_t)grad & 15)) & 15) / (int)sizeof(W);
-        vectors = values > skip ? (values - skip) / N : 0;
-        at = block * (kThreads * kClear);
-        row0 = (at * N + skip) / a.dim;
-        col0 = (unsigned)(at * N + skip - row0 * a.dim);
-    }
-    // hit: whether a token names a row of this block's vectors; far: any row
-    template <typename Hit, typename Far>
-    __device__ __forceinline__ void run(const SumArgs& a, W* grad, Hit hit, Far far) const
-    {
-        if (at == 0) {
-            const int64_t e = threadIdx.x < skip ? threadIdx.x : skip + vectors * N + threadIdx.x - skip;
-            if (e < values && !far(e / a.dim)) grad[e] = W(0.f);
-        }
-        const unsigned dim = a.dim;
-        Pack<W, N> zero;
-        memset(&zero, 0, sizeof(zero));
-#pragma unroll 1
-        for (int i0 = 0; i0 < kClear; i0 += 4) {
-            unsigned col[4];
-            int64_t row[4];
-            bool named[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {     // all four are looked up first
-                const unsigned off = col0 + ((i0 + i) * kThreads + threadIdx.x) * N, more = off / dim;
-                col[i] = off - more * dim;
-                row[i] = row0 + more;
-                named[i] = hit(min64(row[i], a.rows - 1));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int64_t v = at + (i0 + i) * kThreads + threadIdx.x;
-                if (v >= vectors) return;
-                W* const p = grad + skip + v * N;
-                if (col[i] + N <= dim) {
-                    if (!named[i]) *reinterpret_cast<Pack<W, N>*>(p) = zero;
-                } else {
-                    for (int j = 0; j < N; ++j)
-                        if (!hit(row[i] + (col[i] + j) / dim)) p[j] = W(0.f);
-                }
-            }
-        }
-    }
-};
-
+// Its first `joins` blocks: where a run begins in a tile and goes on, they add up its parts, kSplit
+// warps for a slab, each a row of tiles, and then the warps' sums, all in order.  The other blocks
+// clear rows that no token names.
+constexpr int kSplit = 4, kJoinSlabs = kWarps / kSplit;
 template <typename W, int V>
 __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t joins, W* __restrict__ grad)
 {
+    wait_for_kernel_before();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int groups = (a.slabs + kWarps - 1) / kWarps;           // blocks of a tile
+    __shared__ float s_part[kWarps][32 * V];
+    const int groups = (a.slabs + kJoinSlabs - 1) / kJoinSlabs;   // blocks of a tile
     const int64_t tile = blockIdx.x / groups, p0 = tile * a.tile, p1 = p0 + a.tile;
     const bool join = blockIdx.x < joins && p1 < a.n;
     const uint32_t k = join ? a.keys[p1 - 1] : 0u, then = join ? a.keys[p1] : 0u, front = join && p0 > 0 ? a.keys[p0 - 1] : ~0u;
     if (has_error(a.status)) return;
     if (blockIdx.x >= joins) {
-        auto hit = [&](int64_t row) { return a.touched[row >> 5] >> (row & 31) & 1u; };
-        Clear<W>(a, blockIdx.x - joins, grad).run(a, grad, hit, hit);
+        clear_block<W>(a, a.first_clear + (blockIdx.x - joins), grad);
         return;
     }
     // nothing goes on, or it began earlier
     if (!join || k >= (uint32_t)a.rows || then != k || front == k) return;
-    const int c = ((int)((blockIdx.x - tile * groups) * kWarps + wid) * 32 + lane) * V;
-    if (c - lane * V >= a.dim) return;
+    const int split = wid % kSplit, c = ((int)((blockIdx.x - tile * groups) * kJoinSlabs + wid / kSplit) * 32 + lane) * V;
     const bool on = c < a.dim;
     const int at_c = on ? c : 0;
-    // the run's end: each step the lanes split what is left, (lo, hi), into 33
-    int64_t lo = p1, hi = a.n;                                    // keys[lo] = k; keys[hi] is above k or past the end
-    while (hi - lo > 1) {
-        const int64_t step = (hi - lo + 32) / 33, at = lo + step * (lane + 1);
-        const unsigned below = __ballot_sync(kFull, at < hi && a.keys[at] == k);
-        const int m = __popc(below);
-        hi = min64(hi, lo + step * (m + 1));
-        lo = lo + step * m;
+    // the last tile that the run reaches: 32 tiles' first keys at a time
+    int64_t last = tile;                                          // heads of tiles tile + 1 .. last
+    for (;;) {
+        const int64_t p = (last + 1 + lane) * a.tile;
+        const unsigned same = __ballot_sync(kFull, p < a.n && a.keys[min64(p, a.n - 1)] == k);
+        const int m = same == kFull ? 32 : __ffs(~same) - 1;
+        last += m;
+        if (m < 32) break;
     }
-    const int64_t last = lo / a.tile;                             // heads of tiles tile + 1 .. last
     W* const at = grad + (int64_t)k * a.dim + at_c;
     Pack<W, V> old;
-    if (a.accumulate) old = *reinterpret_cast<const Pack<W, V>*>(at);
-    else memset(&old, 0, sizeof(old));
+    memset(&old, 0, sizeof(old));
     float acc[V];
-    load_pack(a.tail + tile * a.dim + at_c, acc);
+    if (split == 0) {
+        load_pack(a.tail + tile * a.dim + at_c, acc);
+        if (a.accumulate) old = *reinterpret_cast<const Pack<W, V>*>(at);
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    }
+    const int64_t each = (last - tile + kSplit - 1) / kSplit, from = tile + 1 + split * each, to = min64(from + each, last + 1);
     constexpr int kParts = 8;                                     // parts on their way at a time
-    for (int64_t t = tile + 1; t <= last; t += kParts) {
+    for (int64_t t = from; t < to; t += kParts) {
         Pack<float, V> x[kParts];
 #pragma unroll
         for (int i = 0; i < kParts; ++i)
-            x[i] = *reinterpret_cast<const Pack<float, V>*>(a.head + min64(t + i, last) * a.dim + at_c);
+            x[i] = *reinterpret_cast<const Pack<float, V>*>(a.head + min64(t + i, to - 1) * a.dim + at_c);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-            if (t + i > last) break;
+            if (t + i >= to) break;
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[j] += x[i].v[j];
         }
     }
-    if (on) finish_row(at, acc, old, a.scale);
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+    __syncthreads();
+    if (split > 0 || !on) return;
+    for (int w = wid + 1; w < wid + kSplit; ++w)
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] += s_part[w][j * 32 + lane];
+    finish_row(at, acc, old, a.scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -549,43 +591,38 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
 // up the few tokens in the rows that it covers.
 // ---------------------------------------------------------------------------
 constexpr int kFew = 512;
-constexpr int kFewRows = kThreads * kClear * 8;   // rows that a block's vectors lie in at most
+constexpr int kFewThreads = 1024, kFewWarps = kFewThreads / 32;
+constexpr int kFewRows = kClearVectors * 8;   // rows that a block's vectors lie in at most
 
 template <typename G, typename W, int V, bool kAdd>
-__global__ void __launch_bounds__(kThreads) k_token_few(TokenArgs t, SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
+__global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
 {
     constexpr int kRows = 4;
-    __shared__ alignas(16) uint32_t s_key[kFew + 4];
-    __shared__ uint32_t s_bits[kFewRows / 32 + 1];
+    __shared__ alignas(16) uint32_t s_key[kFew];
     __shared__ uint32_t s_sorted[kFew + 1];
-    __shared__ int32_t s_place[kFew];
-    __shared__ float s_part[kWarps][32 * V];
+    __shared__ int32_t s_place[kFew], s_front[kFew];
+    __shared__ uint32_t s_bits[kFewRows / 32 + 1];
+    __shared__ float s_part[kFewWarps][32 * V];
     const int n = (int)t.n, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const uint32_t none = (uint32_t)a.rows;
-    constexpr int kMine = kFew / kThreads;
-    int64_t token[kMine];
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) token[j] = token_at(t.tokens, t.token_bytes, min(tid + j * kThreads, n - 1));
-    bool bad = has_error(t.status);
-#pragma unroll
-    for (int j = 0; j < kMine; ++j) {
-        const int i = tid + j * kThreads;
-        if (i < n && (token[j] < 0 || token[j] >= a.rows)) {
-            raise_error(t.status, TT_ERR_INDEX_RANGE, i);
-            bad = true;
-        }
-        s_key[i] = i < n && token[j] != t.pad ? (uint32_t)token[j] : none;
+    // two threads for a key, which count half of the others each
+    const int mine = tid & (kFew - 1), half = tid / kFew;
+    const int64_t token = token_at(t.tokens, t.token_bytes, min(mine, n - 1));
+    const bool bad = token < 0 || token >= a.rows;
+    if (half == 0) {
+        s_key[mine] = mine < n && !bad && token != t.pad ? (uint32_t)token : none;
+        s_front[mine] = 0;
+        if (bad && mine < n) raise_error(t.status, TT_ERR_INDEX_RANGE, mine);
     }
-    if (tid < 4) s_key[kFew + tid] = none;
-    if (__syncthreads_or(bad)) return;
+    if (__syncthreads_or(bad || has_error(t.status))) return;
     if ((int)blockIdx.x >= a.slabs) {
         // the rows of this block's vectors that a token names, as bits
-        const Clear<W> clear(a, blockIdx.x - a.slabs, grad);
-        for (int i = tid; i < kFewRows / 32 + 1; i += kThreads) s_bits[i] = 0;
+        const Clear<W, kFewThreads> clear(a, blockIdx.x - a.slabs, grad);
+        for (int i = tid; i < kFewRows / 32 + 1; i += kFewThreads) s_bits[i] = 0;
         __syncthreads();
-        for (int i = tid; i < n; i += kThreads) {
-            const int64_t r = (int64_t)s_key[i] - clear.row0;
-            if (s_key[i] < none && r >= 0 && r < kFewRows + 32) atomicOr(&s_bits[r >> 5], 1u << (r & 31));
+        if (tid < n) {
+            const int64_t r = (int64_t)s_key[tid] - clear.row0;
+            if (s_key[tid] < none && r >= 0 && r < kFewRows + 32) atomicOr(&s_bits[r >> 5], 1u << (r & 31));
         }
         __syncthreads();
         auto hit = [&](int64_t row) { return s_bits[(row - clear.row0) >> 5] >> ((row - clear.row0) & 31) & 1u; };
@@ -599,35 +636,27 @@ __global__ void __launch_bounds__(kThreads) k_token_few(TokenArgs t, SumArgs a, 
     }
     // places: keys below mine, and equal ones in front
     {
-        uint32_t mine[kMine];
-        int place[kMine];
-#pragma unroll
-        for (int j = 0; j < kMine; ++j) {
-            mine[j] = s_key[tid + j * kThreads];
-            place[j] = 0;
+        const uint32_t key = s_key[mine];
+        const int quads = (n + 3) / 4, from = half ? (quads + 1) / 2 : 0, to = half ? quads : (quads + 1) / 2;
+        int front = 0;
+        for (int i = from; i < to; ++i) {     // what is behind the last token is `none`, never below, and never in front of one
+            const uint4 q = reinterpret_cast<const uint4*>(s_key)[i];
+            front += (q.x < key || (q.x == key && 4 * i < mine)) + (q.y < key || (q.y == key && 4 * i + 1 < mine)) +
+                     (q.z < key || (q.z == key && 4 * i + 2 < mine)) + (q.w < key || (q.w == key && 4 * i + 3 < mine));
         }
-        for (int i = 0; i < n; i += 4) {
-            const uint4 q = *reinterpret_cast<const uint4*>(s_key + i);
-            const uint32_t k[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-#pragma unroll
-                for (int j = 0; j < kMine; ++j)
-                    place[j] += i + e < n && (k[e] < mine[j] || (k[e] == mine[j] && i + e < tid + j * kThreads));
-        }
-#pragma unroll
-        for (int j = 0; j < kMine; ++j)
-            if (tid + j * kThreads < n) {
-                s_sorted[place[j]] = mine[j];
-                s_place[place[j]] = tid + j * kThreads;
-            }
-        if (tid == 0) s_sorted[n] = none;
+        if (mine < n) atomicAdd(&s_front[mine], front);
     }
+    __syncthreads();
+    if (tid < n) {
+        s_sorted[s_front[tid]] = s_key[tid];
+        s_place[s_front[tid]] = tid;
+    }
+    if (tid == 0) s_sorted[n] = none;
     __syncthreads();
     const int c = ((int)blockIdx.x * 32 + lane) * V;
     const bool on = c < a.dim;
     const int at_c = on ? c : 0;
-    const int each = (n + kWarps - 1) / kWarps, p0 = min(n, wid * each), p1 = min(n, p0 + each);
+    const int each = (n + kFewWarps - 1) / kFewWarps, p0 = min(n, wid * each), p1 = min(n, p0 + each);
     float acc[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[j] = 0.f;
@@ -671,7 +700,7 @@ __global__ void __launch_bounds__(kThreads) k_token_few(TokenArgs t, SumArgs a, 
         for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
     __syncthreads();
     if (!goes_on || began) return;
-    for (int w = wid + 1; w < kWarps && w * each < n && s_sorted[w * each] == k; ++w)
+    for (int w = wid + 1; w < kFewWarps && w * each < n && s_sorted[w * each] == k; ++w)
 #pragma unroll
         for (int j = 0; j < V; ++j) acc[j] += s_part[w][j * 32 + lane];
     Pack<W, V> old;
@@ -683,7 +712,7 @@ __global__ void __launch_bounds__(kThreads) k_token_few(TokenArgs t, SumArgs a, 
 // Positions a tile has: longer tiles cut fewer runs, shorter ones give every warp of the card a unit.
 int tile_of(int64_t n, int slabs, int sms)
 {
-    const int64_t units = ceil_div(n, 32) * slabs, want = (int64_t)sms * WT;
+    const int64_t units = ceil_div(n, 32) * slabs, want = (int64_t)sms * 24;
     return 32 * (int)(units <= want ? 1 : units / want >= 8 ? 8 : units / want);
 }
 
@@ -787,22 +816,25 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     a.dim = h->dim;
     a.scale = h->scale;
     a.status = h->d_status;
-    for (a.lanes = 1; a.lanes < vectors && a.lanes < 32;) a.lanes *= 2;
-    const int cols = wide ? V == 4 ? CW4 : CW8 : CA, rows = 32 / a.lanes;
-    a.slabs = (int)ceil_div(vectors, 32 * cols);
-    // as many steps to a unit as leave every warp of the card a unit or more
-    const bool many = ceil_div(n, rows * 4) * a.slabs >= (int64_t)h->num_sms * 16;
-    const int steps = many ? wide ? SW : SA : 1;
-    const unsigned grid = (unsigned)ceil_div(ceil_div(n, rows * steps < 32 ? rows * steps : 32) * a.slabs, kWarps);
+    for (a.lane_bits = 0; (1 << a.lane_bits) < vectors && a.lane_bits < 5;) ++a.lane_bits;
+    const int rows = 32 >> a.lane_bits;
+    constexpr int kAnyCols = 2, kAnySteps = 8;
+    a.slabs = (unsigned)ceil_div(vectors, 32 * (wide ? 1 : kAnyCols));
+    // as many tokens to a unit as leave every warp of the card a unit
+    a.per_unit = rows;
+    while (a.per_unit < 32 && ceil_div(n, a.per_unit * 2) * a.slabs >= (int64_t)h->num_sms * 64) a.per_unit *= 2;
+    const int64_t units = ceil_div(n, a.per_unit) * a.slabs;
+    if (units > UINT32_MAX - kWarps) return TT_ERR_ARG;   // sizes that no device holds
+    const unsigned grid = (unsigned)ceil_div(units, kWarps);
     by_type(h->table_type, [&](auto t) {
         by_type(out_type, [&](auto o) {
             using T = decltype(t);
             using O = decltype(o);
             auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, (const T*)h->table, (O*)out); };
-            constexpr bool f32 = sizeof(T) == 4 && sizeof(O) == 4;
-            constexpr int kWide = f32 ? 4 : 8, kCols = f32 ? CW4 : CW8;
-            if (wide) go(many ? k_lookup<T, O, kWide, kCols, SW> : k_lookup<T, O, kWide, kCols, 1>);
-            else go(many ? k_lookup<T, O, 1, CA, SA> : k_lookup<T, O, 1, CA, 1>);
+            constexpr int kWide = sizeof(T) == 4 && sizeof(O) == 4 ? 4 : 8;
+            const bool many = a.per_unit > rows;
+            if (wide) go(many ? k_lookup<T, O, kWide, 1, 4> : k_lookup<T, O, kWide, 1, 1>);
+            else go(many ? k_lookup<T, O, 1, kAnyCols, kAnySteps> : k_lookup<T, O, 1, kAnyCols, 1>);
         });
     });
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
@@ -818,8 +850,7 @@ cudaError_t sort_tokens(tt_emb_dense_t h, const TokenArgs& a, const DenseLayout&
         auto go = [&](auto kernel, size_t smem) {
             cudaLaunchConfig_t c = {};
             cudaLaunchAttribute at[1];
-            // one block where a thread's one key is enough; the cluster's barriers are dearer than the block's
-            const unsigned blocks = a.n <= kSortThreads ? 1 : kCluster;
+            const unsigned blocks = kCluster;
             at[0].id = cudaLaunchAttributeClusterDimension;
             at[0].val.clusterDim.x = blocks;
             at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -854,6 +885,22 @@ cudaError_t sort_tokens(tt_emb_dense_t h, const TokenArgs& a, const DenseLayout&
     sb.digit_total = (uint32_t*)(h->ws + y.digit_total);
     int nl = 0;
     return radix_sort_pairs(false, a.n, bits, sb, which, h->d_status, s, &nl);
+}
+
+// a launch that may start while the kernel before it still runs (see wait_for_kernel_before)
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, cudaStream_t s, Args... args)
+{
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3(grid);
+    c.blockDim = dim3(kThreads);
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, args...);
 }
 
 int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n, const void* up, int32_t up_type,
@@ -897,17 +944,21 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     a.tail = (float*)(h->ws + y.tail);
     a.touched = ta.touched;
     a.status = h->d_status;
-    const int64_t joins = a.tiles > 1 ? a.tiles * ceil_div(a.slabs, kWarps) : 0;
-    const int64_t clears = accumulate ? 0 : ceil_div(ceil_div(h->rows * h->dim, 16 / type_bytes(h->grad_type)), kThreads * kClear);
-    const unsigned grid = (unsigned)ceil_div(a.tiles * a.slabs, kWarps);
-    if (joins + clears > INT32_MAX) return TT_ERR_ARG;   // sizes that no device holds
+    const int64_t joins = a.tiles > 1 ? a.tiles * ceil_div(a.slabs, kJoinSlabs) : 0;
+    const int64_t clears = accumulate ? 0 : ceil_div(ceil_div(h->rows * h->dim, 16 / type_bytes(h->grad_type)), kClearVectors);
+    // Half of the clearing goes with the sums and half with the joins: few tokens leave the memory idle
+    // in both, and many fill it in either.
+    a.sums = ceil_div(a.tiles * a.slabs, kWarps);
+    a.first_clear = joins ? clears / 2 : clears;
+    const unsigned grid = (unsigned)(a.sums + a.first_clear), grid2 = (unsigned)(joins ? joins + clears - a.first_clear : 0);
+    if (a.sums + joins + clears > INT32_MAX) return TT_ERR_ARG;   // sizes that no device holds
     if (n <= kFew) {
         by_type(h->grad_type, [&](auto w) {
             by_type(up_type, [&](auto g) {
                 using W = decltype(w);
                 using G = decltype(g);
                 auto go = [&](auto kernel) {
-                    kernel<<<(unsigned)(a.slabs + clears), kThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
+                    kernel<<<(unsigned)(a.slabs + clears), kFewThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
                 };
                 constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
                 if (wide) go(accumulate ? k_token_few<G, W, kWide, true> : k_token_few<G, W, kWide, false>);
@@ -921,22 +972,23 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     if (sort_tokens(h, ta, y, bits, &which, s) != cudaSuccess) return TT_ERR_CUDA;
     a.keys = (const uint32_t*)(h->ws + y.keys[which]);
     a.vals = (const int32_t*)(h->ws + y.vals[which]);
+    cudaError_t e = cudaSuccess;
     by_type(h->grad_type, [&](auto w) {
         using W = decltype(w);
         by_type(up_type, [&](auto g) {
             using G = decltype(g);
-            auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, (const G*)up, up_stride, (W*)h->grad); };
+            auto go = [&](auto kernel) { e = launch_early(kernel, grid, s, a, (const G*)up, up_stride, (W*)h->grad); };
             constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
             if (wide) go(accumulate ? k_token_sum<G, W, kWide, true> : k_token_sum<G, W, kWide, false>);
             else go(accumulate ? k_token_sum<G, W, 1, true> : k_token_sum<G, W, 1, false>);
         });
-        if (joins + clears == 0) return;
-        auto go = [&](auto kernel) { kernel<<<(unsigned)(joins + clears), kThreads, 0, s>>>(a, joins, (W*)h->grad); };
+        if (grid2 == 0 || e != cudaSuccess) return;
+        auto go = [&](auto kernel) { e = launch_early(kernel, grid2, s, a, joins, (W*)h->grad); };
         if (V == 1) go(k_token_join<W, 1>);
         else if (V == 8) go(k_token_join<W, 8>);
         else if constexpr (sizeof(W) == 4) go(k_token_join<W, 4>);
     });
-    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
+    return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
 }  // namespace
@@ -965,7 +1017,8 @@ int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float
         return TT_ERR_CUDA;
     }
     auto room = [](auto kernel, size_t smem) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        return e == cudaSuccess ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
     };
     if (cudaMemset(h->d_status, 0, 256) != cudaSuccess ||
         room(k_token_sort<1>, sizeof(SortShared<1>)) != cudaSuccess || room(k_token_sort<2>, sizeof(SortShared<2>)) != cudaSuccess ||
