@@ -319,13 +319,41 @@ struct SumArgs {
     const int32_t* status;
 };
 
-template <typename W, int V>
-__device__ __forceinline__ void finish_row(W* at, const float (&x)[V], const Pack<W, V>& old, float scale)
-{
-    float y[V];
+// A lane's columns of a row: V neighbours, or, where rows begin anywhere (V = 1), four single values 32
+// columns apart.  Columns behind the last are read as the first and not written.
+template <int V> constexpr int kColumns = V == 1 ? 4 : V;
+template <int V> constexpr int kRuns = kColumns<V> / V;
+template <typename T, int V> struct Cols {
+    Pack<T, V> p[kRuns<V>];
+    __device__ __forceinline__ void load(const T* row, int c, int dim)
+    {
 #pragma unroll
-    for (int j = 0; j < V; ++j) y[j] = fmaf(x[j], scale, to_f32(old.v[j]));
-    store_pack(at, y);
+        for (int k = 0; k < kRuns<V>; ++k) {
+            const int at = c + k * 32 * V;
+            p[k] = *reinterpret_cast<const Pack<T, V>*>(row + (at < dim ? at : 0));
+        }
+    }
+    __device__ __forceinline__ void clear() { memset(p, 0, sizeof(p)); }
+    __device__ __forceinline__ float get(int e) const { return to_f32(p[e / V].v[e % V]); }
+};
+template <int V, typename T>
+__device__ __forceinline__ void store_cols(T* row, int c, int dim, const float (&x)[kColumns<V>])
+{
+#pragma unroll
+    for (int k = 0; k < kRuns<V>; ++k) {
+        float y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = x[k * V + j];
+        if (c + k * 32 * V < dim) store_pack(row + c + k * 32 * V, y);
+    }
+}
+template <int V, typename W>
+__device__ __forceinline__ void finish_row(W* row, int c, int dim, const float (&x)[kColumns<V>], const Cols<W, V>& old, float scale)
+{
+    float y[kColumns<V>];
+#pragma unroll
+    for (int e = 0; e < kColumns<V>; ++e) y[e] = fmaf(x[e], scale, old.get(e));
+    store_cols<V>(row, c, dim, y);
 }
 
 // What one block clears: vectors of 16 bytes of the buffer, whatever rows they lie in.  The values in
@@ -433,9 +461,11 @@ __device__ __forceinline__ void clear_block(const SumArgs& a, int64_t block, W* 
 }
 
 template <typename G, typename W, int V, bool kAdd>
-__global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
+__global__ void __launch_bounds__(kThreads, 4) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
 {
-    constexpr int kRows = kAdd ? 2 : 4;   // rows on their way at a time
+    // Rows on their way at a time.  Few, because what hides the memory's latency is warps: four blocks an
+    // SM with four rows each take 70 us for 32768 rows of 4096 bf16 values, with eight rows 78 to 90.
+    constexpr int kRows = kAdd ? 2 : 4;
     let_next_kernel_start();
     wait_for_kernel_before();
     if (has_error(a.status)) return;
@@ -447,15 +477,14 @@ __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __re
     const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
     const int64_t tile = unit / a.slabs;
     if (tile >= a.tiles) return;
-    const int c = ((int)(unit - tile * a.slabs) * 32 + lane) * V;
-    const bool on = c < a.dim;
-    const int at_c = on ? c : 0;      // lanes behind the last column load the first ones
+    const int c = (int)(unit - tile * a.slabs) * 32 * kColumns<V> + lane * V;
     const uint32_t none = (uint32_t)a.rows;
     const int64_t p0 = tile * a.tile, p1 = min64(p0 + a.tile, a.n);
     bool began = p0 > 0 && a.keys[p0 - 1] == a.keys[p0];  // the current run began in an earlier tile
-    F2 acc[(V + 1) / 2];
+    constexpr int E = kColumns<V>;
+    F2 acc[E / 2];
 #pragma unroll
-    for (int j = 0; j < (V + 1) / 2; ++j) acc[j] = both(0.f);
+    for (int j = 0; j < E / 2; ++j) acc[j] = both(0.f);
     for (int64_t p = p0; p < p1; p += 32) {
         // a lane holds one position, and whether its run ends there or at the tile's end
         const bool in = p + lane < p1;
@@ -471,45 +500,39 @@ __global__ void __launch_bounds__(kThreads) k_token_sum(SumArgs a, const G* __re
             // No load hangs on a condition, so that none waits for another.  Places without a sum read a
             // row they do not use (position 0's, row 0); with kAdd each place loads its row of the
             // gradient as it is, which equal neighbours find in the cache.
-            Pack<G, V> x[kRows];
-            Pack<W, V> old[kAdd ? kRows : 1];
+            Cols<G, V> x[kRows];
+            Cols<W, V> old[kAdd ? kRows : 1];
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 const int64_t row = __shfl_sync(kFull, val, q + u);
-                x[u] = *reinterpret_cast<const Pack<G, V>*>(up + row * stride + at_c);
+                x[u].load(up + row * stride, c, a.dim);
                 if constexpr (kAdd) {
                     const uint32_t k = __shfl_sync(kFull, key, q + u);
-                    old[u] = *reinterpret_cast<const Pack<W, V>*>(grad + (int64_t)(k < none ? k : 0u) * a.dim + at_c);
+                    old[u].load(grad + (int64_t)(k < none ? k : 0u) * a.dim, c, a.dim);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 if (q + u >= cnt) break;
-                if constexpr (V > 1) {
 #pragma unroll
-                    for (int j = 0; j < V / 2; ++j) acc[j] = add2(acc[j], {to_f32(x[u].v[2 * j]), to_f32(x[u].v[2 * j + 1])});
-                } else {
-                    acc[0].x += to_f32(x[u].v[0]);
-                }
+                for (int j = 0; j < E / 2; ++j) acc[j] = add2(acc[j], {x[u].get(2 * j), x[u].get(2 * j + 1)});
                 if (!(ends >> (q + u) & 1u)) continue;
-                float sum[V];
+                float sum[E];
 #pragma unroll
-                for (int j = 0; j < V; ++j) sum[j] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+                for (int e = 0; e < E; ++e) sum[e] = e & 1 ? acc[e / 2].y : acc[e / 2].x;
                 const bool here = whole >> (q + u) & 1u;
                 const uint32_t k = __shfl_sync(kFull, key, q + u);
-                if (on) {
-                    if (began) {
-                        store_pack(a.head + tile * a.dim + c, sum);
-                    } else if (!here) {
-                        store_pack(a.tail + tile * a.dim + c, sum);
-                    } else {
-                        if constexpr (!kAdd) memset(&old[0], 0, sizeof(old[0]));
-                        finish_row(grad + (int64_t)k * a.dim + c, sum, old[kAdd ? u : 0], a.scale);
-                    }
+                if (began) {
+                    store_cols<V>(a.head + tile * a.dim, c, a.dim, sum);
+                } else if (!here) {
+                    store_cols<V>(a.tail + tile * a.dim, c, a.dim, sum);
+                } else {
+                    if constexpr (!kAdd) old[0].clear();
+                    finish_row<V>(grad + (int64_t)k * a.dim, c, a.dim, sum, old[kAdd ? u : 0], a.scale);
                 }
                 began = false;
 #pragma unroll
-                for (int j = 0; j < (V + 1) / 2; ++j) acc[j] = both(0.f);
+                for (int j = 0; j < E / 2; ++j) acc[j] = both(0.f);
             }
         }
         if (cnt < 32) break;
@@ -525,7 +548,8 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
 {
     wait_for_kernel_before();
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    __shared__ float s_part[kWarps][32 * V];
+    constexpr int E = kColumns<V>;
+    __shared__ float s_part[kWarps][32 * E];
     const int groups = (a.slabs + kJoinSlabs - 1) / kJoinSlabs;   // blocks of a tile
     const int64_t tile = blockIdx.x / groups, p0 = tile * a.tile, p1 = p0 + a.tile;
     const bool join = blockIdx.x < joins && p1 < a.n;
@@ -537,9 +561,8 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
     }
     // nothing goes on, or it began earlier
     if (!join || k >= (uint32_t)a.rows || then != k || front == k) return;
-    const int split = wid % kSplit, c = ((int)((blockIdx.x - tile * groups) * kJoinSlabs + wid / kSplit) * 32 + lane) * V;
-    const bool on = c < a.dim;
-    const int at_c = on ? c : 0;
+    const int split = wid % kSplit, slab = (int)(blockIdx.x - tile * groups) * kJoinSlabs + wid / kSplit;
+    const int c = slab * 32 * E + lane * V;
     // the last tile that the run reaches: 32 tiles' first keys at a time
     int64_t last = tile;                                          // heads of tiles tile + 1 .. last
     for (;;) {
@@ -549,39 +572,40 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
         last += m;
         if (m < 32) break;
     }
-    W* const at = grad + (int64_t)k * a.dim + at_c;
-    Pack<W, V> old;
-    memset(&old, 0, sizeof(old));
-    float acc[V];
-    if (split == 0) {
-        load_pack(a.tail + tile * a.dim + at_c, acc);
-        if (a.accumulate) old = *reinterpret_cast<const Pack<W, V>*>(at);
-    } else {
+    W* const row = grad + (int64_t)k * a.dim;
+    Cols<W, V> old;
+    old.clear();
+    float acc[E];
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = 0.f;
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (split == 0) {
+        Cols<float, V> x;
+        x.load(a.tail + tile * a.dim, c, a.dim);
+        if (a.accumulate) old.load(row, c, a.dim);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = x.get(e);
     }
     const int64_t each = (last - tile + kSplit - 1) / kSplit, from = tile + 1 + split * each, to = min64(from + each, last + 1);
     constexpr int kParts = 8;                                     // parts on their way at a time
     for (int64_t t = from; t < to; t += kParts) {
-        Pack<float, V> x[kParts];
+        Cols<float, V> x[kParts];
 #pragma unroll
-        for (int i = 0; i < kParts; ++i)
-            x[i] = *reinterpret_cast<const Pack<float, V>*>(a.head + min64(t + i, to - 1) * a.dim + at_c);
+        for (int i = 0; i < kParts; ++i) x[i].load(a.head + min64(t + i, to - 1) * a.dim, c, a.dim);
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
             if (t + i >= to) break;
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += x[i].v[j];
+            for (int e = 0; e < E; ++e) acc[e] += x[i].get(e);
         }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+    for (int e = 0; e < E; ++e) s_part[wid][e * 32 + lane] = acc[e];
     __syncthreads();
-    if (split > 0 || !on) return;
+    if (split > 0) return;
     for (int w = wid + 1; w < wid + kSplit; ++w)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += s_part[w][j * 32 + lane];
-    finish_row(at, acc, old, a.scale);
+        for (int e = 0; e < E; ++e) acc[e] += s_part[w][e * 32 + lane];
+    finish_row<V>(row, c, a.dim, acc, old, a.scale);
 }
 
 // ---------------------------------------------------------------------------
@@ -602,7 +626,8 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
     __shared__ uint32_t s_sorted[kFew + 1];
     __shared__ int32_t s_place[kFew], s_front[kFew];
     __shared__ uint32_t s_bits[kFewRows / 32 + 1];
-    __shared__ float s_part[kFewWarps][32 * V];
+    constexpr int E = kColumns<V>;
+    __shared__ float s_part[kFewWarps][32 * E];
     const int n = (int)t.n, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const uint32_t none = (uint32_t)a.rows;
     // two threads for a key, which count half of the others each
@@ -653,26 +678,24 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
     }
     if (tid == 0) s_sorted[n] = none;
     __syncthreads();
-    const int c = ((int)blockIdx.x * 32 + lane) * V;
-    const bool on = c < a.dim;
-    const int at_c = on ? c : 0;
+    const int c = (int)blockIdx.x * 32 * E + lane * V;
     const int each = (n + kFewWarps - 1) / kFewWarps, p0 = min(n, wid * each), p1 = min(n, p0 + each);
-    float acc[V];
+    float acc[E];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    auto row_of = [&](uint32_t k) { return grad + (int64_t)k * a.dim + at_c; };
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    auto row_of = [&](uint32_t k) { return grad + (int64_t)k * a.dim; };
     // a run that goes over this part's end is left in acc, and what ends one that began before in s_part
     bool began = p0 > 0 && p0 < n && s_sorted[p0 - 1] == s_sorted[p0];
     uint32_t k = none;
     for (int p = p0; p < p1; p += kRows) {
-        Pack<G, V> x[kRows];
-        Pack<W, V> old[kAdd ? kRows : 1];
-        memset(&old[0], 0, sizeof(old[0]));
+        Cols<G, V> x[kRows];
+        Cols<W, V> old[kAdd ? kRows : 1];
+        old[0].clear();
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
             const int q = min(p + u, p1 - 1);
-            x[u] = *reinterpret_cast<const Pack<G, V>*>(up + (int64_t)s_place[q] * stride + at_c);
-            if constexpr (kAdd) old[u] = *reinterpret_cast<const Pack<W, V>*>(row_of(s_sorted[q] < none ? s_sorted[q] : 0u));
+            x[u].load(up + (int64_t)s_place[q] * stride, c, a.dim);
+            if constexpr (kAdd) old[u].load(row_of(s_sorted[q] < none ? s_sorted[q] : 0u), c, a.dim);
         }
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {
@@ -680,33 +703,33 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
             k = s_sorted[p + u];
             if (k >= none) break;
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] += to_f32(x[u].v[j]);
+            for (int e = 0; e < E; ++e) acc[e] += x[u].get(e);
             if (s_sorted[p + u + 1] == k) continue;
             if (began) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+                for (int e = 0; e < E; ++e) s_part[wid][e * 32 + lane] = acc[e];
                 began = false;
-            } else if (on) {
-                finish_row(row_of(k), acc, old[kAdd ? u : 0], a.scale);
+            } else {
+                finish_row<V>(row_of(k), c, a.dim, acc, old[kAdd ? u : 0], a.scale);
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) acc[j] = 0.f;
+            for (int e = 0; e < E; ++e) acc[e] = 0.f;
         }
     }
     // what is left in acc goes on behind this part, or is all of a part that a run covers
     const bool goes_on = p1 > p0 && p1 < n && k < none && s_sorted[p1] == k;
     if (goes_on && began)
 #pragma unroll
-        for (int j = 0; j < V; ++j) s_part[wid][j * 32 + lane] = acc[j];
+        for (int e = 0; e < E; ++e) s_part[wid][e * 32 + lane] = acc[e];
     __syncthreads();
     if (!goes_on || began) return;
     for (int w = wid + 1; w < kFewWarps && w * each < n && s_sorted[w * each] == k; ++w)
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] += s_part[w][j * 32 + lane];
-    Pack<W, V> old;
-    memset(&old, 0, sizeof(old));
-    if constexpr (kAdd) old = *reinterpret_cast<const Pack<W, V>*>(row_of(k));
-    if (on) finish_row(row_of(k), acc, old, a.scale);
+        for (int e = 0; e < E; ++e) acc[e] += s_part[w][e * 32 + lane];
+    Cols<W, V> old;
+    old.clear();
+    if constexpr (kAdd) old.load(row_of(k), c, a.dim);
+    finish_row<V>(row_of(k), c, a.dim, acc, old, a.scale);
 }
 
 // Positions a tile has: longer tiles cut fewer runs, shorter ones give every warp of the card a unit.
@@ -937,7 +960,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     a.dim = h->dim;
     a.scale = h->scale;
     a.accumulate = accumulate;
-    a.slabs = (int)ceil_div(h->dim, 32 * V);
+    a.slabs = (int)ceil_div(h->dim, 32 * (wide ? V : kColumns<1>));
     a.tile = tile_of(n, a.slabs, h->num_sms);
     a.tiles = ceil_div(n, a.tile);
     a.head = (float*)(h->ws + y.head);
