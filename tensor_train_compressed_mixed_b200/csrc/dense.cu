@@ -2,7 +2,7 @@
 //
 // Both move rows and do one or two operations a value, so memory bounds them.
 //
-// Lookup.  One thread moves 16 bytes (of the wider type) of up to four rows, whose loads are all
+// Lookup.  A lane moves 16 bytes (of the narrower type) of four rows at a time, whose loads are all
 // issued before the first store.
 //
 // Gradient.  The tokens are sorted by row (stable, so equal rows stay in input order) and the sorted
@@ -319,9 +319,10 @@ struct SumArgs {
     const int32_t* status;
 };
 
-// A lane's columns of a row: V neighbours, or, where rows begin anywhere (V = 1), four single values 32
-// columns apart.  Columns behind the last are read as the first and not written.
-template <int V> constexpr int kColumns = V == 1 ? 4 : V;
+// A lane's columns of a row: V neighbours, or, where rows begin at places for pairs (V = 2) or for single
+// values only, four of those, each 32 of them behind the last.  Columns behind the row's last are
+// read as its first and not written.
+template <int V> constexpr int kColumns = V <= 2 ? 4 * V : V;
 template <int V> constexpr int kRuns = kColumns<V> / V;
 template <typename T, int V> struct Cols {
     Pack<T, V> p[kRuns<V>];
@@ -460,12 +461,15 @@ __device__ __forceinline__ void clear_block(const SumArgs& a, int64_t block, W* 
     Clear<W, kThreads>(a, block, grad).run(a, grad, hit, hit);
 }
 
-template <typename G, typename W, int V, bool kAdd>
-__global__ void __launch_bounds__(kThreads, 4) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
+// kRows rows are on their way at a time.  With many units few of them, because what hides the memory's
+// latency then is warps: four blocks an SM with four rows of 8 columns a lane take 70 us for 32768
+// rows of 4096 bf16 values, with eight rows 78 to 90.  With few units (a warp of the card has one or
+// none) more: 16205 rows of 4 fp32 values added to a gradient take 15 us two at a time.
+constexpr int rows_many(bool add) { return add ? 2 : 4; }
+constexpr int kRowsFew = 8;
+template <typename G, typename W, int V, bool kAdd, int kRows>
+__global__ void __launch_bounds__(kThreads, kRows == kRowsFew ? 1 : 4) k_token_sum(SumArgs a, const G* __restrict__ up, int64_t stride, W* __restrict__ grad)
 {
-    // Rows on their way at a time.  Few, because what hides the memory's latency is warps: four blocks an
-    // SM with four rows each take 70 us for 32768 rows of 4096 bf16 values, with eight rows 78 to 90.
-    constexpr int kRows = kAdd ? 2 : 4;
     let_next_kernel_start();
     wait_for_kernel_before();
     if (has_error(a.status)) return;
@@ -767,10 +771,19 @@ DenseLayout dense_layout(int64_t n, int dim, int64_t rows)
     return y;
 }
 
-// whether rows of `stride` values at p can be moved eight values at a time
-bool wide_rows(const void* p, int64_t stride, int type)
+// whether rows of `stride` values at p begin at multiples of `bytes`
+bool rows_at(const void* p, int64_t stride, int type, int bytes)
 {
-    return ((uintptr_t)p & 15) == 0 && (stride * type_bytes(type)) % 16 == 0;
+    return ((uintptr_t)p & (bytes - 1)) == 0 && (stride * type_bytes(type)) % bytes == 0;
+}
+
+// Neighbouring values that one access may move in rows of both kinds: 16 bytes of the narrower type, or a
+// pair, or one.
+int width_of(int dim, const void* p, int64_t p_stride, int p_type, const void* q, int64_t q_stride, int q_type)
+{
+    if (dim % 8 == 0 && rows_at(p, p_stride, p_type, 16) && rows_at(q, q_stride, q_type, 16))
+        return p_type == TT_F32 && q_type == TT_F32 ? 4 : 8;
+    return dim % 2 == 0 && rows_at(p, p_stride, p_type, 2 * type_bytes(p_type)) && rows_at(q, q_stride, q_type, 2 * type_bytes(q_type)) ? 2 : 1;
 }
 
 }  // namespace
@@ -826,9 +839,7 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     h->last_stream = s;
     h->used_stream = true;
     if (n == 0) return TT_OK;
-    const bool wide = h->dim % 8 == 0 && wide_rows(h->table, h->dim, h->table_type) && wide_rows(out, out_stride, out_type);
-    // 16 bytes a lane of the narrower type; where rows begin anywhere, single values, two to a lane
-    const int V = !wide ? 1 : h->table_type == TT_F32 && out_type == TT_F32 ? 4 : 8;
+    const int V = width_of(h->dim, h->table, h->dim, h->table_type, out, out_stride, out_type);
     const int64_t vectors = ceil_div(h->dim, V);
     LookupArgs a;
     a.tokens = tokens;
@@ -841,8 +852,8 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     a.status = h->d_status;
     for (a.lane_bits = 0; (1 << a.lane_bits) < vectors && a.lane_bits < 5;) ++a.lane_bits;
     const int rows = 32 >> a.lane_bits;
-    constexpr int kAnyCols = 2, kAnySteps = 8;
-    a.slabs = (unsigned)ceil_div(vectors, 32 * (wide ? 1 : kAnyCols));
+    constexpr int kAnyCols = 2, kAnySteps = 8;            // of pairs and single values
+    a.slabs = (unsigned)ceil_div(vectors, 32 * (V > 2 ? 1 : kAnyCols));
     // as many tokens to a unit as leave every warp of the card a unit
     a.per_unit = rows;
     while (a.per_unit < 32 && ceil_div(n, a.per_unit * 2) * a.slabs >= (int64_t)h->num_sms * 64) a.per_unit *= 2;
@@ -856,7 +867,8 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
             auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, s>>>(a, (const T*)h->table, (O*)out); };
             constexpr int kWide = sizeof(T) == 4 && sizeof(O) == 4 ? 4 : 8;
             const bool many = a.per_unit > rows;
-            if (wide) go(many ? k_lookup<T, O, kWide, 1, 4> : k_lookup<T, O, kWide, 1, 1>);
+            if (V > 2) go(many ? k_lookup<T, O, kWide, 1, 4> : k_lookup<T, O, kWide, 1, 1>);
+            else if (V == 2) go(many ? k_lookup<T, O, 2, kAnyCols, kAnySteps> : k_lookup<T, O, 2, kAnyCols, 1>);
             else go(many ? k_lookup<T, O, 1, kAnyCols, kAnySteps> : k_lookup<T, O, 1, kAnyCols, 1>);
         });
     });
@@ -951,16 +963,14 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     ta.token_bytes = token_bytes;
     ta.touched = accumulate ? nullptr : (uint32_t*)(h->ws + y.touched);
     ta.status = h->d_status;
-    const bool wide = h->dim % 8 == 0 && wide_rows(h->grad, h->dim, h->grad_type) && wide_rows(up, up_stride, up_type);
-    // 16 bytes a lane of the narrower type
-    const int V = !wide ? 1 : h->grad_type == TT_F32 && up_type == TT_F32 ? 4 : 8;
+    const int V = width_of(h->dim, h->grad, h->dim, h->grad_type, up, up_stride, up_type);
     SumArgs a;
     a.n = n;
     a.rows = h->rows;
     a.dim = h->dim;
     a.scale = h->scale;
     a.accumulate = accumulate;
-    a.slabs = (int)ceil_div(h->dim, 32 * (wide ? V : kColumns<1>));
+    a.slabs = (int)ceil_div(h->dim, 32 * (V > 2 ? V : V == 2 ? kColumns<2> : kColumns<1>));
     a.tile = tile_of(n, a.slabs, h->num_sms);
     a.tiles = ceil_div(n, a.tile);
     a.head = (float*)(h->ws + y.head);
@@ -984,7 +994,8 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
                     kernel<<<(unsigned)(a.slabs + clears), kFewThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
                 };
                 constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
-                if (wide) go(accumulate ? k_token_few<G, W, kWide, true> : k_token_few<G, W, kWide, false>);
+                if (V > 2) go(accumulate ? k_token_few<G, W, kWide, true> : k_token_few<G, W, kWide, false>);
+                else if (V == 2) go(accumulate ? k_token_few<G, W, 2, true> : k_token_few<G, W, 2, false>);
                 else go(accumulate ? k_token_few<G, W, 1, true> : k_token_few<G, W, 1, false>);
             });
         });
@@ -1002,12 +1013,20 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
             using G = decltype(g);
             auto go = [&](auto kernel) { e = launch_early(kernel, grid, s, a, (const G*)up, up_stride, (W*)h->grad); };
             constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
-            if (wide) go(accumulate ? k_token_sum<G, W, kWide, true> : k_token_sum<G, W, kWide, false>);
-            else go(accumulate ? k_token_sum<G, W, 1, true> : k_token_sum<G, W, 1, false>);
+            const bool few = a.tiles * a.slabs <= (int64_t)h->num_sms * 8;
+            auto pick = [&](auto v) {
+                constexpr int kV = decltype(v)::value;
+                if (accumulate) go(few ? k_token_sum<G, W, kV, true, kRowsFew> : k_token_sum<G, W, kV, true, rows_many(true)>);
+                else go(few ? k_token_sum<G, W, kV, false, kRowsFew> : k_token_sum<G, W, kV, false, rows_many(false)>);
+            };
+            if (V > 2) pick(std::integral_constant<int, kWide>());
+            else if (V == 2) pick(std::integral_constant<int, 2>());
+            else pick(std::integral_constant<int, 1>());
         });
         if (grid2 == 0 || e != cudaSuccess) return;
         auto go = [&](auto kernel) { e = launch_early(kernel, grid2, s, a, joins, (W*)h->grad); };
         if (V == 1) go(k_token_join<W, 1>);
+        else if (V == 2) go(k_token_join<W, 2>);
         else if (V == 8) go(k_token_join<W, 8>);
         else if constexpr (sizeof(W) == 4) go(k_token_join<W, 4>);
     });
