@@ -49,7 +49,9 @@ struct List {
     int32_t pad;
     int64_t tiles;
     double log_b1, log_b2;
-    float b1, b2, c1, c2, eps, one;   // c = 1 - b, rounded from 64 bits
+    uint64_t b1, b2, c1, c2, one;     // each twice in a pair; c = 1 - b, rounded from 64 bits
+    float eps;
+    int32_t pad2;
     uint64_t seed;
     int64_t* steps;
     uint32_t* ticket;
@@ -107,6 +109,13 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     float r;
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+// the least of three words below 2^31, which order like the floats of their bits
+__device__ __forceinline__ uint32_t min3(uint32_t a, uint32_t b, uint32_t c)
+{
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(__uint_as_float(a)), "f"(__uint_as_float(b)), "f"(__uint_as_float(c)));
+    return __float_as_uint(r);
 }
 __device__ __forceinline__ float block_max(const F2 (&x)[kPairs])
 {
@@ -171,7 +180,7 @@ __device__ __forceinline__ Pack<T, run> narrow(const F2* x)
     return q;
 }
 struct Factors {
-    F2 one, b1, c1, b2, c2, eps, inv_root2, keep, minus_lr;
+    F2 den_u, den_1, keep;      // the update is m / (den_u sqrt(v) + den_1)
     uint64_t start;
 };
 
@@ -289,7 +298,7 @@ __device__ __forceinline__ void store_block(const Place<P, G, k8>& at, int from,
 
 // `random`: the lane's place in the stream of random words
 template <typename P, typename G, bool k8>
-__device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const Factors& f)
+__device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const Factors& f, const List& L)
 {
     constexpr int run = Shape<P, G, k8>::run, groups = Shape<P, G, k8>::groups;
     F2 p[kPairs], g[kPairs], m[kPairs], v[kPairs], u[kPairs];
@@ -309,8 +318,8 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
             u[i] = mul2(decode8(b.codes(b.v, i / 2) >> (16 * (i & 1)) & 0xffffu), both(b.vs));
             v[i] = mul2(u[i], u[i]);
         }
-        m[i] = fma2(mul2(m[i], f.b1), f.one, mul2(g[i], f.c1));
-        v[i] = fma2(mul2(v[i], f.b2), f.one, mul2(mul2(g[i], g[i]), f.c2));
+        m[i] = fma2(mul2(m[i], pair(L.b1)), pair(L.one), mul2(g[i], pair(L.c1)));
+        v[i] = fma2(mul2(v[i], pair(L.b2)), pair(L.one), mul2(mul2(g[i], g[i]), pair(L.c2)));
         if constexpr (k8) u[i] = root2(v[i]);
         else u[i] = {root(v[i].x), root(v[i].y)};
     }
@@ -332,8 +341,8 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
     }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
-        const F2 den = fma2(u[i], f.inv_root2, f.eps);
-        p[i] = fma2(mul2(m[i], f.minus_lr), {rcp(den.x), rcp(den.y)}, mul2(p[i], f.keep));
+        const F2 den = fma2(u[i], f.den_u, f.den_1);
+        p[i] = fma2(m[i], {rcp(den.x), rcp(den.y)}, mul2(p[i], f.keep));
     }
     if constexpr (k8) {
         if (am < 0x1p-100f) am = 0.f;
@@ -356,11 +365,15 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
                 // gives 448's code, as the random bits end 4 places above the lowest.
                 const F2 y = mul2(mul2(u[i], iu), both(0x1p-120f));
                 const uint32_t part = (uint32_t)(word >> (32 * h));
-                code[2 * h] = (__float_as_uint(y.x) << 4) + ((part & 0xffffu) << 8);
-                code[2 * h + 1] = (__float_as_uint(y.y) << 4) + (part >> 16 << 8);
-                // a root above zero (its bits are above 2^24) keeps the least code at least
-                code[2 * h] = max(code[2 * h], min(__float_as_uint(u[i].x), 1u << 24));
-                code[2 * h + 1] = max(code[2 * h + 1], min(__float_as_uint(u[i].y), 1u << 24));
+                code[2 * h] = (__float_as_uint(y.x) << 4) + __byte_perm(part, 0u, 0x4104);
+                code[2 * h + 1] = (__float_as_uint(y.y) << 4) + __byte_perm(part, 0u, 0x4324);
+            }
+            // A root above zero (its bits are above 2^24) keeps the least code at least.  Few blocks have a
+            // code of zero, which is below every float whose exponent the code's lowest bit reaches.
+            if (min3(min3(code[0], code[1], code[2]), code[3], code[3]) < 1u << 24) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    code[e] = max(code[e], min(__float_as_uint(e & 1 ? u[2 * w + e / 2].y : u[2 * w + e / 2].x), 1u << 24));
             }
             b.set_codes(b.m, w, mc[0] | mc[1] << 16);
             b.set_codes(b.v, w, __byte_perm(__byte_perm(code[0], code[1], 0x0073), __byte_perm(code[2], code[3], 0x0073), 0x5410));
@@ -387,14 +400,13 @@ __device__ __forceinline__ Factors factors(const List& L, int64_t t, float lr)
 {
     Factors f;
     // 1 - beta^t without cancellation: the product is formed in 64 bits, the rest in 32
-    f.minus_lr = both(lr / expm1f((float)((double)t * L.log_b1)));
-    f.inv_root2 = both(1.f / sqrtf(-expm1f((float)((double)t * L.log_b2))));
-    f.one = both(L.one);
-    f.b1 = both(L.b1);
-    f.c1 = both(L.c1);
-    f.b2 = both(L.b2);
-    f.c2 = both(L.c2);
-    f.eps = both(L.eps);
+    const float fix1 = -expm1f((float)((double)t * L.log_b1)), root2 = sqrtf(-expm1f((float)((double)t * L.log_b2)));
+    // -lr / (fix1 (sqrt(v) / root2 + eps)) is the reciprocal of a product and a sum, which stay normal
+    // numbers; a step below 1e-30, which moves no weight, makes them -sqrt(v) - infinity
+    const bool moves = lr > 1e-30f;
+    const float by = -fix1 / lr;
+    f.den_u = both(moves ? by / root2 : -1.f);
+    f.den_1 = both(moves ? fminf(by * L.eps, -2.f * FLT_MIN) : -INFINITY);
     f.start = mix64((uint64_t)t * kGamma + L.seed);
     return f;
 }
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constan
     using R = Raw<P, G, false>;
     const int lane = threadIdx.x & 31;
     const int64_t t = *L.steps + 1;
-    if (lr_device) lr = *lr_device;
+    if (lr_device) lr = fmaxf(*lr_device, 0.f);
     Factors f = factors(L, t, lr);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
@@ -448,7 +460,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constan
                 x.v[k] = some_in<R::run, typename R::Moment>(at.v + o, n);
             }
         }
-        update<P, G, false>(x, 0, f);
+        update<P, G, false>(x, 0, f, L);
         store_block<P, G, false>(at, 0, x, whole, left);
     }
     count_step(L, t);
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
     __shared__ Stage<P, G> st[kStages];
     const int lane = threadIdx.x & 31, me = threadIdx.x;
     const int64_t t = *L.steps + 1;
-    if (lr_device) lr = *lr_device;
+    if (lr_device) lr = fmaxf(*lr_device, 0.f);
     Factors f = factors(L, t, lr);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
@@ -539,7 +551,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
                 }
                 x.ms = __shfl_sync(kFull, scale, j);
                 x.vs = __shfl_sync(kFull, scale, 16 + j);
-                update<P, G, true>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f);
+                update<P, G, true>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f, L);
                 store_block<P, G, true>(at, u * Place<P, G, true>::step, x, j < w.whole, left(j));
                 if ((lane & 15) == j) scale = lane < 16 ? x.ms : x.vs;
             }
@@ -617,24 +629,33 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         memset(&base, 0, sizeof(base));
         base.log_b1 = log(opt->beta1);   // beta = 0: -inf, and 1 - beta^t = 1
         base.log_b2 = log(opt->beta2);
-        base.b1 = (float)opt->beta1;
-        base.b2 = (float)opt->beta2;
-        base.c1 = (float)(1.0 - opt->beta1);
-        base.c2 = (float)(1.0 - opt->beta2);
+        auto twice = [](double x) {
+            const float f = (float)x;
+            uint32_t bits;
+            memcpy(&bits, &f, 4);
+            return (uint64_t)bits << 32 | bits;
+        };
+        base.b1 = twice(opt->beta1);
+        base.b2 = twice(opt->beta2);
+        base.c1 = twice(1.0 - opt->beta1);
+        base.c2 = twice(1.0 - opt->beta2);
+        base.one = twice(1.0);
         base.eps = (float)opt->eps;
-        base.one = 1.f;
         base.seed = opt->seed;
         base.steps = steps;
         base.ticket = h->ticket;
         // In 8 bits, where instructions bound, a warp takes up to 16 blocks of a tensor at a time, which
         // spreads what it does once a tile (869 us for 403 M values against 1003 with 4); fewer where
-        // the list has not that many for every warp that fits on the card.  In 32 bits, where memory
+        // that already gives each tile a block of threads of its own.  In 32 bits, where memory
         // bounds, it takes one, so that the whole card reads neighbouring places (284 us for the 55 M
         // values of the rank-64 cores against 299 with 4 and 303 with 16).
-        int64_t all = 0;
-        for (int32_t i = 0; i < count; ++i) all += ceil_div(tensors[i].size, kBlk);
-        const int64_t warps = (int64_t)h->sms * kFit8 * kWarps;
-        base.per_warp = (int32_t)(!k8 || all / warps < 1 ? 1 : all / warps > kPerWarp ? kPerWarp : all / warps);
+        auto tiles = [&](int per_warp) {
+            int64_t t = 0;
+            for (int32_t i = 0; i < count; ++i) t += ceil_div(ceil_div(tensors[i].size, kBlk), (int64_t)per_warp * kWarps);
+            return t;
+        };
+        base.per_warp = 1;
+        while (k8 && base.per_warp < kPerWarp && tiles(base.per_warp) > (int64_t)h->sms * kFit8) ++base.per_warp;
         uint64_t quad = 0;
         for (int32_t i = 0; i < count; ++i) {
             const tt_emb_adamw_tensor& x = tensors[i];
