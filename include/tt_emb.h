@@ -468,7 +468,8 @@ int tt_emb_dense_backward(tt_emb_dense_t h, const void* tokens, int32_t token_by
                           const void* grad_out, int32_t grad_out_type, int64_t grad_out_stride, int32_t accumulate,
                           tt_stream_t stream);
 
-/* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy. */
+/* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy.  The sync waits for the stream of the last
+ * call; a replayed graph's own stream is the caller's to wait for first. */
 int tt_emb_dense_sync(tt_emb_dense_t h);
 int tt_emb_dense_last_error(tt_emb_dense_t h);
 void tt_emb_dense_destroy(tt_emb_dense_t h);
@@ -483,7 +484,8 @@ const int32_t* tt_emb_dense_status_word(tt_emb_dense_t h);
  * element; exp_avg (m) and exp_avg_sq (v) float32 [size].  With 8-bit moments, m and v are
  * [size] bytes in the e4m3 format (m as it is; v as its square root), each block of
  * TT_ADAMW_BLOCK values with one float32 scale in m_scale and v_scale [ceil(size / block)].
- * All pointers are borrowed; those of a tensor of size 0 may be NULL.
+ * All pointers are borrowed; those of a tensor of size 0 may be NULL.  No two buffers that a step
+ * writes may overlap (a parameter named twice, for one).
  *   guard        device, may be NULL: the tensor is left as it is while *guard is not 0 (the
  *                status word of the handle that computed grad, so that no update follows a
  *                failed backward)

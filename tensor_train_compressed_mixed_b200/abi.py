@@ -358,8 +358,8 @@ def _tokens(t):
 
 
 def _rows(t, n: int, dim: int, name: str):
-    """(pointer, type, row stride) of n rows of dim values: contiguous of any shape, or [n][dim] with
-    neighbouring values in a row and any distance between rows."""
+    """(pointer, type, row stride) of n rows of dim values, each of neighbouring values and all the same
+    distance apart (0 for an expanded tensor)."""
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -368,8 +368,12 @@ def _rows(t, n: int, dim: int, name: str):
         raise ValueError(f"{name} must hold {n} rows of {dim} values, got {tuple(t.shape)}")
     if t.is_contiguous():
         return t.data_ptr(), code, dim
-    if t.dim() != 2 or (dim > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be contiguous, or two-dimensional with contiguous rows")
+    try:
+        t = t.view(n, dim)
+    except RuntimeError:
+        raise ValueError(f"{name}'s rows must be the same distance apart") from None
+    if dim > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
     return t.data_ptr(), code, t.stride(0)
 
 

@@ -8,10 +8,12 @@
 // bounds it; at 10 bytes a value the card's memory delivers a value every 55 issue slots, so
 // there the arithmetic is packed in pairs and kept short, and a warp's next blocks travel to
 // shared memory while it computes.
+#include <algorithm>
 #include <float.h>
 #include <math.h>
 #include <new>
 #include <type_traits>
+#include <utility>
 #include <vector>
 
 #include "types.cuh"
@@ -586,6 +588,32 @@ struct tt_emb_adamw_handle {
     uint32_t* ticket = nullptr;
 };
 
+// Whether no two of the buffers that a step writes overlap (false too where there is no memory to tell).
+static bool apart(int32_t count, const tt_emb_adamw_tensor* tensors, bool k8)
+{
+    try {
+        std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+        auto add = [&](const void* p, int64_t bytes) { spans.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
+        for (int32_t i = 0; i < count; ++i) {
+            const tt_emb_adamw_tensor& x = tensors[i];
+            if (x.size == 0) continue;
+            add(x.param, x.size * type_bytes(x.param_type));
+            add(x.exp_avg, x.size * (k8 ? 1 : 4));
+            add(x.exp_avg_sq, x.size * (k8 ? 1 : 4));
+            if (k8) {
+                add(x.m_scale, ceil_div(x.size, kBlk) * 4);
+                add(x.v_scale, ceil_div(x.size, kBlk) * 4);
+            }
+        }
+        std::sort(spans.begin(), spans.end());
+        for (size_t i = 1; i < spans.size(); ++i)
+            if (spans[i].first < spans[i - 1].second) return false;
+        return true;
+    } catch (...) {
+        return false;
+    }
+}
+
 extern "C" {
 
 int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const tt_emb_adamw_options* opt,
@@ -610,6 +638,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         if ((((uintptr_t)x.exp_avg | (uintptr_t)x.exp_avg_sq) & (sb - 1))) return TT_ERR_ARG;
         if (k8 && (!x.m_scale || !x.v_scale || (((uintptr_t)x.m_scale | (uintptr_t)x.v_scale) & 3))) return TT_ERR_ARG;
     }
+    if (!apart(count, tensors, k8)) return TT_ERR_ARG;
     tt_emb_adamw_handle* h = new (std::nothrow) tt_emb_adamw_handle();
     if (!h) return TT_ERR_ARG;
     h->k8 = k8;
@@ -619,7 +648,8 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         delete h;
         return TT_ERR_CUDA;
     }
-    if (cudaMemset(h->ticket, 0, 256) != cudaSuccess) {
+    // waited for, as the first step may run on a stream that is not ordered behind this one
+    if (cudaMemset(h->ticket, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
         cudaFree(h->ticket);
         delete h;
         return TT_ERR_CUDA;

@@ -1062,7 +1062,8 @@ int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         return e == cudaSuccess ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
     };
-    if (cudaMemset(h->d_status, 0, 256) != cudaSuccess ||
+    // the memset is waited for, as the first call may run on a stream that is not ordered behind this one
+    if (cudaMemset(h->d_status, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess ||
         room(k_token_sort<1>, sizeof(SortShared<1>)) != cudaSuccess || room(k_token_sort<2>, sizeof(SortShared<2>)) != cudaSuccess ||
         room(k_token_sort<4>, sizeof(SortShared<4>)) != cudaSuccess || room(k_token_sort<8>, sizeof(SortShared<8>)) != cudaSuccess) {
         cudaFree(h->d_status);

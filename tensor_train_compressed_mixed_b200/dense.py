@@ -20,11 +20,20 @@ def on_device(device: torch.device):
     return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
+def on_stream(stream):
+    """Allocates on `stream` (a torch stream, its handle, or None for the current one), so that memory
+    used there is not handed out again before work there has ended."""
+    if stream is None:
+        return _HERE
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
 class DenseEmbedding:
     """A table of num_rows rows of dim values (float32, bfloat16 or float16).
 
     ``forward`` returns scale * table[tokens]; ``backward`` the gradient of the table for an
-    upstream gradient of those rows.  padding_idx: a row that receives no gradient.
+    upstream gradient of those rows.  padding_idx: a row that receives no gradient.  Calls of one
+    object must be ordered (one stream, or events), replayed graphs that captured them included.
     """
 
     def __init__(self, num_rows: int, dim: int, dtype: torch.dtype = torch.float32, scale: float = 1.0,
@@ -40,7 +49,7 @@ class DenseEmbedding:
         self.num_rows, self.dim, self.dtype = int(num_rows), int(dim), dtype
         self.table = None
         self.grad = None
-        self._ws = None
+        self._ws = []           # the workspace in use is the last; captured calls keep using theirs
         self._ws_tokens = -1
 
     def _check(self, t, name: str, dtype=None):
@@ -64,24 +73,32 @@ class DenseEmbedding:
         abi.tt_emb_dense_set_table(self.handle, table, grad)
         self.table, self.grad = table, grad
 
-    def reserve(self, max_tokens: int):
-        """Allocates (or grows) the backward's workspace for up to this many tokens."""
+    def reserve(self, max_tokens: int, stream=None):
+        """Allocates (or grows) the backward's workspace for up to this many tokens.
+
+        Earlier, smaller ones live as long as the object, since a captured call goes on using the
+        one that it was captured with; each is half as large again as the one before, at least."""
         if max_tokens <= self._ws_tokens:
             return
+        if self._ws:
+            max_tokens = min(max(max_tokens, self._ws_tokens * 3 // 2), 2 ** 31 - 2)
         nbytes = abi.tt_emb_dense_workspace_size(self.handle, max_tokens)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        with on_device(self.device), on_stream(stream):
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
         abi.tt_emb_dense_set_workspace(self.handle, ws, max_tokens)
-        self._ws, self._ws_tokens = ws, max_tokens
+        self._ws.append(ws)
+        self._ws_tokens = max_tokens
 
     def forward(self, tokens: torch.Tensor, out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
                 stream=None) -> torch.Tensor:
         """scale * table[tokens], in out's type, or out_dtype, or the table's.
 
-        out: contiguous, or [n, dim] with rows any distance of at least dim values apart."""
+        out: rows of neighbouring values, all the same distance of at least dim values apart."""
         self._check(tokens, "tokens")
         with on_device(self.device):
             if out is None:
-                out = torch.empty(*tokens.shape, self.dim, dtype=out_dtype or self.dtype, device=self.device)
+                with on_stream(stream):
+                    out = torch.empty(*tokens.shape, self.dim, dtype=out_dtype or self.dtype, device=self.device)
             else:
                 self._check(out, "out", out_dtype)
             abi.tt_emb_dense_forward(self.handle, tokens, out, self.dim, stream)
@@ -93,7 +110,7 @@ class DenseEmbedding:
         self._check(tokens, "tokens")
         self._check(grad_out, "grad_out")
         with on_device(self.device):
-            self.reserve(tokens.numel())
+            self.reserve(tokens.numel(), stream)
             abi.tt_emb_dense_backward(self.handle, tokens, grad_out, self.dim, accumulate, stream)
         return self.grad
 

@@ -8,7 +8,8 @@ from .dense import DenseEmbedding, on_device
 
 
 class AdamW:
-    """AdamW over contiguous CUDA tensors and their gradients (both borrowed).
+    """AdamW over contiguous CUDA tensors and their gradients (both borrowed: gradients are read
+    from the buffers given here at every step).
 
     params, grads: lists of tensors of equal sizes, float32, bfloat16 or float16; weight_decay:
     one number, or one for each tensor.  state_bits 8 holds both moments as e4m3 codes with one
@@ -43,6 +44,7 @@ class AdamW:
             if p.numel() != g.numel():
                 raise ValueError(f"params[{i}] has {p.numel()} values and its gradient {g.numel()}")
         self.params, self.grads = params, grads
+        self.tables = []
         self.state_bits = state_bits
         B = abi.ADAMW_BLOCK
         self.offsets, total = [], 0
@@ -72,13 +74,15 @@ class AdamW:
                 recs.append(r)
             opt = abi.AdamWOptions(beta1=betas[0], beta2=betas[1], eps=eps, state_bits=state_bits,
                                    seed=seed & (2 ** 64 - 1))
+            # the zeroed state is waited for: the first step may be given another stream
+            torch.cuda.current_stream(self.device).synchronize()
             self.handle = abi.tt_emb_adamw_create(recs, opt, self.steps)
 
     @classmethod
     def for_tables(cls, tables, **options):
         """An optimiser of the cores and tables of TTEmbeddingBag and DenseEmbedding objects, whose
-        gradient buffers it reads.  A table whose backward reported a device error is left as it
-        is until its next sync."""
+        gradient buffers it reads: those they have now, so make it after set_cores and set_table.
+        A table whose backward reported a device error is left as it is until its next sync."""
         params, grads, guards = [], [], []
         for e in tables:
             if isinstance(e, DenseEmbedding):
@@ -97,6 +101,11 @@ class AdamW:
     def step(self, lr, stream=None):
         """One step of every tensor.  lr: a number, or a CUDA float32 tensor of one value, which a
         captured step reads anew at each replay."""
+        for t in self.tables:
+            if t.handle is None:
+                raise ValueError("a table of this optimiser has been closed")
+        if isinstance(lr, torch.Tensor) and lr.device != self.device:
+            raise TypeError(f"lr must be a number or a tensor on {self.device}")
         with on_device(self.device):
             abi.tt_emb_adamw_step(self.handle, lr, stream)
 

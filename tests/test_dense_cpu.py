@@ -71,6 +71,17 @@ def test_adamw_create_refuses_bad_options(kw):
     assert _create(**kw) == abi.TT_ERR_ARG
 
 
+def test_adamw_create_refuses_overlapping_buffers():
+    h = ctypes.c_void_p(1)
+    far = dict(exp_avg=2 * P, exp_avg_sq=3 * P, m_scale=4 * P, v_scale=5 * P)
+    o = abi.AdamWOptions(beta1=0.9, beta2=0.999, eps=1e-8, state_bits=32)
+    for a, b in ((_tensor(**far), _tensor(**{k: v * 64 for k, v in far.items()})),      # a parameter named twice
+                 (_tensor(**far), _tensor(param=64 * P, exp_avg=2 * P + 36, exp_avg_sq=65 * P)),
+                 (_tensor(exp_avg=2 * P, exp_avg_sq=2 * P), _tensor(size=0))):
+        arr = (abi.AdamWTensor * 2)(a, b)
+        assert abi.lib().tt_emb_adamw_create(2, arr, ctypes.byref(o), P, ctypes.byref(h)) == abi.TT_ERR_ARG
+
+
 def test_adamw_8_bit_wants_scales():
     assert _create(_tensor(m_scale=None), state_bits=8) == abi.TT_ERR_ARG
     assert _create(_tensor(v_scale=P + 1), state_bits=8) == abi.TT_ERR_ARG

@@ -269,6 +269,33 @@ def test_lr_from_the_device_and_replay():
     assert int(a.steps) == 4
 
 
+def test_lr_of_zero_moves_nothing():
+    p = torch.randn(600, device="cuda")
+    before, g = p.clone(), torch.randn(600, device="cuda")
+    g[5], g[7] = 0.0, 1e30
+    for bits in (32, 8):
+        o = AdamW([p], [g], state_bits=bits)
+        for lr in (0.0, 1e-38, torch.tensor([0.0], device="cuda"), torch.tensor([-1.0], device="cuda"), torch.tensor([float("nan")], device="cuda")):
+            o.step(lr)
+            # the infinite v of value 7 is NaN in 8 bits, and its weight with it from the next step on
+            rest = [i for i in range(600) if bits == 32 or i != 7]
+            assert torch.equal(p[rest], before[rest])
+        assert int(o.steps) == 5
+
+
+def test_tiny_eps_and_untouched_weights():
+    """Weights that never had a gradient stay where they are, whatever eps."""
+    p = torch.randn(600, device="cuda")
+    before, g = p.clone(), torch.zeros(600, device="cuda")
+    g[300:] = 1.0
+    for bits in (32, 8):
+        for eps in (1.2e-38, 1e-8, 1.0):
+            o = AdamW([p], [g], eps=eps, weight_decay=0.0, state_bits=bits)
+            for lr in (1e-3, 100.0):
+                o.step(lr)
+            assert torch.equal(p[:300], before[:300]) and torch.isfinite(p).all()
+
+
 def test_state_can_be_saved_and_put_back():
     p, g = torch.randn(3000, device="cuda"), torch.randn(3000, device="cuda")
     for bits in (32, 8):
@@ -304,6 +331,17 @@ def test_refusals():
         AdamW([p], [g.double()])
     with pytest.raises(TypeError):
         AdamW([p], [g.cpu()])
+    with pytest.raises(abi.TTEmbError) as err:
+        AdamW([p, p[2:]], [g, g[2:]])               # the same weights twice
+    assert err.value.code == abi.TT_ERR_ARG
+    table = DenseEmbedding(4, 4)
+    table.set_table(torch.zeros(4, 4, device="cuda"))
+    o = AdamW.for_tables([table])
+    table.close()
+    with pytest.raises(ValueError):
+        o.step(0.1)
+    with pytest.raises(ValueError):
+        AdamW.for_tables([DenseEmbedding(4, 4)])    # no table set
     o = AdamW([p], [g])
     for lr in (-0.1, float("nan"), float("inf")):
         with pytest.raises(abi.TTEmbError) as err:

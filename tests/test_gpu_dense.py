@@ -175,6 +175,48 @@ def test_broadcast_upstream():
     _check_grad(e, tok, one.expand(700, 24), None, 1.0, None, F32)
 
 
+@pytest.mark.parametrize("make", [lambda u: u.expand(5, 7, 24), lambda u: u.expand(35, 24)])
+def test_expanded_upstream_of_any_shape(make):
+    e, _ = _make(20, 24, F32, grad=F32)
+    tok = torch.randint(20, (35,), device="cuda")
+    up = make(torch.randn(24, device="cuda"))
+    e.backward(tok.view(up.shape[:-1]), up)
+    e.sync()
+    _check_grad(e, tok, up.reshape(35, 24), None, 1.0, None, F32)
+
+
+def test_a_captured_call_keeps_its_workspace():
+    """Growing the workspace after a capture leaves the captured call's own in place."""
+    e, _ = _make(300, 64, F32, grad=F32)
+    tok, u = torch.randint(300, (3000,), device="cuda"), torch.randn(3000, 64, device="cuda")
+    e.reserve(3000)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        e.backward(tok, u)
+    big, v = torch.randint(300, (50000,), device="cuda"), torch.randn(50000, 64, device="cuda")
+    e.backward(big, v)
+    _check_grad(e, big, v, None, 1.0, None, F32)
+    junk = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(64)]
+    graph.replay()
+    torch.cuda.synchronize()
+    _check_grad(e, tok, u, None, 1.0, None, F32)
+    e.sync()
+    assert all((j == 255).all() for j in junk)
+
+
+def test_results_allocated_on_the_given_stream():
+    e, w = _make(64, 4096, F32)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for k in range(20):
+        tok = torch.full((500,), k, device="cuda")
+        torch.cuda.synchronize()
+        out = e.forward(tok, stream=s if k % 2 else s.cuda_stream)
+        s.synchronize()
+        assert torch.equal(out[::250].cpu(), w[[k, k]])
+
+
 def test_offsets_beyond_32_bits():
     rows, dim = 140001, 32768                       # 4.6e9 values
     w = torch.empty(rows, dim, dtype=BF16, device="cuda")
@@ -256,6 +298,7 @@ def test_refusals():
             e.forward(bad)
     up = torch.zeros(3, 4, device="cuda")
     for bad, kind in ((up[:2], ValueError), (up.double(), TypeError), (up.cpu(), TypeError), (up.t().contiguous().t(), ValueError),
+                      (torch.zeros(3, 2, 4, device="cuda")[:, 0].t().contiguous().t(), ValueError),
                       (torch.zeros(4, 3, device="cuda"), ValueError)):
         with pytest.raises(kind):
             e.backward(tok, bad)
