@@ -474,7 +474,7 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(N) : "memory");
 }
 
-constexpr int kFit8 = 3;     // blocks of threads on an SM: 80 registers; 64 would spill (740 against 779 us for 403 M values)
+constexpr int kFit8 = 3;     // blocks of threads on an SM, 80 registers a thread; with four 64 spill (857 against 830 us for 403 M values)
 constexpr int kStages = 2;   // blocks of a warp: one being computed, the next on its way
 
 // Each thread copies its own values to its own place in shared memory and reads them back, so the
@@ -675,7 +675,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         base.steps = steps;
         base.ticket = h->ticket;
         // In 8 bits, where instructions bound, a warp takes up to 16 blocks of a tensor at a time, which
-        // spreads what it does once a tile (869 us for 403 M values against 1003 with 4); fewer where
+        // spreads what it does once a tile (788 us for 403 M values against 844 with 4); fewer where
         // that already gives each tile a block of threads of its own.  In 32 bits, where memory
         // bounds, it takes one, so that the whole card reads neighbouring places (284 us for the 55 M
         // values of the rank-64 cores against 299 with 4 and 303 with 16).
