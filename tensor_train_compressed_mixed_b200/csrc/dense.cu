@@ -134,14 +134,14 @@ __global__ void __launch_bounds__(kThreads) k_token_keys(TokenArgs a, uint32_t* 
 // thread, and sorts them by digits from the lowest up.  A digit's pass ranks the keys within
 // their warp by matching lanes, adds the counts of the warps before (shared memory) and of the blocks
 // before (the cluster's shared memory), and moves each key to its new place in whichever block
-// that is.  One launch instead of ten: 5 us for a thousand tokens, 16 us for 32768 with the rows' bits,
-// against 30 to 40.
+// that is.  One launch instead of ten: a gradient of 2000 tokens over 5000 x 512 fp32 takes 21 us with it and
+// 43 with the radix sort's launches, one of 65536 tokens 60 and 81.
 // It goes on after an error: a cluster's blocks must all reach its barriers, and it writes
 // nothing but workspace.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 constexpr int kCluster = 16;     // needs leave for more than eight blocks, given once a device
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
-constexpr int64_t kClusterTokens = (int64_t)kCluster * kSortThreads * 8;
+constexpr int64_t kClusterTokens = (int64_t)kCluster * kSortThreads * 16;
 static_assert(kDigits == kSortThreads, "a thread for each digit");
 
 template <int kItems> struct SortShared {
@@ -315,6 +315,7 @@ struct SumArgs {
     int slabs;                // units of a tile
     int64_t sums;             // blocks of the first kernel that add up; its others clear rows,
     int64_t first_clear;      // and the second kernel's go on from here
+    int clear_each;           // clearing blocks' worth that a block of the kernel for few tokens takes
     float* head;              // [tiles][dim] part of a run that began in an earlier tile
     float* tail;              // [tiles][dim] part of a run that begins here and goes on
     const uint32_t* touched;  // a bit for every row that a token names (without accumulate)
@@ -621,7 +622,10 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
 // positions, whose ends are joined in shared memory.  The others clear rows; each looks
 // up the few tokens in the rows that it covers.
 // ---------------------------------------------------------------------------
-constexpr int kFew = 512;
+//
+// The counting grows with the square of the tokens: over 5000 x 512 fp32, 256 tokens take 9 us (16 by
+// sort, sums and joins), 512 took 19 (17).
+constexpr int kFew = 256;
 constexpr int kFewThreads = 1024, kFewWarps = kFewThreads / 32;
 constexpr int kFewRows = kClearVectors * 8;   // rows that a block's vectors lie in at most
 
@@ -637,11 +641,12 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
     __shared__ float s_part[kFewWarps][32 * E];
     const int n = (int)t.n, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const uint32_t none = (uint32_t)a.rows;
-    // two threads for a key, which count half of the others each
-    const int mine = tid & (kFew - 1), half = tid / kFew;
+    // kParts threads for a key, which count a part of the others each
+    constexpr int kParts = kFewThreads / kFew;
+    const int mine = tid & (kFew - 1), part = tid / kFew;
     const int64_t token = token_at(t.tokens, t.token_bytes, min(mine, n - 1));
     const bool bad = token < 0 || token >= a.rows;
-    if (half == 0) {
+    if (part == 0) {
         s_key[mine] = mine < n && !bad && token != t.pad ? (uint32_t)token : none;
         s_front[mine] = 0;
         if (bad && mine < n) raise_error(t.status, TT_ERR_INDEX_RANGE, mine);
@@ -649,27 +654,27 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
     if (__syncthreads_or(bad || has_error(t.status))) return;
     if ((int)blockIdx.x >= a.slabs) {
         // the rows of this block's vectors that a token names, as bits
-        const Clear<W, kFewThreads> clear(a, blockIdx.x - a.slabs, grad);
+        const int64_t chunk = ((int64_t)blockIdx.x - a.slabs) * a.clear_each, row0 = Clear<W, kFewThreads>(a, chunk, grad).row0;
         for (int i = tid; i < kFewRows / 32 + 1; i += kFewThreads) s_bits[i] = 0;
         __syncthreads();
         if (tid < n) {
-            const int64_t r = (int64_t)s_key[tid] - clear.row0;
+            const int64_t r = (int64_t)s_key[tid] - row0;
             if (s_key[tid] < none && r >= 0 && r < kFewRows + 32) atomicOr(&s_bits[r >> 5], 1u << (r & 31));
         }
         __syncthreads();
-        auto hit = [&](int64_t row) { return s_bits[(row - clear.row0) >> 5] >> ((row - clear.row0) & 31) & 1u; };
+        auto hit = [&](int64_t row) { return s_bits[(row - row0) >> 5] >> ((row - row0) & 31) & 1u; };
         auto far = [&](int64_t row) {
             bool found = false;
             for (int i = 0; i < n; ++i) found |= s_key[i] == (uint32_t)row;
             return found;
         };
-        clear.run(a, grad, hit, far);
+        for (int i = 0; i < a.clear_each; ++i) Clear<W, kFewThreads>(a, chunk + i, grad).run(a, grad, hit, far);
         return;
     }
     // places: keys below mine, and equal ones in front
     {
         const uint32_t key = s_key[mine];
-        const int quads = (n + 3) / 4, from = half ? (quads + 1) / 2 : 0, to = half ? quads : (quads + 1) / 2;
+        const int quads = (n + 3) / 4, each = (quads + kParts - 1) / kParts, from = part * each, to = min(quads, from + each);
         int front = 0;
         for (int i = from; i < to; ++i) {     // what is behind the last token is `none`, never below, and never in front of one
             const uint4 q = reinterpret_cast<const uint4*>(s_key)[i];
@@ -905,7 +910,8 @@ cudaError_t sort_tokens(tt_emb_dense_t h, const TokenArgs& a, const DenseLayout&
         if (each <= 1) return go(k_token_sort<1>, sizeof(SortShared<1>));
         if (each <= 2) return go(k_token_sort<2>, sizeof(SortShared<2>));
         if (each <= 4) return go(k_token_sort<4>, sizeof(SortShared<4>));
-        return go(k_token_sort<8>, sizeof(SortShared<8>));
+        if (each <= 8) return go(k_token_sort<8>, sizeof(SortShared<8>));
+        return go(k_token_sort<16>, sizeof(SortShared<16>));
     }
     if (a.touched) {
         const cudaError_t e = cudaMemsetAsync(a.touched, 0, (size_t)words * 4, s);
@@ -989,12 +995,14 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     const unsigned grid = (unsigned)(a.sums + a.first_clear), grid2 = (unsigned)(joins ? joins + clears - a.first_clear : 0);
     if (a.sums + joins + clears > INT32_MAX) return TT_ERR_ARG;   // sizes that no device holds
     if (n <= kFew) {
+        // two blocks an SM clear all, if the rows of what one of them clears fit its bits
+        a.clear_each = (int)min64(ceil_div(clears, 2 * h->num_sms) + (clears == 0), h->dim);
         by_type(h->grad_type, [&](auto w) {
             by_type(up_type, [&](auto g) {
                 using W = decltype(w);
                 using G = decltype(g);
                 auto go = [&](auto kernel) {
-                    kernel<<<(unsigned)(a.slabs + clears), kFewThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
+                    kernel<<<(unsigned)(a.slabs + ceil_div(clears, a.clear_each)), kFewThreads, 0, s>>>(ta, a, (const G*)up, up_stride, (W*)h->grad);
                 };
                 constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
                 if (V > 2) go(accumulate ? k_token_few<G, W, kWide, true> : k_token_few<G, W, kWide, false>);
@@ -1068,7 +1076,8 @@ int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float
     // the memset is waited for, as the first call may run on a stream that is not ordered behind this one
     if (cudaMemset(h->d_status, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess ||
         room(k_token_sort<1>, sizeof(SortShared<1>)) != cudaSuccess || room(k_token_sort<2>, sizeof(SortShared<2>)) != cudaSuccess ||
-        room(k_token_sort<4>, sizeof(SortShared<4>)) != cudaSuccess || room(k_token_sort<8>, sizeof(SortShared<8>)) != cudaSuccess) {
+        room(k_token_sort<4>, sizeof(SortShared<4>)) != cudaSuccess || room(k_token_sort<8>, sizeof(SortShared<8>)) != cudaSuccess ||
+        room(k_token_sort<16>, sizeof(SortShared<16>)) != cudaSuccess) {
         cudaFree(h->d_status);
         delete h;
         return TT_ERR_CUDA;

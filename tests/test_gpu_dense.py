@@ -122,8 +122,9 @@ def test_gradient(law, n, rows, dim, up, out, extra, accumulate):
         assert torch.equal(first.view(torch.uint8), e.grad.view(torch.uint8))   # the same bits
 
 
-@pytest.mark.parametrize("n", [20, 512, 513, 4000, 70000])
-@pytest.mark.parametrize("rows,dim,shift", [(3, 1, 1), (50, 3, 1), (7, 24, 1), (1000, 8, 3), (33000, 1, 0), (4099, 20, 5), (2, 5000, 2)])
+@pytest.mark.parametrize("n", [1, 20, 256, 257, 4000, 70000, 140000])
+@pytest.mark.parametrize("rows,dim,shift", [(3, 1, 1), (50, 3, 1), (7, 24, 1), (1000, 8, 3), (33000, 1, 0), (4099, 20, 5), (2, 5000, 2),
+                                            (900001, 2, 1), (3000001, 1, 0), (70001, 40, 0)])
 @pytest.mark.parametrize("out", [F32, BF16])
 def test_gradient_buffer_that_begins_anywhere(n, rows, dim, shift, out):
     """Every value of the buffer is written, none beside it; rows of one value, blocks of many rows."""
