@@ -13,6 +13,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 # TTEMB_LIB names another build of the same library (e.g. a variant compiled for a comparison)
@@ -158,7 +159,6 @@ def _stream(stream):
 
 def _stream_on(stream, device: int) -> int:
     """The given stream, or the current one of device number `device`."""
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
@@ -336,8 +336,7 @@ _CODES = {}
 def dtype_code(dtype) -> int:
     """TT_F32, TT_BF16 or TT_F16 of a torch dtype."""
     if not _CODES:
-        import torch
-        _CODES.update({torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16})
+            _CODES.update({torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16})
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
@@ -346,7 +345,6 @@ def dtype_code(dtype) -> int:
 
 def _tokens(t):
     """(pointer, bytes of a token, tokens) of an integer CUDA tensor of any shape."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("tokens must be a CUDA tensor")
     nbytes = 8 if t.dtype is torch.int64 else 4 if t.dtype is torch.int32 else 0
@@ -360,7 +358,6 @@ def _tokens(t):
 def _rows(t, n: int, dim: int, name: str):
     """(pointer, type, row stride) of n rows of dim values, each of neighbouring values and all the same
     distance apart (0 for an expanded tensor)."""
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     code = dtype_code(t.dtype)
@@ -385,7 +382,6 @@ def tt_emb_dense_create(num_rows: int, dim: int, dtype, scale: float = 1.0, padd
 
 
 def tt_emb_dense_set_table(h, table, grad=None):
-    import torch
     for t, name in ((table, "table"), (grad, "grad")):
         if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda and t.is_contiguous()):
             raise TypeError(f"{name} must be a contiguous CUDA tensor")
@@ -401,7 +397,6 @@ def tt_emb_dense_workspace_size(h, max_tokens: int) -> int:
 
 
 def tt_emb_dense_set_workspace(h, workspace, max_tokens: int):
-    import torch
     ptr = _dev_ptr(workspace, torch.uint8, "workspace")
     _check(lib().tt_emb_dense_set_workspace(h, ptr, workspace.numel(), int(max_tokens)),
            "tt_emb_dense_set_workspace")
@@ -451,7 +446,6 @@ def tt_emb_dense_status_word(h) -> int:
 # ---------------------------------------------------------------------------
 def tt_emb_adamw_create(tensors, options: AdamWOptions, steps):
     """tensors: a list of AdamWTensor; steps: a CUDA int64 tensor of one value."""
-    import torch
     arr = (AdamWTensor * len(tensors))(*tensors)
     h = ctypes.c_void_p()
     _check(lib().tt_emb_adamw_create(len(tensors), arr, ctypes.byref(options),
@@ -461,7 +455,6 @@ def tt_emb_adamw_create(tensors, options: AdamWOptions, steps):
 
 def tt_emb_adamw_step(h, lr, stream=None):
     """lr: a number, or a CUDA float32 tensor of one value that the device reads."""
-    import torch
     at = None
     if isinstance(lr, torch.Tensor):
         if lr.numel() != 1:

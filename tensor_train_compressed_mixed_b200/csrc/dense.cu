@@ -467,8 +467,8 @@ __device__ __forceinline__ void clear_block(const SumArgs& a, int64_t block, W* 
 
 // kRows rows are on their way at a time.  With many units few of them, because what hides the memory's
 // latency then is warps: four blocks an SM with four rows of 8 columns a lane take 70 us for 32768
-// rows of 4096 bf16 values, with eight rows 78 to 90.  With few units (a warp of the card has one or
-// none) more: 16205 rows of 4 fp32 values added to a gradient take 15 us two at a time, 9 eight at a time.
+// rows of 4096 bf16 values, with eight rows 78 to 90.  With few units (what eight
+// rows' registers leave room for) more: 16205 rows of 4 fp32 values added to a gradient take 15 us two at a time, 9 eight at a time.
 constexpr int rows_many(bool add) { return add ? 2 : 4; }
 constexpr int kRowsFew = 8;
 template <typename G, typename W, int V, bool kAdd, int kRows>
@@ -1024,7 +1024,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
             using G = decltype(g);
             auto go = [&](auto kernel) { e = launch_early(kernel, grid, s, a, (const G*)up, up_stride, (W*)h->grad); };
             constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
-            const bool few = a.tiles * a.slabs <= (int64_t)h->num_sms * 8;
+            const bool few = a.tiles * a.slabs <= (int64_t)h->num_sms * 16;
             auto pick = [&](auto v) {
                 constexpr int kV = decltype(v)::value;
                 if (accumulate) go(few ? k_token_sum<G, W, kV, true, kRowsFew> : k_token_sum<G, W, kV, true, rows_many(true)>);
