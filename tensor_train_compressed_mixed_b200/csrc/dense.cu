@@ -116,17 +116,25 @@ __device__ __forceinline__ uint32_t token_key(const TokenArgs& a, int64_t i, int
         raise_error(a.status, TT_ERR_INDEX_RANGE, (int)min64(i, INT32_MAX));
         return (uint32_t)a.rows;
     }
-    if (t == a.pad) return (uint32_t)a.rows;
-    if (a.touched) atomicOr(a.touched + (t >> 5), 1u << (t & 31));
-    return (uint32_t)t;
+    return (uint32_t)(t == a.pad ? a.rows : t);
+}
+
+// The bit of a key's row.  A lane whose left neighbour has the same key leaves it to that one: the bits of
+// a batch of one token would otherwise be set one after the other.  All lanes of a warp call it.
+__device__ __forceinline__ void touch(const TokenArgs& a, uint32_t key, bool in)
+{
+    const uint32_t left = __shfl_up_sync(kFull, in ? key : 0xffffffffu, 1);
+    if (a.touched && in && key < (uint32_t)a.rows && ((threadIdx.x & 31) == 0 || left != key)) atomicOr(a.touched + (key >> 5), 1u << (key & 31));
 }
 
 __global__ void __launch_bounds__(kThreads) k_token_keys(TokenArgs a, uint32_t* __restrict__ keys, int32_t* __restrict__ vals)
 {
-    if (has_error(a.status)) return;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= a.n) return;
-    keys[i] = token_key(a, i, token_at(a.tokens, a.token_bytes, i));
+    const bool in = i < a.n;
+    const uint32_t key = in ? token_key(a, i, token_at(a.tokens, a.token_bytes, i)) : 0u;
+    touch(a, key, in);
+    if (!in) return;
+    keys[i] = key;
     vals[i] = (int32_t)i;
 }
 
@@ -186,6 +194,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) k_token_sort(TokenArgs a, int
             const int e = first + j * 32;
             const int64_t i = (int64_t)me * kChunk + e;
             key[j] = make_uint2(e < cnt ? token_key(a, i, t[j]) : 0u, (uint32_t)i);
+            touch(a, key[j].x, e < cnt);
         }
     }
     const int passes = (bits + kDigitBits - 1) / kDigitBits, width = (bits + passes - 1) / passes, digits = 1 << width;
