@@ -51,7 +51,7 @@ struct List {
     int32_t pad;
     int64_t tiles;
     double log_b1, log_b2;
-    uint64_t b1, b2, c1, c2, one;     // each twice in a pair; c = 1 - b, rounded from 64 bits
+    uint64_t b1, b2, c1, c2, one, minus_b2, minus_c2;     // each twice in a pair; c = 1 - b, rounded from 64 bits
     float eps;
     int32_t pad2;
     uint64_t seed;
@@ -81,18 +81,19 @@ __device__ __forceinline__ float root(float x)
     asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-// Two roots to nearest, in eight instructions and without a branch.  With r near 1 / sqrt(x), s = x r is
-// near the root and e = x - s^2, which the fused multiply-add gives exactly, is what its square is off;
-// Heron's step s + e / (2 s) = s + e r / 2 then rounds once.  Equal to sqrtf for every mantissa and both
-// parities of the exponent from 2^-102 on; below that e loses places.  0 gives 0, values below the
-// least normal number a root that is too small, infinity NaN.
-__device__ __forceinline__ F2 root2(F2 x)
+// Minus the roots of two values, to nearest, from minus the values: signs that packed instructions cannot
+// change are saved that way.  With r near 1 / sqrt(x), s = x r is near the root and s^2 - x, which the
+// fused multiply-add gives exactly, is what its square is off; Heron's step s - (s^2 - x) / (2 s) =
+// s - (s^2 - x) r / 2 then rounds once.  Equal to sqrtf for every mantissa and both parities of the
+// exponent from 2^-102 on; below that the difference loses places.  0 gives 0, values below the least
+// normal number a root that is too small, infinity NaN.
+__device__ __forceinline__ F2 minus_root2(F2 minus_x)
 {
     F2 r;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(x.x, FLT_MIN)));
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(x.y, FLT_MIN)));
-    const F2 s = mul2(x, r);
-    return fma2(fma2({-s.x, -s.y}, s, x), mul2(r, both(0.5f)), s);
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(fmaxf(-minus_x.x, FLT_MIN)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(fmaxf(-minus_x.y, FLT_MIN)));
+    const F2 minus_s = mul2(minus_x, r);
+    return fma2(fma2(minus_s, minus_s, minus_x), mul2(r, both(0.5f)), minus_s);
 }
 
 // 1 / x to nearest, without a branch, by a Newton step on an approximation r: 1 - x r is exact in a fused
@@ -182,7 +183,7 @@ __device__ __forceinline__ Pack<T, run> narrow(const F2* x)
     return q;
 }
 struct Factors {
-    F2 den_u, den_1, keep;      // the update is m / (den_u sqrt(v) + den_1)
+    F2 den_u, den_1, keep;      // the update is m / (den_u u + den_1), u being the root, in 8 bits minus it
     uint64_t start;
 };
 
@@ -321,8 +322,8 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
             v[i] = mul2(u[i], u[i]);
         }
         m[i] = fma2(mul2(m[i], pair(L.b1)), pair(L.one), mul2(g[i], pair(L.c1)));
-        v[i] = fma2(mul2(v[i], pair(L.b2)), pair(L.one), mul2(mul2(g[i], g[i]), pair(L.c2)));
-        if constexpr (k8) u[i] = root2(v[i]);
+        v[i] = fma2(mul2(v[i], pair(k8 ? L.minus_b2 : L.b2)), pair(L.one), mul2(mul2(g[i], g[i]), pair(k8 ? L.minus_c2 : L.c2)));
+        if constexpr (k8) u[i] = minus_root2(v[i]);        // here v is minus v, and u minus the root
         else u[i] = {root(v[i].x), root(v[i].y)};
     }
     float am = 0.f, au = 0.f;
@@ -334,8 +335,8 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
         if (odd) {
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
-                if (v[i].x == INFINITY) u[i].x = INFINITY;
-                if (v[i].y == INFINITY) u[i].y = INFINITY;
+                if (v[i].x == -INFINITY) u[i].x = -INFINITY;
+                if (v[i].y == -INFINITY) u[i].y = -INFINITY;
             }
             am = finite_max(m[0], m[1], m[2], m[3]);
             au = finite_max(u[0], u[1], u[2], u[3]);
@@ -365,7 +366,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
                 // the code is the top bits; 16 random ones below them round up or down.  All are
                 // shifted by 4, which makes the code the top byte.  A product a few ulps above 448 still
                 // gives 448's code, as the random bits end 4 places above the lowest.
-                const F2 y = mul2(mul2(u[i], iu), both(0x1p-120f));
+                const F2 y = mul2(mul2(u[i], iu), both(-0x1p-120f));
                 const uint32_t part = (uint32_t)(word >> (32 * h));
                 code[2 * h] = (__float_as_uint(y.x) << 4) + __byte_perm(part, 0u, 0x4104);
                 code[2 * h + 1] = (__float_as_uint(y.y) << 4) + __byte_perm(part, 0u, 0x4324);
@@ -375,7 +376,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
             if (min3(min3(code[0], code[1], code[2]), code[3], code[3]) < 1u << 24) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    code[e] = max(code[e], min(__float_as_uint(e & 1 ? u[2 * w + e / 2].y : u[2 * w + e / 2].x), 1u << 24));
+                    code[e] = max(code[e], min(__float_as_uint(fabsf(e & 1 ? u[2 * w + e / 2].y : u[2 * w + e / 2].x)), 1u << 24));
             }
             b.set_codes(b.m, w, mc[0] | mc[1] << 16);
             b.set_codes(b.v, w, __byte_perm(__byte_perm(code[0], code[1], 0x0073), __byte_perm(code[2], code[3], 0x0073), 0x5410));
@@ -398,7 +399,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
     }
 }
 
-__device__ __forceinline__ Factors factors(const List& L, int64_t t, float lr)
+__device__ __forceinline__ Factors factors(const List& L, int64_t t, float lr, bool minus_u)
 {
     Factors f;
     // 1 - beta^t without cancellation: the product is formed in 64 bits, the rest in 32
@@ -407,7 +408,8 @@ __device__ __forceinline__ Factors factors(const List& L, int64_t t, float lr)
     // numbers; a step below 1e-30, which moves no weight, makes them -sqrt(v) - infinity
     const bool moves = lr > 1e-30f;
     const float by = -fix1 / lr;
-    f.den_u = both(moves ? by / root2 : -1.f);
+    const float den_u = moves ? by / root2 : -1.f;
+    f.den_u = both(minus_u ? -den_u : den_u);
     f.den_1 = both(moves ? fminf(by * L.eps, -2.f * FLT_MIN) : -INFINITY);
     f.start = mix64((uint64_t)t * kGamma + L.seed);
     return f;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constan
     const int lane = threadIdx.x & 31;
     const int64_t t = *L.steps + 1;
     if (lr_device) lr = fmaxf(*lr_device, 0.f);
-    Factors f = factors(L, t, lr);
+    Factors f = factors(L, t, lr, false);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
     const int lane = threadIdx.x & 31, me = threadIdx.x;
     const int64_t t = *L.steps + 1;
     if (lr_device) lr = fmaxf(*lr_device, 0.f);
-    Factors f = factors(L, t, lr);
+    Factors f = factors(L, t, lr, true);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
@@ -670,6 +672,8 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         base.c1 = twice(1.0 - opt->beta1);
         base.c2 = twice(1.0 - opt->beta2);
         base.one = twice(1.0);
+        base.minus_b2 = twice(-opt->beta2);
+        base.minus_c2 = twice(-(1.0 - opt->beta2));
         base.eps = (float)opt->eps;
         base.seed = opt->seed;
         base.steps = steps;
