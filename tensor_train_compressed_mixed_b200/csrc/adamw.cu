@@ -476,7 +476,7 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(N) : "memory");
 }
 
-constexpr int kFit8 = 3;     // blocks of threads on an SM, 80 registers a thread; with four 64 spill (857 against 830 us for 403 M values)
+constexpr int kFit8 = 2;     // blocks of threads on an SM: 789 us for 403 M values, 803 with three, 855 with four (64 registers)
 constexpr int kStages = 2;   // blocks of a warp: one being computed, the next on its way
 
 // Each thread copies its own values to its own place in shared memory and reads them back, so the
@@ -572,7 +572,6 @@ cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* 
 {
     // Blocks that stay and take tile after tile.  Two on an SM keep enough 32-bit loads on their way, and
     // more of them spread the card's reads: 311 us for the rank-64 cores with three, 285 with two.
-    // In 8 bits as many as its launch bounds let fit.
     int64_t grid = min64(L.tiles, (int64_t)sms * (k8 ? kFit8 : 2));
     if (grid < 1) grid = 1;
     if (k8) k_adamw8<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
