@@ -631,7 +631,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
     for (int32_t i = 0; i < count; ++i) {
         const tt_emb_adamw_tensor& x = tensors[i];
         if (x.size < 0 || x.size > (int64_t)1 << 40 || !type_known(x.param_type) || !type_known(x.grad_type)) return TT_ERR_ARG;
-        if (!(x.weight_decay >= 0.0 && x.weight_decay < INFINITY) || ((uintptr_t)x.guard & 3)) return TT_ERR_ARG;
+        if (!(x.weight_decay >= 0.0 && (float)x.weight_decay < INFINITY) || ((uintptr_t)x.guard & 3)) return TT_ERR_ARG;
         if (x.size == 0) continue;
         if (!x.param || !x.grad || !x.exp_avg || !x.exp_avg_sq) return TT_ERR_ARG;
         if (((uintptr_t)x.param & (type_bytes(x.param_type) - 1)) || ((uintptr_t)x.grad & (type_bytes(x.grad_type) - 1)))

@@ -57,7 +57,7 @@ def _create(tensor=None, count=1, steps=P, **kw):
 @pytest.mark.parametrize("kw", [
     dict(size=-1), dict(param=None), dict(grad=None), dict(exp_avg=None), dict(exp_avg_sq=None), dict(param=P + 2),
     dict(grad=P + 1, grad_type=abi.TT_BF16), dict(exp_avg=P + 2), dict(param_type=3), dict(grad_type=-1),
-    dict(weight_decay=-0.1), dict(weight_decay=float("nan")), dict(guard=P + 2),
+    dict(weight_decay=-0.1), dict(weight_decay=float("nan")), dict(weight_decay=1e300), dict(guard=P + 2),
 ])
 def test_adamw_create_refuses_bad_tensors(kw):
     assert _create(_tensor(**kw)) == abi.TT_ERR_ARG
