@@ -372,8 +372,10 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
                 code[2 * h + 1] = (__float_as_uint(y.y) << 4) + __byte_perm(part, 0u, 0x4324);
             }
             // A root above zero (its bits are above 2^24) keeps the least code at least.  Few blocks have a
-            // code of zero, which is below every float whose exponent the code's lowest bit reaches.
-            if (min3(min3(code[0], code[1], code[2]), code[3], code[3]) < 1u << 24) {
+            // code of zero, which is below every float whose exponent the code's lowest bit reaches.  Words of
+            // roots that are not finite may be 2^31 or more, which do not order like floats: blocks that
+            // hold one look at each value.
+            if (odd || min3(min3(code[0], code[1], code[2]), code[3], code[3]) < 1u << 24) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     code[e] = max(code[e], min(__float_as_uint(fabsf(e & 1 ? u[2 * w + e / 2].y : u[2 * w + e / 2].x)), 1u << 24));
