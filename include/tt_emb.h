@@ -469,7 +469,8 @@ int tt_emb_dense_backward(tt_emb_dense_t h, const void* tokens, int32_t token_by
                           tt_stream_t stream);
 
 /* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy.  The sync waits for the stream of the last
- * call; a replayed graph's own stream is the caller's to wait for first. */
+ * call; a replayed graph's own stream is the caller's to wait for first.  With another device than the
+ * handle's current it reads nothing and returns TT_ERR_STATE. */
 int tt_emb_dense_sync(tt_emb_dense_t h);
 int tt_emb_dense_last_error(tt_emb_dense_t h);
 void tt_emb_dense_destroy(tt_emb_dense_t h);

@@ -1144,6 +1144,8 @@ int tt_emb_dense_backward(tt_emb_dense_t h, const void* tokens, int32_t token_by
 int tt_emb_dense_sync(tt_emb_dense_t h)
 {
     if (!h) return TT_ERR_ARG;
+    // the last stream may be a device's default one, which is another stream where another device is current
+    if (const int rc = ready(h)) return note(h, rc);
     cudaStream_t s = h->used_stream ? h->last_stream : (cudaStream_t)0;
     int32_t st = 0;
     if (cudaMemcpyAsync(&st, h->d_status, sizeof(st), cudaMemcpyDeviceToHost, s) != cudaSuccess ||

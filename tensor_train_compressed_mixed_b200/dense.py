@@ -115,7 +115,8 @@ class DenseEmbedding:
         return self.grad
 
     def sync(self):
-        abi.tt_emb_dense_sync(self.handle)
+        with on_device(self.device):
+            abi.tt_emb_dense_sync(self.handle)
 
     def close(self):
         if getattr(self, "handle", None) is not None:

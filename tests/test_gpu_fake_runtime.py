@@ -1,0 +1,52 @@
+"""What dense tables do where the CUDA runtime answers otherwise than on one GPU: a small library in front of the
+runtime, in a process of its own, changes its answers (no second GPU is needed)."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def fake(tmp_path_factory):
+    out = tmp_path_factory.mktemp("fake") / "libfake.so"
+    subprocess.run(["gcc", "-O1", "-fPIC", "-shared", "-I/usr/local/cuda/include", os.path.join(HERE, "fake_cudart.c"), "-o", str(out), "-ldl"],
+                   check=True)
+    return str(out)
+
+
+def _run(fake, program):
+    env = dict(os.environ, LD_PRELOAD=fake, PYTHONPATH=os.pathsep.join([os.path.dirname(HERE), HERE, os.environ.get("PYTHONPATH", "")]))
+    p = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, timeout=600, env=env)
+    assert p.returncode == 0, p.stdout[-2000:] + p.stderr[-4000:]
+
+
+OTHER_DEVICE = """
+import ctypes
+import torch
+from tensor_train_compressed_mixed_b200 import DenseEmbedding, abi
+fake = ctypes.CDLL(None)
+e = DenseEmbedding(30, 8)
+e.set_table(torch.zeros(30, 8, device="cuda"))
+bad = torch.tensor([1, 30, 2], device="cuda")
+e.forward(bad)
+torch.cuda.synchronize()
+for stream in (None, 1):
+    if stream:                          # a call whose stream is not the device's own
+        e.forward(bad, stream=torch.cuda.Stream())
+        torch.cuda.synchronize()
+    fake.fake_device(1)
+    codes = [abi.lib().tt_emb_dense_sync(e.handle) for _ in range(2)]
+    fake.fake_device(-1)
+    assert codes == [abi.TT_ERR_STATE] * 2, codes
+    assert abi.tt_emb_dense_last_error(e.handle) == abi.TT_ERR_STATE
+    assert abi.lib().tt_emb_dense_sync(e.handle) == abi.TT_ERR_INDEX_RANGE      # the error was not lost
+    assert abi.lib().tt_emb_dense_sync(e.handle) == abi.TT_OK
+"""
+
+
+def test_sync_with_another_device_current_reads_nothing(fake):
+    _run(fake, OTHER_DEVICE)
