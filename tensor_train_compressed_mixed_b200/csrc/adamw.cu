@@ -93,7 +93,7 @@ __device__ __forceinline__ float block_max(const F2 (&x)[kPairs])
     return __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(a)));
 }
 
-// the same of the finite values only (blocks that hold others take this second look)
+// the same of the finite values only (blocks that hold others, or huge ones, take this second look)
 __device__ __noinline__ float finite_max(F2 a, F2 b, F2 c, F2 d)
 {
     F2 x[kPairs] = {a, b, c, d};
@@ -104,6 +104,9 @@ __device__ __noinline__ float finite_max(F2 a, F2 b, F2 c, F2 d)
     }
     return block_max(x);
 }
+
+// 1 / x to nearest where x is too large for `inverse`, whose approximation is 0 there
+__device__ __noinline__ float any_inverse(float x) { return __frcp_rn(x); }
 
 // four codes, NaN's in the place of those whose values are not finite
 __device__ __noinline__ uint32_t without_infinities(uint32_t codes, F2 a, F2 b)
@@ -290,12 +293,13 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
         if constexpr (k8) u[i] = minus_root2(v[i]);        // here v is minus v, and u minus the root
         else u[i] = {root(v[i].x), root(v[i].y)};
     }
-    float am = 0.f, au = 0.f;
-    bool odd = false;                                // a value of the block is not finite
+    float am = 0.f, au = 0.f, by_m = 0.f;
+    bool odd = false;                                // a value of the block is not finite, or beyond what inverse takes
     if constexpr (k8) {
         am = block_max(m);
         au = block_max(u);
-        odd = !(am < INFINITY && au < INFINITY);
+        odd = !(am < 0x1p126f && au < INFINITY);     // (finite roots stay below 2^64)
+        by_m = inverse(am);
         if (odd) {
 #pragma unroll
             for (int i = 0; i < kPairs; ++i) {
@@ -304,6 +308,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
             }
             am = finite_max(m[0], m[1], m[2], m[3]);
             au = finite_max(u[0], u[1], u[2], u[3]);
+            by_m = any_inverse(am);
         }
     }
 #pragma unroll
@@ -316,7 +321,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
         if (au < 0x1p-100f) au = 0.f;
         b.ms = am * (1.f / 448.f);
         b.vs = au * (1.f / 448.f);
-        const F2 im = both(am > 0.f ? __fmul_rn(448.f, inverse(am)) : 0.f), iu = both(au > 0.f ? __fmul_rn(448.f, inverse(au)) : 0.f);
+        const F2 im = both(am > 0.f ? __fmul_rn(448.f, by_m) : 0.f), iu = both(au > 0.f ? __fmul_rn(448.f, inverse(au)) : 0.f);
 #pragma unroll
         for (int w = 0; w < kPairs / 2; ++w) {       // four neighbours: one word of random bits
             const uint64_t word = mix64(random + (run == 8 ? w : w * 32) * kGamma);
@@ -337,8 +342,8 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
             }
             // A root above zero (its bits are above 2^24) keeps the least code at least.  Few blocks have a
             // code of zero, which is below every float whose exponent the code's lowest bit reaches.  Words of
-            // roots that are not finite may be 2^31 or more, which do not order like floats: blocks that
-            // hold one look at each value.
+            // roots that are not finite may be 2^31 or more, which do not order like floats: odd blocks
+            // look at each value.
             if (odd || min3(min3(code[0], code[1], code[2]), code[3], code[3]) < 1u << 24) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
