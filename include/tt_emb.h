@@ -486,7 +486,8 @@ const int32_t* tt_emb_dense_status_word(tt_emb_dense_t h);
  * [size] bytes in the e4m3 format (m as it is; v as its square root), each block of
  * TT_ADAMW_BLOCK values with one float32 scale in m_scale and v_scale [ceil(size / block)].
  * All pointers are borrowed; those of a tensor of size 0 may be NULL.  No two buffers that a step
- * writes may overlap (a parameter named twice, for one).
+ * writes may overlap (a parameter named twice, for one; the step count is one of them), and no
+ * gradient may overlap one of them.  Gradients may overlap each other.
  *   guard        device, may be NULL: the tensor is left as it is while *guard is not 0 (the
  *                status word of the handle that computed grad, so that no update follows a
  *                failed backward)
@@ -522,7 +523,7 @@ typedef struct tt_emb_adamw_handle* tt_emb_adamw_t;
  *   tensors      host [count]
  *   steps        device int64 [1], 8-byte aligned, borrowed: the number of steps taken
  * Returns TT_OK, TT_ERR_ARG (a null or misaligned pointer, an unknown type, an option outside
- * its range) or TT_ERR_CUDA.
+ * its range, buffers that overlap) or TT_ERR_CUDA.
  */
 int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const tt_emb_adamw_options* opt,
                         int64_t* steps, tt_emb_adamw_t* out);

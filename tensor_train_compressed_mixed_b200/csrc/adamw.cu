@@ -560,26 +560,37 @@ struct tt_emb_adamw_handle {
     uint32_t* ticket = nullptr;
 };
 
-// Whether no two of the buffers that a step writes overlap (false too where there is no memory to tell).
-static bool apart(int32_t count, const tt_emb_adamw_tensor* tensors, bool k8)
+// Whether no two of the buffers that a step writes overlap, and no gradient one of them (false too where there is no
+// memory to tell).
+static bool apart(int32_t count, const tt_emb_adamw_tensor* tensors, bool k8, const int64_t* steps)
 {
+    using Span = std::pair<uintptr_t, uintptr_t>;
     try {
-        std::vector<std::pair<uintptr_t, uintptr_t>> spans;
-        auto add = [&](const void* p, int64_t bytes) { spans.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
+        std::vector<Span> spans;
+        auto span = [](const void* p, int64_t bytes) { return Span((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
+        spans.push_back(span(steps, sizeof(*steps)));
         for (int32_t i = 0; i < count; ++i) {
             const tt_emb_adamw_tensor& x = tensors[i];
             if (x.size == 0) continue;
-            add(x.param, x.size * type_bytes(x.param_type));
-            add(x.exp_avg, x.size * (k8 ? 1 : 4));
-            add(x.exp_avg_sq, x.size * (k8 ? 1 : 4));
+            spans.push_back(span(x.param, x.size * type_bytes(x.param_type)));
+            spans.push_back(span(x.exp_avg, x.size * (k8 ? 1 : 4)));
+            spans.push_back(span(x.exp_avg_sq, x.size * (k8 ? 1 : 4)));
             if (k8) {
-                add(x.m_scale, ceil_div(x.size, kBlk) * 4);
-                add(x.v_scale, ceil_div(x.size, kBlk) * 4);
+                spans.push_back(span(x.m_scale, ceil_div(x.size, kBlk) * 4));
+                spans.push_back(span(x.v_scale, ceil_div(x.size, kBlk) * 4));
             }
         }
         std::sort(spans.begin(), spans.end());
         for (size_t i = 1; i < spans.size(); ++i)
             if (spans[i].first < spans[i - 1].second) return false;
+        for (int32_t i = 0; i < count; ++i) {
+            const tt_emb_adamw_tensor& x = tensors[i];
+            if (x.size == 0) continue;
+            const Span g = span(x.grad, x.size * type_bytes(x.grad_type));
+            // the last span that begins before the gradient ends: the others of those end before that one begins
+            const auto after = std::lower_bound(spans.begin(), spans.end(), Span(g.second, 0));
+            if (after != spans.begin() && (after - 1)->second > g.first) return false;
+        }
         return true;
     } catch (...) {
         return false;
@@ -610,7 +621,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         if ((((uintptr_t)x.exp_avg | (uintptr_t)x.exp_avg_sq) & (sb - 1))) return TT_ERR_ARG;
         if (k8 && (!x.m_scale || !x.v_scale || (((uintptr_t)x.m_scale | (uintptr_t)x.v_scale) & 3))) return TT_ERR_ARG;
     }
-    if (!apart(count, tensors, k8)) return TT_ERR_ARG;
+    if (!apart(count, tensors, k8, steps)) return TT_ERR_ARG;
     tt_emb_adamw_handle* h = new (std::nothrow) tt_emb_adamw_handle();
     if (!h) return TT_ERR_ARG;
     h->k8 = k8;
