@@ -12,10 +12,11 @@ class AdamW:
     from the buffers given here at every step).
 
     params, grads: lists of tensors of equal sizes, float32, bfloat16 or float16, no parameter on
-    the memory of another or of a gradient; weight_decay: one number, or one for each tensor.  state_bits 8 holds both moments as e4m3 codes with one
-    float32 scale for each 256 values; the second one, held as its root, is rounded up or down
-    at random from `seed`.  guards: for each tensor None or the address of a device status
-    word, while which is not 0 the tensor is left as it is.
+    the memory of another or of a gradient; weight_decay: one number, or one for each tensor.
+    state_bits 8 holds both moments as e4m3 codes with one float32 scale for each 256 values; the
+    second one, held as its root, is rounded up or down at random from `seed`.  guards: for each
+    tensor None or the address of a device status word, while which is not 0 the tensor is left as
+    it is.
 
     The state is public and can be saved and put back: ``steps`` (int64 [1], on the device),
     and flat buffers ``m`` and ``v`` in which tensor i begins at ``offsets[i]``, with
