@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) k_token_keys(TokenArgs a, uint32_t* 
 // It goes on after an error: a cluster's blocks must all reach its barriers, and it writes
 // nothing but workspace.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
-constexpr int kCluster = 16;     // needs leave for more than eight blocks, given once a device
+constexpr int kCluster = 16;     // needs leave for more than eight blocks (see sort_fits)
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int64_t kClusterTokens = (int64_t)kCluster * kSortThreads * 16;
 static_assert(kDigits == kSortThreads, "a thread for each digit");
@@ -818,6 +818,7 @@ struct tt_emb_dense_handle {
     int64_t ws_n = -1;
     int32_t* d_status = nullptr;
     int device = 0, num_sms = 148;
+    bool clusters = false;       // one of k_token_sort fits this device
     cudaStream_t last_stream = nullptr;
     bool used_stream = false;
     int last_error = TT_OK;
@@ -896,27 +897,54 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
+// The launch of k_token_sort: one cluster of blocks with `smem` bytes each.
+struct SortLaunch {
+    cudaLaunchConfig_t config = {};
+    cudaLaunchAttribute at[1];
+    SortLaunch(size_t smem, cudaStream_t s)
+    {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kCluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        config.gridDim = dim3(kCluster);
+        config.blockDim = dim3(kSortThreads);
+        config.dynamicSmemBytes = smem;
+        config.stream = s;
+        config.attrs = at;
+        config.numAttrs = 1;
+    }
+    SortLaunch(const SortLaunch&) = delete;
+};
+
+// Gives k_token_sort leave for its shared memory and for more than eight blocks a cluster on the current device, and
+// tells whether such a cluster fits there.  It fits a whole B200; a part of one without sixteen SMs side by side sorts
+// by the radix sort's launches, whatever the number of tokens.
+bool sort_fits()
+{
+    auto fits = [](auto kernel, size_t smem) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+        const SortLaunch l(smem, nullptr);
+        int clusters = 0;
+        return cudaOccupancyMaxActiveClusters(&clusters, kernel, &l.config) == cudaSuccess && clusters > 0;
+    };
+    const bool all = fits(k_token_sort<1>, sizeof(SortShared<1>)) && fits(k_token_sort<2>, sizeof(SortShared<2>)) &&
+                     fits(k_token_sort<4>, sizeof(SortShared<4>)) && fits(k_token_sort<8>, sizeof(SortShared<8>)) &&
+                     fits(k_token_sort<16>, sizeof(SortShared<16>));
+    if (!all) cudaGetLastError();     // a refusal here is an answer, not an error of the next launch
+    return all;
+}
+
 // Sorted keys and positions in buffer *which of the workspace.
 cudaError_t sort_tokens(tt_emb_dense_t h, const TokenArgs& a, const DenseLayout& y, int bits, int* which, cudaStream_t s)
 {
     uint32_t* const keys = (uint32_t*)(h->ws + y.keys[0]);
     int32_t* const vals = (int32_t*)(h->ws + y.vals[0]);
     const int64_t words = ceil_div(h->rows, 32);
-    if (a.n <= kClusterTokens) {
+    if (a.n <= kClusterTokens && h->clusters) {
         auto go = [&](auto kernel, size_t smem) {
-            cudaLaunchConfig_t c = {};
-            cudaLaunchAttribute at[1];
-            const unsigned blocks = kCluster;
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = blocks;
-            at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-            c.gridDim = dim3(blocks);
-            c.blockDim = dim3(kSortThreads);
-            c.dynamicSmemBytes = smem;
-            c.stream = s;
-            c.attrs = at;
-            c.numAttrs = 1;
-            return cudaLaunchKernelEx(&c, kernel, a, bits, keys, vals, words);
+            const SortLaunch l(smem, s);
+            return cudaLaunchKernelEx(&l.config, kernel, a, bits, keys, vals, words);
         };
         *which = 0;
         const int64_t each = ceil_div(a.n, kCluster * kSortThreads);
@@ -1082,15 +1110,9 @@ int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float
         delete h;
         return TT_ERR_CUDA;
     }
-    auto room = [](auto kernel, size_t smem) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        return e == cudaSuccess ? cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : e;
-    };
+    h->clusters = sort_fits();
     // the memset is waited for, as the first call may run on a stream that is not ordered behind this one
-    if (cudaMemset(h->d_status, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess ||
-        room(k_token_sort<1>, sizeof(SortShared<1>)) != cudaSuccess || room(k_token_sort<2>, sizeof(SortShared<2>)) != cudaSuccess ||
-        room(k_token_sort<4>, sizeof(SortShared<4>)) != cudaSuccess || room(k_token_sort<8>, sizeof(SortShared<8>)) != cudaSuccess ||
-        room(k_token_sort<16>, sizeof(SortShared<16>)) != cudaSuccess) {
+    if (cudaMemset(h->d_status, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
         cudaFree(h->d_status);
         delete h;
         return TT_ERR_CUDA;
