@@ -149,7 +149,6 @@ def _check(rc: int, where: str):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
@@ -165,7 +164,6 @@ def _stream_on(stream, device: int) -> int:
 
 
 def _dev_ptr(t, dtype, name):
-    import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -205,7 +203,6 @@ def tt_emb_create(n_factors, n_rows, d_factors, ranks, options: Options | None =
 
 def tt_emb_set_cores(h, cores, core_grads=None):
     """cores / core_grads: flat lists of T*k float32 CUDA tensors, table-major."""
-    import torch
     ptrs = (ctypes.c_void_p * len(cores))(*[_dev_ptr(c, torch.float32, "core").value for c in cores])
     gptrs = None
     if core_grads is not None:
@@ -222,14 +219,12 @@ def tt_emb_workspace_size(h, max_lookups: int, batch: int) -> int:
 
 
 def tt_emb_set_workspace(h, workspace, max_lookups: int, batch: int):
-    import torch
     ptr = _dev_ptr(workspace, torch.uint8, "workspace")
     _check(lib().tt_emb_set_workspace(h, ptr, workspace.numel(), int(max_lookups), int(batch)),
            "tt_emb_set_workspace")
 
 
 def tt_emb_forward(h, indices, offsets, batch: int, out, stream=None):
-    import torch
     _check(lib().tt_emb_forward(h, _dev_ptr(indices, torch.int64, "indices"),
                                 _dev_ptr(offsets, torch.int64, "offsets"), indices.numel(),
                                 int(batch), _dev_ptr(out, torch.float32, "out"), _stream(stream)),
@@ -237,7 +232,6 @@ def tt_emb_forward(h, indices, offsets, batch: int, out, stream=None):
 
 
 def tt_emb_backward(h, grad_out, stream=None):
-    import torch
     _check(lib().tt_emb_backward(h, _dev_ptr(grad_out, torch.float32, "grad_out"), _stream(stream)),
            "tt_emb_backward")
 
@@ -247,7 +241,6 @@ def tt_emb_sgd_update(h, lr: float, stream=None):
 
 
 def tt_emb_backward_sgd(h, grad_out, lr: float, stream=None):
-    import torch
     _check(lib().tt_emb_backward_sgd(h, _dev_ptr(grad_out, torch.float32, "grad_out"), float(lr),
                                      _stream(stream)), "tt_emb_backward_sgd")
 
@@ -285,7 +278,6 @@ def tt_emb_copy_segmentation(h) -> dict:
 
 def tt_emb_forward_noalloc(h, indices, offsets, batch: int, out, stream=None):
     """Forward pass using the library's fixed device scratch instead of a workspace."""
-    import torch
     _check(lib().tt_emb_forward_noalloc(h, _dev_ptr(indices, torch.int64, "indices"),
                                         _dev_ptr(offsets, torch.int64, "offsets"), indices.numel(),
                                         int(batch), _dev_ptr(out, torch.float32, "out"),
@@ -312,7 +304,6 @@ def tt_emb_last_error(h) -> int:
 
 def tt_emb_set_probe(h, records, max_blocks: int):
     """Balance probe: records is a CUDA int64 tensor of 2 * max_blocks * 4 entries, or None."""
-    import torch
     ptr = ctypes.c_void_p(0) if records is None else _dev_ptr(records, torch.int64, "records")
     _check(lib().tt_emb_set_probe(h, ptr, int(max_blocks) if records is not None else 0), "tt_emb_set_probe")
 
@@ -330,13 +321,11 @@ def tt_emb_destroy(h):
 # ---------------------------------------------------------------------------
 # Dense tables
 # ---------------------------------------------------------------------------
-_CODES = {}
+_CODES = {torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16}
 
 
 def dtype_code(dtype) -> int:
     """TT_F32, TT_BF16 or TT_F16 of a torch dtype."""
-    if not _CODES:
-            _CODES.update({torch.float32: TT_F32, torch.bfloat16: TT_BF16, torch.float16: TT_F16})
     code = _CODES.get(dtype)
     if code is None:
         raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")

@@ -203,7 +203,7 @@ template <typename P, typename G, bool k8> struct Raw {
 // The lane's values in memory, moving from one of the warp's blocks to the next.
 template <typename P, typename G, bool k8> struct Place {
     using R = Raw<P, G, k8>;
-    static constexpr int run = R::run, step = kBlk;
+    static constexpr int run = R::run;
     P* p;
     const G* g;
     typename R::M *m, *v;
@@ -217,10 +217,10 @@ template <typename P, typename G, bool k8> struct Place {
     }
     __device__ __forceinline__ void next(int blocks)
     {
-        p += blocks * step;
-        g += blocks * step;
-        m += blocks * step;
-        v += blocks * step;
+        p += blocks * kBlk;
+        g += blocks * kBlk;
+        m += blocks * kBlk;
+        v += blocks * kBlk;
     }
 };
 
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
         auto left = [&](int j) { return r.size - ((w.first + j) * kBlk + lane * R::run); };
         // block j, which is `ahead` blocks behind where `at` stands, to a stage
         auto fetch = [&](int j, int ahead, Stage<P, G>& s) {
-            const int far = ahead * Place<P, G, true>::step;
+            const int far = ahead * kBlk;
             if (j < w.whole) {
 #pragma unroll
                 for (int k = 0; k < R::groups; ++k) {
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
                 x.ms = __shfl_sync(kFull, scale, j);
                 x.vs = __shfl_sync(kFull, scale, 16 + j);
                 update<P, G, true>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f, L);
-                store_block<P, G, true>(at, u * Place<P, G, true>::step, x, j < w.whole, left(j));
+                store_block<P, G, true>(at, u * kBlk, x, j < w.whole, left(j));
                 if ((lane & 15) == j) scale = lane < 16 ? x.ms : x.vs;
             }
             at.next(kStages);

@@ -1027,13 +1027,13 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     a.tail = (float*)(h->ws + y.tail);
     a.touched = ta.touched;
     a.status = h->d_status;
-    const int64_t joins = a.tiles > 1 ? a.tiles * ceil_div(a.slabs, kJoinSlabs) : 0;
+    const int64_t joins = a.tiles * ceil_div(a.slabs, kJoinSlabs);
     const int64_t clears = accumulate ? 0 : ceil_div(ceil_div(h->rows * h->dim, 16 / type_bytes(h->grad_type)), kClearVectors);
     // Half of the clearing goes with the sums and half with the joins: few tokens leave the memory idle
     // in both, and many fill it in either (128000 x 4096 bf16: 216 us so, 227 with all of it with the joins).
     a.sums = ceil_div(a.tiles * a.slabs, kWarps);
-    a.first_clear = joins ? clears / 2 : clears;
-    const unsigned grid = (unsigned)(a.sums + a.first_clear), grid2 = (unsigned)(joins ? joins + clears - a.first_clear : 0);
+    a.first_clear = clears / 2;
+    const unsigned grid = (unsigned)(a.sums + a.first_clear), grid2 = (unsigned)(joins + clears - a.first_clear);
     if (a.sums + joins + clears > INT32_MAX) return TT_ERR_ARG;   // sizes that no device holds
     if (n <= kFew) {
         // two blocks an SM clear all, if the rows of what one of them clears fit its bits
@@ -1075,7 +1075,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
             else if (V == 2) pick(std::integral_constant<int, 2>());
             else pick(std::integral_constant<int, 1>());
         });
-        if (grid2 == 0 || e != cudaSuccess) return;
+        if (e != cudaSuccess) return;
         auto go = [&](auto kernel) { e = launch_early(kernel, grid2, s, a, joins, (W*)h->grad); };
         if (V == 1) go(k_token_join<W, 1>);
         else if (V == 2) go(k_token_join<W, 2>);

@@ -29,13 +29,6 @@ template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return
 template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Pack { T v[N]; };
 
 template <int N, typename T>
-__device__ __forceinline__ void load_pack(const T* p, float (&x)[N])
-{
-    const Pack<T, N> q = *reinterpret_cast<const Pack<T, N>*>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(q.v[i]);
-}
-template <int N, typename T>
 __device__ __forceinline__ void store_pack(T* p, const float (&x)[N])
 {
     Pack<T, N> q;
