@@ -447,7 +447,9 @@ __device__ __forceinline__ void copy_async(void* to, const void* from)
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "n"(N) : "memory");
 }
 
-constexpr int kFit8 = 2;     // blocks of threads on an SM: 789 us for 403 M values, 803 with three, 855 with four (64 registers)
+// blocks of threads on an SM: 800 to 814 us for 403 M values, 814 to 818 with three, 879 with four (64 registers); 12.3, 13.2
+// and 14.4 us for 4 M in twelve tensors
+constexpr int kFit8 = 2;
 constexpr int kStages = 2;   // blocks of a warp: one being computed, the next on its way
 
 // Each thread copies its own values to its own place in shared memory and reads them back, so the
@@ -542,7 +544,7 @@ template <typename P, typename G>
 cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* lr_device, cudaStream_t s)
 {
     // Blocks that stay and take tile after tile.  Two on an SM keep enough 32-bit loads on their way, and
-    // more of them spread the card's reads: 311 us for the rank-64 cores with three, 285 with two.
+    // more of them spread the card's reads: 309 us for the rank-64 cores with three, 285 with two.
     int64_t grid = min64(L.tiles, (int64_t)sms * (k8 ? kFit8 : 2));
     if (grid < 1) grid = 1;
     if (k8) k_adamw8<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
@@ -660,7 +662,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         base.steps = steps;
         base.ticket = h->ticket;
         // In 8 bits, where instructions bound, a warp takes up to 16 blocks of a tensor at a time, which
-        // spreads what it does once a tile (788 us for 403 M values against 844 with 4); fewer where
+        // spreads what it does once a tile (800 to 814 us for 403 M values against 879 with 4); fewer where
         // that already gives each tile a block of threads of its own.  In 32 bits, where memory
         // bounds, it takes one, so that the whole card reads neighbouring places (284 us for the 55 M
         // values of the rank-64 cores against 299 with 4 and 303 with 16).

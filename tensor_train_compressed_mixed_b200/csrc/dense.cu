@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) k_token_keys(TokenArgs a, uint32_t* 
 // their warp by matching lanes, adds the counts of the warps before (shared memory) and of the blocks
 // before (the cluster's shared memory), and moves each key to its new place in whichever block
 // that is.  One launch instead of ten: a gradient of 2000 tokens over 5000 x 512 fp32 takes 21 us with it and
-// 43 with the radix sort's launches, one of 65536 tokens 60 and 81.
+// 40 with the radix sort's launches, one of 65536 tokens 60 and 81, one of 131072 tokens 104 and 118.
 // It goes on after an error: a cluster's blocks must all reach its barriers, and it writes
 // nothing but workspace.
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
@@ -475,10 +475,10 @@ __device__ __forceinline__ void clear_block(const SumArgs& a, int64_t block, W* 
 }
 
 // kRows rows are on their way at a time.  With many units few of them, because what hides the memory's
-// latency then is warps: four blocks an SM with four rows of 8 columns a lane take 70 us for 32768
-// rows of 4096 bf16 values, with eight rows 78 to 90.  With few units, for which eight rows'
-// registers leave room, more: 16205 rows of 4 fp32 values added to a gradient take 15 us two at a
-// time, 9 eight at a time.
+// latency then is warps: a gradient of 32768 tokens over 128000 x 4096 bf16 takes 212 us with four blocks an
+// SM and four rows of 8 columns a lane, 224 with eight rows.  With few units, for which eight rows'
+// registers leave room, more: 16205 rows of 4 fp32 values added to a gradient of 250000 take 26 us two
+// at a time, 21 eight at a time.
 constexpr int rows_many(bool add) { return add ? 2 : 4; }
 constexpr int kRowsFew = 8;
 template <typename G, typename W, int V, bool kAdd, int kRows>
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kThreads) k_token_join(SumArgs a, int64_t join
 // ---------------------------------------------------------------------------
 //
 // The counting grows with the square of the tokens: over 5000 x 512 fp32, 256 tokens take 9 us (16 by
-// sort, sums and joins), 512 took 19 (17).
+// sort, sums and joins), 512 took 19 (16).
 constexpr int kFew = 256;
 constexpr int kFewThreads = 1024, kFewWarps = kFewThreads / 32;
 constexpr int kFewRows = kClearVectors * 8;   // rows that a block's vectors lie in at most
@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kFewThreads) k_token_few(TokenArgs t, SumArgs 
 }
 
 // Positions a tile has: longer tiles cut fewer runs, shorter ones give every warp of the card a unit.  24
-// units an SM: 32768 tokens over 128000 x 4096 bf16 took 234 us so, 259 with 12 and 253 with 48.
+// units an SM: 32768 tokens over 128000 x 4096 bf16 take 212 us so, 221 with 12 and 218 with 48.
 int tile_of(int64_t n, int slabs, int sms)
 {
     const int64_t units = ceil_div(n, 32) * slabs, want = (int64_t)sms * 24;
@@ -797,8 +797,10 @@ bool rows_at(const void* p, int64_t stride, int type, int bytes)
 }
 
 // Neighbouring values that one access may move in rows of both kinds: 16 bytes of the narrower type, or a
-// pair, or one.  (16 bytes of the wider type, 8 of the other, took 185 to 215 us to look up 131072 fp32
-// rows of 2048 into bf16, where this took 172 to 184.)
+// pair, or one.  Against 16 bytes of the wider type and 8 of the other: 65536 bf16 rows of 2048 added to an fp32
+// gradient of 256000 take 147 us, 188 so; fp32 rows of 2048 looked up into bf16 13.0 us, 13.7 so, for 8192 tokens, and as
+// long for 131072 (164 us).  It loses where a wide type is written by few warps: 8192 bf16 rows looked up into fp32
+// take 19.1 us, 15.6 so, and 200 of 512 summed into fp32 12.1 us, 8.5 so.
 int width_of(int dim, const void* p, int64_t p_stride, int p_type, const void* q, int64_t q_stride, int q_type)
 {
     const int most = p_type == TT_F32 && q_type == TT_F32 ? 4 : 8;
@@ -875,8 +877,8 @@ int forward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n
     const int rows = 32 >> a.lane_bits;
     constexpr int kAnyCols = 2, kAnySteps = 8;            // of pairs and single values
     a.slabs = (unsigned)ceil_div(vectors, 32 * (V > 2 ? 1 : kAnyCols));
-    // As many tokens to a unit as leave 64 units an SM: 8192 rows of 4096 bf16 took 24 us so, 25 with 24
-    // units and 29 with 128.
+    // As many tokens to a unit as leave 64 units an SM: 8192 rows of 4096 bf16 take 20.5 us so, 21.3 with 24
+    // units and 22.5 with 128.
     a.per_unit = rows;
     while (a.per_unit < 32 && ceil_div(n, a.per_unit * 2) * a.slabs >= (int64_t)h->num_sms * 64) a.per_unit *= 2;
     const int64_t units = ceil_div(n, a.per_unit) * a.slabs;
@@ -1030,7 +1032,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
     const int64_t joins = a.tiles * ceil_div(a.slabs, kJoinSlabs);
     const int64_t clears = accumulate ? 0 : ceil_div(ceil_div(h->rows * h->dim, 16 / type_bytes(h->grad_type)), kClearVectors);
     // Half of the clearing goes with the sums and half with the joins: few tokens leave the memory idle
-    // in both, and many fill it in either (128000 x 4096 bf16: 216 us so, 227 with all of it with the joins).
+    // in both, and many fill it in either (128000 x 4096 bf16: 212 us so, 221 with all of it with the joins).
     a.sums = ceil_div(a.tiles * a.slabs, kWarps);
     a.first_clear = clears / 2;
     const unsigned grid = (unsigned)(a.sums + a.first_clear), grid2 = (unsigned)(joins + clears - a.first_clear);

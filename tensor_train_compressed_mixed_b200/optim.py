@@ -83,7 +83,12 @@ class AdamW:
     def for_tables(cls, tables, **options):
         """An optimiser of the cores and tables of TTEmbeddingBag and DenseEmbedding objects, whose
         gradient buffers it reads: those they have now, so make it after set_cores and set_table.
-        A table whose backward reported a device error is left as it is until its next sync."""
+        A table whose backward reported a device error is left as it is until its next sync.
+
+        Where several ranks train copies of the tables, the caller exchanges the gradients (a bag's
+        ``grad_flat``, a dense table's ``grad``) before the step, and sees every rank's sync succeed first:
+        a guard is this rank's own, and a rank whose backward failed would leave a table that the others
+        update."""
         params, grads, guards = [], [], []
         for e in tables:
             if isinstance(e, DenseEmbedding):
@@ -101,7 +106,8 @@ class AdamW:
 
     def step(self, lr, stream=None):
         """One step of every tensor.  lr: a number, or a CUDA float32 tensor of one value, which a
-        captured step reads anew at each replay."""
+        captured step reads anew at each replay.  Steps of one object must be ordered (one stream, or
+        events), replayed graphs that captured them included."""
         for t in self.tables:
             if t.handle is None:
                 raise ValueError("a table of this optimiser has been closed")
