@@ -545,7 +545,7 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
  * be computed bit for bit elsewhere, of a v of 2^-102 at least.
  *   lr           host, >= 0 and finite; or lr_device (device float32 [1], may be NULL) in its
  *                place, so that a captured graph follows a schedule (there below 0 and NaN count as 0).
- *                An lr of 1e-30 or below moves no weight; eps (1 - beta1^t) / lr counts as 2.4e-38 at least.
+ *                For an lr of 1e-30 or below the quotient counts as 0; eps (1 - beta1^t) / lr as 2.4e-38 at least.
  * Steps of one handle must be ordered; they share its device block and the step count.
  * Enqueues on stream.  Returns TT_OK, TT_ERR_ARG, TT_ERR_STATE (another device than the
  * handle's is current) or TT_ERR_CUDA.
