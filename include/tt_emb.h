@@ -468,6 +468,80 @@ int tt_emb_dense_backward(tt_emb_dense_t h, const void* tokens, int32_t token_by
                           const void* grad_out, int32_t grad_out_type, int64_t grad_out_stride, int32_t accumulate,
                           tt_stream_t stream);
 
+/*
+ * The table read as a matrix W [num_rows][dim]: the output head of a model that shares its token
+ * table, or the projection of a narrow table's rows to another width.  For every row r < n and c < num_rows
+ *   z[r][c] = sum over k of x[r][k] W[c][k] + bias[c]
+ *   out[r][c] = act(z[r][c]) + residual[r][c]
+ * The handle's scale does not enter.  Strides count elements.  Sums are formed in fp32 and rounded
+ * once to each result's type.  fp32 operands take part as three bf16 terms each, which hold all their bits:
+ * an infinity among them may give NaN where fp32 arithmetic gives an infinity.
+ */
+typedef enum {
+    TT_ACT_NONE = 0,
+    TT_ACT_RELU = 1,         /* z where z > 0, else 0 */
+    TT_ACT_GELU = 2,         /* z Phi(z), Phi the normal distribution function */
+    TT_ACT_SILU = 3,         /* z / (1 + e^-z) */
+    TT_ACT_SOFTCAP = 4       /* cap tanh(z / cap) */
+} tt_activation;
+
+typedef struct {
+    const void* x;           /* device [n][dim], of the table's type, rows x_stride (>= 0; 0 repeats one) apart */
+    const void* bias;        /* device [num_rows], bias_type; may be NULL */
+    const void* residual;    /* device [n][num_rows], residual_type, rows residual_stride (>= 0) apart; may be
+                                NULL, or out itself with the same type and stride */
+    void* pre;               /* device [n][num_rows], pre_type: receives z; may be NULL */
+    void* out;               /* device [n][num_rows], out_type */
+    int64_t x_stride, residual_stride, pre_stride, out_stride;   /* the last two >= num_rows; values between rows
+                                are left as they were */
+    int64_t n;               /* 0 .. 2^31 - 2 */
+    int32_t bias_type, residual_type, pre_type, out_type;        /* tt_dtype */
+    int32_t activation;      /* tt_activation */
+    float cap;               /* of TT_ACT_SOFTCAP, > 0 and finite */
+} tt_emb_project;
+
+/*
+ * The gradients: with dz[r][c] = grad_out[r][c] act'(pre[r][c]),
+ *   grad_x[r][k] = sum over c of dz[r][c] W[c][k]
+ *   grad[c][k]   = (accumulate ? grad[c][k] : 0) + sum over r of dz[r][c] x[r][k]      (the table's gradient buffer)
+ *   grad_bias[c] = (accumulate ? grad_bias[c] : 0) + sum over r of dz[r][c]
+ * The residual's is grad_out itself.  The table's padding_row receives no gradient.  Sums are formed in
+ * fp32 in an order that depends on the sizes, strides and places only: the same call gives the same bits.  Where
+ * the table, grad_out and a result are of 16 bits, that result's products take dz rounded to the table's type
+ * (grad_out of fp32 beside a bf16 table too); all others take it as three bf16 terms.
+ */
+typedef struct {
+    const void* x;           /* as the forward's; not read without table_grad */
+    const void* grad_out;    /* device [n][num_rows], grad_out_type, rows grad_out_stride (>= 0) apart */
+    const void* pre;         /* device [n][num_rows], pre_type: z; not read without an activation */
+    void* grad_x;            /* device [n][dim], grad_x_type, rows grad_x_stride (>= dim) apart; may be NULL */
+    void* grad_bias;         /* device [num_rows], grad_bias_type; may be NULL */
+    int64_t x_stride, grad_out_stride, pre_stride, grad_x_stride;
+    int64_t n;
+    int32_t grad_out_type, pre_type, grad_x_type, grad_bias_type;
+    int32_t activation;
+    float cap;
+    int32_t table_grad;      /* 1: the table's gradient too (needs the handle's buffer) */
+    int32_t accumulate;      /* 0 or 1 */
+} tt_emb_project_grad;
+
+/*
+ * Device workspace that exactly these calls need (host calls; 0 for many).  What they need depends on
+ * sizes, types, strides and alignments.  Errors as those of the calls themselves.
+ */
+int tt_emb_dense_project_workspace_size(tt_emb_dense_t h, const tt_emb_project* call, size_t* bytes);
+int tt_emb_dense_project_backward_workspace_size(tt_emb_dense_t h, const tt_emb_project_grad* call, size_t* bytes);
+
+/* Registers caller-owned device workspace (256-byte aligned) for both.  Nothing in it lives from one call to
+ * the next; two calls that overlap on the GPU must not share it.  Returns TT_OK or TT_ERR_ARG. */
+int tt_emb_dense_set_project_workspace(tt_emb_dense_t h, void* workspace, size_t bytes);
+
+/* Enqueue on `stream`.  Host errors: TT_ERR_ARG (also an output that overlaps another buffer of the call),
+ * TT_ERR_STATE (no table, no gradient buffer, another device), TT_ERR_WORKSPACE (less than the call needs),
+ * TT_ERR_CUDA.  While a device error waits for tt_emb_dense_sync they do nothing. */
+int tt_emb_dense_project(tt_emb_dense_t h, const tt_emb_project* call, tt_stream_t stream);
+int tt_emb_dense_project_backward(tt_emb_dense_t h, const tt_emb_project_grad* call, tt_stream_t stream);
+
 /* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy.  The sync waits for the stream of the last
  * call; a replayed graph's own stream is the caller's to wait for first.  With another device than the
  * handle's current it reads nothing and returns TT_ERR_STATE. */
@@ -552,8 +626,56 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
  */
 int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_stream_t stream);
 
-/* Destroys the handle (host + its device block).  NULL is ignored. */
+/*
+ * As tt_emb_adamw_step on gradients clipped by their global norm: every gradient counts as
+ * factor * g, rounded to fp32, where
+ *   norm = sqrt(sum over all tensors of g^2),  factor = max_norm / norm if norm > max_norm, else 1
+ * (formed in fp64, factor rounded once to fp32).  Gradients are read only, and tensors whose guard
+ * is set do not count.  Where the norm is not a number (an infinity or NaN in a gradient) the step
+ * leaves everything as it is, the step count too.  The same gradients give the same bits.
+ *   max_norm     host, > 0; infinity clips nothing
+ *   norm         device float32 [1], may be NULL: receives the norm (infinity above fp32's range);
+ *                on no other buffer of the step
+ */
+int tt_emb_adamw_step_clipped(tt_emb_adamw_t h, float lr, const float* lr_device, float max_norm, float* norm,
+                              tt_stream_t stream);
+
+/* Destroys the handle (host + its device blocks).  NULL is ignored. */
 void tt_emb_adamw_destroy(tt_emb_adamw_t h);
+
+/*
+ * The global norm of many gradients, and clipping by it in place (before tt_emb_sgd_update or
+ * another optimiser's step; tt_emb_adamw_step_clipped needs no clipping before it).
+ * One tensor: size contiguous values, aligned to their element; borrowed; NULL for size 0.
+ *   guard        device, may be NULL: while *guard is not 0 the tensor counts as absent
+ */
+typedef struct {
+    void* grad;
+    const int32_t* guard;
+    int64_t size;
+    int32_t grad_type;       /* tt_dtype */
+    int32_t reserved;        /* must be zero */
+} tt_emb_norm_tensor;
+
+typedef struct tt_emb_norm_handle* tt_emb_norm_t;
+
+/* Creates a handle over count tensors (host call; allocates the handle and a small device block on
+ * the current device, which later calls want to be current).  Returns TT_OK, TT_ERR_ARG or TT_ERR_CUDA. */
+int tt_emb_norm_create(int32_t count, const tt_emb_norm_tensor* tensors, tt_emb_norm_t* out);
+
+/*
+ * *norm (device float32 [1]) = the norm defined above.  Reads the gradients only.  The clipping
+ * call then multiplies every gradient by the factor defined above, computed in fp32 and rounded
+ * once to its type; where the norm is not a number it leaves them as they are, and its norm may be
+ * NULL.  Calls of one handle must be ordered; they share its device block.  Return TT_OK,
+ * TT_ERR_ARG (also a norm on one of the gradients, and for clipping gradients that overlap each
+ * other), TT_ERR_STATE (another device than the handle's is current) or TT_ERR_CUDA.
+ */
+int tt_emb_norm_measure(tt_emb_norm_t h, float* norm, tt_stream_t stream);
+int tt_emb_norm_clip(tt_emb_norm_t h, float max_norm, float* norm, tt_stream_t stream);
+
+/* Destroys the handle (host + its device block).  NULL is ignored. */
+void tt_emb_norm_destroy(tt_emb_norm_t h);
 
 /* ABI version of the loaded library (TT_EMB_ABI_VERSION). */
 int tt_emb_abi_version(void);

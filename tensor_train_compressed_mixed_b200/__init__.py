@@ -4,6 +4,6 @@ from . import abi, dp
 from .abi import TTEmbError
 from .dense import DenseEmbedding
 from .embedding import TTEmbeddingBag, from_workload
-from .optim import AdamW
+from .optim import AdamW, GradNorm
 
-__all__ = ["abi", "dp", "TTEmbError", "AdamW", "DenseEmbedding", "TTEmbeddingBag", "from_workload"]
+__all__ = ["abi", "dp", "TTEmbError", "AdamW", "DenseEmbedding", "GradNorm", "TTEmbeddingBag", "from_workload"]

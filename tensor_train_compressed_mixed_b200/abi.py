@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -26,6 +27,7 @@ TT_GROUP_PREFIX, TT_GROUP_UNIQUE_ONLY = 0, 1
 TT_PREC_FP32, TT_PREC_BF16_TC, TT_PREC_FP32_SPLIT_TC = 0, 1, 2
 TT_INJECT_NONE, TT_INJECT_POOL_WAIT, TT_INJECT_MMA_WAIT_FWD, TT_INJECT_MMA_WAIT_BWD = 0, 1, 2, 3
 TT_F32, TT_BF16, TT_F16 = 0, 1, 2
+TT_ACT_NONE, TT_ACT_RELU, TT_ACT_GELU, TT_ACT_SILU, TT_ACT_SOFTCAP = 0, 1, 2, 3, 4
 MAX_TABLES, MAX_CORES = 64, 4
 ADAMW_BLOCK = 256      # values that share one scale of an 8-bit moment
 
@@ -62,6 +64,11 @@ class AdamWTensor(ctypes.Structure):
 class AdamWOptions(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
                 ("state_bits", ctypes.c_int32), ("reserved", ctypes.c_int32), ("seed", ctypes.c_uint64)]
+
+
+class NormTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("guard", ctypes.c_void_p), ("size", ctypes.c_int64),
+                ("grad_type", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 _LIB = None
@@ -106,6 +113,13 @@ _SIGS = {
                               ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_backward": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
                                ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_project_workspace_size": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)],
+                                            ctypes.c_int),
+    "tt_emb_dense_project_backward_workspace_size": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.POINTER(ctypes.c_size_t)],
+                                                     ctypes.c_int),
+    "tt_emb_dense_set_project_workspace": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t], ctypes.c_int),
+    "tt_emb_dense_project": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_project_backward": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_sync": ([ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_last_error": ([ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_destroy": ([ctypes.c_void_p], None),
@@ -114,7 +128,13 @@ _SIGS = {
     "tt_emb_adamw_create": ([ctypes.c_int32, ctypes.POINTER(AdamWTensor), ctypes.POINTER(AdamWOptions),
                              ctypes.c_void_p, ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
     "tt_emb_adamw_step": ([ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_adamw_step_clipped": ([ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+                                   ctypes.c_void_p], ctypes.c_int),
     "tt_emb_adamw_destroy": ([ctypes.c_void_p], None),
+    "tt_emb_norm_create": ([ctypes.c_int32, ctypes.POINTER(NormTensor), ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int),
+    "tt_emb_norm_measure": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_norm_clip": ([ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_norm_destroy": ([ctypes.c_void_p], None),
 }
 
 NOALLOC_MAX_LOOKUPS = 262144
@@ -408,6 +428,95 @@ def tt_emb_dense_backward(h, tokens, grad_out, dim: int, accumulate: bool = Fals
         raise TTEmbError(rc, "tt_emb_dense_backward")
 
 
+_ACTS = {None: TT_ACT_NONE, "relu": TT_ACT_RELU, "gelu": TT_ACT_GELU, "silu": TT_ACT_SILU, "softcap": TT_ACT_SOFTCAP}
+_PROJECT = struct.Struct("5P5q5if")           # tt_emb_project
+_PROJECT_GRAD = struct.Struct("5P5q5if2i")    # tt_emb_project_grad
+_NO_ROWS = (0, TT_F32, 0)
+
+
+def _activation(activation, cap):
+    """(TT_ACT_*, cap) of an activation's name."""
+    code = _ACTS.get(activation)
+    if code is None:
+        raise ValueError(f"activation must be None, 'relu', 'gelu', 'silu' or 'softcap', got {activation!r}")
+    if (cap is not None) != (code == TT_ACT_SOFTCAP):
+        raise ValueError("cap belongs to activation='softcap', which needs it")
+    return code, 0.0 if cap is None else float(cap)
+
+
+def _vector(t, n: int, name: str):
+    """(pointer, type) of n neighbouring values, or of None."""
+    if t is None:
+        return 0, TT_F32
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous values, got {tuple(t.shape)}")
+    return t.data_ptr(), dtype_code(t.dtype)
+
+
+def project_call(x, rows: int, dim: int, out, bias=None, residual=None, pre=None, activation=None, cap=None) -> bytes:
+    """A tt_emb_project of these tensors."""
+    n = x.numel() // dim
+    act, cap = _activation(activation, cap)
+    xp, _, xs = _rows(x, n, dim, "x")
+    bp, bt = _vector(bias, rows, "bias")
+    rp, rt, rs = _NO_ROWS if residual is None else _rows(residual, n, rows, "residual")
+    pp, pt, ps = _NO_ROWS if pre is None else _rows(pre, n, rows, "pre")
+    op, ot, os_ = _rows(out, n, rows, "out")
+    return _PROJECT.pack(xp, bp, rp, pp, op, xs, rs, ps, os_, n, bt, rt, pt, ot, act, cap)
+
+
+def project_grad_call(x, rows: int, dim: int, grad_out, pre=None, activation=None, cap=None, grad_x=None, grad_bias=None,
+                      table_grad: bool = True, accumulate: bool = False) -> bytes:
+    """A tt_emb_project_grad of these tensors."""
+    n = grad_out.numel() // rows
+    act, cap = _activation(activation, cap)
+    if act and pre is None:
+        raise ValueError("an activation's gradient needs pre")
+    xp, _, xs = _NO_ROWS if not table_grad else _rows(x, n, dim, "x")
+    gp, gt, gs = _rows(grad_out, n, rows, "grad_out")
+    pp, pt, ps = _NO_ROWS if not act else _rows(pre, n, rows, "pre")
+    ip, it, is_ = _NO_ROWS if grad_x is None else _rows(grad_x, n, dim, "grad_x")
+    bp, bt = _vector(grad_bias, rows, "grad_bias")
+    return _PROJECT_GRAD.pack(xp, gp, pp, ip, bp, xs, gs, ps, is_, n, gt, pt, it, bt, act, cap, int(table_grad), int(accumulate))
+
+
+def tt_emb_dense_project_workspace_size(h, call: bytes) -> int:
+    out = ctypes.c_size_t()
+    rc = lib().tt_emb_dense_project_workspace_size(h, call, ctypes.byref(out))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_project_workspace_size")
+    return out.value
+
+
+def tt_emb_dense_project_backward_workspace_size(h, call: bytes) -> int:
+    out = ctypes.c_size_t()
+    rc = lib().tt_emb_dense_project_backward_workspace_size(h, call, ctypes.byref(out))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_project_backward_workspace_size")
+    return out.value
+
+
+def tt_emb_dense_set_project_workspace(h, workspace):
+    _check(lib().tt_emb_dense_set_project_workspace(h, _dev_ptr(workspace, torch.uint8, "workspace"), workspace.numel()),
+           "tt_emb_dense_set_project_workspace")
+
+
+def tt_emb_dense_project(h, call: bytes, stream: int):
+    """call: of project_call; stream: a CUDA stream's handle."""
+    rc = lib().tt_emb_dense_project(h, call, stream)
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_project")
+
+
+def tt_emb_dense_project_backward(h, call: bytes, stream: int):
+    """call: of project_grad_call; stream: a CUDA stream's handle."""
+    rc = lib().tt_emb_dense_project_backward(h, call, stream)
+    if rc:
+        raise TTEmbError(rc, "tt_emb_dense_project_backward")
+
+
 def tt_emb_dense_sync(h):
     _check(lib().tt_emb_dense_sync(h), "tt_emb_dense_sync")
 
@@ -442,18 +551,68 @@ def tt_emb_adamw_create(tensors, options: AdamWOptions, steps):
     return h
 
 
+def _rate(lr):
+    """(number, device pointer or None) of a learning rate."""
+    if not isinstance(lr, torch.Tensor):
+        return float(lr), None
+    if lr.numel() != 1:
+        raise ValueError("lr must have one value")
+    return 0.0, _dev_ptr(lr, torch.float32, "lr")
+
+
 def tt_emb_adamw_step(h, lr, stream=None):
     """lr: a number, or a CUDA float32 tensor of one value that the device reads."""
-    at = None
-    if isinstance(lr, torch.Tensor):
-        if lr.numel() != 1:
-            raise ValueError("lr must have one value")
-        at, lr = _dev_ptr(lr, torch.float32, "lr"), 0.0
-    rc = lib().tt_emb_adamw_step(h, float(lr), at, _stream_on(stream, torch.cuda.current_device()))
+    lr, at = _rate(lr)
+    rc = lib().tt_emb_adamw_step(h, lr, at, _stream_on(stream, torch.cuda.current_device()))
     if rc:
         raise TTEmbError(rc, "tt_emb_adamw_step")
+
+
+def tt_emb_adamw_step_clipped(h, lr, max_norm: float, norm=None, stream=None):
+    """lr as above; norm: None, or a CUDA float32 tensor of one value that receives the norm."""
+    lr, at = _rate(lr)
+    rc = lib().tt_emb_adamw_step_clipped(h, lr, at, float(max_norm), _one(norm), _stream_on(stream, torch.cuda.current_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_adamw_step_clipped")
 
 
 def tt_emb_adamw_destroy(h):
     if h is not None and h.value:
         lib().tt_emb_adamw_destroy(h)
+
+
+# ---------------------------------------------------------------------------
+# global gradient norm
+# ---------------------------------------------------------------------------
+def _one(norm):
+    """Pointer of a CUDA float32 tensor of one value, or None."""
+    if norm is None:
+        return None
+    if isinstance(norm, torch.Tensor) and norm.numel() != 1:
+        raise ValueError("norm must have one value")
+    return _dev_ptr(norm, torch.float32, "norm")
+
+
+def tt_emb_norm_create(tensors):
+    """tensors: a list of NormTensor."""
+    arr = (NormTensor * len(tensors))(*tensors)
+    h = ctypes.c_void_p()
+    _check(lib().tt_emb_norm_create(len(tensors), arr, ctypes.byref(h)), "tt_emb_norm_create")
+    return h
+
+
+def tt_emb_norm_measure(h, norm, stream=None):
+    rc = lib().tt_emb_norm_measure(h, _one(norm), _stream_on(stream, torch.cuda.current_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_norm_measure")
+
+
+def tt_emb_norm_clip(h, max_norm: float, norm=None, stream=None):
+    rc = lib().tt_emb_norm_clip(h, float(max_norm), _one(norm), _stream_on(stream, torch.cuda.current_device()))
+    if rc:
+        raise TTEmbError(rc, "tt_emb_norm_clip")
+
+
+def tt_emb_norm_destroy(h):
+    if h is not None and h.value:
+        lib().tt_emb_norm_destroy(h)

@@ -16,6 +16,7 @@
 #include <utility>
 #include <vector>
 
+#include "norm.cuh"
 #include "roots.cuh"
 
 using namespace tt;
@@ -151,6 +152,7 @@ __device__ __forceinline__ Pack<T, run> narrow(const F2* x)
 }
 struct Factors {
     F2 den_u, den_1, keep;      // the update is m / (den_u u + den_1), u being the root, in 8 bits minus it
+    F2 clip;                    // of the gradients
     uint64_t start;
 };
 
@@ -267,7 +269,7 @@ __device__ __forceinline__ void store_block(const Place<P, G, k8>& at, int from,
 }
 
 // `random`: the lane's place in the stream of random words
-template <typename P, typename G, bool k8>
+template <typename P, typename G, bool k8, bool kClip>
 __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const Factors& f, const List& L)
 {
     constexpr int run = Shape<P, G, k8>::run, groups = Shape<P, G, k8>::groups;
@@ -283,6 +285,7 @@ __device__ __forceinline__ void update(Raw<P, G, k8>& b, uint64_t random, const 
     }
 #pragma unroll
     for (int i = 0; i < kPairs; ++i) {
+        if constexpr (kClip) g[i] = mul2(g[i], f.clip);
         if constexpr (k8) {
             m[i] = mul2(decode8(b.codes(b.m, i / 2) >> (16 * (i & 1)) & 0xffffu), both(b.ms));
             u[i] = mul2(decode8(b.codes(b.v, i / 2) >> (16 * (i & 1)) & 0xffffu), both(b.vs));
@@ -400,15 +403,19 @@ __device__ __forceinline__ void count_step(const List& L, int64_t t)
     }
 }
 
-template <typename P, typename G>
+// kClip: gradients are multiplied by the factor that their norm has left, and a norm that is not a number leaves
+// everything as it is (every block returns, and none advances the step count)
+template <typename P, typename G, bool kClip>
 __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constant__ List L, float lr,
-                                                          const float* __restrict__ lr_device)
+                                                          const float* __restrict__ lr_device, const NormResult* res)
 {
+    if (kClip && !res->finite) return;
     using R = Raw<P, G, false>;
     const int lane = threadIdx.x & 31;
     const int64_t t = *L.steps + 1;
     if (lr_device) lr = fmaxf(*lr_device, 0.f);
     Factors f = factors(L, t, lr, false);
+    if constexpr (kClip) f.clip = both(res->factor);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
@@ -435,7 +442,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constan
                 x.v[k] = some_in<R::run, typename R::Moment>(at.v + o, n);
             }
         }
-        update<P, G, false>(x, 0, f, L);
+        update<P, G, false, kClip>(x, 0, f, L);
         store_block<P, G, false>(at, 0, x, whole, left);
     }
     count_step(L, t);
@@ -461,16 +468,18 @@ template <typename P, typename G> struct Stage {
     typename R::Moment m[R::groups][kWarps * 32], v[R::groups][kWarps * 32];
 };
 
-template <typename P, typename G>
+template <typename P, typename G, bool kClip>
 __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_constant__ List L, float lr,
-                                                          const float* __restrict__ lr_device)
+                                                          const float* __restrict__ lr_device, const NormResult* res)
 {
+    if (kClip && !res->finite) return;
     using R = Raw<P, G, true>;
     __shared__ Stage<P, G> st[kStages];
     const int lane = threadIdx.x & 31, me = threadIdx.x;
     const int64_t t = *L.steps + 1;
     if (lr_device) lr = fmaxf(*lr_device, 0.f);
     Factors f = factors(L, t, lr, true);
+    if constexpr (kClip) f.clip = both(res->factor);
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const Rec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
@@ -528,7 +537,7 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
                 }
                 x.ms = __shfl_sync(kFull, scale, j);
                 x.vs = __shfl_sync(kFull, scale, 16 + j);
-                update<P, G, true>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f, L);
+                update<P, G, true, kClip>(x, random + (uint64_t)(u * kBlk / 4) * kGamma, f, L);
                 store_block<P, G, true>(at, u * kBlk, x, j < w.whole, left(j));
                 if ((lane & 15) == j) scale = lane < 16 ? x.ms : x.vs;
             }
@@ -541,14 +550,15 @@ __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_cons
 }
 
 template <typename P, typename G>
-cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* lr_device, cudaStream_t s)
+cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* lr_device, const NormResult* res, cudaStream_t s)
 {
     // Blocks that stay and take tile after tile.  Two on an SM keep enough 32-bit loads on their way, and
     // more of them spread the card's reads: 309 us for the rank-64 cores with three, 285 with two.
     int64_t grid = min64(L.tiles, (int64_t)sms * (k8 ? kFit8 : 2));
     if (grid < 1) grid = 1;
-    if (k8) k_adamw8<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
-    else k_adamw32<P, G><<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device);
+    auto go = [&](auto kernel) { kernel<<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device, res); };
+    if (k8) go(res ? k_adamw8<P, G, true> : k_adamw8<P, G, false>);
+    else go(res ? k_adamw32<P, G, true> : k_adamw32<P, G, false>);
     return cudaGetLastError();
 }
 
@@ -560,7 +570,16 @@ struct tt_emb_adamw_handle {
     bool k8 = false;
     int device = 0, sms = 148;
     uint32_t* ticket = nullptr;
+    NormPlan norm;
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // of every buffer of the step
 };
+
+static void free_step(tt_emb_adamw_t h)
+{
+    if (h->ticket) cudaFree(h->ticket);
+    norm_free(h->norm);
+    delete h;
+}
 
 // Whether no two of the buffers that a step writes overlap, and no gradient one of them (false too where there is no
 // memory to tell).
@@ -696,16 +715,32 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         }
         if (h->parts.empty()) h->parts.push_back({TT_F32, TT_F32, base});   // still advances the step
         h->parts.back().list.last = 1;
+        std::vector<tt_emb_norm_tensor> grads(count);
+        for (int32_t i = 0; i < count; ++i) {
+            const tt_emb_adamw_tensor& x = tensors[i];
+            grads[i] = {const_cast<void*>(x.grad), x.guard, x.size, x.grad_type, 0};
+            auto note = [&](const void* p, int64_t bytes) { if (x.size > 0) h->spans.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
+            note(x.param, x.size * type_bytes(x.param_type));
+            note(x.grad, x.size * type_bytes(x.grad_type));
+            note(x.exp_avg, x.size * sb);
+            note(x.exp_avg_sq, x.size * sb);
+            if (k8) note(x.m_scale, ceil_div(x.size, kBlk) * 4);
+            if (k8) note(x.v_scale, ceil_div(x.size, kBlk) * 4);
+        }
+        h->spans.emplace_back((uintptr_t)steps, (uintptr_t)(steps + 1));
+        if (norm_plan(h->norm, count, grads.data()) != cudaSuccess) {
+            free_step(h);
+            return TT_ERR_CUDA;
+        }
     } catch (...) {
-        cudaFree(h->ticket);
-        delete h;
+        free_step(h);
         return TT_ERR_ARG;
     }
     *out = h;
     return TT_OK;
 }
 
-int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_stream_t stream)
+static int step(tt_emb_adamw_t h, float lr, const float* lr_device, bool clip, float max_norm, float* norm, tt_stream_t stream)
 {
     if (!h || ((uintptr_t)lr_device & 3)) return TT_ERR_ARG;
     if (!lr_device && !(lr >= 0.f && lr < INFINITY)) return TT_ERR_ARG;
@@ -713,12 +748,14 @@ int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_str
     if (cudaGetDevice(&dev) != cudaSuccess) return TT_ERR_CUDA;
     if (dev != h->device) return TT_ERR_STATE;
     cudaStream_t s = (cudaStream_t)stream;
+    if (clip && norm_launch(h->norm, max_norm, norm, s) != cudaSuccess) return TT_ERR_CUDA;
+    const NormResult* res = clip ? h->norm.result() : nullptr;
     for (const auto& part : h->parts) {
         const cudaError_t e = by_type(part.ptype, [&](auto p) {
             return by_type(part.gtype, [&](auto g) {
                 using P = decltype(p);
                 using G = decltype(g);
-                return launch_step<P, G>(h->k8, part.list, h->sms, lr, lr_device, s);
+                return launch_step<P, G>(h->k8, part.list, h->sms, lr, lr_device, res, s);
             });
         });
         if (e != cudaSuccess) return TT_ERR_CUDA;
@@ -726,11 +763,24 @@ int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_str
     return TT_OK;
 }
 
+int tt_emb_adamw_step(tt_emb_adamw_t h, float lr, const float* lr_device, tt_stream_t stream)
+{
+    return step(h, lr, lr_device, false, 0.f, nullptr, stream);
+}
+
+int tt_emb_adamw_step_clipped(tt_emb_adamw_t h, float lr, const float* lr_device, float max_norm, float* norm, tt_stream_t stream)
+{
+    if (!h || !(max_norm > 0.f) || ((uintptr_t)norm & 3)) return TT_ERR_ARG;
+    const uintptr_t at = (uintptr_t)norm;
+    for (const auto& x : h->spans)
+        if (norm && at < x.second && at + sizeof(float) > x.first) return TT_ERR_ARG;
+    if (norm && lr_device && at < (uintptr_t)(lr_device + 1) && at + sizeof(float) > (uintptr_t)lr_device) return TT_ERR_ARG;
+    return step(h, lr, lr_device, true, max_norm, norm, stream);
+}
+
 void tt_emb_adamw_destroy(tt_emb_adamw_t h)
 {
-    if (!h) return;
-    if (h->ticket) cudaFree(h->ticket);
-    delete h;
+    if (h) free_step(h);
 }
 
 }  // extern "C"

@@ -16,7 +16,7 @@
 #include <new>
 #include <type_traits>
 
-#include "types.cuh"
+#include "dense.cuh"
 
 using namespace tt;
 
@@ -810,36 +810,7 @@ int width_of(int dim, const void* p, int64_t p_stride, int p_type, const void* q
 
 }  // namespace
 
-struct tt_emb_dense_handle {
-    int64_t rows = 0, pad = -1;
-    int dim = 0, table_type = TT_F32, grad_type = TT_F32;
-    float scale = 1.f;
-    const void* table = nullptr;
-    void* grad = nullptr;
-    char* ws = nullptr;
-    int64_t ws_n = -1;
-    int32_t* d_status = nullptr;
-    int device = 0, num_sms = 148;
-    bool clusters = false;       // one of k_token_sort fits this device
-    cudaStream_t last_stream = nullptr;
-    bool used_stream = false;
-    int last_error = TT_OK;
-};
-
 namespace {
-
-int note(tt_emb_dense_t h, int rc)
-{
-    if (h && rc != TT_OK) h->last_error = rc;
-    return rc;
-}
-
-int ready(tt_emb_dense_t h)
-{
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return TT_ERR_CUDA;
-    return dev == h->device ? TT_OK : TT_ERR_STATE;
-}
 
 bool tokens_ok(const void* tokens, int32_t token_bytes, int64_t n)
 {

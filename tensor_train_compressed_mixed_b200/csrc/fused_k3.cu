@@ -29,7 +29,7 @@
 #include <cuda_bf16.h>
 #include <string.h>
 
-#include "tt_common.cuh"
+#include "tcgen05.cuh"
 
 #define TT_K3_CASES_INNER(X) \
     X(4, 4, 8, 64)           \
@@ -198,93 +198,6 @@ __device__ __forceinline__ int next_task(int sched, int* head, int iter)
     return sched == TT_SCHED_STATIC ? (int)blockIdx.x + iter * (int)gridDim.x : atomicAdd(head, 1);
 }
 
-// ---------------------------------------------------------------------------
-// fifth-generation tensor cores: tensor memory, mbarrier, tcgen05.mma (bf16 x bf16 -> f32)
-// ---------------------------------------------------------------------------
-constexpr int kMbarSpin = 1 << 20;   // bounded wait for an MMA completion (tens of ms at most)
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// Shared-memory matrix descriptor for a K-major operand without swizzle.  The operand is
-// stored as 8-row x 16-byte core matrices (8 rows of 8 bf16 along K, 128 contiguous bytes);
-// lbo = bytes between the two K-adjacent core matrices one MMA (K = 16) reads, sbo = bytes
-// between consecutive 8-row groups.  Bits: start >> 4 [0,14), lbo >> 4 [16,30),
-// sbo >> 4 [32,46), descriptor version 1 [46,48), base offset 0, layout 0 (no swizzle).
-__device__ __forceinline__ uint64_t umma_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-           ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | ((uint64_t)1 << 46);
-}
-
-// Instruction descriptor of kind::f16: f32 accumulator [4,6) = 1, A = bf16 [7,10) = 1,
-// B = bf16 [10,13) = 1, A / B major at bits 15 / 16 (0 = K-major, 1 = MN-major),
-// N >> 3 at [17,23), M >> 4 at [24,29).
-__host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N, bool a_mn = false, bool b_mn = false)
-{
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
-           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// Descriptor of an MN-major operand without swizzle over the same 8 x 16-byte core matrices:
-// each core matrix holds 8 K-rows of 8 contiguous MN-elements; sbo = bytes between
-// MN-adjacent core matrices, lbo = bytes between K-adjacent ones.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t sbo, uint32_t lbo)
-{
-    return umma_desc(saddr, lbo, sbo);
-}
-
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols)   // one warp
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)   // the same warp
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// makes this thread's generic-proxy shared-memory writes visible to the tensor cores
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tc_mma_bf16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
-        ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(0), "r"(0), "r"(0), "r"(0)
-        : "memory");
-}
-// arrives once on the mbarrier when every MMA this thread issued so far has completed
-__device__ __forceinline__ void tc_commit(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-// bounded wait for the completion of phase `parity`; false when the bound ran out
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity)
-{
-    const uint32_t a = smem_u32(bar);
-    for (int it = 0; it < kMbarSpin; ++it) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.b32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(a), "r"(parity)
-            : "memory");
-        if (done) return true;
-        if (it >= 8) __nanosleep(64);
-    }
-    return false;
-}
 // eight fp32 values as two bf16 terms: hi = bf16(x), lo = bf16(x - hi); |x - hi - lo| <= 2^-18 |x|
 __device__ __forceinline__ void split_bf16x8(const float (&v)[8], uint4& hi, uint4& lo)
 {

@@ -1,0 +1,342 @@
+// The norm over the gradients of many tensors, and gradients scaled by it.
+//
+//   norm = sqrt(sum over all values of g^2),   factor = bound / norm where norm > bound, else 1
+//
+// The sums read every gradient once and memory bounds them.  A thread squares and adds the 16 or 32 values of its
+// four vectors in fp32 and goes on in fp64: squares of values beyond 2^63, or all below 2^-45, leave fp32, and such
+// a group is squared again in fp64, so that the norm is right over the whole range of the types.  Each block has a
+// place for its sum, and the last block adds them in their order: the same gradients give the same bits.
+#include <algorithm>
+#include <math.h>
+#include <new>
+#include <type_traits>
+#include <utility>
+
+#include "norm.cuh"
+
+using namespace tt;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVectors = 4;                          // of 16 bytes, in flight per thread
+constexpr int kTile = kThreads * kVectors * 2;       // vectors of a tile
+constexpr int kFit = 4;                              // blocks of threads on an SM
+
+template <typename T> struct Vec {
+    static constexpr int n = 16 / sizeof(T);
+    T v[n];
+};
+
+// squares of values that fp32 cannot hold, or would lose
+template <typename T, int N>
+__device__ __noinline__ double squares64(const T (&x)[N])
+{
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const double v = (double)to_f32(x[i]);
+        s = fma(v, v, s);
+    }
+    return s;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ double squares(const T (&x)[N])
+{
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float v = to_f32(x[i]);
+        a[i & 3] = fmaf(v, v, a[i & 3]);
+    }
+    const float s = (a[0] + a[1]) + (a[2] + a[3]);
+    if constexpr (sizeof(T) == 2 && std::is_same_v<T, __half>) return (double)s;   // all squares fit: 2^-48 to 2^32
+    if (s >= 0x1p-90f && s < 0x1p126f) return (double)s;
+    bool some = false;      // gradients of rows that no token touched are all zero
+#pragma unroll
+    for (int i = 0; i < N; ++i) some |= to_f32(x[i]) != 0.f;
+    return some ? squares64(x) : 0.0;
+}
+
+__device__ __forceinline__ const NormRec& tensor_of(const NormList& L, int64_t tile)
+{
+    int lo = 0, hi = L.count;   // r[lo].tile0 <= tile < r[hi].tile0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (L.r[mid].tile0 <= tile) lo = mid; else hi = mid;
+    }
+    return L.r[lo];
+}
+
+// Values of a tensor: `lead` single ones, whole vectors from there on, single ones behind the last.
+template <typename T>
+__device__ __forceinline__ double tile_squares(const NormRec& r, int64_t tile)
+{
+    const T* g = (const T*)r.grad;
+    const Vec<T>* body = (const Vec<T>*)(g + r.lead);
+    const int64_t vectors = (r.size - r.lead) / Vec<T>::n;
+    double sum = 0.0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int64_t v0 = (tile - r.tile0) * kTile + half * (kThreads * kVectors) + threadIdx.x;
+        T x[kVectors * Vec<T>::n];
+#pragma unroll
+        for (int k = 0; k < kVectors; ++k) {
+            Vec<T> q;
+            const int64_t v = v0 + k * kThreads;
+            if (v < vectors) *(uint4*)&q = __ldg((const uint4*)(body + v));
+            else *(uint4*)&q = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n; ++i) x[k * Vec<T>::n + i] = q.v[i];
+        }
+        sum += squares(x);
+    }
+    if (tile == r.tile0) {      // the single values, at most 14 of them
+        const int64_t behind = r.lead + vectors * Vec<T>::n;
+        const int64_t at = threadIdx.x < r.lead ? threadIdx.x : behind + threadIdx.x - r.lead;
+        if (at < r.size) {
+            const T x[1] = {g[at]};
+            sum += squares64(x);
+        }
+    }
+    return sum;
+}
+
+// sum over the block, in thread 0
+__device__ __forceinline__ double block_sum(double x)
+{
+    __shared__ double part[kThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = x;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        x = 0.0;
+        for (int i = 0; i < kThreads / 32; ++i) x += part[i];
+    }
+    __syncthreads();
+    return x;
+}
+
+__global__ void __launch_bounds__(kThreads, kFit) k_norm(const __grid_constant__ NormList L, char* mem, int slots, float bound, float* norm)
+{
+    double sum = 0.0;
+    for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
+        const NormRec& r = tensor_of(L, b);
+        if (r.guard && has_error(r.guard)) continue;
+        if (r.type == TT_BF16) sum += tile_squares<__nv_bfloat16>(r, b);
+        else if (r.type == TT_F16) sum += tile_squares<__half>(r, b);
+        else sum += tile_squares<float>(r, b);
+    }
+    NormResult* res = (NormResult*)mem;
+    double* part = (double*)(mem + 256);
+    __shared__ bool last;
+    sum = block_sum(sum);
+    if (threadIdx.x == 0) {
+        part[L.first_slot + blockIdx.x] = sum;
+        __threadfence();
+        last = slots > 0 && atomicAdd(&res->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;      // the call's last launch alone has slots; those before it have ended
+    __threadfence();
+    double all = 0.0;
+    for (int i = threadIdx.x; i < slots; i += kThreads) all += *(volatile double*)(part + i);
+    all = block_sum(all);
+    if (threadIdx.x == 0) {
+        const double root = sqrt(all);
+        res->ticket = 0;
+        res->sum = all;
+        res->finite = root < INFINITY;      // also false for NaN
+        res->factor = root > (double)bound ? (float)((double)bound / root) : 1.f;
+        if (norm) *norm = (float)root;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void tile_scale(const NormRec& r, int64_t tile, float by)
+{
+    T* g = (T*)r.grad;
+    Vec<T>* body = (Vec<T>*)(g + r.lead);
+    const int64_t vectors = (r.size - r.lead) / Vec<T>::n;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int64_t v0 = (tile - r.tile0) * kTile + half * (kThreads * kVectors) + threadIdx.x;
+        Vec<T> q[kVectors];
+#pragma unroll
+        for (int k = 0; k < kVectors; ++k)
+            if (v0 + k * kThreads < vectors) *(uint4*)&q[k] = *(const uint4*)(body + v0 + k * kThreads);
+#pragma unroll
+        for (int k = 0; k < kVectors; ++k) {
+            if (v0 + k * kThreads >= vectors) continue;
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n; ++i) q[k].v[i] = from_f32<T>(to_f32(q[k].v[i]) * by);
+            *(uint4*)(body + v0 + k * kThreads) = *(const uint4*)&q[k];
+        }
+    }
+    if (tile == r.tile0) {
+        const int64_t behind = r.lead + vectors * Vec<T>::n;
+        const int64_t at = threadIdx.x < r.lead ? threadIdx.x : behind + threadIdx.x - r.lead;
+        if (at < r.size) g[at] = from_f32<T>(to_f32(g[at]) * by);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, kFit) k_scale(const __grid_constant__ NormList L, const NormResult* res)
+{
+    const float by = res->factor;
+    if (by == 1.f || !res->finite) return;
+    // from the end, where the sums have just been and the cache still holds the gradients
+    for (int64_t b = L.tiles - 1 - blockIdx.x; b >= 0; b -= gridDim.x) {
+        const NormRec& r = tensor_of(L, b);
+        if (r.guard && has_error(r.guard)) continue;
+        if (r.type == TT_BF16) tile_scale<__nv_bfloat16>(r, b, by);
+        else if (r.type == TT_F16) tile_scale<__half>(r, b, by);
+        else tile_scale<float>(r, b, by);
+    }
+}
+
+}  // namespace
+
+namespace tt {
+
+bool norm_tensors_ok(int32_t count, const tt_emb_norm_tensor* tensors)
+{
+    if (!tensors || count < 1) return false;
+    for (int32_t i = 0; i < count; ++i) {
+        const tt_emb_norm_tensor& x = tensors[i];
+        if (x.size < 0 || x.size > (int64_t)1 << 40 || !type_known(x.grad_type) || x.reserved != 0) return false;
+        if ((uintptr_t)x.guard & 3) return false;
+        if (x.size > 0 && (!x.grad || ((uintptr_t)x.grad & (type_bytes(x.grad_type) - 1)))) return false;
+    }
+    return true;
+}
+
+cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tensors)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    NormList empty;
+    memset(&empty, 0, sizeof(empty));
+    p.lists.push_back(empty);
+    for (int32_t i = 0; i < count; ++i) {
+        const tt_emb_norm_tensor& x = tensors[i];
+        if (x.size == 0) continue;
+        if (p.lists.back().count == kNormTensors) p.lists.push_back(empty);
+        NormList& L = p.lists.back();
+        const int bytes = type_bytes(x.grad_type);
+        const int64_t lead = min64(x.size, (int64_t)((16 - ((uintptr_t)x.grad & 15)) & 15) / bytes);
+        L.r[L.count++] = {x.grad, x.guard, x.size, L.tiles, x.grad_type, (int32_t)lead};
+        L.tiles += std::max<int64_t>(1, ((x.size - lead) / (16 / bytes) + kTile - 1) / kTile);
+    }
+    for (NormList& L : p.lists) {
+        L.first_slot = p.slots;
+        p.grids.push_back((int)std::max<int64_t>(1, min64(L.tiles, (int64_t)p.sms * kFit)));
+        p.slots += p.grids.back();
+    }
+    const size_t bytes = 256 + (size_t)p.slots * sizeof(double);
+    e = cudaMalloc((void**)&p.mem, bytes);
+    if (e != cudaSuccess) return e;
+    // waited for, as the first call may run on a stream that is not ordered behind this one
+    e = cudaMemset(p.mem, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+    if (e != cudaSuccess) norm_free(p);
+    return e;
+}
+
+void norm_free(NormPlan& p)
+{
+    if (p.mem) cudaFree(p.mem);
+    p.mem = nullptr;
+}
+
+cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s)
+{
+    for (size_t i = 0; i < p.lists.size(); ++i)
+        k_norm<<<p.grids[i], kThreads, 0, s>>>(p.lists[i], p.mem, i + 1 == p.lists.size() ? p.slots : 0, bound, norm);
+    return cudaGetLastError();
+}
+
+cudaError_t norm_scale(const NormPlan& p, cudaStream_t s)
+{
+    for (size_t i = p.lists.size(); i-- > 0;) k_scale<<<p.grids[i], kThreads, 0, s>>>(p.lists[i], p.result());
+    return cudaGetLastError();
+}
+
+}  // namespace tt
+
+struct tt_emb_norm_handle {
+    NormPlan plan;
+    int device = 0;
+    bool apart = true;
+    std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // of the gradients, sorted
+};
+
+namespace {
+
+int measure(tt_emb_norm_t h, bool scale, float max_norm, float* norm, cudaStream_t s)
+{
+    if (!h || ((uintptr_t)norm & 3) || !(max_norm > 0.f)) return TT_ERR_ARG;
+    if (scale && !h->apart) return TT_ERR_ARG;
+    for (const auto& x : h->spans)
+        if (norm && (uintptr_t)norm < x.second && (uintptr_t)(norm + 1) > x.first) return TT_ERR_ARG;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return TT_ERR_CUDA;
+    if (dev != h->device) return TT_ERR_STATE;
+    if (norm_launch(h->plan, max_norm, norm, s) != cudaSuccess) return TT_ERR_CUDA;
+    if (scale && norm_scale(h->plan, s) != cudaSuccess) return TT_ERR_CUDA;
+    return TT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int tt_emb_norm_create(int32_t count, const tt_emb_norm_tensor* tensors, tt_emb_norm_t* out)
+{
+    if (!out) return TT_ERR_ARG;
+    *out = nullptr;
+    if (!norm_tensors_ok(count, tensors)) return TT_ERR_ARG;
+    tt_emb_norm_handle* h = new (std::nothrow) tt_emb_norm_handle();
+    if (!h) return TT_ERR_ARG;
+    int rc = TT_OK;
+    try {
+        for (int32_t i = 0; i < count; ++i)
+            if (tensors[i].size > 0)
+                h->spans.emplace_back((uintptr_t)tensors[i].grad, (uintptr_t)tensors[i].grad + tensors[i].size * type_bytes(tensors[i].grad_type));
+        std::sort(h->spans.begin(), h->spans.end());
+        for (size_t i = 1; i < h->spans.size(); ++i) h->apart = h->apart && h->spans[i - 1].second <= h->spans[i].first;
+        if (cudaGetDevice(&h->device) != cudaSuccess || norm_plan(h->plan, count, tensors) != cudaSuccess) rc = TT_ERR_CUDA;
+    } catch (...) {
+        rc = TT_ERR_ARG;
+    }
+    if (rc != TT_OK) {
+        norm_free(h->plan);
+        delete h;
+        return rc;
+    }
+    *out = h;
+    return TT_OK;
+}
+
+int tt_emb_norm_measure(tt_emb_norm_t h, float* norm, tt_stream_t stream)
+{
+    if (!norm) return TT_ERR_ARG;
+    return measure(h, false, INFINITY, norm, (cudaStream_t)stream);
+}
+
+int tt_emb_norm_clip(tt_emb_norm_t h, float max_norm, float* norm, tt_stream_t stream)
+{
+    return measure(h, true, max_norm, norm, (cudaStream_t)stream);
+}
+
+void tt_emb_norm_destroy(tt_emb_norm_t h)
+{
+    if (!h) return;
+    norm_free(h->plan);
+    delete h;
+}
+
+}  // extern "C"

@@ -1,0 +1,55 @@
+// The norm over all gradients of a list of tensors, on the device: what clipping and AdamW's clipped step share.
+#pragma once
+
+#include <vector>
+
+#include "types.cuh"
+
+namespace tt {
+
+constexpr int kNormTensors = 128;   // tensors of one launch; their records travel as its parameters
+
+struct NormRec {
+    void* grad;
+    const int32_t* guard;
+    int64_t size;
+    int64_t tile0;     // first tile of the tensor, counted over the launch
+    int32_t type;      // tt_dtype
+    int32_t lead;      // values before the first one that begins a vector of 16 bytes
+};
+struct NormList {
+    int32_t count;
+    int32_t first_slot;   // of the launch's partial sums
+    int64_t tiles;
+    NormRec r[kNormTensors];
+};
+
+// What a call leaves for the kernels behind it.
+struct NormResult {
+    uint32_t ticket;
+    int32_t finite;    // whether the norm is a number
+    float factor;      // of every gradient: bound / norm where the norm is above the bound, else 1
+    float pad;
+    double sum;        // of the squares
+};
+
+// The plan of one list (host) and its device memory: a NormResult, and the partial sums from byte 256 on.
+struct NormPlan {
+    std::vector<NormList> lists;
+    std::vector<int> grids;
+    int sms = 148, slots = 0;
+    char* mem = nullptr;
+    NormResult* result() const { return (NormResult*)mem; }
+};
+
+// May throw std::bad_alloc.  The device memory is allocated on the current device and cleared before it returns.
+cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tensors);
+void norm_free(NormPlan& p);
+// Sums, the norm (rounded once to *norm, which may be null) and the factor for `bound`.
+cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s);
+// Every gradient times the factor of the preceding norm_launch, in place.
+cudaError_t norm_scale(const NormPlan& p, cudaStream_t s);
+// Whether a list can be taken at all, and whether its buffers are apart.
+bool norm_tensors_ok(int32_t count, const tt_emb_norm_tensor* tensors);
+
+}  // namespace tt

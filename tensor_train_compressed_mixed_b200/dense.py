@@ -1,4 +1,4 @@
-"""DenseEmbedding: one dense table, its scaled lookup and its gradient.
+"""DenseEmbedding: one dense table, its scaled lookup, the table read as a matrix, and the gradients of both.
 
 The tables that are not worth compressing (a model's token table, small categorical
 ones) live beside the TT tables: same library, same streams, same errors.  As in
@@ -51,6 +51,7 @@ class DenseEmbedding:
         self.grad = None
         self._ws = []           # the workspace in use is the last; captured calls keep using theirs
         self._ws_tokens = -1
+        self._project_ws = []   # likewise
 
     def _check(self, t, name: str, dtype=None):
         if not isinstance(t, torch.Tensor) or t.get_device() != self.device.index:   # -1 on the CPU
@@ -113,6 +114,74 @@ class DenseEmbedding:
             self.reserve(tokens.numel(), stream)
             abi.tt_emb_dense_backward(self.handle, tokens, grad_out, self.dim, accumulate, stream)
         return self.grad
+
+    def _workspace(self, nbytes: int, stream):
+        """A workspace of this size for the projection's calls; earlier, smaller ones live on, as reserve's do."""
+        last = self._project_ws[-1].numel() if self._project_ws else 0
+        if nbytes > last:
+            with on_stream(stream):
+                ws = torch.empty(max(nbytes, last * 3 // 2), dtype=torch.uint8, device=self.device)
+            abi.tt_emb_dense_set_project_workspace(self.handle, ws)
+            self._project_ws.append(ws)
+
+    def project(self, x: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
+                cap: float | None = None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                out_dtype: torch.dtype | None = None, pre: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """act(x tableᵀ + bias) + residual, in out's type, or out_dtype, or the table's: the output head that shares a
+        token table, or a narrow table's rows at a model's width.  The table's scale does not enter.
+
+        x: [..., dim], of the table's type.  bias: [num_rows].  activation: None, 'relu', 'gelu' (exact), 'silu', or
+        'softcap', which is cap * tanh(z / cap).  residual, out: [..., num_rows]; residual may be out.  pre: a buffer of
+        that shape that receives x tableᵀ + bias, which the backward of an activation wants.  All of these may be of any of the
+        three types, and their rows may lie any one distance apart; no output may overlap another buffer."""
+        self._check(x, "x", self.dtype)
+        if x.dim() == 0 or x.size(-1) != self.dim:
+            raise ValueError(f"x must hold rows of {self.dim} values, got {tuple(x.shape)}")
+        for t, name in ((bias, "bias"), (residual, "residual"), (pre, "pre")):
+            if t is not None:
+                self._check(t, name)
+        with on_device(self.device):
+            if out is None:
+                with on_stream(stream):
+                    out = torch.empty(*x.shape[:-1], self.num_rows, dtype=out_dtype or self.dtype, device=self.device)
+            else:
+                self._check(out, "out", out_dtype)
+            call = abi.project_call(x, self.num_rows, self.dim, out, bias, residual, pre, activation, cap)
+            self._workspace(abi.tt_emb_dense_project_workspace_size(self.handle, call), stream)
+            abi.tt_emb_dense_project(self.handle, call, abi._stream_on(stream, self.device.index))
+        return out
+
+    def project_backward(self, x: torch.Tensor | None, grad_out: torch.Tensor, pre: torch.Tensor | None = None,
+                         activation: str | None = None, cap: float | None = None, accumulate: bool = False,
+                         grad_x: torch.Tensor | bool = True, grad_bias: torch.Tensor | None = None,
+                         table_grad: bool = True, stream=None):
+        """The gradients of ``project`` for an upstream gradient grad_out [..., num_rows]: the table's, written to (or
+        with accumulate added to) ``self.grad``, the bias's likewise to grad_bias if it is given, and x's, which is
+        returned: in grad_x if that is a buffer, in a new tensor of the table's type, or not at all if it is False.
+
+        pre: what ``project`` left there; not needed without an activation.  The residual's gradient is grad_out.
+        The table's padding row receives none.  table_grad=False leaves the table's out, and needs no x."""
+        self._check(grad_out, "grad_out")
+        if grad_out.dim() == 0 or grad_out.size(-1) != self.num_rows:
+            raise ValueError(f"grad_out must hold rows of {self.num_rows} values, got {tuple(grad_out.shape)}")
+        if table_grad:
+            self._check(x, "x", self.dtype)
+        for t, name in ((pre, "pre"), (grad_bias, "grad_bias")):
+            if t is not None:
+                self._check(t, name)
+        with on_device(self.device):
+            if grad_x is True:
+                with on_stream(stream):
+                    grad_x = torch.empty(*grad_out.shape[:-1], self.dim, dtype=self.dtype, device=self.device)
+            elif grad_x is False:
+                grad_x = None
+            else:
+                self._check(grad_x, "grad_x")
+            call = abi.project_grad_call(x, self.num_rows, self.dim, grad_out, pre, activation, cap, grad_x, grad_bias, table_grad,
+                                         accumulate)
+            self._workspace(abi.tt_emb_dense_project_backward_workspace_size(self.handle, call), stream)
+            abi.tt_emb_dense_project_backward(self.handle, call, abi._stream_on(stream, self.device.index))
+        return grad_x
 
     def sync(self):
         with on_device(self.device):

@@ -1,10 +1,102 @@
-"""AdamW: one optimiser step over many tensors in one launch, moments in 32 or 8 bits."""
+"""AdamW: one optimiser step over many tensors in one launch, moments in 32 or 8 bits; the global gradient norm and
+clipping by it, in place or within the step."""
 from __future__ import annotations
 
 import torch
 
 from . import abi
 from .dense import DenseEmbedding, on_device
+
+
+def _trained(tables):
+    """(parameters, gradients, guards) of TTEmbeddingBag and DenseEmbedding objects."""
+    params, grads, guards = [], [], []
+    for e in tables:
+        if isinstance(e, DenseEmbedding):
+            ps, gs, word = [e.table], [e.grad], abi.tt_emb_dense_status_word(e.handle)
+        else:
+            ps, gs, word = e.cores, e.grads, abi.tt_emb_status_word(e.handle)
+        if ps is None or ps[0] is None or gs is None or gs[0] is None:
+            raise ValueError("every table needs its cores (or table) and gradient buffers set")
+        params += ps
+        grads += gs
+        guards += [word] * len(ps)
+    return params, grads, guards
+
+
+def _all_open(tables, of):
+    for t in tables:
+        if t.handle is None:
+            raise ValueError(f"a table of this {of} has been closed")
+
+
+class GradNorm:
+    """The norm over the gradients of many tensors (root of the sum of all their squares), and clipping by it.
+
+    grads: a list of contiguous CUDA tensors (float32, bfloat16 or float16), borrowed: they are read anew at every
+    call.  guards: as AdamW's; a tensor whose guard is set counts as absent.  Calls of one object must be ordered (one
+    stream, or events), replayed graphs that captured them included.  To clip before an AdamW step, give the bound to
+    ``AdamW.step`` instead, which leaves the gradients as they are and reads them once less.
+    """
+
+    def __init__(self, grads, guards=None):
+        grads = list(grads)
+        if not grads:
+            raise ValueError("grads must be a non-empty list")
+        guards = [None] * len(grads) if guards is None else list(guards)
+        if len(guards) != len(grads):
+            raise ValueError("guards must have one entry for each tensor")
+        self.device = grads[0].device if isinstance(grads[0], torch.Tensor) else None
+        recs = []
+        for i, (g, guard) in enumerate(zip(grads, guards)):
+            if not isinstance(g, torch.Tensor) or not g.is_cuda or g.device != self.device:
+                raise TypeError(f"grads[{i}] must be a CUDA tensor on the first one's device")
+            if not g.is_contiguous():
+                raise ValueError(f"grads[{i}] must be contiguous")
+            recs.append(abi.NormTensor(grad=g.data_ptr(), guard=guard, size=g.numel(), grad_type=abi.dtype_code(g.dtype)))
+        self.grads = grads
+        self.tables = []
+        with on_device(self.device):
+            self.value = torch.zeros(1, dtype=torch.float32, device=self.device)
+            torch.cuda.current_stream(self.device).synchronize()    # the first call may be given another stream
+            self.handle = abi.tt_emb_norm_create(recs)
+
+    @classmethod
+    def for_tables(cls, tables):
+        """Over the gradient buffers of TTEmbeddingBag and DenseEmbedding objects: those they have now.  A table whose
+        backward reported a device error is left out until its next sync."""
+        tables = list(tables)
+        _, grads, guards = _trained(tables)
+        self = cls(grads, guards=guards)
+        self.tables = tables   # the guards are theirs
+        return self
+
+    def norm(self, stream=None) -> torch.Tensor:
+        """The norm, as ``self.value``: a CUDA float32 tensor of one value that the next call overwrites."""
+        _all_open(self.tables, "norm")
+        with on_device(self.device):
+            abi.tt_emb_norm_measure(self.handle, self.value, stream)
+        return self.value
+
+    def clip(self, max_norm: float, stream=None) -> torch.Tensor:
+        """Multiplies every gradient by max_norm / norm where the norm is above max_norm (> 0), in place, and
+        returns the norm before that, as ``norm`` does.  A norm that is not a number (an infinity or NaN in a
+        gradient) leaves the gradients as they are.  Gradients that overlap each other cannot be clipped."""
+        _all_open(self.tables, "norm")
+        with on_device(self.device):
+            abi.tt_emb_norm_clip(self.handle, max_norm, self.value, stream)
+        return self.value
+
+    def close(self):
+        if getattr(self, "handle", None) is not None:
+            abi.tt_emb_norm_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 class AdamW:
@@ -54,6 +146,7 @@ class AdamW:
             total += (p.numel() + B - 1) // B * B
         with on_device(self.device):
             self.steps = torch.zeros(1, dtype=torch.int64, device=self.device)
+            self.norm = torch.zeros(1, dtype=torch.float32, device=self.device)
             kind = torch.float32 if state_bits == 32 else torch.uint8
             self.m = torch.zeros(total, dtype=kind, device=self.device)
             self.v = torch.zeros(total, dtype=kind, device=self.device)
@@ -89,32 +182,30 @@ class AdamW:
         ``grad_flat``, a dense table's ``grad``) before the step, and sees every rank's sync succeed first:
         a guard is this rank's own, and a rank whose backward failed would leave a table that the others
         update."""
-        params, grads, guards = [], [], []
-        for e in tables:
-            if isinstance(e, DenseEmbedding):
-                ps, gs, word = [e.table], [e.grad], abi.tt_emb_dense_status_word(e.handle)
-            else:
-                ps, gs, word = e.cores, e.grads, abi.tt_emb_status_word(e.handle)
-            if ps is None or ps[0] is None or gs is None or gs[0] is None:
-                raise ValueError("every table needs its cores (or table) and gradient buffers set")
-            params += ps
-            grads += gs
-            guards += [word] * len(ps)
+        tables = list(tables)
+        params, grads, guards = _trained(tables)
         self = cls(params, grads, guards=guards, **options)
-        self.tables = list(tables)   # the guards are theirs
+        self.tables = tables   # the guards are theirs
         return self
 
-    def step(self, lr, stream=None):
+    def step(self, lr, stream=None, max_norm=None):
         """One step of every tensor.  lr: a number, or a CUDA float32 tensor of one value, which a
         captured step reads anew at each replay.  Steps of one object must be ordered (one stream, or
-        events), replayed graphs that captured them included."""
-        for t in self.tables:
-            if t.handle is None:
-                raise ValueError("a table of this optimiser has been closed")
+        events), replayed graphs that captured them included.
+
+        max_norm (> 0): the step's gradients are first multiplied by max_norm / norm where their global norm is above
+        max_norm; the buffers keep what they hold.  Returns that norm then, as ``self.norm``: a CUDA float32 tensor of
+        one value that the next such step overwrites.  A norm that is not a number (an infinity or NaN in a gradient)
+        makes the step leave everything as it is, ``steps`` too."""
+        _all_open(self.tables, "optimiser")
         if isinstance(lr, torch.Tensor) and lr.device != self.device:
             raise TypeError(f"lr must be a number or a tensor on {self.device}")
         with on_device(self.device):
-            abi.tt_emb_adamw_step(self.handle, lr, stream)
+            if max_norm is None:
+                abi.tt_emb_adamw_step(self.handle, lr, stream)
+                return None
+            abi.tt_emb_adamw_step_clipped(self.handle, lr, max_norm, self.norm, stream)
+        return self.norm
 
     def close(self):
         if getattr(self, "handle", None) is not None:
