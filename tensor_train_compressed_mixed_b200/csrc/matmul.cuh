@@ -1,0 +1,32 @@
+// Products on the tensor cores (matmul.cu) as project.cu calls them.
+#pragma once
+
+#include "project.cuh"
+
+namespace tt {
+
+// A 16-bit matrix [outer][inner] that tensor maps can take: rows `stride` values apart, and `parts` such matrices
+// part_stride values apart (the bf16 terms of values that have more bits than one holds).
+struct Operand {
+    const void* p = nullptr;
+    int64_t outer = 0, inner = 0, stride = 0, part_stride = 0;
+    int32_t type = TT_BF16, parts = 1;
+};
+// whether a matrix can be read as it lies: 16-byte aligned rows
+inline bool mappable(const void* p, int64_t stride, int64_t outer, int64_t inner)
+{
+    return ((uintptr_t)p & 15) == 0 && (outer == 1 || ((stride & 7) == 0 && stride >= inner && stride < (int64_t)1 << 38));
+}
+
+// C[r][c] = sum over k of A(c, k) B(r, k), finished by e: r < rows, c < cols, k < deep.  A is [cols][deep], or with a_mn
+// [deep][cols]; B is [rows][deep], or with b_mn [deep][rows].  Both of one type.
+struct Product {
+    Operand a, b;
+    bool a_mn = false, b_mn = false;
+    int64_t rows = 0, cols = 0, deep = 0;
+    Epilogue e = {};
+};
+// Returns a tt_status.
+int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s);
+
+}  // namespace tt

@@ -3,11 +3,16 @@
 //   z = x W^T + bias,   out = act(z) + residual
 //   dz = grad_out . act'(z),   grad_x = dz W,   grad_W = dz^T x,   grad_bias = sum over rows of dz
 //
-// Three products of the same kind: C[r][c] = sum over k of A(r, k) B(c, k).
+// Three products of the same kind.  The tensor cores take them (matmul.cu) on 16-bit operands whose rows begin at 16-byte
+// places.  What is not like that is laid out first, in the workspace: rows at other places are copied; fp32
+// values (and dz, where its rounding to 16 bits would show in a result) are written as three bf16 terms
+// x = t0 + t1 + t2 + rest, each the nearest bf16 to what the ones before leave, |rest| <= 2^-27 |x|, fp16 values beside them
+// as two.  dz is formed in the same pass, and the bias's gradient with it.  Small products, whose time is that of their
+// launches, run on the FP32 pipes from where their operands lie, in one launch each.
 #include <math.h>
 
 #include "dense.cuh"
-#include "project.cuh"
+#include "matmul.cuh"
 
 using namespace tt;
 
@@ -78,25 +83,110 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Sm
 }
 
 // ---------------------------------------------------------------------------
-// the bias's gradient
+// operands laid out, dz, the bias's gradient
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(kThreads) k_bias_grad(Upstream u, int64_t rows, int64_t cols, void* out, int32_t out_type, int32_t accumulate,
+constexpr int kPackCols = 256;       // columns of a block: eight a lane
+
+struct PackArgs {
+    Upstream u;           // the values: u.up, times the slope at u.pre
+    int64_t rows, cols, ld;
+    int64_t each;         // rows of a block
+    void* narrow;         // [rows][ld] of narrow_type; may be null
+    uint16_t* wide;       // [parts][rows][ld] bf16 terms; may be null
+    float* sums;          // [blocks of rows][cols] sums over a block's rows; may be null
+    const int32_t* status;
+    int32_t narrow_type, parts;
+    int32_t vectors;      // every row begins at a place that vector loads can take
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const void* p, int64_t at, bool whole, int n, float (&x)[8])
+{
+    const T* q = (const T*)p + at;
+    if (whole) {
+        constexpr int kPer = 16 / sizeof(T);
+        Pack<T, kPer> v[8 / kPer];
+#pragma unroll
+        for (int i = 0; i < 8 / kPer; ++i) v[i] = ((const Pack<T, kPer>*)q)[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = to_f32(v[i / kPer].v[i % kPer]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f32(q[i]) : 0.f;
+    }
+}
+__device__ __forceinline__ void load8(const void* p, int type, int64_t at, bool whole, int n, float (&x)[8])
+{
+    if (type == TT_BF16) load8<__nv_bfloat16>(p, at, whole, n, x);
+    else if (type == TT_F16) load8<__half>(p, at, whole, n, x);
+    else load8<float>(p, at, whole, n, x);
+}
+// the nearest bf16 value; the largest finite one where that would be an infinity of a finite x
+__device__ __forceinline__ float term(float x)
+{
+    const float t = to_f32(__float2bfloat16_rn(x));
+    return fabsf(t) == INFINITY && fabsf(x) < INFINITY ? copysignf(0x1.fep127f, x) : t;
+}
+
+__global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackArgs g)
+{
+    if (has_error(g.status)) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * kPackCols + lane * 8;
+    const int n = (int)min64(8, g.cols - c);
+    const int64_t from = (int64_t)blockIdx.y * g.each, to = min64(g.rows, from + g.each);
+    const bool whole = g.vectors && n == 8;
+    float sum[8] = {};
+    if (n > 0)
+        for (int64_t r = from + warp; r < to; r += kThreads / 32) {
+            float x[8];
+            load8(g.u.up, g.u.up_type, r * g.u.up_stride + c, whole, n, x);
+            if (g.u.act != TT_ACT_NONE) {
+                float z[8];
+                load8(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c, whole, n, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] * slope(g.u.act, z[i], g.u.cap) : 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += x[i];
+            if (g.narrow) {
+                if (g.narrow_type == TT_F16) store_pack((__half*)g.narrow + r * g.ld + c, x);
+                else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
+            }
+            if (g.wide) {
+                for (int p = 0; p < g.parts; ++p) {
+                    float t[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        t[i] = term(x[i]);
+                        x[i] = fabsf(x[i]) < INFINITY ? x[i] - t[i] : 0.f;
+                    }
+                    store_pack((__nv_bfloat16*)g.wide + ((int64_t)p * g.rows + r) * g.ld + c, t);
+                }
+            }
+        }
+    if (!g.sums) return;
+    __shared__ float part[kThreads / 32][kPackCols];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = sum[i];
+    __syncthreads();
+    float all = 0.f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) all += part[w][threadIdx.x];
+    const int64_t at = (int64_t)blockIdx.x * kPackCols + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    if (at < g.cols) g.sums[blockIdx.y * g.cols + at] = all;
+}
+
+__global__ void __launch_bounds__(kThreads) k_bias_grad(const float* sums, int64_t blocks, int64_t cols, void* out, int32_t type, int32_t accumulate,
                                                         const int32_t* status)
 {
     if (has_error(status)) return;
-    __shared__ float part[8][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (c >= cols) return;
     float sum = 0.f;
-    if (c < cols)
-        for (int64_t r = warp; r < rows; r += 8) sum += upstream(u, r, c);
-    part[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && c < cols) {
-        for (int i = 1; i < 8; ++i) sum += part[i][lane];
-        if (accumulate) sum += load_any(out, out_type, c);
-        store_any(out, out_type, c, sum);
-    }
+    for (int64_t i = 0; i < blocks; ++i) sum += sums[i * cols + c];
+    if (accumulate) sum += load_any(out, type, c);
+    store_any(out, type, c, sum);
 }
 
 // ---------------------------------------------------------------------------
@@ -190,74 +280,231 @@ int launch_product(const SmallArgs& g, cudaStream_t s)
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-int project(tt_emb_dense_t h, const tt_emb_project* a, cudaStream_t s)
+// The workspace's parts, one after another.
+struct Space {
+    char* base;
+    size_t used = 0;
+    explicit Space(char* at) : base(at) {}
+    void* take(int64_t bytes)
+    {
+        const size_t at = used;
+        used += (size_t)(bytes + 255) / 256 * 256;
+        return base ? base + at : nullptr;
+    }
+};
+
+// One matrix of a call in the forms that its products want.
+struct Forms {
+    PackArgs pack = {};
+    bool packs = false;       // the pass over the values is needed
+    Operand narrow, wide;
+};
+
+// forms of u's values [rows][cols], which are 16-bit values as they lie if `plain`
+Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t cols, int table_type, bool want_narrow, int wide_parts, bool want_sums,
+               int sms, int32_t* status)
 {
-    if (const int rc = check_forward(h, a)) return rc;
-    if (const int rc = ready(h)) return rc;
-    h->last_stream = s;
-    h->used_stream = true;
-    if (a->n == 0) return TT_OK;
-    SmallArgs g = {};
-    g.a = {a->x, a->x_stride, 1, h->table_type};
-    g.b = {h->table, h->dim, 1, h->table_type};
-    g.e = {a->out, a->residual, a->pre, a->bias, a->out_stride, a->residual_stride, a->pre_stride, -1,
-           a->out_type, a->residual_type, a->pre_type, a->bias_type, a->activation, a->cap};
-    g.rows = a->n;
-    g.cols = h->rows;
-    g.deep = h->dim;
-    g.status = h->d_status;
-    return launch_product(g, s);
+    Forms f;
+    const int64_t ld = ceil_div(cols, 8) * 8;
+    const bool direct = plain && mappable(u.up, u.up_stride, rows, cols);
+    f.pack.u = u;
+    f.pack.rows = rows;
+    f.pack.cols = cols;
+    f.pack.ld = ld;
+    f.pack.status = status;
+    f.pack.narrow_type = table_type;
+    // one bf16 term is the value itself
+    if (wide_parts == 1) want_narrow = true;
+    if (want_narrow) {
+        f.narrow.type = table_type;
+        f.narrow.outer = rows;
+        f.narrow.inner = cols;
+        f.narrow.stride = direct ? u.up_stride : ld;
+        f.narrow.p = direct ? u.up : f.pack.narrow = w.take(rows * ld * 2);
+        f.packs = !direct;
+    }
+    if (wide_parts == 1) f.wide = f.narrow;
+    if (wide_parts > 1) {
+        f.pack.wide = (uint16_t*)w.take(wide_parts * rows * ld * 2);
+        f.pack.parts = wide_parts;
+        f.wide = {f.pack.wide, rows, cols, ld, rows * ld, TT_BF16, wide_parts};
+        f.packs = true;
+    }
+    f.packs = f.packs || want_sums;
+    // Blocks of rows: eight blocks an SM in all, of 32 rows at least.
+    const int64_t across = ceil_div(cols, kPackCols);
+    int64_t down = ceil_div((int64_t)sms * 8, across);
+    if (down > ceil_div(rows, 32)) down = ceil_div(rows, 32);
+    if (down > 65535) down = 65535;
+    f.pack.each = ceil_div(rows, down);
+    if (want_sums) f.pack.sums = (float*)w.take(ceil_div(rows, f.pack.each) * cols * 4);
+    auto vectors = [&](const void* p, int type, int64_t stride) {
+        return ((uintptr_t)p & 15) == 0 && (stride * type_bytes(type) & 15) == 0;
+    };
+    f.pack.vectors = vectors(u.up, u.up_type, u.up_stride) && (u.act == TT_ACT_NONE || vectors(u.pre, u.pre_type, u.pre_stride));
+    return f;
+}
+Forms forms_of(Space& w, const void* p, int64_t stride, int64_t rows, int64_t cols, int type, bool want_narrow, bool want_wide, int sms, int32_t* status)
+{
+    const Upstream u = {p, nullptr, stride, 0, type, TT_F32, TT_ACT_NONE, 0.f};
+    return forms_of(w, u, type != TT_F32, rows, cols, type, want_narrow, !want_wide ? 0 : type == TT_F32 ? 3 : type == TT_F16 ? 2 : 1, false, sms, status);
+}
+int launch_pack(const Forms& f, cudaStream_t s)
+{
+    if (!f.packs) return TT_OK;
+    const int64_t across = ceil_div(f.pack.cols, kPackCols);
+    if (across > INT32_MAX) return TT_ERR_ARG;
+    k_pack<<<dim3((unsigned)across, (unsigned)ceil_div(f.pack.rows, f.pack.each)), kThreads, 0, s>>>(f.pack);
+    return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, cudaStream_t s)
+// Products small enough for the FP32 pipes, a block of which takes about a microsecond for 64 of k
+bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 256 && rows * cols <= 65536; }
+
+Matrix matrix(const void* p, int64_t si, int64_t sk, int type) { return {p, si, sk, type}; }
+
+int enter(tt_emb_dense_t h, cudaStream_t s)
 {
-    if (const int rc = check_backward(h, a)) return rc;
     if (const int rc = ready(h)) return rc;
     h->last_stream = s;
     h->used_stream = true;
+    return TT_OK;
+}
+
+// The call, or with `size` only the workspace that it needs.
+int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_t s)
+{
+    if (size) *size = 0;
+    if (const int rc = check_forward(h, a)) return rc;
+    if (!size)
+        if (const int rc = enter(h, s)) return rc;
+    if (a->n == 0) return TT_OK;
+    const Epilogue e = {a->out, a->residual, a->pre, a->bias, a->out_stride, a->residual_stride, a->pre_stride, -1,
+                        a->out_type, a->residual_type, a->pre_type, a->bias_type, a->activation, a->cap};
+    if (is_small(a->n, h->rows, h->dim)) {
+        if (size) return TT_OK;
+        SmallArgs g = {};
+        g.a = matrix(a->x, a->x_stride, 1, h->table_type);
+        g.b = matrix(h->table, h->dim, 1, h->table_type);
+        g.e = e;
+        g.rows = a->n;
+        g.cols = h->rows;
+        g.deep = h->dim;
+        g.status = h->d_status;
+        return launch_product(g, s);
+    }
+    Space w(size ? nullptr : h->project_ws);
+    const bool wide = h->table_type == TT_F32;
+    const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, h->table_type, !wide, wide, h->num_sms, h->d_status);
+    const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, h->table_type, !wide, wide, h->num_sms, h->d_status);
+    if (size) {
+        *size = w.used;
+        return TT_OK;
+    }
+    if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
+    if (const int rc = launch_pack(x, s)) return rc;
+    if (const int rc = launch_pack(t, s)) return rc;
+    Product p;
+    p.a = wide ? t.wide : t.narrow;
+    p.b = wide ? x.wide : x.narrow;
+    p.rows = a->n;
+    p.cols = h->rows;
+    p.deep = h->dim;
+    p.e = e;
+    return matmul(p, h->d_status, h->num_sms, s);
+}
+
+int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* size, cudaStream_t s)
+{
+    if (size) *size = 0;
+    if (const int rc = check_backward(h, a)) return rc;
+    if (!size)
+        if (const int rc = enter(h, s)) return rc;
     if (a->n == 0) {
-        if (a->accumulate) return TT_OK;
+        if (a->accumulate || size) return TT_OK;
         if (a->table_grad && cudaMemsetAsync(h->grad, 0, (size_t)h->rows * h->dim * type_bytes(h->grad_type), s) != cudaSuccess) return TT_ERR_CUDA;
         if (a->grad_bias && cudaMemsetAsync(a->grad_bias, 0, (size_t)h->rows * type_bytes(a->grad_bias_type), s) != cudaSuccess) return TT_ERR_CUDA;
         return TT_OK;
     }
     const Upstream u = {a->grad_out, a->pre, a->grad_out_stride, a->pre_stride, a->grad_out_type, a->pre_type, a->activation, a->cap};
+    Epilogue ex = {}, et = {};
+    ex.out = a->grad_x;
+    ex.out_stride = a->grad_x_stride;
+    ex.out_type = a->grad_x_type;
+    ex.skip_row = -1;
+    et.out = h->grad;
+    et.out_stride = h->dim;
+    et.out_type = h->grad_type;
+    et.skip_row = h->pad;
+    if (a->accumulate) {
+        et.residual = h->grad;
+        et.residual_stride = h->dim;
+        et.residual_type = h->grad_type;
+    }
+    // Which operands each product takes.  Where grad_out is of the table's 16 bits and is dz itself, as they lie.  Where dz
+    // is computed, a 16-bit result takes it rounded to the table's type: its own rounding is as large.  fp32
+    // results keep fp32's accuracy by terms, and so does what an fp16 table gets from fp32, whose range fp16 has not.
+    const int type = h->table_type;
+    const bool plain = type != TT_F32 && a->grad_out_type == type && a->activation == TT_ACT_NONE;
+    auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || (type == TT_F16 && a->grad_out_type == TT_F32))); };
+    const bool small_x = a->grad_x && is_small(a->n, h->dim, h->rows), small_t = a->table_grad && is_small(h->rows, h->dim, a->n);
+    const bool big_x = a->grad_x && !small_x, big_t = a->table_grad && !small_t;
+    const bool wide_x = big_x && wide_for(a->grad_x_type), wide_t = big_t && wide_for(h->grad_type);
+    Space w(size ? nullptr : h->project_ws);
+    const Forms d = forms_of(w, u, plain, a->n, h->rows, type, (big_x && !wide_x) || (big_t && !wide_t), wide_x || wide_t ? 3 : 0, a->grad_bias != nullptr,
+                             h->num_sms, h->d_status);
+    const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, type, big_x && !wide_x, wide_x, h->num_sms, h->d_status);
+    const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, type, big_t && !wide_t, wide_t, h->num_sms, h->d_status);
+    if (size) {
+        *size = w.used;
+        return TT_OK;
+    }
+    if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
+    for (const Forms* f : {&d, &t, &x})
+        if (const int rc = launch_pack(*f, s)) return rc;
     SmallArgs g = {};
     g.u = u;
     g.status = h->d_status;
-    if (a->grad_x) {
-        g.b = {h->table, 1, h->dim, h->table_type};
-        g.e = {};
-        g.e.out = a->grad_x;
-        g.e.out_stride = a->grad_x_stride;
-        g.e.out_type = a->grad_x_type;
-        g.e.skip_row = -1;
+    if (small_x) {
+        g.b = matrix(h->table, 1, h->dim, type);
+        g.e = ex;
         g.rows = a->n;
         g.cols = h->dim;
         g.deep = h->rows;
-        g.u_t = 0;
         if (const int rc = launch_product(g, s)) return rc;
     }
-    if (a->table_grad) {
-        g.b = {a->x, 1, a->x_stride, h->table_type};
-        g.e = {};
-        g.e.out = h->grad;
-        g.e.out_stride = h->dim;
-        g.e.out_type = h->grad_type;
-        if (a->accumulate) {
-            g.e.residual = h->grad;
-            g.e.residual_stride = h->dim;
-            g.e.residual_type = h->grad_type;
-        }
-        g.e.skip_row = h->pad;
+    if (small_t) {
+        g.b = matrix(a->x, 1, a->x_stride, type);
+        g.e = et;
         g.rows = h->rows;
         g.cols = h->dim;
         g.deep = a->n;
         g.u_t = 1;
         if (const int rc = launch_product(g, s)) return rc;
     }
+    Product p;
+    p.cols = h->dim;
+    p.a_mn = true;
+    if (big_x) {
+        p.a = wide_x ? t.wide : t.narrow;
+        p.b = wide_x ? d.wide : d.narrow;
+        p.rows = a->n;
+        p.deep = h->rows;
+        p.e = ex;
+        if (const int rc = matmul(p, h->d_status, h->num_sms, s)) return rc;
+    }
+    if (big_t) {
+        p.a = wide_t ? x.wide : x.narrow;
+        p.b = wide_t ? d.wide : d.narrow;
+        p.b_mn = true;
+        p.rows = h->rows;
+        p.deep = a->n;
+        p.e = et;
+        if (const int rc = matmul(p, h->d_status, h->num_sms, s)) return rc;
+    }
     if (a->grad_bias) {
-        k_bias_grad<<<(unsigned)ceil_div(h->rows, 32), kThreads, 0, s>>>(u, a->n, h->rows, a->grad_bias, a->grad_bias_type, a->accumulate, h->d_status);
+        k_bias_grad<<<(unsigned)ceil_div(h->rows, kThreads), kThreads, 0, s>>>(d.pack.sums, ceil_div(a->n, d.pack.each), h->rows, a->grad_bias,
+                                                                              a->grad_bias_type, a->accumulate, h->d_status);
         if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
     }
     return TT_OK;
@@ -270,17 +517,13 @@ extern "C" {
 int tt_emb_dense_project_workspace_size(tt_emb_dense_t h, const tt_emb_project* call, size_t* bytes)
 {
     if (!bytes) return note(h, TT_ERR_ARG);
-    if (const int rc = check_forward(h, call)) return note(h, rc);
-    *bytes = 0;
-    return TT_OK;
+    return note(h, project(h, call, bytes, nullptr));
 }
 
 int tt_emb_dense_project_backward_workspace_size(tt_emb_dense_t h, const tt_emb_project_grad* call, size_t* bytes)
 {
     if (!bytes) return note(h, TT_ERR_ARG);
-    if (const int rc = check_backward(h, call)) return note(h, rc);
-    *bytes = 0;
-    return TT_OK;
+    return note(h, project_backward(h, call, bytes, nullptr));
 }
 
 int tt_emb_dense_set_project_workspace(tt_emb_dense_t h, void* workspace, size_t bytes)
@@ -293,12 +536,12 @@ int tt_emb_dense_set_project_workspace(tt_emb_dense_t h, void* workspace, size_t
 
 int tt_emb_dense_project(tt_emb_dense_t h, const tt_emb_project* call, tt_stream_t stream)
 {
-    return note(h, project(h, call, (cudaStream_t)stream));
+    return note(h, project(h, call, nullptr, (cudaStream_t)stream));
 }
 
 int tt_emb_dense_project_backward(tt_emb_dense_t h, const tt_emb_project_grad* call, tt_stream_t stream)
 {
-    return note(h, project_backward(h, call, (cudaStream_t)stream));
+    return note(h, project_backward(h, call, nullptr, (cudaStream_t)stream));
 }
 
 }  // extern "C"
