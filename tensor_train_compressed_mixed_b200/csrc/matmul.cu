@@ -1,13 +1,16 @@
 // C[r][c] = sum over k of A(c, k) B(r, k) on the fifth-generation tensor cores, finished in the same kernel.
 //
 // The columns of the result are the M side of the tensor cores' tile (128 of them, a lane of tensor memory each) and its
-// rows the N side (16 to 256, a column of tensor memory each).  A thread that reads a lane then holds one column of
-// C, and the 32 threads of a warp write 32 neighbouring values of a row at a time whatever its stride or alignment; and few
-// rows (single tokens) make a narrow tile that reads the large operand once and wastes nothing.
+// rows the N side (16 to 256, a column of tensor memory each), so that few rows (single tokens) make a narrow tile that reads the
+// large operand once and wastes nothing.
 //
-// One warp copies tiles of 64 k into a ring of stages (TMA, 128-byte swizzle), one thread issues the products, eight warps read the
-// sums.  The sums of `chunk` steps of k are formed in tensor memory, which cuts the last bits off at each step, and those of
-// all chunks in fp32 registers; two areas of tensor memory take turns, so that products go on meanwhile.
+// One warp copies tiles of 64 k into a ring of stages (TMA, 128-byte swizzle), one thread issues the products, eight warps take the
+// sums from tensor memory through shared memory, 64 rows at a time, where rows lie as they do in the result: a warp
+// then works on whole pieces of 128 values of a row, and reads the residual of the next rows ahead.  Two areas of tensor memory
+// take turns, so that products go on meanwhile.
+// Tensor cores cut the last bits of a sum off at each step.  16-bit results round far above that; for others (kLong) the sums
+// of a few blocks of k at a time are formed in tensor memory and added in fp32 registers, and of operands of several terms the
+// small products come first, so that few steps are made on a large sum.
 // Where there are fewer tiles than SMs a cluster of blocks shares one tile's k, and its partial sums are added through
 // distributed shared memory in the order of the blocks.
 #include <cuda.h>
@@ -32,17 +35,19 @@ struct Args {
     Epilogue e;
     int32_t* status;
     int64_t rows, cols;
-    int32_t its;          // stages of one tile's sum: blocks of k times pairs of terms
+    int32_t blocks;       // of 64 k
     int32_t pairs;
     uint32_t pair_list;   // four bits each: A's term, B's term << 2
-    int32_t chunk;        // stages whose sums stay in tensor memory
+    int32_t chunk;        // blocks of k whose sums stay in tensor memory
     uint32_t idesc;
     int32_t tiles_c, tiles_r;
     int32_t split;        // blocks of a cluster that share a tile
+    int32_t vectors;      // four neighbouring values of a row of the result, residual and pre make one access
 };
 
 __host__ __device__ constexpr int stage_bytes(int bn) { return (kCols + bn) * kDeep * 2; }
 __host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 4 : bn == 128 ? 6 : bn == 64 ? 8 : bn == 32 ? 9 : 10; }
+__host__ __device__ constexpr int passing_of(int bn) { return bn < 64 ? bn : 64; }      // rows on their way through shared memory
 
 // waits that end early where another role of the block has given up, and tell it where this one does
 constexpr int kGone = 1, kTimedOut = 2;
@@ -76,13 +81,17 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float peer_value(uint32_t at, int rank)
+// four of the sums of a row in another block's shared memory, as Lane::sums takes them
+__device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, int lane, float (&x)[4])
 {
     uint32_t there;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(there) : "memory");
-    return v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(row), "r"(rank));
+    if (vectors) {
+        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(there + lane * 16) : "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[i]) : "r"(there + (lane + 32 * i) * 4) : "memory");
+    }
 }
 
 // Descriptor of an operand tile with the 128-byte swizzle.  k along the rows of 128 bytes: groups of eight rows 1024 bytes
@@ -111,74 +120,144 @@ __device__ __forceinline__ void load_columns(uint32_t at, uint32_t* r)
     }
 }
 
-// The epilogue of 8 or 16 rows of a thread's column.  Types and activation are the same for the whole launch, so each is
-// looked at once for all of them.
-template <typename T, int N>
-__device__ __forceinline__ void load_rows(const void* p, int64_t at, int64_t stride, int n, float (&x)[N])
+// Four values of a row as a thread holds them: neighbours where they make one access (two words hold four 16-bit
+// values), else those 32 apart, so that a warp's accesses are of neighbouring places either way.
+struct Four { uint32_t w[4]; };
+__device__ __forceinline__ Four load_four(const void* p, int type, int64_t at, bool vectors, int n)
 {
-    const T* q = (const T*)p + at;
+    Four q = {};
+    if (vectors) {
+        if (type == TT_F32) *(uint4*)&q = *(const uint4*)((const float*)p + at);
+        else *(uint2*)&q = *(const uint2*)((const uint16_t*)p + at);
+    } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = j < n ? to_f32(q[j * stride]) : 0.f;
+        for (int i = 0; i < 4; ++i)
+            if (i < n) q.w[i] = type == TT_F32 ? ((const uint32_t*)p)[at + 32 * i] : ((const uint16_t*)p)[at + 32 * i];
+    }
+    return q;
 }
-template <typename T, int N>
-__device__ __forceinline__ void store_rows(void* p, int64_t at, int64_t stride, int n, const float (&x)[N])
+__device__ __forceinline__ void add_four(const Four& q, int type, bool vectors, float (&x)[4])
 {
-    T* q = (T*)p + at;
 #pragma unroll
-    for (int j = 0; j < N; ++j)
-        if (j < n) q[j * stride] = from_f32<T>(x[j]);
+    for (int i = 0; i < 4; ++i) {
+        if (type == TT_F32) {
+            x[i] += __uint_as_float(q.w[i]);
+            continue;
+        }
+        const uint32_t h = vectors ? q.w[i / 2] >> (16 * (i & 1)) & 0xffffu : q.w[i];
+        x[i] += type == TT_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+    }
 }
-template <int N>
-__device__ __forceinline__ void store_rows(void* p, int type, int64_t at, int64_t stride, int n, const float (&x)[N])
+template <typename T>
+__device__ __forceinline__ void store_four(T* p, bool vectors, int n, const float (&x)[4])
 {
-    if (type == TT_BF16) store_rows<__nv_bfloat16>(p, at, stride, n, x);
-    else if (type == TT_F16) store_rows<__half>(p, at, stride, n, x);
-    else store_rows<float>(p, at, stride, n, x);
+    if (vectors) {
+        store_pack(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n) p[32 * i] = from_f32<T>(x[i]);
+    }
 }
-template <int N>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, int64_t r, int64_t c, int n, float bias, float (&z)[N])
+__device__ __forceinline__ void store_four(void* p, int type, int64_t at, bool vectors, int n, const float (&x)[4])
 {
-    if (e.skip_row >= r && e.skip_row < r + n) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (r + j == e.skip_row) z[j] = 0.f;
-    }
-    float res[N];
-    if (e.residual) {
-        const int64_t at = r * e.residual_stride + c;
-        if (e.residual_type == TT_BF16) load_rows<__nv_bfloat16>(e.residual, at, e.residual_stride, n, res);
-        else if (e.residual_type == TT_F16) load_rows<__half>(e.residual, at, e.residual_stride, n, res);
-        else load_rows<float>(e.residual, at, e.residual_stride, n, res);
-    }
-    if (e.bias) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] += bias;
-    }
-    if (e.pre) store_rows(e.pre, e.pre_type, r * e.pre_stride + c, e.pre_stride, n, z);
-    if (e.act == TT_ACT_RELU) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = activate(TT_ACT_RELU, z[j], 0.f);
-    } else if (e.act == TT_ACT_GELU) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = activate(TT_ACT_GELU, z[j], 0.f);
-    } else if (e.act == TT_ACT_SILU) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = activate(TT_ACT_SILU, z[j], 0.f);
-    } else if (e.act == TT_ACT_SOFTCAP) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] = activate(TT_ACT_SOFTCAP, z[j], e.cap);
-    }
-    if (e.residual) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) z[j] += res[j];
-    }
-    store_rows(e.out, e.out_type, r * e.out_stride + c, e.out_stride, n, z);
+    if (type == TT_BF16) store_four((__nv_bfloat16*)p + at, vectors, n, x);
+    else if (type == TT_F16) store_four((__half*)p + at, vectors, n, x);
+    else store_four((float*)p + at, vectors, n, x);
 }
 
-template <int BN, bool kAmn, bool kBmn>
+// A thread's place in the result's rows: its first column, how many of its four values are in the matrix, the bias of each.
+struct Lane {
+    int64_t c;
+    int n;
+    bool vectors;
+    float bias[4];
+    __device__ __forceinline__ Lane(const Epilogue& e, int64_t c0, int64_t cols, bool v, int lane)
+    {
+        vectors = v;
+        c = c0 + (v ? 4 * lane : lane);
+        n = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t at = c + (v ? i : 32 * i);
+            n += at < cols;
+            bias[i] = at < cols && e.bias ? load_any(e.bias, e.bias_type, at) : 0.f;
+        }
+    }
+    __device__ __forceinline__ void sums(const float* row, int lane, float (&z)[4]) const
+    {
+        if (vectors) {
+            const float4 q = *(const float4*)(row + 4 * lane);
+            z[0] = q.x, z[1] = q.y, z[2] = q.z, z[3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = row[lane + 32 * i];
+        }
+    }
+};
+// the residual of up to R rows
+template <int R>
+__device__ __forceinline__ void fetch_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, Four (&res)[R])
+{
+    if (!e.residual || l.n == 0) return;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (j < rows) res[j] = load_four(e.residual, e.residual_type, (r + j) * e.residual_stride + l.c, l.vectors, l.n);
+}
+// Up to R rows finished from their sums.  Types and activation are the same for the whole launch: each is looked at once
+// for all of them.
+template <int R>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, float (&z)[R][4], const Four (&res)[R])
+{
+    if (e.skip_row >= r && e.skip_row < r + rows) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (r + j == e.skip_row) z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
+    }
+    if (l.n == 0) return;
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[j][i] += l.bias[i];
+    if (e.pre) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (j < rows) store_four(e.pre, e.pre_type, (r + j) * e.pre_stride + l.c, l.vectors, l.n, z[j]);
+    }
+    auto all = [&](auto act) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[j][i] = activate(decltype(act)::value, z[j][i], e.cap);
+    };
+    if (e.act == TT_ACT_RELU) all(std::integral_constant<int, TT_ACT_RELU>());
+    else if (e.act == TT_ACT_GELU) all(std::integral_constant<int, TT_ACT_GELU>());
+    else if (e.act == TT_ACT_SILU) all(std::integral_constant<int, TT_ACT_SILU>());
+    else if (e.act == TT_ACT_SOFTCAP) all(std::integral_constant<int, TT_ACT_SOFTCAP>());
+    if (e.residual) {
+#pragma unroll
+        for (int j = 0; j < R; ++j) add_four(res[j], e.residual_type, l.vectors, z[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+        if (j < rows) store_four(e.out, e.out_type, (r + j) * e.out_stride + l.c, l.vectors, l.n, z[j]);
+}
+
+// barriers of the eight finishing warps; the first tells whether all of them say yes
+__device__ __forceinline__ bool all_agree(bool yes)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)yes) : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+
+template <int BN, bool kAmn, bool kBmn, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ Args g)
 {
     constexpr int kStages = stages_of(BN), kStage = stage_bytes(BN), kHalf = BN / 2;
+    constexpr int kPass = passing_of(BN), kRows = kPass / 8;       // rows at a time of a block and of a finishing warp
     constexpr uint32_t kTmem = 2 * BN < 32 ? 32 : 2 * BN;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
@@ -204,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     tc_fence_after();
     const uint32_t tmem = tmem_at;
     const int split = g.split, rank = (int)blockIdx.x % split;
-    const int first = (int)((int64_t)g.its * rank / split), last = (int)((int64_t)g.its * (rank + 1) / split);
+    const int first = (int)((int64_t)g.blocks * rank / split), last = (int)((int64_t)g.blocks * (rank + 1) / split);
     const int step = (int)gridDim.x / split, tiles = gone ? 0 : g.tiles_c * g.tiles_r;
     const int group_tiles = kGroup * g.tiles_c;
     // a tile's place: groups of kGroup row tiles, in each a column tile for all of the group's rows after another
@@ -215,31 +294,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
         r0 = (group * kGroup + in % here) * BN;
     };
 
+    const int chunk = kLong ? g.chunk : last - first;
     if (warp == 0 && lane == 0) {
         int n = 0;      // stages filled
         bool ok = true;
         for (int tile = blockIdx.x / split; ok && tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
-            for (int it = first; it < last; ++it, ++n) {
-                const int s = n % kStages;
-                if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
-                const int kb = it / g.pairs;
-                const uint32_t pair = g.pair_list >> (4 * (it - kb * g.pairs));
-                const int k = kb * kDeep, pa = pair & 3, pb = (pair >> 2) & 3;
-                const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2;
-                expect(&full[s], kStage);
-                if constexpr (kAmn) {
+            for (int k0 = first; ok && k0 < last; k0 += chunk) {
+                const int end = min(k0 + chunk, last);
+                for (int q = 0; ok && q < g.pairs; ++q) {
+                    const int pa = g.pair_list >> (4 * q) & 3, pb = g.pair_list >> (4 * q + 2) & 3;
+                    for (int kb = k0; kb < end; ++kb, ++n) {
+                        const int s = n % kStages, k = kb * kDeep;
+                        if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
+                        const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2;
+                        expect(&full[s], kStage);
+                        if constexpr (kAmn) {
 #pragma unroll
-                    for (int i = 0; i < kCols / 64; ++i) copy_tile(a + i * 8192, &g.a, c0 + 64 * i, k, pa, &full[s]);
-                } else {
-                    copy_tile(a, &g.a, k, c0, pa, &full[s]);
-                }
-                if constexpr (kBmn) {
+                            for (int i = 0; i < kCols / 64; ++i) copy_tile(a + i * 8192, &g.a, c0 + 64 * i, k, pa, &full[s]);
+                        } else {
+                            copy_tile(a, &g.a, k, c0, pa, &full[s]);
+                        }
+                        if constexpr (kBmn) {
 #pragma unroll
-                    for (int i = 0; i < BN / 64; ++i) copy_tile(b + i * 8192, &g.b, r0 + 64 * i, k, pb, &full[s]);
-                } else {
-                    copy_tile(b, &g.b, k, r0, pb, &full[s]);
+                            for (int i = 0; i < BN / 64; ++i) copy_tile(b + i * 8192, &g.b, r0 + 64 * i, k, pb, &full[s]);
+                        } else {
+                            copy_tile(b, &g.b, k, r0, pb, &full[s]);
+                        }
+                    }
                 }
             }
         }
@@ -249,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
         int n = 0, seq = 0;
         bool ok = true;
         for (int tile = blockIdx.x / split; ok && tile < tiles; tile += step)
-            for (int c = first; ok && c < last; c += g.chunk, ++seq) {
-                const int buf = seq & 1, end = min(c + g.chunk, last);
+            for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
+                const int buf = seq & 1, here = (min(k0 + chunk, last) - k0) * g.pairs;
                 if (seq >= 2 && !wait_for(&sums_empty[buf], (seq / 2 - 1) & 1, &gone)) { ok = false; break; }
                 tc_fence_after();
-                for (int it = c; it < end; ++it, ++n) {
+                for (int i = 0; i < here; ++i, ++n) {
                     const int s = n % kStages;
                     if (!wait_for(&full[s], (n / kStages) & 1, &gone)) { ok = false; break; }
                     tc_fence_after();
@@ -261,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     uint64_t da = swizzled(a, kAmn), db = swizzled(b, kBmn);
 #pragma unroll
                     for (int k = 0; k < kDeep / 16; ++k) {
-                        tc_mma_bf16(tmem + buf * BN, da, db, g.idesc, it > c || k > 0);
+                        tc_mma_bf16(tmem + buf * BN, da, db, g.idesc, i > 0 || k > 0);
                         da += (kAmn ? 2048 : 32) >> 4;
                         db += (kBmn ? 2048 : 32) >> 4;
                     }
@@ -276,55 +359,82 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     } else if (warp >= 2) {
         const int quarter = warp & 3, half = (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        float* const passing = (float*)(raw + (ring - smem_u32(raw)) + kStages * kStage);
+        constexpr int kLoad = kPass / 2;                          // rows that a warp takes from tensor memory at a time
+        const int mine = (warp - 2) * kRows;                      // the first of the passing rows that this warp finishes
         int seq = 0;
-        bool ok = true;
-        for (int tile = blockIdx.x / split; ok && tile < tiles; tile += step) {
+        for (int tile = blockIdx.x / split; tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
-            const int64_t col = c0 + quarter * 32 + lane;
-            const bool mine = col < g.cols;
-            const float bias = mine && g.e.bias ? load_any(g.e.bias, g.e.bias_type, col) : 0.f;
-            float acc[kHalf];
-            for (int c = first; c < last; c += g.chunk, ++seq) {
-                const int buf = seq & 1;
-                if (!wait_for(&sums_full[buf], (seq / 2) & 1, &gone)) { ok = false; break; }
-                tc_fence_after();
-                constexpr int kLoad = kHalf < 32 ? kHalf : kHalf > 64 ? 16 : 32;
+            const Lane l(g.e, c0, g.cols, g.vectors, lane);
+            // passing rows 0 .. kLoad - 1 are the first half's, the others the second's
+            const int64_t row = r0 + mine / kLoad * kHalf + mine % kLoad;
+            Four res[kRows];
+            if (split == 1) fetch_rows(g.e, l, row, (int)max((int64_t)0, min64(kRows, g.rows - row)), res);
+            float acc[kLong ? kHalf : 1];
+            bool ok = true;
+            int buf = 0;
+            if constexpr (kLong) {
+                for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
+                    buf = seq & 1;
+                    ok = wait_for(&sums_full[buf], (seq / 2) & 1, &gone);
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < kHalf; j += kLoad) {
-                    uint32_t x[kLoad];
+                    for (int j = 0; j < kHalf; j += kLoad) {
+                        uint32_t x[kLoad];
+                        load_columns<kLoad>(at + buf * BN + j, x);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                        for (int i = 0; i < kLoad; ++i) acc[j + i] = (k0 == first ? 0.f : acc[j + i]) + __uint_as_float(x[i]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive(&sums_empty[buf]);
+                }
+            } else {
+                buf = seq & 1;
+                ok = wait_for(&sums_full[buf], (seq / 2) & 1, &gone);
+                tc_fence_after();
+                ++seq;
+            }
+            // all eight give up, or none: the barriers below want all
+            if (!all_agree(ok)) break;
+            // of a shared tile all sums go to the ring, which is free: every product that read it has ended
+            float* const to = split > 1 ? (float*)(raw + (ring - smem_u32(raw))) + half * kHalf * kCols : passing + half * kLoad * kCols;
+#pragma unroll 1
+            for (int j = 0; j < kHalf; j += kLoad) {
+                uint32_t x[kLoad];
+                if constexpr (kLong) {
+#pragma unroll
+                    for (int i = 0; i < kLoad; ++i) x[i] = __float_as_uint(acc[i]);
+#pragma unroll
+                    for (int i = 0; i + kLoad < kHalf; ++i) acc[i] = acc[i + kLoad];      // registers have no index
+                } else {
                     load_columns<kLoad>(at + buf * BN + j, x);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    if (c == first) {
-#pragma unroll
-                        for (int i = 0; i < kLoad; ++i) acc[j + i] = __uint_as_float(x[i]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kLoad; ++i) acc[j + i] += __uint_as_float(x[i]);
+                    if (j + kLoad == kHalf) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive(&sums_empty[buf]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) arrive(&sums_empty[buf]);
-            }
-            if (!ok) break;
-            if (split > 1) {        // the ring is free: every product that read it has ended
-                float* part = (float*)(raw + (ring - smem_u32(raw)));
+                if (split > 1) {
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j) part[(half * kHalf + j) * kCols + quarter * 32 + lane] = acc[j];
-                continue;
-            }
-            constexpr int kRows = kHalf < 16 || kHalf > 64 ? 8 : 16;
-#pragma unroll 1
-            for (int j = 0; j < kHalf; j += kRows) {
-                const int64_t r = r0 + half * kHalf + j;
-                if (r >= g.rows) break;
-                float z[kRows];
+                    for (int i = 0; i < kLoad; ++i) to[(j + i) * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
+                    continue;
+                }
+                if (j > 0) finishing_sync();        // the rows before have been read
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) z[i] = acc[i];
-                if (mine) finish_rows(g.e, r, col, (int)min64(kRows, g.rows - r), bias, z);
+                for (int i = 0; i < kLoad; ++i) to[i * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
+                finishing_sync();
+                const int64_t r = row + j;
+                float z[kRows][4];
 #pragma unroll
-                for (int i = 0; i + kRows < kHalf; ++i) acc[i] = acc[i + kRows];      // registers have no index
+                for (int i = 0; i < kRows; ++i) l.sums(passing + (mine + i) * kCols, lane, z[i]);
+                const int rows = (int)max((int64_t)0, min64(kRows, g.rows - r));
+                finish_rows(g.e, l, r, rows, z, res);
+                if (j + kLoad < kHalf) fetch_rows(g.e, l, r + kLoad, (int)max((int64_t)0, min64(kRows, g.rows - r - kLoad)), res);
             }
         }
     }
@@ -332,15 +442,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     if (split > 1) {
         cluster_sync();
         if (warp >= 2 && !gone) {
+            constexpr int kBatch = BN >= 128 ? 4 : 2;
             int c0, r0;
             place(blockIdx.x / split, c0, r0);
+            const Lane l(g.e, c0, g.cols, g.vectors, lane);
             const int each = BN / split;
-            for (int i = threadIdx.x - 64; i < each * kCols; i += kThreads - 64) {
-                const int j = rank * each + i / kCols, c = i % kCols;
-                if (r0 + j >= g.rows || c0 + c >= g.cols) continue;
-                float sum = 0.f;
-                for (int s = 0; s < split; ++s) sum += peer_value(ring + (j * kCols + c) * 4, s);
-                finish(g.e, r0 + j, c0 + c, sum);
+            for (int j = (warp - 2) * kBatch; j < each; j += 8 * kBatch) {
+                const int64_t r = r0 + rank * each + j;
+                const int rows = (int)max((int64_t)0, min64(min(kBatch, each - j), g.rows - r));
+                Four res[kBatch];
+                fetch_rows(g.e, l, r, rows, res);
+                float z[kBatch][4] = {};
+#pragma unroll 2
+                for (int s = 0; s < split; ++s) {
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        float x[4];
+                        const uint32_t from = ring + ((rank * each + j + (i < rows ? i : 0)) * kCols) * 4;
+                        peer_four(from, s, l.vectors, lane, x);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) z[i][q] += x[q];
+                    }
+                }
+                finish_rows(g.e, l, r, rows, z, res);
             }
         }
         cluster_sync();
@@ -380,11 +504,11 @@ bool encode(CUtensorMap* map, const Operand& o, int high)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool kAmn, bool kBmn>
+template <int BN, bool kAmn, bool kBmn, bool kLong>
 cudaError_t launch(Args& g, int sms, cudaStream_t s)
 {
-    constexpr int kBytes = stages_of(BN) * stage_bytes(BN) + 1024;
-    auto* kernel = k_matmul<BN, kAmn, kBmn>;
+    constexpr int kBytes = stages_of(BN) * stage_bytes(BN) + passing_of(BN) * kCols * 4 + 1024;
+    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
@@ -413,46 +537,61 @@ int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s)
     g.status = status;
     g.rows = p.rows;
     g.cols = p.cols;
-    // terms i and j of the operands give a product of 2^-8(i + j) of the first ones: those beyond 2^-16 are below fp32's last bit
-    for (int i = 0; i < p.a.parts; ++i)
-        for (int j = 0; j < p.b.parts && i + j < 3; ++j) g.pair_list |= (uint32_t)(i | j << 2) << (4 * g.pairs++);
-    const int64_t its = ceil_div(p.deep, kDeep) * g.pairs, tiles_c = ceil_div(p.cols, kCols);
+    // Terms i and j of the operands give a product of 2^-8(i + j) of the first ones: those beyond 2^-16 are below fp32's last
+    // bit.  The smallest first.
+    for (int far = 2; far >= 0; --far)
+        for (int i = 0; i <= far; ++i)
+            if (i < p.a.parts && far - i < p.b.parts) g.pair_list |= (uint32_t)(i | (far - i) << 2) << (4 * g.pairs++);
+    const int64_t blocks = ceil_div(p.deep, kDeep), tiles_c = ceil_div(p.cols, kCols), its = blocks * g.pairs;
+    // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
+    // off by up to 2^-23 of it.
+    const bool by_chunks = p.e.out_type == TT_F32 || (p.e.pre && p.e.pre_type == TT_F32) || g.pairs > 1 || blocks > 1024;
+    g.chunk = 4;
     // The tile's height and the blocks that share a tile: what a model of the time likes best.  A stage takes what its
     // products take (half a cycle for each of its rows and 16 k, at 128 columns), or what its bytes take, about 40 a cycle.
     int bn = 0, split = 1;
     double best = 0.0;
-    for (int n = p.b_mn ? 64 : 16; n <= 256; n *= 2) {
+    for (int n = p.b_mn ? 64 : 16; n <= (by_chunks ? 128 : 256); n *= 2) {
         const int64_t tiles = tiles_c * ceil_div(p.rows, n);
         const double stage = std::max(2.0 * n, stage_bytes(n) / 40.0);
         for (int k = 1; k <= kMaxSplit; k *= 2) {
-            if (k > 1 && (tiles * k > sms || its < 4 * k)) break;
+            if (k > 1 && (tiles * k > sms || blocks < 2 * k)) break;
             const double t = (double)ceil_div(tiles * k, sms) * ((double)its / k * stage + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
             if (bn == 0 || t < best) best = t, bn = n, split = k;
         }
     }
     const int64_t tiles_r = ceil_div(p.rows, bn);
-    if (its > INT32_MAX || tiles_c * tiles_r > INT32_MAX / kMaxSplit) return TT_ERR_ARG;   // sizes that no device holds
-    g.its = (int)its;
-    // 64 products of 16 k: their sum in tensor memory is cut off at each, by up to 2^-23 of it
-    g.chunk = 16;
+    if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / kMaxSplit) return TT_ERR_ARG;   // sizes that no device holds
+    g.blocks = (int)blocks;
     g.tiles_c = (int)tiles_c;
     g.tiles_r = (int)tiles_r;
     g.split = split;
+    auto four = [&](const void* q, int type, int64_t stride) {
+        return !q || (((uintptr_t)q & (4 * type_bytes(type) - 1)) == 0 && (stride & 3) == 0);
+    };
+    g.vectors = (p.cols & 3) == 0 && four(p.e.out, p.e.out_type, p.e.out_stride) && four(p.e.pre, p.e.pre_type, p.e.pre_stride) &&
+                four(p.e.residual, p.e.residual_type, p.e.residual_stride);
     g.idesc = (1u << 4) | (p.a.type == TT_BF16 ? 1u << 7 | 1u << 10 : 0u) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u) |
               (uint32_t)(bn >> 3) << 17 | (uint32_t)(kCols >> 4) << 24;
     if (!encode(&g.a, p.a, p.a_mn ? kDeep : kCols) || !encode(&g.b, p.b, p.b_mn ? kDeep : bn)) return TT_ERR_CUDA;
-    auto by_height = [&](auto amn, auto bmn) {
-        constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value;
-        if (bn == 256) return launch<256, A, B>(g, sms, s);
-        if (bn == 128) return launch<128, A, B>(g, sms, s);
-        if constexpr (!B) {
-            if (bn == 16) return launch<16, A, B>(g, sms, s);
-            if (bn == 32) return launch<32, A, B>(g, sms, s);
+    auto by_height = [&](auto amn, auto bmn, auto chunks) {
+        constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value, L = decltype(chunks)::value;
+        if constexpr (!L) {
+            if (bn == 256) return launch<256, A, B, L>(g, sms, s);
         }
-        return launch<64, A, B>(g, sms, s);
+        if (bn == 128) return launch<128, A, B, L>(g, sms, s);
+        if constexpr (!B) {
+            if (bn == 16) return launch<16, A, B, L>(g, sms, s);
+            if (bn == 32) return launch<32, A, B, L>(g, sms, s);
+        }
+        return launch<64, A, B, L>(g, sms, s);
     };
-    const cudaError_t e = p.b_mn ? by_height(std::true_type(), std::true_type())
-                                 : p.a_mn ? by_height(std::true_type(), std::false_type()) : by_height(std::false_type(), std::false_type());
+    auto by_sides = [&](auto chunks) {
+        using Yes = std::true_type;
+        using No = std::false_type;
+        return p.b_mn ? by_height(Yes(), Yes(), chunks) : p.a_mn ? by_height(Yes(), No(), chunks) : by_height(No(), No(), chunks);
+    };
+    const cudaError_t e = by_chunks ? by_sides(std::true_type()) : by_sides(std::false_type());
     return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
