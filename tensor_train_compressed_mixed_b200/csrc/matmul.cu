@@ -4,7 +4,7 @@
 // rows the N side (16 to 256, a column of tensor memory each), so that few rows (single tokens) make a narrow tile that reads the
 // large operand once and wastes nothing.
 //
-// One warp copies tiles of 64 k into a ring of stages (TMA, 128-byte swizzle), one thread issues the products, eight warps take the
+// One warp copies tiles of 64 k into a ring of stages (TMA, 128-byte swizzle), one thread issues the products, sixteen warps take the
 // sums from tensor memory through shared memory, 64 rows at a time, where rows lie as they do in the result: a warp
 // then works on whole pieces of 128 values of a row, and reads the residual of the next rows ahead.  Two areas of tensor memory
 // take turns, so that products go on meanwhile.
@@ -24,7 +24,8 @@ using namespace tt;
 
 namespace {
 
-constexpr int kThreads = 320;        // the copying warp, the issuing warp, eight that finish
+constexpr int kFinish = 16;          // warps that finish
+constexpr int kThreads = 64 + kFinish * 32;
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
 constexpr int kGroup = 16;           // row tiles that are taken in turn before the next column tile: they stay in L2
@@ -106,18 +107,16 @@ __device__ __forceinline__ uint64_t swizzled(uint32_t at, bool mn)
 template <int N>
 __device__ __forceinline__ void load_columns(uint32_t at, uint32_t* r)
 {
-    static_assert(N == 8 || N == 16 || N == 32, "");
-    if constexpr (N == 8)
+    static_assert(N == 4 || N == 8 || N == 16, "");
+    if constexpr (N == 4)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    else if constexpr (N == 8)
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]) : "r"(at) : "memory");
-    else if constexpr (N == 16)
+    else
         asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
                        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(at) : "memory");
-    else {
-        load_columns<16>(at, r);
-        load_columns<16>(at + 16, r + 16);
-    }
 }
 
 // Four values of a row as a thread holds them: neighbours where they make one access (two words hold four 16-bit
@@ -228,7 +227,11 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) z[j][i] = activate(decltype(act)::value, z[j][i], e.cap);
+            for (int i = 0; i < 4; i += 2) {
+                const F2 y = activate(decltype(act)::value, F2{z[j][i], z[j][i + 1]}, e.cap);
+                z[j][i] = y.x;
+                z[j][i + 1] = y.y;
+            }
     };
     if (e.act == TT_ACT_RELU) all(std::integral_constant<int, TT_ACT_RELU>());
     else if (e.act == TT_ACT_GELU) all(std::integral_constant<int, TT_ACT_GELU>());
@@ -243,21 +246,21 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
         if (j < rows) store_four(e.out, e.out_type, (r + j) * e.out_stride + l.c, l.vectors, l.n, z[j]);
 }
 
-// barriers of the eight finishing warps; the first tells whether all of them say yes
+// barriers of the finishing warps; the first tells whether all of them say yes
 __device__ __forceinline__ bool all_agree(bool yes)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 512, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
                  : "=r"(r) : "r"((uint32_t)yes) : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
 
 template <int BN, bool kAmn, bool kBmn, bool kLong>
 __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ Args g)
 {
-    constexpr int kStages = stages_of(BN), kStage = stage_bytes(BN), kHalf = BN / 2;
-    constexpr int kPass = passing_of(BN), kRows = kPass / 8;       // rows at a time of a block and of a finishing warp
+    constexpr int kStages = stages_of(BN), kStage = stage_bytes(BN), kPart = BN / (kFinish / 4);
+    constexpr int kPass = passing_of(BN), kRows = kPass / kFinish;       // rows at a time of a block and of a finishing warp
     constexpr uint32_t kTmem = 2 * BN < 32 ? 32 : 2 * BN;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sums_full[i], 1);
-            mbar_init(&sums_empty[i], 8);
+            mbar_init(&sums_empty[i], kFinish);
         }
         mbar_init(&drained, 1);
         gone = has_error(g.status) ? kGone : 0;
@@ -357,21 +360,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
             mbar_wait(&drained, 0);
         }
     } else if (warp >= 2) {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        const int quarter = warp & 3, part = (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
+        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
         float* const passing = (float*)(raw + (ring - smem_u32(raw)) + kStages * kStage);
-        constexpr int kLoad = kPass / 2;                          // rows that a warp takes from tensor memory at a time
+        constexpr int kLoad = kPass / (kFinish / 4);              // rows that a warp takes from tensor memory at a time
         const int mine = (warp - 2) * kRows;                      // the first of the passing rows that this warp finishes
         int seq = 0;
         for (int tile = blockIdx.x / split; tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
-            // passing rows 0 .. kLoad - 1 are the first half's, the others the second's
-            const int64_t row = r0 + mine / kLoad * kHalf + mine % kLoad;
+            // each part of the tile gives kLoad of the passing rows in turn
+            const int64_t row = r0 + mine / kLoad * kPart + mine % kLoad;
             Four res[kRows];
             if (split == 1) fetch_rows(g.e, l, row, (int)max((int64_t)0, min64(kRows, g.rows - row)), res);
-            float acc[kLong ? kHalf : 1];
+            float acc[kLong ? kPart : 1];
             bool ok = true;
             int buf = 0;
             if constexpr (kLong) {
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < kHalf; j += kLoad) {
+                    for (int j = 0; j < kPart; j += kLoad) {
                         uint32_t x[kLoad];
                         load_columns<kLoad>(at + buf * BN + j, x);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -398,22 +401,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                 tc_fence_after();
                 ++seq;
             }
-            // all eight give up, or none: the barriers below want all
+            // all finishing warps give up, or none: the barriers below want all
             if (!all_agree(ok)) break;
             // of a shared tile all sums go to the ring, which is free: every product that read it has ended
-            float* const to = split > 1 ? (float*)(raw + (ring - smem_u32(raw))) + half * kHalf * kCols : passing + half * kLoad * kCols;
+            float* const to = split > 1 ? (float*)(raw + (ring - smem_u32(raw))) + part * kPart * kCols : passing + part * kLoad * kCols;
 #pragma unroll 1
-            for (int j = 0; j < kHalf; j += kLoad) {
+            for (int j = 0; j < kPart; j += kLoad) {
                 uint32_t x[kLoad];
                 if constexpr (kLong) {
 #pragma unroll
                     for (int i = 0; i < kLoad; ++i) x[i] = __float_as_uint(acc[i]);
 #pragma unroll
-                    for (int i = 0; i + kLoad < kHalf; ++i) acc[i] = acc[i + kLoad];      // registers have no index
+                    for (int i = 0; i + kLoad < kPart; ++i) acc[i] = acc[i + kLoad];      // registers have no index
                 } else {
                     load_columns<kLoad>(at + buf * BN + j, x);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                    if (j + kLoad == kHalf) {
+                    if (j + kLoad == kPart) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) arrive(&sums_empty[buf]);
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                 for (int i = 0; i < kRows; ++i) l.sums(passing + (mine + i) * kCols, lane, z[i]);
                 const int rows = (int)max((int64_t)0, min64(kRows, g.rows - r));
                 finish_rows(g.e, l, r, rows, z, res);
-                if (j + kLoad < kHalf) fetch_rows(g.e, l, r + kLoad, (int)max((int64_t)0, min64(kRows, g.rows - r - kLoad)), res);
+                if (j + kLoad < kPart) fetch_rows(g.e, l, r + kLoad, (int)max((int64_t)0, min64(kRows, g.rows - r - kLoad)), res);
             }
         }
     }
@@ -442,12 +445,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     if (split > 1) {
         cluster_sync();
         if (warp >= 2 && !gone) {
-            constexpr int kBatch = BN >= 128 ? 4 : 2;
+            constexpr int kBatch = BN >= 64 ? 2 : 1;
             int c0, r0;
             place(blockIdx.x / split, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
             const int each = BN / split;
-            for (int j = (warp - 2) * kBatch; j < each; j += 8 * kBatch) {
+            for (int j = (warp - 2) * kBatch; j < each; j += kFinish * kBatch) {
                 const int64_t r = r0 + rank * each + j;
                 const int rows = (int)max((int64_t)0, min64(min(kBatch, each - j), g.rows - r));
                 Four res[kBatch];

@@ -2,8 +2,8 @@
 //
 //   norm = sqrt(sum over all values of g^2),   factor = bound / norm where norm > bound, else 1
 //
-// The sums read every gradient once and memory bounds them.  A thread squares and adds the 16 or 32 values of its
-// four vectors in fp32 and goes on in fp64: squares of values beyond 2^63, or all below 2^-45, leave fp32, and such
+// The sums read every gradient once and memory bounds them.  A thread squares and adds the 32 or 64 values of its
+// eight vectors in fp32 and goes on in fp64: squares of values beyond 2^63, or all below 2^-45, leave fp32, and such
 // a group is squared again in fp64, so that the norm is right over the whole range of the types.  Each block has a
 // place for its sum, and the last block adds them in their order: the same gradients give the same bits.
 #include <algorithm>
@@ -19,8 +19,8 @@ using namespace tt;
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kVectors = 4;                          // of 16 bytes, in flight per thread
-constexpr int kTile = kThreads * kVectors * 2;       // vectors of a tile
+constexpr int kVectors = 8;                          // of 16 bytes, on their way per thread
+constexpr int kTile = kThreads * kVectors;           // vectors of a tile
 constexpr int kFit = 4;                              // blocks of threads on an SM
 
 template <typename T> struct Vec {
@@ -28,35 +28,21 @@ template <typename T> struct Vec {
     T v[n];
 };
 
-// squares of values that fp32 cannot hold, or would lose
-template <typename T, int N>
-__device__ __noinline__ double squares64(const T (&x)[N])
+// The squares of a thread's vectors v0, v0 + kThreads, .. of a tensor in fp64, read once more: of values whose squares fp32
+// cannot hold, or would lose.
+template <typename T>
+__device__ __noinline__ double squares64(const Vec<T>* body, int64_t v0, int64_t vectors)
 {
     double s = 0.0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const double v = (double)to_f32(x[i]);
-        s = fma(v, v, s);
+    for (int k = 0; k < kVectors; ++k) {
+        const int64_t v = v0 + k * kThreads;
+        if (v >= vectors) break;
+        for (int i = 0; i < Vec<T>::n; ++i) {
+            const double x = (double)to_f32(body[v].v[i]);
+            s = fma(x, x, s);
+        }
     }
     return s;
-}
-
-template <typename T, int N>
-__device__ __forceinline__ double squares(const T (&x)[N])
-{
-    float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float v = to_f32(x[i]);
-        a[i & 3] = fmaf(v, v, a[i & 3]);
-    }
-    const float s = (a[0] + a[1]) + (a[2] + a[3]);
-    if constexpr (sizeof(T) == 2 && std::is_same_v<T, __half>) return (double)s;   // all squares fit: 2^-48 to 2^32
-    if (s >= 0x1p-90f && s < 0x1p126f) return (double)s;
-    bool some = false;      // gradients of rows that no token touched are all zero
-#pragma unroll
-    for (int i = 0; i < N; ++i) some |= to_f32(x[i]) != 0.f;
-    return some ? squares64(x) : 0.0;
 }
 
 __device__ __forceinline__ const NormRec& tensor_of(const NormList& L, int64_t tile)
@@ -76,28 +62,34 @@ __device__ __forceinline__ double tile_squares(const NormRec& r, int64_t tile)
     const T* g = (const T*)r.grad;
     const Vec<T>* body = (const Vec<T>*)(g + r.lead);
     const int64_t vectors = (r.size - r.lead) / Vec<T>::n;
-    double sum = 0.0;
+    const int64_t v0 = (tile - r.tile0) * kTile + threadIdx.x;
+    uint4 w[kVectors];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int64_t v0 = (tile - r.tile0) * kTile + half * (kThreads * kVectors) + threadIdx.x;
-        T x[kVectors * Vec<T>::n];
+    for (int k = 0; k < kVectors; ++k) w[k] = v0 + k * kThreads < vectors ? __ldg((const uint4*)(body + v0 + k * kThreads)) : make_uint4(0, 0, 0, 0);
+    F2 a[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
+    bool some = false;          // gradients of rows that no token touched are all zero
 #pragma unroll
-        for (int k = 0; k < kVectors; ++k) {
-            Vec<T> q;
-            const int64_t v = v0 + k * kThreads;
-            if (v < vectors) *(uint4*)&q = __ldg((const uint4*)(body + v));
-            else *(uint4*)&q = make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kVectors; ++k) {
+        Vec<T> q;
+        memcpy(&q, &w[k], 16);
+        some |= ((w[k].x | w[k].y | w[k].z | w[k].w) & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
 #pragma unroll
-            for (int i = 0; i < Vec<T>::n; ++i) x[k * Vec<T>::n + i] = q.v[i];
+        for (int i = 0; i < Vec<T>::n; i += 2) {
+            const F2 v = {to_f32(q.v[i]), to_f32(q.v[i + 1])};
+            a[i / 2 + 2 * k & 3] = fma2(v, v, a[i / 2 + 2 * k & 3]);
         }
-        sum += squares(x);
     }
+    const F2 p = add2(add2(a[0], a[1]), add2(a[2], a[3]));
+    const float s = p.x + p.y;
+    // all squares of fp16 values fit: 2^-48 to 2^32
+    const bool fits = std::is_same_v<T, __half> || (s >= 0x1p-90f && s < 0x1p126f);
+    double sum = fits ? (double)s : some ? squares64(body, v0, vectors) : 0.0;
     if (tile == r.tile0) {      // the single values, at most 14 of them
         const int64_t behind = r.lead + vectors * Vec<T>::n;
         const int64_t at = threadIdx.x < r.lead ? threadIdx.x : behind + threadIdx.x - r.lead;
         if (at < r.size) {
-            const T x[1] = {g[at]};
-            sum += squares64(x);
+            const double x = (double)to_f32(g[at]);
+            sum = fma(x, x, sum);
         }
     }
     return sum;
@@ -160,20 +152,18 @@ __device__ __forceinline__ void tile_scale(const NormRec& r, int64_t tile, float
     T* g = (T*)r.grad;
     Vec<T>* body = (Vec<T>*)(g + r.lead);
     const int64_t vectors = (r.size - r.lead) / Vec<T>::n;
+    const int64_t v0 = (tile - r.tile0) * kTile + threadIdx.x;
+    uint4 w[kVectors];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int64_t v0 = (tile - r.tile0) * kTile + half * (kThreads * kVectors) + threadIdx.x;
-        Vec<T> q[kVectors];
+    for (int k = 0; k < kVectors; ++k) w[k] = v0 + k * kThreads < vectors ? *(const uint4*)(body + v0 + k * kThreads) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int k = 0; k < kVectors; ++k)
-            if (v0 + k * kThreads < vectors) *(uint4*)&q[k] = *(const uint4*)(body + v0 + k * kThreads);
+    for (int k = 0; k < kVectors; ++k) {
+        Vec<T> q;
+        memcpy(&q, &w[k], 16);
 #pragma unroll
-        for (int k = 0; k < kVectors; ++k) {
-            if (v0 + k * kThreads >= vectors) continue;
-#pragma unroll
-            for (int i = 0; i < Vec<T>::n; ++i) q[k].v[i] = from_f32<T>(to_f32(q[k].v[i]) * by);
-            *(uint4*)(body + v0 + k * kThreads) = *(const uint4*)&q[k];
-        }
+        for (int i = 0; i < Vec<T>::n; ++i) q.v[i] = from_f32<T>(to_f32(q.v[i]) * by);
+        memcpy(&w[k], &q, 16);
+        if (v0 + k * kThreads < vectors) *(uint4*)(body + v0 + k * kThreads) = w[k];
     }
     if (tile == r.tile0) {
         const int64_t behind = r.lead + vectors * Vec<T>::n;

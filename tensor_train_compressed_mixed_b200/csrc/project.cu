@@ -23,18 +23,37 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------
 // products on the FP32 pipes: any type, stride and size
 // ---------------------------------------------------------------------------
-constexpr int kSide = 64, kDeep = 16;
+constexpr int kSide = 64, kDeep = 32;
+constexpr int kEach = kSide * kDeep / kThreads;     // values of an operand that a thread brings
 
 struct SmallArgs {
     Matrix a, b;          // A(r, k) and B(c, k)
-    Upstream u;           // where u.up is set, A is its dz (u_t = 0) or the transpose (u_t = 1)
+    Upstream u;           // with u.act, A's values are times the slope at those of u.pre, which lie likewise
     Epilogue e;
+    int64_t pre_si, pre_sk;
     int64_t rows, cols, deep;
-    int32_t u_t;
     const int32_t* status;
 };
 
-// A block computes 64 x 64 values, a thread 4 x 4 of them, 16 steps of k at a time through shared memory.
+template <typename T>
+__device__ __forceinline__ void bring(const void* p, const int64_t (&at)[kEach], float (&x)[kEach])
+{
+    T q[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) q[i] = at[i] >= 0 ? ((const T*)p)[at[i]] : T(0.f);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = to_f32(q[i]);
+}
+// a thread's values of a tile, all on their way before the first is used; zero where the place is none
+__device__ __forceinline__ void bring(const void* p, int type, const int64_t (&at)[kEach], float (&x)[kEach])
+{
+    if (type == TT_BF16) bring<__nv_bfloat16>(p, at, x);
+    else if (type == TT_F16) bring<__half>(p, at, x);
+    else bring<float>(p, at, x);
+}
+
+// A block computes 64 x 64 values, a thread 4 x 4 of them, 32 steps of k at a time through shared memory; the next 32 are
+// on their way meanwhile.
 __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ SmallArgs g)
 {
     if (has_error(g.status)) return;
@@ -44,42 +63,91 @@ __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ Sm
     const int64_t r0 = blockIdx.x / tiles_c * kSide, c0 = blockIdx.x % tiles_c * kSide;
     float acc[4][4] = {};
     // neighbouring threads read neighbouring places: along k, or along r and c where those are the near ones
-    const bool a_k = g.u.up ? !g.u_t : g.a.sk == 1, b_k = g.b.sk == 1;
-    for (int64_t k0 = 0; k0 < g.deep; k0 += kDeep) {
+    const bool a_k = g.a.sk == 1, b_k = g.b.sk == 1;
+    float a[kEach], z[kEach], b[kEach];
+    auto fetch = [&](int64_t k0) {
+        int64_t at[kEach];
 #pragma unroll
-        for (int q = 0; q < kSide * kDeep / kThreads; ++q) {
-            const int at = threadIdx.x + q * kThreads;
-            const int ak = a_k ? at % kDeep : at / kSide, ar = a_k ? at / kDeep : at % kSide;
-            const int bk = b_k ? at % kDeep : at / kSide, bc = b_k ? at / kDeep : at % kSide;
-            float a = 0.f, b = 0.f;
-            if (r0 + ar < g.rows && k0 + ak < g.deep) {
-                if (!g.u.up) a = load_any(g.a.p, g.a.type, (r0 + ar) * g.a.si + (k0 + ak) * g.a.sk);
-                else a = g.u_t ? upstream(g.u, k0 + ak, r0 + ar) : upstream(g.u, r0 + ar, k0 + ak);
+        for (int q = 0; q < kEach; ++q) {
+            const int i = threadIdx.x + q * kThreads;
+            const int64_t k = k0 + (b_k ? i % kDeep : i / kSide), c = c0 + (b_k ? i / kDeep : i % kSide);
+            at[q] = c < g.cols && k < g.deep ? c * g.b.si + k * g.b.sk : -1;
+        }
+        bring(g.b.p, g.b.type, at, b);
+        int64_t pre_at[kEach];
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int i = threadIdx.x + q * kThreads;
+            const int64_t k = k0 + (a_k ? i % kDeep : i / kSide), r = r0 + (a_k ? i / kDeep : i % kSide);
+            const bool in = r < g.rows && k < g.deep;
+            at[q] = in ? r * g.a.si + k * g.a.sk : -1;
+            pre_at[q] = in ? r * g.pre_si + k * g.pre_sk : -1;
+        }
+        bring(g.a.p, g.a.type, at, a);
+        if (g.u.act != TT_ACT_NONE) bring(g.u.pre, g.u.pre_type, pre_at, z);
+    };
+    fetch(0);
+    for (int64_t k0 = 0; k0 < g.deep; k0 += kDeep) {
+        if (g.u.act != TT_ACT_NONE) {
+#pragma unroll
+            for (int q = 0; q < kEach; q += 2) {
+                const F2 d = slope(g.u.act, F2{z[q], z[q + 1]}, g.u.cap);
+                a[q] *= d.x;
+                a[q + 1] *= d.y;
             }
-            if (c0 + bc < g.cols && k0 + bk < g.deep) b = load_any(g.b.p, g.b.type, (c0 + bc) * g.b.si + (k0 + bk) * g.b.sk);
-            As[ak][ar] = a;
-            Bs[bk][bc] = b;
+        }
+#pragma unroll
+        for (int q = 0; q < kEach; ++q) {
+            const int i = threadIdx.x + q * kThreads;
+            As[a_k ? i % kDeep : i / kSide][a_k ? i / kDeep : i % kSide] = a[q];
+            Bs[b_k ? i % kDeep : i / kSide][b_k ? i / kDeep : i % kSide] = b[q];
         }
         __syncthreads();
-#pragma unroll
+        if (k0 + kDeep < g.deep) fetch(k0 + kDeep);
+#pragma unroll 8
         for (int k = 0; k < kDeep; ++k) {
-            float a[4], b[4];
+            float x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[i] = As[k][ty * 4 + i];
+            for (int i = 0; i < 4; ++i) x[i] = As[k][ty * 4 + i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) b[j] = Bs[k][tx + 16 * j];
+            for (int j = 0; j < 4; ++j) y[j] = Bs[k][tx + 16 * j];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
         }
         __syncthreads();
     }
+    const Epilogue& e = g.e;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        const int64_t c = c0 + tx + 16 * j;
+        if (c >= g.cols) break;
+        const int64_t r = r0 + ty * 4;
+        const int rows = (int)min64(4, g.rows - r);
+        const float bias = e.bias ? load_any(e.bias, e.bias_type, c) : 0.f;
+        float y[4], res[4] = {};
+        if (e.residual) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
+                if (i < rows) res[i] = load_any(e.residual, e.residual_type, (r + i) * e.residual_stride + c);
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (r0 + ty * 4 + i < g.rows && c0 + tx + 16 * j < g.cols) finish(g.e, r0 + ty * 4 + i, c0 + tx + 16 * j, acc[i][j]);
+        for (int i = 0; i < 4; ++i) {
+            const float s = j == 0 ? acc[i][0] : j == 1 ? acc[i][1] : j == 2 ? acc[i][2] : acc[i][3];
+            y[i] = (r + i == e.skip_row ? 0.f : s) + bias;
+            if (e.pre && i < rows) store_any(e.pre, e.pre_type, (r + i) * e.pre_stride + c, y[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const F2 v = activate(e.act, F2{y[i], y[i + 1]}, e.cap);
+            y[i] = v.x + res[i];
+            y[i + 1] = v.y + res[i + 1];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < rows) store_any(e.out, e.out_type, (r + i) * e.out_stride + c, y[i]);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -136,32 +204,47 @@ __global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackA
     const int n = (int)min64(8, g.cols - c);
     const int64_t from = (int64_t)blockIdx.y * g.each, to = min64(g.rows, from + g.each);
     const bool whole = g.vectors && n == 8;
+    constexpr int kAhead = 2;        // rows of a warp on their way
     float sum[8] = {};
     if (n > 0)
-        for (int64_t r = from + warp; r < to; r += kThreads / 32) {
-            float x[8];
-            load8(g.u.up, g.u.up_type, r * g.u.up_stride + c, whole, n, x);
-            if (g.u.act != TT_ACT_NONE) {
-                float z[8];
-                load8(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c, whole, n, z);
+        for (int64_t r0 = from + warp; r0 < to; r0 += kAhead * (kThreads / 32)) {
+            float v[kAhead][8], z[kAhead][8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = i < n ? x[i] * slope(g.u.act, z[i], g.u.cap) : 0.f;
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t r = r0 + j * (kThreads / 32);
+                const int m = r < to ? n : 0;
+                load8(g.u.up, g.u.up_type, r * g.u.up_stride + c, whole && m > 0, m, v[j]);
+                if (g.u.act != TT_ACT_NONE) load8(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c, whole && m > 0, m, z[j]);
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += x[i];
-            if (g.narrow) {
-                if (g.narrow_type == TT_F16) store_pack((__half*)g.narrow + r * g.ld + c, x);
-                else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
-            }
-            if (g.wide) {
-                for (int p = 0; p < g.parts; ++p) {
-                    float t[8];
+            for (int j = 0; j < kAhead; ++j) {
+                const int64_t r = r0 + j * (kThreads / 32);
+                if (r >= to) break;
+                float(&x)[8] = v[j];
+                if (g.u.act != TT_ACT_NONE) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        t[i] = term(x[i]);
-                        x[i] = fabsf(x[i]) < INFINITY ? x[i] - t[i] : 0.f;
+                    for (int i = 0; i < 8; i += 2) {
+                        const F2 d = mul2(slope(g.u.act, F2{z[j][i], z[j][i + 1]}, g.u.cap), F2{x[i], x[i + 1]});
+                        x[i] = i < n ? d.x : 0.f;
+                        x[i + 1] = i + 1 < n ? d.y : 0.f;
                     }
-                    store_pack((__nv_bfloat16*)g.wide + ((int64_t)p * g.rows + r) * g.ld + c, t);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[i] += x[i];
+                if (g.narrow) {
+                    if (g.narrow_type == TT_F16) store_pack((__half*)g.narrow + r * g.ld + c, x);
+                    else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
+                }
+                if (g.wide) {
+                    for (int p = 0; p < g.parts; ++p) {
+                        float t[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            t[i] = term(x[i]);
+                            x[i] = fabsf(x[i]) < INFINITY ? x[i] - t[i] : 0.f;
+                        }
+                        store_pack((__nv_bfloat16*)g.wide + ((int64_t)p * g.rows + r) * g.ld + c, t);
+                    }
                 }
             }
         }
@@ -466,6 +549,9 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     g.u = u;
     g.status = h->d_status;
     if (small_x) {
+        g.a = matrix(u.up, u.up_stride, 1, u.up_type);
+        g.pre_si = u.pre_stride;
+        g.pre_sk = 1;
         g.b = matrix(h->table, 1, h->dim, type);
         g.e = ex;
         g.rows = a->n;
@@ -474,12 +560,14 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         if (const int rc = launch_product(g, s)) return rc;
     }
     if (small_t) {
+        g.a = matrix(u.up, 1, u.up_stride, u.up_type);
+        g.pre_si = 1;
+        g.pre_sk = u.pre_stride;
         g.b = matrix(a->x, 1, a->x_stride, type);
         g.e = et;
         g.rows = h->rows;
         g.cols = h->dim;
         g.deep = a->n;
-        g.u_t = 1;
         if (const int rc = launch_product(g, s)) return rc;
     }
     Product p;

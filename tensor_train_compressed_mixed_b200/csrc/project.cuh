@@ -7,65 +7,96 @@ namespace tt {
 
 inline bool activation_known(int a) { return a >= TT_ACT_NONE && a <= TT_ACT_SOFTCAP; }
 
-// Phi(-|z|), the normal distribution function's tail, and e = exp(-z^2 / 2), which gelu's slope needs too.  With x = |z| / sqrt(2),
-// Phi(-|z|) = e erfcx(x) / 2, and erfcx(x) = exp(x^2) erfc(x) falls smoothly from 1 like 1 / x: a polynomial of t = 1 / (1 + 0.4 x)
-// without a constant term, fitted to the least relative error, is within 1.4e-7 of it for all x >= 0.  What z^2 / 2 loses in its
-// rounding is put back, so that the tail is right in relative terms: Phi is off by 5 steps of 2^-23 at most.
-__device__ __forceinline__ float normal_tail(float z, float& e)
+// 2^(hi + lo) for hi <= 0 and a small lo: what the rounding of hi has lost, so that far tails are right in relative terms
+__device__ __forceinline__ F2 exp2_sum(F2 hi, F2 lo)
 {
-    const float w = fminf(fabsf(z), 40.f), h = -0.5f * w, a = h * w;
-    e = expf(a);
-    e = fmaf(e, fmaf(h, w, -a), e);
-    const float t = rcp(fmaf(0.4f * 0.70710678f, fabsf(z), 1.f));
-    float p = 0.050265081f;
-    p = fmaf(p, t, -0.18291025f);
-    p = fmaf(p, t, 0.16909297f);
-    p = fmaf(p, t, -0.0056056734f);
-    p = fmaf(p, t, 0.14142445f);
-    p = fmaf(p, t, 0.16854656f);
-    p = fmaf(p, t, 0.20784137f);
-    p = fmaf(p, t, 0.22566977f);
-    p = fmaf(p, t, 0.22567585f);
-    return 0.5f * e * (p * t);
+    F2 e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(hi.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(hi.y));
+    return fma2(mul2(e, lo), both(0.69314718f), e);
+}
+constexpr float kLog2e = 1.4426950216293335f, kLog2eRest = 1.9259629911266175e-8f;     // their sum is log2(e)
+__device__ __forceinline__ float magnitude_to(float z, float most)     // NaN stays NaN
+{
+    float w;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(w) : "f"(fabsf(z)), "f"(most));
+    return w;
+}
+// e^-w for w >= 0
+__device__ __forceinline__ F2 exp_minus(F2 w)
+{
+    const F2 hi = mul2(w, both(-kLog2e));
+    return exp2_sum(hi, fma2(w, both(-kLog2eRest), fma2(w, both(-kLog2e), {-hi.x, -hi.y})));
 }
 
-// act(z).  A z below -1e30 counts as that where an infinity times 0 would give NaN.
-__device__ __forceinline__ float activate(int act, float z, float cap)
+// Phi(-w), the normal distribution function's tail, and e = exp(-w^2 / 2), for 0 <= w <= 40.  With x = w / sqrt(2),
+// Phi(-w) = e erfcx(x) / 2, and erfcx(x) = exp(x^2) erfc(x) falls smoothly from 1 like 1 / x: a polynomial of t = 1 / (1 + 0.4 x)
+// without a constant term, fitted to the least relative error, is within 1.4e-7 of it for all x >= 0.
+__device__ __forceinline__ F2 normal_tail(F2 w, F2& e)
 {
-    if (act == TT_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (act == TT_ACT_GELU) {
-        float e;
-        const float q = normal_tail(z, e);
-        return (z < -1e30f ? -1e30f : z) * (z > 0.f ? 1.f - q : q);
+    const F2 s = mul2(w, w), s_lost = fma2(w, w, {-s.x, -s.y}), hi = mul2(s, both(-0.5f * kLog2e));
+    F2 lo = fma2(s, both(-0.5f * kLog2e), {-hi.x, -hi.y});
+    lo = fma2(s, both(-0.5f * kLog2eRest), lo);
+    e = exp2_sum(hi, fma2(s_lost, both(-0.5f * kLog2e), lo));
+    const F2 d = fma2(w, both(0.4f * 0.70710678f), both(1.f)), t = {rcp(d.x), rcp(d.y)};
+    F2 p = both(0.050265081f);
+    p = fma2(p, t, both(-0.18291025f));
+    p = fma2(p, t, both(0.16909297f));
+    p = fma2(p, t, both(-0.0056056734f));
+    p = fma2(p, t, both(0.14142445f));
+    p = fma2(p, t, both(0.16854656f));
+    p = fma2(p, t, both(0.20784137f));
+    p = fma2(p, t, both(0.22566977f));
+    p = fma2(p, t, both(0.22567585f));
+    return mul2(mul2(mul2(e, both(0.5f)), t), p);
+}
+
+__device__ __forceinline__ float not_below_zero(float z)     // NaN stays NaN
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(0.f));
+    return r;
+}
+// act(z) of two values; infinities take their limits, and NaN stays NaN
+__device__ __forceinline__ F2 activate(int act, F2 z, float cap)
+{
+    if (act == TT_ACT_RELU) return {not_below_zero(z.x), not_below_zero(z.y)};
+    if (act == TT_ACT_GELU) {       // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+        const F2 w = {magnitude_to(z.x, 40.f), magnitude_to(z.y, 40.f)};
+        F2 e;
+        const F2 q = normal_tail(w, e);
+        return fma2({-w.x, -w.y}, q, {not_below_zero(z.x), not_below_zero(z.y)});
     }
-    if (act == TT_ACT_SILU) {
-        const float e = expf(-fabsf(z));
-        return (z < -1e30f ? -1e30f : z) * ((z < 0.f ? e : 1.f) * rcp(1.f + e));
+    if (act == TT_ACT_SILU) {       // z / (1 + e^-z) = max(z, 0) - |z| e^-|z| / (1 + e^-|z|)
+        const F2 w = {magnitude_to(z.x, 100.f), magnitude_to(z.y, 100.f)}, e = exp_minus(w), d = add2(e, both(1.f));
+        return fma2(mul2({-w.x, -w.y}, e), {rcp(d.x), rcp(d.y)}, {not_below_zero(z.x), not_below_zero(z.y)});
     }
-    if (act == TT_ACT_SOFTCAP) return cap * tanhf(z / cap);
+    if (act == TT_ACT_SOFTCAP) return {cap * tanhf(z.x / cap), cap * tanhf(z.y / cap)};
     return z;
 }
 
-// act'(z), without differences of nearly equal numbers where it is small
-__device__ __forceinline__ float slope(int act, float z, float cap)
+// act'(z) of two values, without differences of nearly equal numbers where it is small
+__device__ __forceinline__ F2 slope(int act, F2 z, float cap)
 {
-    if (act == TT_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
-    if (act == TT_ACT_GELU) {
-        float e;
-        const float q = normal_tail(z, e), c = z > 100.f ? 100.f : z < -100.f ? -100.f : z;
-        return fmaf(c * 0.39894228f, e, z > 0.f ? 1.f - q : q);
+    if (act == TT_ACT_RELU) return {z.x > 0.f ? 1.f : z.x <= 0.f ? 0.f : z.x, z.y > 0.f ? 1.f : z.y <= 0.f ? 0.f : z.y};
+    if (act == TT_ACT_GELU) {       // Phi(z) + z phi(z); of -z it is 1 less that of z
+        const F2 w = {magnitude_to(z.x, 40.f), magnitude_to(z.y, 40.f)};
+        F2 e;
+        const F2 q = normal_tail(w, e), d = fma2(mul2(w, both(-0.39894228f)), e, q);
+        return {z.x > 0.f ? 1.f - d.x : d.x, z.y > 0.f ? 1.f - d.y : d.y};
     }
-    if (act == TT_ACT_SILU) {
-        const float c = z > 1e30f ? 1e30f : z < -1e30f ? -1e30f : z;
-        const float e = expf(-fabsf(c)), by = rcp(1.f + e);
-        const float p = (c < 0.f ? e : 1.f) * by, q = (c < 0.f ? 1.f : e) * by;   // q = 1 - p
-        return p * fmaf(c, q, 1.f);
+    if (act == TT_ACT_SILU) {       // p (1 + z (1 - p)) with p = 1 / (1 + e^-z); likewise
+        const F2 w = {magnitude_to(z.x, 100.f), magnitude_to(z.y, 100.f)}, e = exp_minus(w), d = add2(e, both(1.f));
+        const F2 p = {rcp(d.x), rcp(d.y)}, q = mul2(e, p);
+        const F2 v = mul2(q, fma2({-w.x, -w.y}, p, both(1.f)));
+        return {z.x > 0.f ? 1.f - v.x : v.x, z.y > 0.f ? 1.f - v.y : v.y};
     }
-    if (act == TT_ACT_SOFTCAP) {       // 1 - tanh^2(u) = 4 e^-2u / (1 + e^-2u)^2
-        const float e = expf(-2.f * fabsf(z / cap)), d = rcp(1.f + e);
-        return 4.f * e * d * d;
+    if (act == TT_ACT_SOFTCAP) {    // 1 - tanh^2(u) = 4 e^-2u / (1 + e^-2u)^2
+        const F2 e = exp_minus({magnitude_to(2.f * (z.x / cap), 200.f), magnitude_to(2.f * (z.y / cap), 200.f)}), d = add2(e, both(1.f));
+        const F2 p = {rcp(d.x), rcp(d.y)};
+        return mul2(mul2(mul2(e, both(4.f)), p), p);
     }
-    return 1.f;
+    return both(1.f);
 }
 
 __device__ __forceinline__ float load_any(const void* p, int type, int64_t i)
@@ -95,16 +126,6 @@ struct Epilogue {
     int32_t act;
     float cap;
 };
-__device__ __forceinline__ void finish(const Epilogue& e, int64_t r, int64_t c, float s)
-{
-    float z = r == e.skip_row ? 0.f : s;
-    if (e.bias) z += load_any(e.bias, e.bias_type, c);
-    if (e.pre) store_any(e.pre, e.pre_type, r * e.pre_stride + c, z);
-    float y = activate(e.act, z, e.cap);
-    if (e.residual) y += load_any(e.residual, e.residual_type, r * e.residual_stride + c);
-    store_any(e.out, e.out_type, r * e.out_stride + c, y);
-}
-
 // A matrix in memory: value (i, k) lies at p[i * si + k * sk].
 struct Matrix {
     const void* p;
@@ -120,11 +141,5 @@ struct Upstream {
     int32_t act;
     float cap;
 };
-__device__ __forceinline__ float upstream(const Upstream& u, int64_t r, int64_t c)
-{
-    float d = load_any(u.up, u.up_type, r * u.up_stride + c);
-    if (u.act != TT_ACT_NONE) d *= slope(u.act, load_any(u.pre, u.pre_type, r * u.pre_stride + c), u.cap);
-    return d;
-}
 
 }  // namespace tt
