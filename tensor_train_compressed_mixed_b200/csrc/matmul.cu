@@ -11,9 +11,13 @@
 // Tensor cores cut the last bits of a sum off at each step.  16-bit results round far above that; for others (kLong) the sums
 // of a few blocks of k at a time are formed in tensor memory and added in fp32 registers, and of operands of several terms the
 // small products come first, so that few steps are made on a large sum.
+// Two blocks on neighbouring SMs make a pair where there are many tiles: one tile of 256 columns, of which each block brings its half of
+// both operands and finishes its half, so that a block reads half of B.
 // Where there are fewer tiles than SMs a cluster of blocks shares one tile's k, and its partial sums are added through
 // distributed shared memory in the order of the blocks.
 #include <cuda.h>
+
+#include <math.h>
 
 #include <algorithm>
 
@@ -24,8 +28,6 @@ using namespace tt;
 
 namespace {
 
-constexpr int kFinish = 16;          // warps that finish
-constexpr int kThreads = 64 + kFinish * 32;
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
 constexpr int kGroup = 16;           // row tiles that are taken in turn before the next column tile: they stay in L2
@@ -46,19 +48,29 @@ struct Args {
     int32_t vectors;      // four neighbouring values of a row of the result, residual and pre make one access
 };
 
-__host__ __device__ constexpr int stage_bytes(int bn) { return (kCols + bn) * kDeep * 2; }
-__host__ __device__ constexpr int stages_of(int bn) { return bn == 256 ? 4 : bn == 128 ? 6 : bn == 64 ? 8 : bn == 32 ? 9 : 10; }
-__host__ __device__ constexpr int passing_of(int bn) { return bn < 64 ? bn : 64; }      // rows on their way through shared memory
+// A tile's height bn, and whether a pair of blocks shares a tile: warps that finish, bytes of a stage (the block's own columns of
+// A, its rows of B), stages of the ring, rows on their way through shared memory, blocks on an SM.
+__host__ __device__ constexpr int finish_of(int bn) { return bn <= 32 ? 4 : 16; }
+__host__ __device__ constexpr int threads_of(int bn) { return 64 + 32 * finish_of(bn); }
+__host__ __device__ constexpr int stage_bytes(int bn, bool pair) { return (kCols + (pair ? bn / 2 : bn)) * kDeep * 2; }
+__host__ __device__ constexpr int stages_of(int bn, bool pair) { return bn == 256 ? (pair ? 6 : 4) : bn == 128 ? (pair ? 8 : 6) : bn == 64 ? 8 : 5; }
+__host__ __device__ constexpr int passing_of(int bn) { return bn <= 32 ? 16 : 64; }
+__host__ __device__ constexpr int fit_of(int bn) { return bn <= 32 ? 2 : 1; }
 
 // waits that end early where another role of the block has given up, and tell it where this one does
 constexpr int kGone = 1, kTimedOut = 2;
+template <bool kCluster = false>      // whether other blocks of the cluster arrive there
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gone)
 {
     const uint32_t a = smem_u32(bar);
     for (int it = 0; it < kMbarSpin; ++it) {
         uint32_t done;
-        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-                     : "=r"(done) : "r"(a), "r"(parity) : "memory");
+        if constexpr (kCluster)
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done) : "r"(a), "r"(parity) : "memory");
+        else
+            asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+                         : "=r"(done) : "r"(a), "r"(parity) : "memory");
         if (done) return true;
         if (it >= 64) {
             if (*gone) return false;
@@ -73,10 +85,46 @@ __device__ __forceinline__ void expect(uint64_t* bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void copy_tile(uint32_t to, const CUtensorMap* map, int x, int y, int part, uint64_t* bar)
+// bar: shared-memory address; of a pair's, that of the first block's barrier
+template <bool kPair>
+__device__ __forceinline__ void copy_tile(uint32_t to, const CUtensorMap* map, int x, int y, int part, uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
-                 ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(part), "r"(smem_u32(bar)) : "memory");
+    if constexpr (kPair)
+        asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                     ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(part), "r"(bar) : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                     ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(part), "r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t in_block(uint32_t at, int rank)      // the same place in another block of the cluster
+{
+    uint32_t there;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(rank));
+    return there;
+}
+__device__ __forceinline__ void arrive_at_first(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_block(smem_u32(bar), 0)) : "memory");
+}
+// the pair's products: operands' halves and the accumulators' in both blocks at the same places
+template <bool kPair>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    if constexpr (kPair)
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    else
+        tc_mma_bf16(d, a, b, idesc, accumulate);
+}
+// arrives at the barrier, of a pair's at those of both blocks, when all products issued so far have ended
+template <bool kPair>
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    if constexpr (kPair)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+    else
+        tc_commit(bar);
 }
 __device__ __forceinline__ void cluster_sync()
 {
@@ -85,8 +133,7 @@ __device__ __forceinline__ void cluster_sync()
 // four of the sums of a row in another block's shared memory, as Lane::sums takes them
 __device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, int lane, float (&x)[4])
 {
-    uint32_t there;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(row), "r"(rank));
+    const uint32_t there = in_block(row, rank);
     if (vectors) {
         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(there + lane * 16) : "memory");
     } else {
@@ -246,21 +293,24 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
         if (j < rows) store_four(e.out, e.out_type, (r + j) * e.out_stride + l.c, l.vectors, l.n, z[j]);
 }
 
-// barriers of the finishing warps; the first tells whether all of them say yes
+// barriers of the finishing warps' N threads; the first tells whether all of them say yes
+template <int N>
 __device__ __forceinline__ bool all_agree(bool yes)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, 512, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)yes) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)yes), "n"(N) : "memory");
     return r != 0;
 }
-__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, 512;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory"); }
 
-template <int BN, bool kAmn, bool kBmn, bool kLong>
-__global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ Args g)
+template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
+__global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __grid_constant__ Args g)
 {
-    constexpr int kStages = stages_of(BN), kStage = stage_bytes(BN), kPart = BN / (kFinish / 4);
+    constexpr int kFinish = finish_of(BN), kStages = stages_of(BN, kPair), kStage = stage_bytes(BN, kPair), kPart = BN / (kFinish / 4);
     constexpr int kPass = passing_of(BN), kRows = kPass / kFinish;       // rows at a time of a block and of a finishing warp
+    constexpr int kSide = kPair ? 2 : 1, kOwn = BN / kSide;              // blocks of a pair, rows of B that each brings
     constexpr uint32_t kTmem = 2 * BN < 32 ? 32 : 2 * BN;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
@@ -275,25 +325,40 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sums_full[i], 1);
-            mbar_init(&sums_empty[i], kFinish);
+            mbar_init(&sums_empty[i], kFinish * kSide);
         }
         mbar_init(&drained, 1);
         gone = has_error(g.status) ? kGone : 0;
     }
-    if (warp == 1) tmem_alloc(&tmem_at, kTmem);
+    if (warp == 1) {
+        if constexpr (kPair) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmem) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            tmem_alloc(&tmem_at, kTmem);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_at;
-    const int split = g.split, rank = (int)blockIdx.x % split;
-    const int first = (int)((int64_t)g.blocks * rank / split), last = (int)((int64_t)g.blocks * (rank + 1) / split);
-    const int step = (int)gridDim.x / split, tiles = gone ? 0 : g.tiles_c * g.tiles_r;
+    // blocks that share a tile: a pair halves its columns, others its k
+    const int split = kPair ? 1 : g.split, share = kPair ? 2 : split, rank = (int)blockIdx.x % share;
+    int skip = gone;
+    if constexpr (kPair) {      // either both work or none
+        cluster_sync();
+        uint32_t other;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(in_block(smem_u32((const void*)&gone), rank ^ 1)) : "memory");
+        skip |= (int)other;
+    }
+    const int first = kPair ? 0 : (int)((int64_t)g.blocks * rank / split), last = kPair ? g.blocks : (int)((int64_t)g.blocks * (rank + 1) / split);
+    const int start = blockIdx.x / share, step = (int)gridDim.x / share, tiles = skip ? 0 : g.tiles_c * g.tiles_r;
     const int group_tiles = kGroup * g.tiles_c;
     // a tile's place: groups of kGroup row tiles, in each a column tile for all of the group's rows after another
     auto place = [&](int tile, int& c0, int& r0) {
         const int group = tile / group_tiles, in = tile - group * group_tiles;
         const int here = min(kGroup, g.tiles_r - group * kGroup);
-        c0 = in / here * kCols;
+        c0 = in / here * (kCols * kSide) + (kPair ? rank * kCols : 0);
         r0 = (group * kGroup + in % here) * BN;
     };
 
@@ -301,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     if (warp == 0 && lane == 0) {
         int n = 0;      // stages filled
         bool ok = true;
-        for (int tile = blockIdx.x / split; ok && tile < tiles; tile += step) {
+        for (int tile = start; ok && tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
             for (int k0 = first; ok && k0 < last; k0 += chunk) {
@@ -311,33 +376,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     for (int kb = k0; kb < end; ++kb, ++n) {
                         const int s = n % kStages, k = kb * kDeep;
                         if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
-                        const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2;
-                        expect(&full[s], kStage);
+                        const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2, bar = kPair ? in_block(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
+                        const int rb = r0 + (kPair ? rank * kOwn : 0);
+                        if (!kPair || rank == 0) expect(&full[s], kStage * kSide);
                         if constexpr (kAmn) {
 #pragma unroll
-                            for (int i = 0; i < kCols / 64; ++i) copy_tile(a + i * 8192, &g.a, c0 + 64 * i, k, pa, &full[s]);
+                            for (int i = 0; i < kCols / 64; ++i) copy_tile<kPair>(a + i * 8192, &g.a, c0 + 64 * i, k, pa, bar);
                         } else {
-                            copy_tile(a, &g.a, k, c0, pa, &full[s]);
+                            copy_tile<kPair>(a, &g.a, k, c0, pa, bar);
                         }
                         if constexpr (kBmn) {
 #pragma unroll
-                            for (int i = 0; i < BN / 64; ++i) copy_tile(b + i * 8192, &g.b, r0 + 64 * i, k, pb, &full[s]);
+                            for (int i = 0; i < kOwn / 64; ++i) copy_tile<kPair>(b + i * 8192, &g.b, rb + 64 * i, k, pb, bar);
                         } else {
-                            copy_tile(b, &g.b, k, r0, pb, &full[s]);
+                            copy_tile<kPair>(b, &g.b, k, rb, pb, bar);
                         }
                     }
                 }
             }
         }
-        if (gone == kTimedOut)      // copies on their way land before the block's memory is given up
+        if (gone == kTimedOut && (!kPair || rank == 0))      // copies on their way land before the block's memory is given up
             for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
         int n = 0, seq = 0;
         bool ok = true;
-        for (int tile = blockIdx.x / split; ok && tile < tiles; tile += step)
+        for (int tile = start; ok && tile < tiles; tile += step)
             for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
                 const int buf = seq & 1, here = (min(k0 + chunk, last) - k0) * g.pairs;
-                if (seq >= 2 && !wait_for(&sums_empty[buf], (seq / 2 - 1) & 1, &gone)) { ok = false; break; }
+                if (seq >= 2 && !wait_for<kPair>(&sums_empty[buf], (seq / 2 - 1) & 1, &gone)) { ok = false; break; }
                 tc_fence_after();
                 for (int i = 0; i < here; ++i, ++n) {
                     const int s = n % kStages;
@@ -347,16 +413,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     uint64_t da = swizzled(a, kAmn), db = swizzled(b, kBmn);
 #pragma unroll
                     for (int k = 0; k < kDeep / 16; ++k) {
-                        tc_mma_bf16(tmem + buf * BN, da, db, g.idesc, i > 0 || k > 0);
+                        multiply<kPair>(tmem + buf * BN, da, db, g.idesc, i > 0 || k > 0);
                         da += (kAmn ? 2048 : 32) >> 4;
                         db += (kBmn ? 2048 : 32) >> 4;
                     }
-                    tc_commit(&empty[s]);
+                    commit<kPair>(&empty[s]);
                 }
-                if (ok) tc_commit(&sums_full[buf]);
+                if (ok) commit<kPair>(&sums_full[buf]);
             }
         if (gone == kTimedOut) {    // products on their way end before tensor memory is given up
-            tc_commit(&drained);
+            commit<kPair>(&drained);
             mbar_wait(&drained, 0);
         }
     } else if (warp >= 2) {
@@ -366,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
         constexpr int kLoad = kPass / (kFinish / 4);              // rows that a warp takes from tensor memory at a time
         const int mine = (warp - 2) * kRows;                      // the first of the passing rows that this warp finishes
         int seq = 0;
-        for (int tile = blockIdx.x / split; tile < tiles; tile += step) {
+        for (int tile = start; tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
@@ -393,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive(&sums_empty[buf]);
+                    if (lane == 0) kPair ? arrive_at_first(&sums_empty[buf]) : arrive(&sums_empty[buf]);
                 }
             } else {
                 buf = seq & 1;
@@ -402,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                 ++seq;
             }
             // all finishing warps give up, or none: the barriers below want all
-            if (!all_agree(ok)) break;
+            if (!all_agree<kFinish * 32>(ok)) break;
             // of a shared tile all sums go to the ring, which is free: every product that read it has ended
             float* const to = split > 1 ? (float*)(raw + (ring - smem_u32(raw))) + part * kPart * kCols : passing + part * kLoad * kCols;
 #pragma unroll 1
@@ -419,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     if (j + kLoad == kPart) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) arrive(&sums_empty[buf]);
+                        if (lane == 0) kPair ? arrive_at_first(&sums_empty[buf]) : arrive(&sums_empty[buf]);
                     }
                 }
                 if (split > 1) {
@@ -427,10 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
                     for (int i = 0; i < kLoad; ++i) to[(j + i) * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
                     continue;
                 }
-                if (j > 0) finishing_sync();        // the rows before have been read
+                if (j > 0) finishing_sync<kFinish * 32>();        // the rows before have been read
 #pragma unroll
                 for (int i = 0; i < kLoad; ++i) to[i * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
-                finishing_sync();
+                finishing_sync<kFinish * 32>();
                 const int64_t r = row + j;
                 float z[kRows][4];
 #pragma unroll
@@ -444,10 +510,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     __syncwarp();
     if (split > 1) {
         cluster_sync();
-        if (warp >= 2 && !gone) {
+        if (warp >= 2 && !skip && !gone) {
             constexpr int kBatch = BN >= 64 ? 2 : 1;
             int c0, r0;
-            place(blockIdx.x / split, c0, r0);
+            place(start, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
             const int each = BN / split;
             for (int j = (warp - 2) * kBatch; j < each; j += kFinish * kBatch) {
@@ -474,8 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_matmul(const __grid_constant__ 
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();       // neither block's memory is given up while the other's products may read it
     tc_fence_after();
-    if (warp == 1) tmem_dealloc(tmem, kTmem);
+    if (warp == 1) {
+        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+        else tmem_dealloc(tmem, kTmem);
+    }
     if (threadIdx.x == 0 && gone == kTimedOut) raise_error(g.status, TT_ERR_TIMEOUT, (int)blockIdx.x);
 }
 
@@ -507,21 +577,21 @@ bool encode(CUtensorMap* map, const Operand& o, int high)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool kAmn, bool kBmn, bool kLong>
+template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
 cudaError_t launch(Args& g, int sms, cudaStream_t s)
 {
-    constexpr int kBytes = stages_of(BN) * stage_bytes(BN) + passing_of(BN) * kCols * 4 + 1024;
-    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong>;
+    constexpr int kBytes = stages_of(BN, kPair) * stage_bytes(BN, kPair) + passing_of(BN) * kCols * 4 + 1024;
+    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = g.split;
+    at[0].val.clusterDim.x = kPair ? 2 : g.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     const int64_t tiles = (int64_t)g.tiles_c * g.tiles_r;
-    c.gridDim = dim3((unsigned)(g.split > 1 ? tiles * g.split : min64(tiles, sms)));
-    c.blockDim = dim3(kThreads);
+    c.gridDim = dim3((unsigned)(kPair ? 2 * min64(tiles, sms / 2) : g.split > 1 ? tiles * g.split : min64(tiles, (int64_t)sms * fit_of(BN))));
+    c.blockDim = dim3(threads_of(BN));
     c.dynamicSmemBytes = kBytes;
     c.stream = s;
     c.attrs = at;
@@ -545,25 +615,33 @@ int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s)
     for (int far = 2; far >= 0; --far)
         for (int i = 0; i <= far; ++i)
             if (i < p.a.parts && far - i < p.b.parts) g.pair_list |= (uint32_t)(i | (far - i) << 2) << (4 * g.pairs++);
-    const int64_t blocks = ceil_div(p.deep, kDeep), tiles_c = ceil_div(p.cols, kCols), its = blocks * g.pairs;
+    const int64_t blocks = ceil_div(p.deep, kDeep), its = blocks * g.pairs;
     // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
     // off by up to 2^-23 of it.
     const bool by_chunks = p.e.out_type == TT_F32 || (p.e.pre && p.e.pre_type == TT_F32) || g.pairs > 1 || blocks > 1024;
     g.chunk = 4;
-    // The tile's height and the blocks that share a tile: what a model of the time likes best.  A stage takes what its
-    // products take (half a cycle for each of its rows and 16 k, at 128 columns), or what its bytes take, about 40 a cycle.
+    // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  A stage takes what its
+    // products take (half a cycle for each of its rows and 16 k, at 128 columns), or what its bytes take, about 45 a cycle and SM.
     int bn = 0, split = 1;
+    bool pair = false;
     double best = 0.0;
     for (int n = p.b_mn ? 64 : 16; n <= (by_chunks ? 128 : 256); n *= 2) {
-        const int64_t tiles = tiles_c * ceil_div(p.rows, n);
-        const double stage = std::max(2.0 * n, stage_bytes(n) / 40.0);
+        const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n);
+        const double stage = std::max(2.0 * n, stage_bytes(n, false) / 45.0);
         for (int k = 1; k <= kMaxSplit; k *= 2) {
-            if (k > 1 && (tiles * k > sms || blocks < 2 * k)) break;
-            const double t = (double)ceil_div(tiles * k, sms) * ((double)its / k * stage + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
-            if (bn == 0 || t < best) best = t, bn = n, split = k;
+            if (k > 1 && (tiles * k > sms * fit_of(n) || blocks < 2 * k)) break;
+            // two blocks on an SM share its bandwidth
+            const double turns = fit_of(n) > 1 ? std::max(1.0, tiles * k / sms) : ceil(tiles * k / sms);
+            const double t = turns * ((double)its / k * stage + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
+            if (bn == 0 || t < best) best = t, bn = n, split = k, pair = false;
+        }
+        if (n >= 128) {
+            const double pairs = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
+            const double t = ceil(pairs / (sms / 2)) * ((double)its * std::max(2.0 * n, stage_bytes(n, true) / 45.0) + 8.0 * n) + 2000.0;
+            if (t < best) best = t, bn = n, split = 1, pair = true;
         }
     }
-    const int64_t tiles_r = ceil_div(p.rows, bn);
+    const int64_t tiles_c = ceil_div(p.cols, pair ? 2 * kCols : kCols), tiles_r = ceil_div(p.rows, bn);
     if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / kMaxSplit) return TT_ERR_ARG;   // sizes that no device holds
     g.blocks = (int)blocks;
     g.tiles_c = (int)tiles_c;
@@ -575,19 +653,19 @@ int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s)
     g.vectors = (p.cols & 3) == 0 && four(p.e.out, p.e.out_type, p.e.out_stride) && four(p.e.pre, p.e.pre_type, p.e.pre_stride) &&
                 four(p.e.residual, p.e.residual_type, p.e.residual_stride);
     g.idesc = (1u << 4) | (p.a.type == TT_BF16 ? 1u << 7 | 1u << 10 : 0u) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u) |
-              (uint32_t)(bn >> 3) << 17 | (uint32_t)(kCols >> 4) << 24;
-    if (!encode(&g.a, p.a, p.a_mn ? kDeep : kCols) || !encode(&g.b, p.b, p.b_mn ? kDeep : bn)) return TT_ERR_CUDA;
+              (uint32_t)(bn >> 3) << 17 | (uint32_t)((pair ? 2 * kCols : kCols) >> 4) << 24;
+    if (!encode(&g.a, p.a, p.a_mn ? kDeep : kCols) || !encode(&g.b, p.b, p.b_mn ? kDeep : pair ? bn / 2 : bn)) return TT_ERR_CUDA;
     auto by_height = [&](auto amn, auto bmn, auto chunks) {
         constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value, L = decltype(chunks)::value;
         if constexpr (!L) {
-            if (bn == 256) return launch<256, A, B, L>(g, sms, s);
+            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, sms, s) : launch<256, A, B, L, false>(g, sms, s);
         }
-        if (bn == 128) return launch<128, A, B, L>(g, sms, s);
+        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, sms, s) : launch<128, A, B, L, false>(g, sms, s);
         if constexpr (!B) {
-            if (bn == 16) return launch<16, A, B, L>(g, sms, s);
-            if (bn == 32) return launch<32, A, B, L>(g, sms, s);
+            if (bn == 16) return launch<16, A, B, L, false>(g, sms, s);
+            if (bn == 32) return launch<32, A, B, L, false>(g, sms, s);
         }
-        return launch<64, A, B, L>(g, sms, s);
+        return launch<64, A, B, L, false>(g, sms, s);
     };
     auto by_sides = [&](auto chunks) {
         using Yes = std::true_type;
