@@ -126,6 +126,14 @@ __device__ __forceinline__ void commit(uint64_t* bar)
     else
         tc_commit(bar);
 }
+// One thread of a warp, told so that the compiler knows that what it guards runs in one: it keeps descriptors in the
+// warp's own registers then.
+__device__ __forceinline__ bool elected()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -194,24 +202,6 @@ __device__ __forceinline__ void add_four(const Four& q, int type, bool vectors, 
         x[i] += type == TT_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
     }
 }
-template <typename T>
-__device__ __forceinline__ void store_four(T* p, bool vectors, int n, const float (&x)[4])
-{
-    if (vectors) {
-        store_pack(p, x);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) p[32 * i] = from_f32<T>(x[i]);
-    }
-}
-__device__ __forceinline__ void store_four(void* p, int type, int64_t at, bool vectors, int n, const float (&x)[4])
-{
-    if (type == TT_BF16) store_four((__nv_bfloat16*)p + at, vectors, n, x);
-    else if (type == TT_F16) store_four((__half*)p + at, vectors, n, x);
-    else store_four((float*)p + at, vectors, n, x);
-}
-
 // A thread's place in the result's rows: its first column, how many of its four values are in the matrix, the bias of each.
 struct Lane {
     int64_t c;
@@ -241,18 +231,41 @@ struct Lane {
         }
     }
 };
+template <typename T, int R>
+__device__ __forceinline__ void store_rows(T* p, int64_t stride, const Lane& l, int rows, const float (&z)[R][4])
+{
+    if (l.vectors) {
+#pragma unroll
+        for (int j = 0; j < R; ++j, p += stride)
+            if (j < rows) store_pack(p, z[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < R; ++j, p += stride)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (j < rows && i < l.n) p[32 * i] = from_f32<T>(z[j][i]);
+    }
+}
+template <int R>
+__device__ __forceinline__ void store_rows(void* p, int type, int64_t at, int64_t stride, const Lane& l, int rows, const float (&z)[R][4])
+{
+    if (type == TT_BF16) store_rows((__nv_bfloat16*)p + at, stride, l, rows, z);
+    else if (type == TT_F16) store_rows((__half*)p + at, stride, l, rows, z);
+    else store_rows((float*)p + at, stride, l, rows, z);
+}
 // the residual of up to R rows
 template <int R>
 __device__ __forceinline__ void fetch_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, Four (&res)[R])
 {
     if (!e.residual || l.n == 0) return;
+    int64_t at = r * e.residual_stride + l.c;
 #pragma unroll
-    for (int j = 0; j < R; ++j)
-        if (j < rows) res[j] = load_four(e.residual, e.residual_type, (r + j) * e.residual_stride + l.c, l.vectors, l.n);
+    for (int j = 0; j < R; ++j, at += e.residual_stride)
+        if (j < rows) res[j] = load_four(e.residual, e.residual_type, at, l.vectors, l.n);
 }
 // Up to R rows finished from their sums.  Types and activation are the same for the whole launch: each is looked at once
 // for all of them.
-template <int R>
+template <int R, bool kCoarse>
 __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, float (&z)[R][4], const Four (&res)[R])
 {
     if (e.skip_row >= r && e.skip_row < r + rows) {
@@ -265,17 +278,15 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
     for (int j = 0; j < R; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[j][i] += l.bias[i];
-    if (e.pre) {
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (j < rows) store_four(e.pre, e.pre_type, (r + j) * e.pre_stride + l.c, l.vectors, l.n, z[j]);
-    }
+    if (e.pre) store_rows(e.pre, e.pre_type, r * e.pre_stride + l.c, e.pre_stride, l, rows, z);
     auto all = [&](auto act) {
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {
-                const F2 y = activate(decltype(act)::value, F2{z[j][i], z[j][i + 1]}, e.cap);
+                constexpr int kAct = decltype(act)::value;
+                const F2 x = {z[j][i], z[j][i + 1]};
+                const F2 y = kCoarse ? F2{activate_coarse(kAct, x.x, e.cap), activate_coarse(kAct, x.y, e.cap)} : activate(kAct, x, e.cap);
                 z[j][i] = y.x;
                 z[j][i + 1] = y.y;
             }
@@ -288,9 +299,7 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
 #pragma unroll
         for (int j = 0; j < R; ++j) add_four(res[j], e.residual_type, l.vectors, z[j]);
     }
-#pragma unroll
-    for (int j = 0; j < R; ++j)
-        if (j < rows) store_four(e.out, e.out_type, (r + j) * e.out_stride + l.c, l.vectors, l.n, z[j]);
+    store_rows(e.out, e.out_type, r * e.out_stride + l.c, e.out_stride, l, rows, z);
 }
 
 // barriers of the finishing warps' N threads; the first tells whether all of them say yes
@@ -363,7 +372,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     };
 
     const int chunk = kLong ? g.chunk : last - first;
-    if (warp == 0 && lane == 0) {
+    if (warp == 0 && elected()) {
         int n = 0;      // stages filled
         bool ok = true;
         for (int tile = start; ok && tile < tiles; tile += step) {
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         }
         if (gone == kTimedOut && (!kPair || rank == 0))      // copies on their way land before the block's memory is given up
             for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
-    } else if (warp == 1 && lane == 0 && (!kPair || rank == 0)) {
+    } else if (warp == 1 && (!kPair || rank == 0) && elected()) {
         int n = 0, seq = 0;
         bool ok = true;
         for (int tile = start; ok && tile < tiles; tile += step)
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) l.sums(passing + (mine + i) * kCols, lane, z[i]);
                 const int rows = (int)max((int64_t)0, min64(kRows, g.rows - r));
-                finish_rows(g.e, l, r, rows, z, res);
+                finish_rows<kRows, !kLong>(g.e, l, r, rows, z, res);
                 if (j + kLoad < kPart) fetch_rows(g.e, l, r + kLoad, (int)max((int64_t)0, min64(kRows, g.rows - r - kLoad)), res);
             }
         }
@@ -533,7 +542,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                         for (int q = 0; q < 4; ++q) z[i][q] += x[q];
                     }
                 }
-                finish_rows(g.e, l, r, rows, z, res);
+                finish_rows<kBatch, !kLong>(g.e, l, r, rows, z, res);
             }
         }
         cluster_sync();

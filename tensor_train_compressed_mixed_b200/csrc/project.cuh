@@ -57,6 +57,32 @@ __device__ __forceinline__ float not_below_zero(float z)     // NaN stays NaN
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(0.f));
     return r;
 }
+// act(z) for a result of 16 bits, within 2^-15 of it: gelu's polynomial is within 5.2e-6, and the two roundings of an exponent
+// below 2^7 leave 1.0e-5.
+__device__ __forceinline__ float activate_coarse(int act, float z, float cap)
+{
+    if (act == TT_ACT_GELU) {
+        const float w = fminf(fabsf(z), 13.f), t = rcp(fmaf(0.44f * 0.70710678f, w, 1.f));
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(w * (-0.5f * kLog2e) * w));
+        float p = -0.14610514f;
+        p = fmaf(p, t, 0.35065132f);
+        p = fmaf(p, t, 0.0407319f);
+        p = fmaf(p, t, 0.26358627f);
+        p = fmaf(p, t, 0.24256945f);
+        p = fmaf(p, t, 0.24856104f);
+        return fmaf(-w, 0.5f * e * t * p, not_below_zero(z));
+    }
+    if (act == TT_ACT_SILU) {
+        const float w = fminf(fabsf(z), 100.f);
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(w * -kLog2e));
+        return fmaf(-w * e, rcp(1.f + e), not_below_zero(z));
+    }
+    if (act == TT_ACT_SOFTCAP) return cap * tanhf(z / cap);
+    return act == TT_ACT_RELU ? not_below_zero(z) : z;
+}
+
 // act(z) of two values; infinities take their limits, and NaN stays NaN
 __device__ __forceinline__ F2 activate(int act, F2 z, float cap)
 {
