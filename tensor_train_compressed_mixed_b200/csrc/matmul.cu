@@ -138,16 +138,19 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// four of the sums of a row in another block's shared memory, as Lane::sums takes them
-__device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, int lane, float (&x)[4])
+// a row's sums from another block's shared memory, as row_sums takes them, added to z
+__device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, int lane, F2 (&z)[2])
 {
     const uint32_t there = in_block(row, rank);
+    float x[4];
     if (vectors) {
         asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]) : "r"(there + lane * 16) : "memory");
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[i]) : "r"(there + (lane + 32 * i) * 4) : "memory");
     }
+    z[0] = add2(z[0], {x[0], x[1]});
+    z[1] = add2(z[1], {x[2], x[3]});
 }
 
 // Descriptor of an operand tile with the 128-byte swizzle.  k along the rows of 128 bytes: groups of eight rows 1024 bytes
@@ -174,121 +177,161 @@ __device__ __forceinline__ void load_columns(uint32_t at, uint32_t* r)
                        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]) : "r"(at) : "memory");
 }
 
-// Four values of a row as a thread holds them: neighbours where they make one access (two words hold four 16-bit
+// Four values of a row as a thread holds them: neighbours where they make one access (kVec; two words hold four 16-bit
 // values), else those 32 apart, so that a warp's accesses are of neighbouring places either way.
 struct Four { uint32_t w[4]; };
-__device__ __forceinline__ Four load_four(const void* p, int type, int64_t at, bool vectors, int n)
-{
-    Four q = {};
-    if (vectors) {
-        if (type == TT_F32) *(uint4*)&q = *(const uint4*)((const float*)p + at);
-        else *(uint2*)&q = *(const uint2*)((const uint16_t*)p + at);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < n) q.w[i] = type == TT_F32 ? ((const uint32_t*)p)[at + 32 * i] : ((const uint16_t*)p)[at + 32 * i];
-    }
-    return q;
-}
-__device__ __forceinline__ void add_four(const Four& q, int type, bool vectors, float (&x)[4])
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (type == TT_F32) {
-            x[i] += __uint_as_float(q.w[i]);
-            continue;
-        }
-        const uint32_t h = vectors ? q.w[i / 2] >> (16 * (i & 1)) & 0xffffu : q.w[i];
-        x[i] += type == TT_BF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
-    }
-}
+
 // A thread's place in the result's rows: its first column, how many of its four values are in the matrix, the bias of each.
 struct Lane {
     int64_t c;
     int n;
     bool vectors;
-    float bias[4];
+    F2 bias[2];
     __device__ __forceinline__ Lane(const Epilogue& e, int64_t c0, int64_t cols, bool v, int lane)
     {
         vectors = v;
         c = c0 + (v ? 4 * lane : lane);
         n = 0;
+        float b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int64_t at = c + (v ? i : 32 * i);
             n += at < cols;
-            bias[i] = at < cols && e.bias ? load_any(e.bias, e.bias_type, at) : 0.f;
+            b[i] = at < cols && e.bias ? load_any(e.bias, e.bias_type, at) : 0.f;
         }
-    }
-    __device__ __forceinline__ void sums(const float* row, int lane, float (&z)[4]) const
-    {
-        if (vectors) {
-            const float4 q = *(const float4*)(row + 4 * lane);
-            z[0] = q.x, z[1] = q.y, z[2] = q.z, z[3] = q.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = row[lane + 32 * i];
-        }
+        bias[0] = {b[0], b[1]};
+        bias[1] = {b[2], b[3]};
     }
 };
-template <typename T, int R>
-__device__ __forceinline__ void store_rows(T* p, int64_t stride, const Lane& l, int rows, const float (&z)[R][4])
+// a row's sums from shared memory
+__device__ __forceinline__ void row_sums(const float* row, bool vectors, int lane, F2 (&z)[2])
 {
-    if (l.vectors) {
-#pragma unroll
-        for (int j = 0; j < R; ++j, p += stride)
-            if (j < rows) store_pack(p, z[j]);
+    if (vectors) {
+        const float4 q = *(const float4*)(row + 4 * lane);
+        z[0] = {q.x, q.y};
+        z[1] = {q.z, q.w};
     } else {
-#pragma unroll
-        for (int j = 0; j < R; ++j, p += stride)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (j < rows && i < l.n) p[32 * i] = from_f32<T>(z[j][i]);
+        z[0] = {row[lane], row[lane + 32]};
+        z[1] = {row[lane + 64], row[lane + 96]};
     }
 }
-template <int R>
-__device__ __forceinline__ void store_rows(void* p, int type, int64_t at, int64_t stride, const Lane& l, int rows, const float (&z)[R][4])
+template <typename T>
+__device__ __forceinline__ uint32_t packed(F2 x)      // two 16-bit values
 {
-    if (type == TT_BF16) store_rows((__nv_bfloat16*)p + at, stride, l, rows, z);
-    else if (type == TT_F16) store_rows((__half*)p + at, stride, l, rows, z);
-    else store_rows((float*)p + at, stride, l, rows, z);
+    uint32_t r;
+    if constexpr (std::is_same_v<T, __half>) {
+        const __half2 h = __floats2half2_rn(x.x, x.y);
+        memcpy(&r, &h, 4);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+        memcpy(&r, &h, 4);
+    }
+    return r;
 }
-// the residual of up to R rows
+template <typename T>
+__device__ __forceinline__ F2 unpacked(uint32_t w)
+{
+    if constexpr (std::is_same_v<T, __half>) {
+        __half2 h;
+        memcpy(&h, &w, 4);
+        const float2 f = __half22float2(h);
+        return {f.x, f.y};
+    }
+    return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+}
+template <typename T, bool kVec, int R>
+__device__ __forceinline__ void store_rows(T* p, int64_t stride, int n, int rows, const F2 (&z)[R][2])
+{
+#pragma unroll
+    for (int j = 0; j < R; ++j, p += stride) {
+        if (j >= rows) break;
+        if constexpr (!kVec) {
+            const float x[4] = {z[j][0].x, z[j][0].y, z[j][1].x, z[j][1].y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) p[32 * i] = from_f32<T>(x[i]);
+        } else if constexpr (sizeof(T) == 4) {
+            *(float4*)p = make_float4(z[j][0].x, z[j][0].y, z[j][1].x, z[j][1].y);
+        } else {
+            *(uint2*)p = make_uint2(packed<T>(z[j][0]), packed<T>(z[j][1]));
+        }
+    }
+}
+template <bool kVec, int R>
+__device__ __forceinline__ void store_rows(void* p, int type, int64_t at, int64_t stride, int n, int rows, const F2 (&z)[R][2])
+{
+    if (type == TT_BF16) store_rows<__nv_bfloat16, kVec>((__nv_bfloat16*)p + at, stride, n, rows, z);
+    else if (type == TT_F16) store_rows<__half, kVec>((__half*)p + at, stride, n, rows, z);
+    else store_rows<float, kVec>((float*)p + at, stride, n, rows, z);
+}
+// the residual of up to R rows, and what it adds
+template <typename T, bool kVec, int R>
+__device__ __forceinline__ void fetch_rows(const T* p, int64_t stride, int n, int rows, Four (&res)[R])
+{
+#pragma unroll
+    for (int j = 0; j < R; ++j, p += stride) {
+        if (j >= rows) break;
+        if constexpr (!kVec) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < n) res[j].w[i] = p[32 * i];
+        } else if constexpr (sizeof(T) == 4) {
+            const uint4 q = *(const uint4*)p;
+            res[j] = {{q.x, q.y, q.z, q.w}};
+        } else {
+            const uint2 q = *(const uint2*)p;
+            res[j].w[0] = q.x;
+            res[j].w[1] = q.y;
+        }
+    }
+}
 template <int R>
 __device__ __forceinline__ void fetch_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, Four (&res)[R])
 {
     if (!e.residual || l.n == 0) return;
-    int64_t at = r * e.residual_stride + l.c;
+    const int64_t at = r * e.residual_stride + l.c;
+    if (e.residual_type == TT_F32) {
+        const uint32_t* p = (const uint32_t*)e.residual + at;
+        l.vectors ? fetch_rows<uint32_t, true>(p, e.residual_stride, l.n, rows, res) : fetch_rows<uint32_t, false>(p, e.residual_stride, l.n, rows, res);
+    } else {
+        const uint16_t* p = (const uint16_t*)e.residual + at;
+        l.vectors ? fetch_rows<uint16_t, true>(p, e.residual_stride, l.n, rows, res) : fetch_rows<uint16_t, false>(p, e.residual_stride, l.n, rows, res);
+    }
+}
+template <typename T, bool kVec, int R>
+__device__ __forceinline__ void add_rows(const Four (&res)[R], F2 (&z)[R][2])
+{
 #pragma unroll
-    for (int j = 0; j < R; ++j, at += e.residual_stride)
-        if (j < rows) res[j] = load_four(e.residual, e.residual_type, at, l.vectors, l.n);
+    for (int j = 0; j < R; ++j) {
+        const uint32_t(&w)[4] = res[j].w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            F2 x;
+            if constexpr (sizeof(T) == 4) x = {__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])};
+            else if constexpr (kVec) x = unpacked<T>(w[i]);
+            else x = unpacked<T>(__byte_perm(w[2 * i], w[2 * i + 1], 0x5410));
+            z[j][i] = add2(z[j][i], x);
+        }
+    }
 }
 // Up to R rows finished from their sums.  Types and activation are the same for the whole launch: each is looked at once
 // for all of them.
-template <int R, bool kCoarse>
-__device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, int64_t r, int rows, float (&z)[R][4], const Four (&res)[R])
+template <int R, bool kCoarse, bool kVec>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, int r, int rows, F2 (&z)[R][2], const Four (&res)[R])
 {
-    if (e.skip_row >= r && e.skip_row < r + rows) {
-#pragma unroll
-        for (int j = 0; j < R; ++j)
-            if (r + j == e.skip_row) z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
-    }
-    if (l.n == 0) return;
 #pragma unroll
     for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[j][i] += l.bias[i];
-    if (e.pre) store_rows(e.pre, e.pre_type, r * e.pre_stride + l.c, e.pre_stride, l, rows, z);
+        for (int i = 0; i < 2; ++i) z[j][i] = add2(z[j][i], l.bias[i]);
+    if (e.pre) store_rows<kVec>(e.pre, e.pre_type, r * e.pre_stride + l.c, e.pre_stride, l.n, rows, z);
     auto all = [&](auto act) {
+        constexpr int kAct = decltype(act)::value;
 #pragma unroll
         for (int j = 0; j < R; ++j)
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                constexpr int kAct = decltype(act)::value;
-                const F2 x = {z[j][i], z[j][i + 1]};
-                const F2 y = kCoarse ? F2{activate_coarse(kAct, x.x, e.cap), activate_coarse(kAct, x.y, e.cap)} : activate(kAct, x, e.cap);
-                z[j][i] = y.x;
-                z[j][i + 1] = y.y;
+            for (int i = 0; i < 2; ++i) {
+                if constexpr (kCoarse) z[j][i] = {activate_coarse(kAct, z[j][i].x, e.cap), activate_coarse(kAct, z[j][i].y, e.cap)};
+                else z[j][i] = activate(kAct, z[j][i], e.cap);
             }
     };
     if (e.act == TT_ACT_RELU) all(std::integral_constant<int, TT_ACT_RELU>());
@@ -296,23 +339,49 @@ __device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, in
     else if (e.act == TT_ACT_SILU) all(std::integral_constant<int, TT_ACT_SILU>());
     else if (e.act == TT_ACT_SOFTCAP) all(std::integral_constant<int, TT_ACT_SOFTCAP>());
     if (e.residual) {
-#pragma unroll
-        for (int j = 0; j < R; ++j) add_four(res[j], e.residual_type, l.vectors, z[j]);
+        if (e.residual_type == TT_BF16) add_rows<__nv_bfloat16, kVec>(res, z);
+        else if (e.residual_type == TT_F16) add_rows<__half, kVec>(res, z);
+        else add_rows<float, kVec>(res, z);
     }
-    store_rows(e.out, e.out_type, r * e.out_stride + l.c, e.out_stride, l, rows, z);
+    store_rows<kVec>(e.out, e.out_type, r * e.out_stride + l.c, e.out_stride, l.n, rows, z);
+}
+template <int R, bool kCoarse>
+__device__ __forceinline__ void finish_rows(const Epilogue& e, const Lane& l, int r, int rows, F2 (&z)[R][2], const Four (&res)[R])
+{
+    const int skip = (int)e.skip_row - r;        // (rows are below 2^31)
+    if (skip >= 0 && skip < rows) {
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (j == skip) z[j][0] = z[j][1] = both(0.f);
+    }
+    if (l.n == 0) return;
+    if (l.vectors) finish_rows<R, kCoarse, true>(e, l, r, rows, z, res);
+    else finish_rows<R, kCoarse, false>(e, l, r, rows, z, res);
 }
 
-// barriers of the finishing warps' N threads; the first tells whether all of them say yes
-template <int N>
-__device__ __forceinline__ bool all_agree(bool yes)
+// Barriers of the four warps that finish the same part of a tile; the first tells whether all of them say yes.
+__device__ __forceinline__ bool all_agree(int part, bool yes)
 {
     uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                 : "=r"(r) : "r"((uint32_t)yes), "n"(N) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, %2, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"((uint32_t)yes), "r"(1 + part) : "memory");
     return r != 0;
 }
-template <int N>
-__device__ __forceinline__ void finishing_sync() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void part_sync(int part) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + part) : "memory"); }
+
+// asks for the residual of a tile that comes later: what its rows wait for is then in L2
+template <int BN, int kAll, typename Place>
+__device__ __forceinline__ void prefetch_residual(const Args& g, const Place& place, int tile)
+{
+    if (!g.e.residual) return;
+    int c0, r0;
+    place(tile, c0, r0);
+    const int size = g.e.residual_type == TT_F32 ? 4 : 2, lines = size;       // of 128 bytes, in a row of the tile
+    for (int i = threadIdx.x - 64; i < BN * lines; i += kAll) {
+        const int64_t r = r0 + i / lines, c = c0 + i % lines * (128 / size);
+        if (r < g.rows && c < g.cols) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)g.e.residual + (r * g.e.residual_stride + c) * size));
+    }
+}
 
 template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
 __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __grid_constant__ Args g)
@@ -435,20 +504,24 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             mbar_wait(&drained, 0);
         }
     } else if (warp >= 2) {
-        const int quarter = warp & 3, part = (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
+        const int quarter = warp & 3, part = kFinish == 4 ? 0 : (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
         const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
         float* const passing = (float*)(raw + (ring - smem_u32(raw)) + kStages * kStage);
         constexpr int kLoad = kPass / (kFinish / 4);              // rows that a warp takes from tensor memory at a time
         const int mine = (warp - 2) * kRows;                      // the first of the passing rows that this warp finishes
+        const int height = (int)g.rows;
         int seq = 0;
         for (int tile = start; tile < tiles; tile += step) {
             int c0, r0;
             place(tile, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
             // each part of the tile gives kLoad of the passing rows in turn
-            const int64_t row = r0 + mine / kLoad * kPart + mine % kLoad;
+            const int row = r0 + mine / kLoad * kPart + mine % kLoad;
             Four res[kRows];
-            if (split == 1) fetch_rows(g.e, l, row, (int)max((int64_t)0, min64(kRows, g.rows - row)), res);
+            if (split == 1) {
+                fetch_rows(g.e, l, row, min(kRows, height - row), res);
+                if (tile + step < tiles) prefetch_residual<BN, kFinish * 32>(g, place, tile + step);
+            }
             float acc[kLong ? kPart : 1];
             bool ok = true;
             int buf = 0;
@@ -476,8 +549,8 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                 tc_fence_after();
                 ++seq;
             }
-            // all finishing warps give up, or none: the barriers below want all
-            if (!all_agree<kFinish * 32>(ok)) break;
+            // all four warps give up, or none: the barriers below want all
+            if (!all_agree(part, ok)) break;
             // of a shared tile all sums go to the ring, which is free: every product that read it has ended
             float* const to = split > 1 ? (float*)(raw + (ring - smem_u32(raw))) + part * kPart * kCols : passing + part * kLoad * kCols;
 #pragma unroll 1
@@ -502,17 +575,16 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                     for (int i = 0; i < kLoad; ++i) to[(j + i) * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
                     continue;
                 }
-                if (j > 0) finishing_sync<kFinish * 32>();        // the rows before have been read
+                if (j > 0) part_sync(part);        // the rows before have been read
 #pragma unroll
                 for (int i = 0; i < kLoad; ++i) to[i * kCols + quarter * 32 + lane] = __uint_as_float(x[i]);
-                finishing_sync<kFinish * 32>();
-                const int64_t r = row + j;
-                float z[kRows][4];
+                part_sync(part);
+                const int r = row + j, rows = min(kRows, height - r);
+                F2 z[kRows][2];
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) l.sums(passing + (mine + i) * kCols, lane, z[i]);
-                const int rows = (int)max((int64_t)0, min64(kRows, g.rows - r));
+                for (int i = 0; i < kRows; ++i) row_sums(passing + (mine + i) * kCols, l.vectors, lane, z[i]);
                 finish_rows<kRows, !kLong>(g.e, l, r, rows, z, res);
-                if (j + kLoad < kPart) fetch_rows(g.e, l, r + kLoad, (int)max((int64_t)0, min64(kRows, g.rows - r - kLoad)), res);
+                if (j + kLoad < kPart) fetch_rows(g.e, l, r + kLoad, min(kRows, height - r - kLoad), res);
             }
         }
     }
@@ -526,20 +598,15 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
             const int each = BN / split;
             for (int j = (warp - 2) * kBatch; j < each; j += kFinish * kBatch) {
-                const int64_t r = r0 + rank * each + j;
-                const int rows = (int)max((int64_t)0, min64(min(kBatch, each - j), g.rows - r));
+                const int r = r0 + rank * each + j, rows = max(0, min(min(kBatch, each - j), (int)g.rows - r));
                 Four res[kBatch];
                 fetch_rows(g.e, l, r, rows, res);
-                float z[kBatch][4] = {};
+                F2 z[kBatch][2] = {};
 #pragma unroll 2
                 for (int s = 0; s < split; ++s) {
 #pragma unroll
                     for (int i = 0; i < kBatch; ++i) {
-                        float x[4];
-                        const uint32_t from = ring + ((rank * each + j + (i < rows ? i : 0)) * kCols) * 4;
-                        peer_four(from, s, l.vectors, lane, x);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) z[i][q] += x[q];
+                        peer_four(ring + ((rank * each + j + (i < rows ? i : 0)) * kCols) * 4, s, l.vectors, lane, z[i]);
                     }
                 }
                 finish_rows<kBatch, !kLong>(g.e, l, r, rows, z, res);
