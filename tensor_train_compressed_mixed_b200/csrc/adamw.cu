@@ -409,7 +409,10 @@ template <typename P, typename G, bool kClip>
 __global__ void __launch_bounds__(kWarps * 32, 2) k_adamw32(const __grid_constant__ List L, float lr,
                                                           const float* __restrict__ lr_device, const NormResult* res)
 {
-    if (kClip && !res->finite) return;
+    if constexpr (kClip) {
+        wait_for_kernel_before();
+        if (!res->finite) return;
+    }
     using R = Raw<P, G, false>;
     const int lane = threadIdx.x & 31;
     const int64_t t = *L.steps + 1;
@@ -472,7 +475,10 @@ template <typename P, typename G, bool kClip>
 __global__ void __launch_bounds__(kWarps * 32, kFit8) k_adamw8(const __grid_constant__ List L, float lr,
                                                           const float* __restrict__ lr_device, const NormResult* res)
 {
-    if (kClip && !res->finite) return;
+    if constexpr (kClip) {
+        wait_for_kernel_before();
+        if (!res->finite) return;
+    }
     using R = Raw<P, G, true>;
     __shared__ Stage<P, G> st[kStages];
     const int lane = threadIdx.x & 31, me = threadIdx.x;
@@ -556,10 +562,13 @@ cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* 
     // more of them spread the card's reads: 309 us for the rank-64 cores with three, 285 with two.
     int64_t grid = min64(L.tiles, (int64_t)sms * (k8 ? kFit8 : 2));
     if (grid < 1) grid = 1;
-    auto go = [&](auto kernel) { kernel<<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device, res); };
-    if (k8) go(res ? k_adamw8<P, G, true> : k_adamw8<P, G, false>);
-    else go(res ? k_adamw32<P, G, true> : k_adamw32<P, G, false>);
-    return cudaGetLastError();
+    auto go = [&](auto kernel) {
+        if (res) return launch_early(kernel, (unsigned)grid, kWarps * 32, s, L, lr, lr_device, res);
+        kernel<<<(unsigned)grid, kWarps * 32, 0, s>>>(L, lr, lr_device, res);
+        return cudaGetLastError();
+    };
+    if (k8) return go(res ? k_adamw8<P, G, true> : k_adamw8<P, G, false>);
+    return go(res ? k_adamw32<P, G, true> : k_adamw32<P, G, false>);
 }
 
 }  // namespace

@@ -92,11 +92,6 @@ __global__ void __launch_bounds__(kThreads) k_lookup(LookupArgs a, const T* __re
     if (bad && lane < cnt) raise_error(a.status, TT_ERR_INDEX_RANGE, (int)min64(i0 + lane, INT32_MAX));
 }
 
-// The gradient's kernels are launched with leave to start while the one before still runs: each
-// waits here until that one has ended and its writes can be read, which hides the launch.
-__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------------------
 // Sorted tokens: keys ascending, each with its input position, equal keys in input order.  A key is
 // the token, or `rows` (behind every row) for one that gets no gradient.  `touched`, where wanted, has
@@ -945,22 +940,6 @@ cudaError_t sort_tokens(tt_emb_dense_t h, const TokenArgs& a, const DenseLayout&
     return radix_sort_pairs(false, a.n, bits, sb, which, h->d_status, s, &nl);
 }
 
-// a launch that may start while the kernel before it still runs (see wait_for_kernel_before)
-template <typename... Params, typename... Args>
-cudaError_t launch_early(void (*kernel)(Params...), unsigned grid, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    c.gridDim = dim3(grid);
-    c.blockDim = dim3(kThreads);
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, kernel, args...);
-}
-
 int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t n, const void* up, int32_t up_type,
              int64_t up_stride, int32_t accumulate, cudaStream_t s)
 {
@@ -1036,7 +1015,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
         using W = decltype(w);
         by_type(up_type, [&](auto g) {
             using G = decltype(g);
-            auto go = [&](auto kernel) { e = launch_early(kernel, grid, s, a, (const G*)up, up_stride, (W*)h->grad); };
+            auto go = [&](auto kernel) { e = launch_early(kernel, grid, kThreads, s, a, (const G*)up, up_stride, (W*)h->grad); };
             constexpr int kWide = sizeof(W) == 4 && sizeof(G) == 4 ? 4 : 8;
             const bool few = a.tiles * a.slabs <= (int64_t)h->num_sms * 16;
             auto pick = [&](auto v) {
@@ -1049,7 +1028,7 @@ int backward(tt_emb_dense_t h, const void* tokens, int32_t token_bytes, int64_t 
             else pick(std::integral_constant<int, 1>());
         });
         if (e != cudaSuccess) return;
-        auto go = [&](auto kernel) { e = launch_early(kernel, grid2, s, a, joins, (W*)h->grad); };
+        auto go = [&](auto kernel) { e = launch_early(kernel, grid2, kThreads, s, a, joins, (W*)h->grad); };
         if (V == 1) go(k_token_join<W, 1>);
         else if (V == 2) go(k_token_join<W, 2>);
         else if (V == 8) go(k_token_join<W, 8>);

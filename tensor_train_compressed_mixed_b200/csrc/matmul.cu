@@ -20,6 +20,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "matmul.cuh"
 #include "tcgen05.cuh"
@@ -406,8 +407,10 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             mbar_init(&sums_empty[i], kFinish * kSide);
         }
         mbar_init(&drained, 1);
-        gone = has_error(g.status) ? kGone : 0;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&g.a) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&g.b) : "memory");
     }
+    let_next_kernel_start();
     if (warp == 1) {
         if constexpr (kPair) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmem) : "memory");
@@ -416,6 +419,8 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             tmem_alloc(&tmem_at, kTmem);
         }
     }
+    wait_for_kernel_before();
+    if (threadIdx.x == 0) gone = has_error(g.status) ? kGone : 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -654,14 +659,22 @@ bool encode(CUtensorMap* map, const Operand& o, int high)
 }
 
 template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
-cudaError_t launch(Args& g, int sms, cudaStream_t s)
+cudaError_t launch(Args& g, int sms, bool early, cudaStream_t s)
 {
     constexpr int kBytes = stages_of(BN, kPair) * stage_bytes(BN, kPair) + passing_of(BN) * kCols * 4 + 1024;
     auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+    static std::atomic<uint64_t> told{0};      // devices on which the kernel has leave for its shared memory
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e == cudaSuccess && (device >= 64 || !(told.load(std::memory_order_relaxed) >> device & 1))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        if (e == cudaSuccess && device < 64) told.fetch_or((uint64_t)1 << device, std::memory_order_relaxed);
+    }
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = kPair ? 2 : g.split;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
@@ -671,7 +684,7 @@ cudaError_t launch(Args& g, int sms, cudaStream_t s)
     c.dynamicSmemBytes = kBytes;
     c.stream = s;
     c.attrs = at;
-    c.numAttrs = 1;
+    c.numAttrs = early ? 2 : 1;
     return cudaLaunchKernelEx(&c, kernel, g);
 }
 
@@ -679,7 +692,7 @@ cudaError_t launch(Args& g, int sms, cudaStream_t s)
 
 namespace tt {
 
-int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s)
+int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t s)
 {
     Args g = {};
     g.e = p.e;
@@ -734,14 +747,14 @@ int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s)
     auto by_height = [&](auto amn, auto bmn, auto chunks) {
         constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value, L = decltype(chunks)::value;
         if constexpr (!L) {
-            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, sms, s) : launch<256, A, B, L, false>(g, sms, s);
+            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, sms, early, s) : launch<256, A, B, L, false>(g, sms, early, s);
         }
-        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, sms, s) : launch<128, A, B, L, false>(g, sms, s);
+        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, sms, early, s) : launch<128, A, B, L, false>(g, sms, early, s);
         if constexpr (!B) {
-            if (bn == 16) return launch<16, A, B, L, false>(g, sms, s);
-            if (bn == 32) return launch<32, A, B, L, false>(g, sms, s);
+            if (bn == 16) return launch<16, A, B, L, false>(g, sms, early, s);
+            if (bn == 32) return launch<32, A, B, L, false>(g, sms, early, s);
         }
-        return launch<64, A, B, L, false>(g, sms, s);
+        return launch<64, A, B, L, false>(g, sms, early, s);
     };
     auto by_sides = [&](auto chunks) {
         using Yes = std::true_type;

@@ -26,7 +26,7 @@ struct Product {
     int64_t rows = 0, cols = 0, deep = 0;
     Epilogue e = {};
 };
-// Returns a tt_status.
-int matmul(const Product& p, int32_t* status, int sms, cudaStream_t s);
+// early: a kernel of the same call is before it on the stream.  Returns a tt_status.
+int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t s);
 
 }  // namespace tt

@@ -113,6 +113,7 @@ __device__ __forceinline__ double block_sum(double x)
 
 __global__ void __launch_bounds__(kThreads, kFit) k_norm(const __grid_constant__ NormList L, char* mem, int slots, float bound, float* norm)
 {
+    let_next_kernel_start();
     double sum = 0.0;
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const NormRec& r = tensor_of(L, b);
@@ -174,6 +175,7 @@ __device__ __forceinline__ void tile_scale(const NormRec& r, int64_t tile, float
 
 __global__ void __launch_bounds__(kThreads, kFit) k_scale(const __grid_constant__ NormList L, const NormResult* res)
 {
+    wait_for_kernel_before();
     const float by = res->factor;
     if (by == 1.f || !res->finite) return;
     // from the end, where the sums have just been and the cache still holds the gradients
@@ -251,8 +253,11 @@ cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_
 
 cudaError_t norm_scale(const NormPlan& p, cudaStream_t s)
 {
-    for (size_t i = p.lists.size(); i-- > 0;) k_scale<<<p.grids[i], kThreads, 0, s>>>(p.lists[i], p.result());
-    return cudaGetLastError();
+    for (size_t i = p.lists.size(); i-- > 0;) {
+        const cudaError_t e = launch_early(k_scale, p.grids[i], kThreads, s, p.lists[i], (const NormResult*)p.result());
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace tt

@@ -11,6 +11,8 @@
 // launches, run on the FP32 pipes from where their operands lie, in one launch each.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "dense.cuh"
 #include "matmul.cuh"
 
@@ -165,6 +167,13 @@ struct PackArgs {
     const int32_t* status;
     int32_t narrow_type, parts;
     int32_t vectors;      // every row begins at a place that vector loads can take
+    int32_t across;       // blocks side by side
+};
+constexpr int kJobs = 3;
+struct PackList {
+    PackArgs job[kJobs];
+    unsigned first[kJobs + 1];     // blocks
+    int32_t early;                 // so few blocks that the next kernel's may wait beside them
 };
 
 template <typename T>
@@ -189,20 +198,40 @@ __device__ __forceinline__ void load8(const void* p, int type, int64_t at, bool 
     else if (type == TT_F16) load8<__half>(p, at, whole, n, x);
     else load8<float>(p, at, whole, n, x);
 }
-// the nearest bf16 value; the largest finite one where that would be an infinity of a finite x
-__device__ __forceinline__ float term(float x)
+// One bf16 term of eight values, which become what it leaves.  `odd`: some value is not finite, or its nearest bf16 value is not:
+// an infinity then leaves 0, and the largest bf16 value stands for what rounds to one.
+__device__ __forceinline__ uint4 next_term(float (&x)[8], bool odd)
 {
-    const float t = to_f32(__float2bfloat16_rn(x));
-    return fabsf(t) == INFINITY && fabsf(x) < INFINITY ? copysignf(0x1.fep127f, x) : t;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        memcpy(&w[i], &h, 4);
+        if (odd) {
+            const bool big0 = fabsf(x[2 * i]) < INFINITY && (w[i] & 0x7fffu) == 0x7f80u, big1 = fabsf(x[2 * i + 1]) < INFINITY && (w[i] >> 16 & 0x7fffu) == 0x7f80u;
+            w[i] -= (big0 ? 1u : 0u) + (big1 ? 0x10000u : 0u);
+        }
+        x[2 * i] -= __uint_as_float(w[i] << 16);
+        x[2 * i + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+        if (odd) {      // infinity less itself
+            x[2 * i] = x[2 * i] == x[2 * i] ? x[2 * i] : 0.f;
+            x[2 * i + 1] = x[2 * i + 1] == x[2 * i + 1] ? x[2 * i + 1] : 0.f;
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackArgs g)
+__global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackList list)
 {
+    if (list.early) let_next_kernel_start();
+    const int job = blockIdx.x >= list.first[2] ? 2 : blockIdx.x >= list.first[1] ? 1 : 0;
+    const PackArgs& g = list.job[job];
     if (has_error(g.status)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * kPackCols + lane * 8;
+    const unsigned block = blockIdx.x - list.first[job], bx = block % g.across, by = block / g.across;
+    const int64_t c = (int64_t)bx * kPackCols + lane * 8;
     const int n = (int)min64(8, g.cols - c);
-    const int64_t from = (int64_t)blockIdx.y * g.each, to = min64(g.rows, from + g.each);
+    const int64_t from = (int64_t)by * g.each, to = min64(g.rows, from + g.each);
     const bool whole = g.vectors && n == 8;
     constexpr int kAhead = 2;        // rows of a warp on their way
     float sum[8] = {};
@@ -236,15 +265,12 @@ __global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackA
                     else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
                 }
                 if (g.wide) {
-                    for (int p = 0; p < g.parts; ++p) {
-                        float t[8];
+                    float most = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            t[i] = term(x[i]);
-                            x[i] = fabsf(x[i]) < INFINITY ? x[i] - t[i] : 0.f;
-                        }
-                        store_pack((__nv_bfloat16*)g.wide + ((int64_t)p * g.rows + r) * g.ld + c, t);
-                    }
+                    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(x[i])));
+                    const bool odd = !(most < 0x1.fep127f);
+                    uint16_t* to_term = g.wide + r * g.ld + c;
+                    for (int p = 0; p < g.parts; ++p, to_term += g.rows * g.ld) *(uint4*)to_term = next_term(x, odd);
                 }
             }
         }
@@ -256,13 +282,14 @@ __global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackA
     float all = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) all += part[w][threadIdx.x];
-    const int64_t at = (int64_t)blockIdx.x * kPackCols + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
-    if (at < g.cols) g.sums[blockIdx.y * g.cols + at] = all;
+    const int64_t at = (int64_t)bx * kPackCols + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    if (at < g.cols) g.sums[by * g.cols + at] = all;
 }
 
 __global__ void __launch_bounds__(kThreads) k_bias_grad(const float* sums, int64_t blocks, int64_t cols, void* out, int32_t type, int32_t accumulate,
                                                         const int32_t* status)
 {
+    wait_for_kernel_before();
     if (has_error(status)) return;
     const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (c >= cols) return;
@@ -434,17 +461,31 @@ Forms forms_of(Space& w, const void* p, int64_t stride, int64_t rows, int64_t co
     const Upstream u = {p, nullptr, stride, 0, type, TT_F32, TT_ACT_NONE, 0.f};
     return forms_of(w, u, type != TT_F32, rows, cols, type, want_narrow, !want_wide ? 0 : type == TT_F32 ? 3 : type == TT_F16 ? 2 : 1, false, sms, status);
 }
-int launch_pack(const Forms& f, cudaStream_t s)
+// all passes of a call in one launch; *any: whether there was one
+int launch_pack(std::initializer_list<const Forms*> forms, int sms, bool* any, cudaStream_t s)
 {
-    if (!f.packs) return TT_OK;
-    const int64_t across = ceil_div(f.pack.cols, kPackCols);
-    if (across > INT32_MAX) return TT_ERR_ARG;
-    k_pack<<<dim3((unsigned)across, (unsigned)ceil_div(f.pack.rows, f.pack.each)), kThreads, 0, s>>>(f.pack);
+    PackList list = {};
+    int64_t blocks = 0;
+    int jobs = 0;
+    for (const Forms* f : forms) {
+        if (!f->packs) continue;
+        const int64_t across = ceil_div(f->pack.cols, kPackCols);
+        list.job[jobs] = f->pack;
+        list.job[jobs].across = (int)across;
+        list.first[jobs++] = (unsigned)blocks;
+        blocks += across * ceil_div(f->pack.rows, f->pack.each);
+        if (blocks > INT32_MAX) return TT_ERR_ARG;     // sizes that no device holds
+    }
+    *any = jobs > 0;
+    if (jobs == 0) return TT_OK;
+    for (int i = jobs; i <= kJobs; ++i) list.first[i] = (unsigned)blocks;
+    list.early = blocks <= 2 * sms;
+    k_pack<<<(unsigned)blocks, kThreads, 0, s>>>(list);
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
 // Products small enough for the FP32 pipes, a block of which takes about a microsecond for 64 of k
-bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 256 && rows * cols <= 65536; }
+bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 64 && rows * cols <= 65536; }
 
 Matrix matrix(const void* p, int64_t si, int64_t sk, int type) { return {p, si, sk, type}; }
 
@@ -487,8 +528,8 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
         return TT_OK;
     }
     if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
-    if (const int rc = launch_pack(x, s)) return rc;
-    if (const int rc = launch_pack(t, s)) return rc;
+    bool packed = false;
+    if (const int rc = launch_pack({&t, &x}, h->num_sms, &packed, s)) return rc;
     Product p;
     p.a = wide ? t.wide : t.narrow;
     p.b = wide ? x.wide : x.narrow;
@@ -496,7 +537,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     p.cols = h->rows;
     p.deep = h->dim;
     p.e = e;
-    return matmul(p, h->d_status, h->num_sms, s);
+    return matmul(p, h->d_status, h->num_sms, packed, s);
 }
 
 int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* size, cudaStream_t s)
@@ -545,8 +586,8 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         return TT_OK;
     }
     if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
-    for (const Forms* f : {&d, &t, &x})
-        if (const int rc = launch_pack(*f, s)) return rc;
+    bool early = false;
+    if (const int rc = launch_pack({&d, &t, &x}, h->num_sms, &early, s)) return rc;
     SmallArgs g = {};
     g.u = u;
     g.status = h->d_status;
@@ -581,7 +622,8 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         p.rows = a->n;
         p.deep = h->rows;
         p.e = ex;
-        if (const int rc = matmul(p, h->d_status, h->num_sms, s)) return rc;
+        if (const int rc = matmul(p, h->d_status, h->num_sms, early, s)) return rc;
+        early = true;
     }
     if (big_t) {
         p.a = wide_t ? x.wide : x.narrow;
@@ -590,13 +632,12 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         p.rows = h->rows;
         p.deep = a->n;
         p.e = et;
-        if (const int rc = matmul(p, h->d_status, h->num_sms, s)) return rc;
+        if (const int rc = matmul(p, h->d_status, h->num_sms, early, s)) return rc;
     }
-    if (a->grad_bias) {
-        k_bias_grad<<<(unsigned)ceil_div(h->rows, kThreads), kThreads, 0, s>>>(d.pack.sums, ceil_div(a->n, d.pack.each), h->rows, a->grad_bias,
-                                                                              a->grad_bias_type, a->accumulate, h->d_status);
-        if (cudaGetLastError() != cudaSuccess) return TT_ERR_CUDA;
-    }
+    if (a->grad_bias &&
+        launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, kThreads), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
+                     a->grad_bias, a->grad_bias_type, a->accumulate, (const int32_t*)h->d_status) != cudaSuccess)
+        return TT_ERR_CUDA;
     return TT_OK;
 }
 
