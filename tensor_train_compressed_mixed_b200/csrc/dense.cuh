@@ -1,7 +1,7 @@
 // The handle of a dense table: its lookup and gradient (dense.cu), and its projection (project.cu).
 #pragma once
 
-#include "types.cuh"
+#include "matmul.cuh"
 
 struct tt_emb_dense_handle {
     int64_t rows = 0, pad = -1;
@@ -13,6 +13,7 @@ struct tt_emb_dense_handle {
     int64_t ws_n = -1;
     char* project_ws = nullptr;
     size_t project_bytes = 0;
+    tt::MatmulFits fits;
     int32_t* d_status = nullptr;
     int device = 0, num_sms = 148;
     bool clusters = false;       // one of k_token_sort fits this device

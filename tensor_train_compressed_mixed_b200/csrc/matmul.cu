@@ -32,7 +32,6 @@ namespace {
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
 constexpr int kGroup = 16;           // row tiles that are taken in turn before the next column tile: they stay in L2
-constexpr int kMaxSplit = 8;
 
 struct Args {
     CUtensorMap a, b;
@@ -658,41 +657,92 @@ bool encode(CUtensorMap* map, const Operand& o, int high)
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
-cudaError_t launch(Args& g, int sms, bool early, cudaStream_t s)
+template <int BN, bool kPair>
+constexpr int block_bytes() { return stages_of(BN, kPair) * stage_bytes(BN, kPair) + passing_of(BN) * kCols * 4 + 1024; }
+
+// A launch of `blocks` blocks in clusters of `cluster`.
+struct Launch {
+    cudaLaunchConfig_t c = {};
+    cudaLaunchAttribute at[2];
+    Launch(int64_t blocks, int threads, int bytes, int cluster, bool early, cudaStream_t s)
+    {
+        int n = 0;
+        if (cluster > 1) {
+            at[n].id = cudaLaunchAttributeClusterDimension;
+            at[n].val.clusterDim.x = cluster;
+            at[n].val.clusterDim.y = at[n].val.clusterDim.z = 1;
+            ++n;
+        }
+        if (early) {
+            at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[n].val.programmaticStreamSerializationAllowed = 1;
+            ++n;
+        }
+        c.gridDim = dim3((unsigned)blocks);
+        c.blockDim = dim3(threads);
+        c.dynamicSmemBytes = bytes;
+        c.stream = s;
+        c.attrs = at;
+        c.numAttrs = n;
+    }
+    Launch(const Launch&) = delete;
+};
+
+// leave for its shared memory, once for each device
+template <typename Kernel>
+cudaError_t allow(Kernel kernel, int bytes, std::atomic<uint64_t>& told)
 {
-    constexpr int kBytes = stages_of(BN, kPair) * stage_bytes(BN, kPair) + passing_of(BN) * kCols * 4 + 1024;
-    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
-    static std::atomic<uint64_t> told{0};      // devices on which the kernel has leave for its shared memory
     int device = 0;
     cudaError_t e = cudaGetDevice(&device);
     if (e == cudaSuccess && (device >= 64 || !(told.load(std::memory_order_relaxed) >> device & 1))) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess && device < 64) told.fetch_or((uint64_t)1 << device, std::memory_order_relaxed);
     }
+    return e;
+}
+
+template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
+cudaError_t launch(Args& g, const MatmulFits& fits, bool early, cudaStream_t s)
+{
+    static std::atomic<uint64_t> told{0};
+    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
+    const cudaError_t e = allow(kernel, block_bytes<BN, kPair>(), told);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t c = {};
-    cudaLaunchAttribute at[2];
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = kPair ? 2 : g.split;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     const int64_t tiles = (int64_t)g.tiles_c * g.tiles_r;
-    c.gridDim = dim3((unsigned)(kPair ? 2 * min64(tiles, sms / 2) : g.split > 1 ? tiles * g.split : min64(tiles, (int64_t)sms * fit_of(BN))));
-    c.blockDim = dim3(threads_of(BN));
-    c.dynamicSmemBytes = kBytes;
-    c.stream = s;
-    c.attrs = at;
-    c.numAttrs = early ? 2 : 1;
-    return cudaLaunchKernelEx(&c, kernel, g);
+    const int64_t blocks = kPair ? 2 * min64(tiles, fits.one[1]) : g.split > 1 ? tiles * g.split : min64(tiles, (int64_t)fits.sms * fit_of(BN));
+    const Launch l(blocks, threads_of(BN), block_bytes<BN, kPair>(), kPair ? 2 : g.split, early, s);
+    return cudaLaunchKernelEx(&l.c, kernel, g);
+}
+
+// clusters of 2, 4 and 8 blocks of a kernel that the current device holds at a time
+template <int BN, bool kPair>
+void count_clusters(int (&n)[4])
+{
+    auto* kernel = k_matmul<BN, false, false, false, kPair>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block_bytes<BN, kPair>()) != cudaSuccess) return;
+    for (int i = 1; i < 4; ++i) {
+        const Launch l(1 << i, threads_of(BN), block_bytes<BN, kPair>(), 1 << i, false, nullptr);
+        if (cudaOccupancyMaxActiveClusters(&n[i], kernel, &l.c) != cudaSuccess) n[i] = 0;
+    }
 }
 
 }  // namespace
 
 namespace tt {
 
-int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t s)
+MatmulFits matmul_fits(int sms)
+{
+    MatmulFits f;
+    f.sms = sms;
+    f.one[0] = sms;
+    f.two[0] = 2 * sms;
+    count_clusters<256, true>(f.one);
+    count_clusters<16, false>(f.two);
+    cudaGetLastError();     // a refusal here is an answer, not an error of the next launch
+    return f;
+}
+
+int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s)
 {
     Args g = {};
     g.e = p.e;
@@ -717,21 +767,23 @@ int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t 
     for (int n = p.b_mn ? 64 : 16; n <= (by_chunks ? 128 : 256); n *= 2) {
         const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n);
         const double stage = std::max(2.0 * n, stage_bytes(n, false) / 45.0);
-        for (int k = 1; k <= kMaxSplit; k *= 2) {
-            if (k > 1 && (tiles * k > sms * fit_of(n) || blocks < 2 * k)) break;
+        const int(&room)[4] = fit_of(n) > 1 ? fits.two : fits.one;
+        for (int i = 0; i < 4; ++i) {
+            const int k = 1 << i;
+            if (i > 0 && (tiles > room[i] || blocks < 2 * k)) break;
             // two blocks on an SM share its bandwidth
-            const double turns = fit_of(n) > 1 ? std::max(1.0, tiles * k / sms) : ceil(tiles * k / sms);
+            const double turns = fit_of(n) > 1 ? std::max(1.0, tiles * k / fits.sms) : ceil(tiles * k / fits.sms);
             const double t = turns * ((double)its / k * stage + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
             if (bn == 0 || t < best) best = t, bn = n, split = k, pair = false;
         }
-        if (n >= 128) {
+        if (n >= 128 && fits.one[1] > 0) {
             const double pairs = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
-            const double t = ceil(pairs / (sms / 2)) * ((double)its * std::max(2.0 * n, stage_bytes(n, true) / 45.0) + 8.0 * n) + 2000.0;
+            const double t = ceil(pairs / fits.one[1]) * ((double)its * std::max(2.0 * n, stage_bytes(n, true) / 45.0) + 8.0 * n) + 2000.0;
             if (t < best) best = t, bn = n, split = 1, pair = true;
         }
     }
     const int64_t tiles_c = ceil_div(p.cols, pair ? 2 * kCols : kCols), tiles_r = ceil_div(p.rows, bn);
-    if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / kMaxSplit) return TT_ERR_ARG;   // sizes that no device holds
+    if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / 8) return TT_ERR_ARG;   // sizes that no device holds
     g.blocks = (int)blocks;
     g.tiles_c = (int)tiles_c;
     g.tiles_r = (int)tiles_r;
@@ -747,14 +799,14 @@ int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t 
     auto by_height = [&](auto amn, auto bmn, auto chunks) {
         constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value, L = decltype(chunks)::value;
         if constexpr (!L) {
-            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, sms, early, s) : launch<256, A, B, L, false>(g, sms, early, s);
+            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, fits, early, s) : launch<256, A, B, L, false>(g, fits, early, s);
         }
-        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, sms, early, s) : launch<128, A, B, L, false>(g, sms, early, s);
+        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, fits, early, s) : launch<128, A, B, L, false>(g, fits, early, s);
         if constexpr (!B) {
-            if (bn == 16) return launch<16, A, B, L, false>(g, sms, early, s);
-            if (bn == 32) return launch<32, A, B, L, false>(g, sms, early, s);
+            if (bn == 16) return launch<16, A, B, L, false>(g, fits, early, s);
+            if (bn == 32) return launch<32, A, B, L, false>(g, fits, early, s);
         }
-        return launch<64, A, B, L, false>(g, sms, early, s);
+        return launch<64, A, B, L, false>(g, fits, early, s);
     };
     auto by_sides = [&](auto chunks) {
         using Yes = std::true_type;

@@ -18,6 +18,14 @@ inline bool mappable(const void* p, int64_t stride, int64_t outer, int64_t inner
     return ((uintptr_t)p & 15) == 0 && (outer == 1 || ((stride & 7) == 0 && stride >= inner && stride < (int64_t)1 << 38));
 }
 
+// Blocks of the product kernels that a device holds at a time: those of one an SM and those of two, alone and in clusters of
+// 2, 4 and 8 (0: none of that size).
+struct MatmulFits {
+    int sms = 148;
+    int one[4] = {}, two[4] = {};
+};
+MatmulFits matmul_fits(int sms);     // of the current device
+
 // C[r][c] = sum over k of A(c, k) B(r, k), finished by e: r < rows, c < cols, k < deep.  A is [cols][deep], or with a_mn
 // [deep][cols]; B is [rows][deep], or with b_mn [deep][rows].  Both of one type.
 struct Product {
@@ -27,6 +35,6 @@ struct Product {
     Epilogue e = {};
 };
 // early: a kernel of the same call is before it on the stream.  Returns a tt_status.
-int matmul(const Product& p, int32_t* status, int sms, bool early, cudaStream_t s);
+int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s);
 
 }  // namespace tt

@@ -537,7 +537,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     p.cols = h->rows;
     p.deep = h->dim;
     p.e = e;
-    return matmul(p, h->d_status, h->num_sms, packed, s);
+    return matmul(p, h->d_status, h->fits, packed, s);
 }
 
 int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* size, cudaStream_t s)
@@ -622,7 +622,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         p.rows = a->n;
         p.deep = h->rows;
         p.e = ex;
-        if (const int rc = matmul(p, h->d_status, h->num_sms, early, s)) return rc;
+        if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
         early = true;
     }
     if (big_t) {
@@ -632,7 +632,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         p.rows = h->rows;
         p.deep = a->n;
         p.e = et;
-        if (const int rc = matmul(p, h->d_status, h->num_sms, early, s)) return rc;
+        if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
     }
     if (a->grad_bias &&
         launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, kThreads), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
