@@ -9,8 +9,10 @@
 // then works on whole pieces of 128 values of a row, and reads the residual of the next rows ahead.  Two areas of tensor memory
 // take turns, so that products go on meanwhile.
 // Tensor cores cut the last bits of a sum off at each step.  16-bit results round far above that; for others (kLong) the sums
-// of a few blocks of k at a time are formed in tensor memory and added in fp32 registers, and of operands of several terms the
-// small products come first, so that few steps are made on a large sum.
+// of a few blocks of k at a time are formed in tensor memory and added in fp32 registers.  Operands of several terms
+// (x = t0 + t1 + t2, each 2^-8 of the one before) bring each term once for all products that it is part of: those of terms i and j
+// with i + j < 3, as the others are below fp32's last bit.  All but the first terms' product are summed in an area of their
+// own, so that few steps are made on a large sum.
 // Two blocks on neighbouring SMs make a pair where there are many tiles: one tile of 256 columns, of which each block brings its half of
 // both operands and finishes its half, so that a block reads half of B.
 // Where there are fewer tiles than SMs a cluster of blocks shares one tile's k, and its partial sums are added through
@@ -39,8 +41,7 @@ struct Args {
     int32_t* status;
     int64_t rows, cols;
     int32_t blocks;       // of 64 k
-    int32_t pairs;
-    uint32_t pair_list;   // four bits each: A's term, B's term << 2
+    int32_t a_terms, b_terms;     // of the operands' values, 1 to 3; with kLong only
     int32_t chunk;        // blocks of k whose sums stay in tensor memory
     uint32_t idesc;
     int32_t tiles_c, tiles_r;
@@ -306,7 +307,7 @@ __device__ __forceinline__ void add_rows(const Four (&res)[R], F2 (&z)[R][2])
         const uint32_t(&w)[4] = res[j].w;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            F2 x;
+            F2 x = {};
             if constexpr (sizeof(T) == 4) x = {__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])};
             else if constexpr (kVec) x = unpacked<T>(w[i]);
             else x = unpacked<T>(__byte_perm(w[2 * i], w[2 * i + 1], 0x5410));
@@ -389,12 +390,13 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     constexpr int kFinish = finish_of(BN), kStages = stages_of(BN, kPair), kStage = stage_bytes(BN, kPair), kPart = BN / (kFinish / 4);
     constexpr int kPass = passing_of(BN), kRows = kPass / kFinish;       // rows at a time of a block and of a finishing warp
     constexpr int kSide = kPair ? 2 : 1, kOwn = BN / kSide;              // blocks of a pair, rows of B that each brings
-    constexpr uint32_t kTmem = 2 * BN < 32 ? 32 : 2 * BN;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int gone;
     const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+    const int terms = kLong ? max(g.a_terms, g.b_terms) : 1;
+    const uint32_t area = terms > 1 ? 4 * BN : 2 * BN, columns = area < 32 ? 32 : area;      // of tensor memory: two of sums, and two of the small terms'
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -412,10 +414,10 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     let_next_kernel_start();
     if (warp == 1) {
         if constexpr (kPair) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(kTmem) : "memory");
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_at)), "r"(columns) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         } else {
-            tmem_alloc(&tmem_at, kTmem);
+            tmem_alloc(&tmem_at, columns);
         }
     }
     wait_for_kernel_before();
@@ -453,28 +455,31 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             place(tile, c0, r0);
             for (int k0 = first; ok && k0 < last; k0 += chunk) {
                 const int end = min(k0 + chunk, last);
-                for (int q = 0; ok && q < g.pairs; ++q) {
-                    const int pa = g.pair_list >> (4 * q) & 3, pb = g.pair_list >> (4 * q + 2) & 3;
-                    for (int kb = k0; kb < end; ++kb, ++n) {
+                for (int kb = k0; ok && kb < end; ++kb)
+                    for (int t = 0; t < terms; ++t, ++n) {
                         const int s = n % kStages, k = kb * kDeep;
                         if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
                         const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2, bar = kPair ? in_block(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
                         const int rb = r0 + (kPair ? rank * kOwn : 0);
-                        if (!kPair || rank == 0) expect(&full[s], kStage * kSide);
-                        if constexpr (kAmn) {
+                        const bool with_a = !kLong || t < g.a_terms, with_b = !kLong || t < g.b_terms;
+                        if (!kPair || rank == 0) expect(&full[s], ((with_a ? kCols : 0) + (with_b ? kOwn : 0)) * kDeep * 2 * kSide);
+                        if (with_a) {
+                            if constexpr (kAmn) {
 #pragma unroll
-                            for (int i = 0; i < kCols / 64; ++i) copy_tile<kPair>(a + i * 8192, &g.a, c0 + 64 * i, k, pa, bar);
-                        } else {
-                            copy_tile<kPair>(a, &g.a, k, c0, pa, bar);
+                                for (int i = 0; i < kCols / 64; ++i) copy_tile<kPair>(a + i * 8192, &g.a, c0 + 64 * i, k, t, bar);
+                            } else {
+                                copy_tile<kPair>(a, &g.a, k, c0, t, bar);
+                            }
                         }
-                        if constexpr (kBmn) {
+                        if (with_b) {
+                            if constexpr (kBmn) {
 #pragma unroll
-                            for (int i = 0; i < kOwn / 64; ++i) copy_tile<kPair>(b + i * 8192, &g.b, rb + 64 * i, k, pb, bar);
-                        } else {
-                            copy_tile<kPair>(b, &g.b, k, rb, pb, bar);
+                                for (int i = 0; i < kOwn / 64; ++i) copy_tile<kPair>(b + i * 8192, &g.b, rb + 64 * i, k, t, bar);
+                            } else {
+                                copy_tile<kPair>(b, &g.b, k, rb, t, bar);
+                            }
                         }
                     }
-                }
             }
         }
         if (gone == kTimedOut && (!kPair || rank == 0))      // copies on their way land before the block's memory is given up
@@ -484,22 +489,53 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         bool ok = true;
         for (int tile = start; ok && tile < tiles; tile += step)
             for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
-                const int buf = seq & 1, here = (min(k0 + chunk, last) - k0) * g.pairs;
+                const int buf = seq & 1, end = min(k0 + chunk, last);
                 if (seq >= 2 && !wait_for<kPair>(&sums_empty[buf], (seq / 2 - 1) & 1, &gone)) { ok = false; break; }
                 tc_fence_after();
-                for (int i = 0; i < here; ++i, ++n) {
-                    const int s = n % kStages;
-                    if (!wait_for(&full[s], (n / kStages) & 1, &gone)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2;
-                    uint64_t da = swizzled(a, kAmn), db = swizzled(b, kBmn);
+                const uint32_t sums = tmem + buf * BN;
+                auto product = [&](uint32_t to, int a_slot, int b_slot, bool add) {
+                    uint64_t da = swizzled(ring + a_slot * kStage, kAmn), db = swizzled(ring + b_slot * kStage + kCols * kDeep * 2, kBmn);
 #pragma unroll
                     for (int k = 0; k < kDeep / 16; ++k) {
-                        multiply<kPair>(tmem + buf * BN, da, db, g.idesc, i > 0 || k > 0);
+                        multiply<kPair>(to, da, db, g.idesc, add || k > 0);
                         da += (kAmn ? 2048 : 32) >> 4;
                         db += (kBmn ? 2048 : 32) >> 4;
                     }
-                    commit<kPair>(&empty[s]);
+                };
+                if (!kLong || terms == 1) {
+                    for (int kb = k0; kb < end; ++kb, ++n) {
+                        const int s = n % kStages;
+                        if (!wait_for(&full[s], (n / kStages) & 1, &gone)) { ok = false; break; }
+                        tc_fence_after();
+                        product(sums, s, s, kb > k0);
+                        commit<kPair>(&empty[s]);
+                    }
+                } else {
+                    for (int kb = k0; ok && kb < end; ++kb, n += terms) {
+                        int slot[3];
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) slot[t] = (n + t) % kStages;
+                        bool small = kb > k0;       // the small terms' sum has begun
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) {
+                            if (t >= terms) break;
+                            if (!wait_for(&full[slot[t]], ((n + t) / kStages) & 1, &gone)) { ok = false; break; }
+                            tc_fence_after();
+                            if (t == 0) product(sums, slot[0], slot[0], kb > k0);
+                            // the products whose later term is this one
+#pragma unroll
+                            for (int i = 0; i <= t; ++i)
+#pragma unroll
+                                for (int j = 0; j <= t; ++j)
+                                    if ((i == t || j == t) && i + j > 0 && i + j < 3 && i < g.a_terms && j < g.b_terms) {
+                                        product(sums + 2 * BN, slot[i], slot[j], small);
+                                        small = true;
+                                    }
+                        }
+#pragma unroll
+                        for (int t = 0; t < 3; ++t)
+                            if (ok && t < terms) commit<kPair>(&empty[slot[t]]);
+                    }
                 }
                 if (ok) commit<kPair>(&sums_full[buf]);
             }
@@ -542,6 +578,12 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                         for (int i = 0; i < kLoad; ++i) acc[j + i] = (k0 == first ? 0.f : acc[j + i]) + __uint_as_float(x[i]);
+                        if (terms > 1) {
+                            load_columns<kLoad>(at + 2 * BN + buf * BN + j, x);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                            for (int i = 0; i < kLoad; ++i) acc[j + i] += __uint_as_float(x[i]);
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -623,8 +665,8 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     if constexpr (kPair) cluster_sync();       // neither block's memory is given up while the other's products may read it
     tc_fence_after();
     if (warp == 1) {
-        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
-        else tmem_dealloc(tmem, kTmem);
+        if constexpr (kPair) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns) : "memory");
+        else tmem_dealloc(tmem, columns);
     }
     if (threadIdx.x == 0 && gone == kTimedOut) raise_error(g.status, TT_ERR_TIMEOUT, (int)blockIdx.x);
 }
@@ -749,36 +791,37 @@ int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early
     g.status = status;
     g.rows = p.rows;
     g.cols = p.cols;
-    // Terms i and j of the operands give a product of 2^-8(i + j) of the first ones: those beyond 2^-16 are below fp32's last
-    // bit.  The smallest first.
-    for (int far = 2; far >= 0; --far)
-        for (int i = 0; i <= far; ++i)
-            if (i < p.a.parts && far - i < p.b.parts) g.pair_list |= (uint32_t)(i | (far - i) << 2) << (4 * g.pairs++);
-    const int64_t blocks = ceil_div(p.deep, kDeep), its = blocks * g.pairs;
+    g.a_terms = p.a.parts;
+    g.b_terms = p.b.parts;
+    int pairs = 0;
+    for (int i = 0; i < p.a.parts; ++i)
+        for (int j = 0; j < p.b.parts && i + j < 3; ++j) ++pairs;
+    const int64_t blocks = ceil_div(p.deep, kDeep);
     // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
     // off by up to 2^-23 of it.
-    const bool by_chunks = p.e.out_type == TT_F32 || (p.e.pre && p.e.pre_type == TT_F32) || g.pairs > 1 || blocks > 1024;
+    const bool by_chunks = p.e.out_type == TT_F32 || (p.e.pre && p.e.pre_type == TT_F32) || pairs > 1 || blocks > 1024;
     g.chunk = 4;
-    // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  A stage takes what its
-    // products take (half a cycle for each of its rows and 16 k, at 128 columns), or what its bytes take, about 45 a cycle and SM.
+    // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  64 k take what their
+    // products take (half a cycle for each row and 16 k, at 128 columns), or what their bytes take, about 55 a cycle and SM.
     int bn = 0, split = 1;
     bool pair = false;
     double best = 0.0;
     for (int n = p.b_mn ? 64 : 16; n <= (by_chunks ? 128 : 256); n *= 2) {
-        const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n);
-        const double stage = std::max(2.0 * n, stage_bytes(n, false) / 45.0);
+        const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n), products = 2.0 * n * pairs;
+        const double each = std::max(products, (kCols * p.a.parts + n * p.b.parts) * (kDeep * 2 / 55.0));
         const int(&room)[4] = fit_of(n) > 1 ? fits.two : fits.one;
         for (int i = 0; i < 4; ++i) {
             const int k = 1 << i;
             if (i > 0 && (tiles > room[i] || blocks < 2 * k)) break;
             // two blocks on an SM share its bandwidth
             const double turns = fit_of(n) > 1 ? std::max(1.0, tiles * k / fits.sms) : ceil(tiles * k / fits.sms);
-            const double t = turns * ((double)its / k * stage + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
+            const double t = turns * ((double)blocks / k * each + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
             if (bn == 0 || t < best) best = t, bn = n, split = k, pair = false;
         }
         if (n >= 128 && fits.one[1] > 0) {
-            const double pairs = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
-            const double t = ceil(pairs / fits.one[1]) * ((double)its * std::max(2.0 * n, stage_bytes(n, true) / 45.0) + 8.0 * n) + 2000.0;
+            const double count = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
+            const double two = std::max(products, (kCols * p.a.parts + n / 2 * p.b.parts) * (kDeep * 2 / 55.0));
+            const double t = ceil(count / fits.one[1]) * ((double)blocks * two + 8.0 * n) + 2000.0;
             if (t < best) best = t, bn = n, split = 1, pair = true;
         }
     }
