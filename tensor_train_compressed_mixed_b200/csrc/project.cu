@@ -166,7 +166,7 @@ struct PackArgs {
     float* sums;          // [blocks of rows][cols] sums over a block's rows; may be null
     const int32_t* status;
     int32_t narrow_type, parts;
-    int32_t vectors;      // every row begins at a place that vector loads can take
+    int32_t vectors;      // every row begins at a place that vector loads can take, and is a multiple of eight values
     int32_t across;       // blocks side by side
 };
 constexpr int kJobs = 3;
@@ -176,28 +176,56 @@ struct PackList {
     int32_t early;                 // so few blocks that the next kernel's may wait beside them
 };
 
-template <typename T>
-__device__ __forceinline__ void load8(const void* p, int64_t at, bool whole, int n, float (&x)[8])
+// Eight neighbouring values as they lie in memory, 16-byte aligned.
+struct Raw8 { uint4 a, b; };
+__device__ __forceinline__ Raw8 load8(const void* p, int type, int64_t at)
 {
-    const T* q = (const T*)p + at;
-    if (whole) {
-        constexpr int kPer = 16 / sizeof(T);
-        Pack<T, kPer> v[8 / kPer];
-#pragma unroll
-        for (int i = 0; i < 8 / kPer; ++i) v[i] = ((const Pack<T, kPer>*)q)[i];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = to_f32(v[i / kPer].v[i % kPer]);
+    Raw8 q;
+    if (type == TT_F32) {
+        q.a = ((const uint4*)((const float*)p + at))[0];
+        q.b = ((const uint4*)((const float*)p + at))[1];
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < n ? to_f32(q[i]) : 0.f;
+        q.a = *(const uint4*)((const uint16_t*)p + at);
     }
+    return q;
 }
-__device__ __forceinline__ void load8(const void* p, int type, int64_t at, bool whole, int n, float (&x)[8])
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8& q, float (&x)[8])
 {
-    if (type == TT_BF16) load8<__nv_bfloat16>(p, at, whole, n, x);
-    else if (type == TT_F16) load8<__half>(p, at, whole, n, x);
-    else load8<float>(p, at, whole, n, x);
+    T v[32 / sizeof(T)];
+    memcpy(v, &q, 32);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(v[i]);
 }
+__device__ __forceinline__ void widen8(const Raw8& q, int type, float (&x)[8])
+{
+    if (type == TT_BF16) widen8<__nv_bfloat16>(q, x);
+    else if (type == TT_F16) widen8<__half>(q, x);
+    else widen8<float>(q, x);
+}
+// A row of up to 256 values from any place: neighbouring lanes read neighbouring values, which go to shared memory, from
+// where each lane takes its eight.
+template <typename T>
+__device__ __forceinline__ void load_row(const T* p, int n, int lane, float* buf)
+{
+    T v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lane + 32 * i < n ? p[lane + 32 * i] : T(0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) buf[lane + 32 * i] = to_f32(v[i]);
+}
+__device__ __forceinline__ void load_row(const void* p, int type, int64_t at, int n, int lane, float* buf)
+{
+    if (type == TT_BF16) load_row((const __nv_bfloat16*)p + at, n, lane, buf);
+    else if (type == TT_F16) load_row((const __half*)p + at, n, lane, buf);
+    else load_row((const float*)p + at, n, lane, buf);
+}
+__device__ __forceinline__ void take8(const float* buf, int lane, float (&x)[8])
+{
+    const float4 a = ((const float4*)buf)[2 * lane], b = ((const float4*)buf)[2 * lane + 1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
 // One bf16 term of eight values, which become what it leaves.  `odd`: some value is not finite, or its nearest bf16 value is not:
 // an infinity then leaves 0, and the largest bf16 value stands for what rounds to one.
 __device__ __forceinline__ uint4 next_term(float (&x)[8], bool odd)
@@ -221,80 +249,117 @@ __device__ __forceinline__ uint4 next_term(float (&x)[8], bool odd)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__global__ void __launch_bounds__(kThreads) k_pack(const __grid_constant__ PackList list)
+// One row's eight values of a lane (those beyond the last column 0): times the slope, summed, and written in the forms wanted.
+__device__ __forceinline__ void pack_row(const PackArgs& g, int64_t r, int64_t c, float (&x)[8], const float (&z)[8], float (&sum)[8])
 {
+    auto times = [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const F2 d = mul2(slope(decltype(act)::value, F2{z[i], z[i + 1]}, g.u.cap), F2{x[i], x[i + 1]});
+            x[i] = d.x;
+            x[i + 1] = d.y;
+        }
+    };
+    if (g.u.act == TT_ACT_RELU) times(std::integral_constant<int, TT_ACT_RELU>());
+    else if (g.u.act == TT_ACT_GELU) times(std::integral_constant<int, TT_ACT_GELU>());
+    else if (g.u.act == TT_ACT_SILU) times(std::integral_constant<int, TT_ACT_SILU>());
+    else if (g.u.act == TT_ACT_SOFTCAP) times(std::integral_constant<int, TT_ACT_SOFTCAP>());
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const F2 t = add2({sum[i], sum[i + 1]}, {x[i], x[i + 1]});
+        sum[i] = t.x;
+        sum[i + 1] = t.y;
+    }
+    if (c >= g.cols) return;
+    if (g.narrow) {
+        if (g.narrow_type == TT_F16) store_pack((__half*)g.narrow + r * g.ld + c, x);
+        else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
+    }
+    if (g.wide) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(x[i])));
+        const bool odd = !(most < 0x1.fep127f);
+        uint16_t* to = g.wide + r * g.ld + c;
+        for (int p = 0; p < g.parts; ++p, to += g.rows * g.ld) *(uint4*)to = next_term(x, odd);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 4) k_pack(const __grid_constant__ PackList list)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ float part[2 * kWarps][kPackCols];
     if (list.early) let_next_kernel_start();
     const int job = blockIdx.x >= list.first[2] ? 2 : blockIdx.x >= list.first[1] ? 1 : 0;
     const PackArgs& g = list.job[job];
     if (has_error(g.status)) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const unsigned block = blockIdx.x - list.first[job], bx = block % g.across, by = block / g.across;
-    const int64_t c = (int64_t)bx * kPackCols + lane * 8;
-    const int n = (int)min64(8, g.cols - c);
-    const int64_t from = (int64_t)by * g.each, to = min64(g.rows, from + g.each);
-    const bool whole = g.vectors && n == 8;
-    constexpr int kAhead = 2;        // rows of a warp on their way
-    float sum[8] = {};
-    if (n > 0)
-        for (int64_t r0 = from + warp; r0 < to; r0 += kAhead * (kThreads / 32)) {
-            float v[kAhead][8], z[kAhead][8];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int64_t r = r0 + j * (kThreads / 32);
-                const int m = r < to ? n : 0;
-                load8(g.u.up, g.u.up_type, r * g.u.up_stride + c, whole && m > 0, m, v[j]);
-                if (g.u.act != TT_ACT_NONE) load8(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c, whole && m > 0, m, z[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                const int64_t r = r0 + j * (kThreads / 32);
-                if (r >= to) break;
-                float(&x)[8] = v[j];
-                if (g.u.act != TT_ACT_NONE) {
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const F2 d = mul2(slope(g.u.act, F2{z[j][i], z[j][i + 1]}, g.u.cap), F2{x[i], x[i + 1]});
-                        x[i] = i < n ? d.x : 0.f;
-                        x[i + 1] = i + 1 < n ? d.y : 0.f;
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] += x[i];
-                if (g.narrow) {
-                    if (g.narrow_type == TT_F16) store_pack((__half*)g.narrow + r * g.ld + c, x);
-                    else store_pack((__nv_bfloat16*)g.narrow + r * g.ld + c, x);
-                }
-                if (g.wide) {
-                    float most = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(most) : "f"(fabsf(x[i])));
-                    const bool odd = !(most < 0x1.fep127f);
-                    uint16_t* to_term = g.wide + r * g.ld + c;
-                    for (int p = 0; p < g.parts; ++p, to_term += g.rows * g.ld) *(uint4*)to_term = next_term(x, odd);
-                }
-            }
+    const int64_t c0 = (int64_t)bx * kPackCols, c = c0 + lane * 8;
+    const int64_t to = min64(g.rows, ((int64_t)by + 1) * g.each);
+    int64_t r = (int64_t)by * g.each + warp;
+    const bool act = g.u.act != TT_ACT_NONE;
+    float sum[8] = {}, x[8], z[8];
+    if (g.vectors) {        // (the columns are whole vectors then)
+        Raw8 v = {}, w = {};
+        auto fetch = [&] {
+            if (c >= g.cols || r >= to) return;
+            v = load8(g.u.up, g.u.up_type, r * g.u.up_stride + c);
+            if (act) w = load8(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c);
+        };
+        fetch();
+        while (r < to) {
+            widen8(v, g.u.up_type, x);
+            if (act) widen8(w, g.u.pre_type, z);
+            const int64_t here = r;
+            r += kWarps;
+            fetch();
+            pack_row(g, here, c, x, z, sum);
         }
+    } else {
+        float *a = part[2 * warp], *b = part[2 * warp + 1];
+        const int n = (int)min64(kPackCols, g.cols - c0);
+        for (; r < to; r += kWarps) {
+            load_row(g.u.up, g.u.up_type, r * g.u.up_stride + c0, n, lane, a);
+            if (act) load_row(g.u.pre, g.u.pre_type, r * g.u.pre_stride + c0, n, lane, b);
+            __syncwarp();
+            take8(a, lane, x);
+            if (act) take8(b, lane, z);
+            __syncwarp();
+            pack_row(g, r, c, x, z, sum);
+        }
+    }
     if (!g.sums) return;
-    __shared__ float part[kThreads / 32][kPackCols];
+    __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = sum[i];
     __syncthreads();
     float all = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) all += part[w][threadIdx.x];
-    const int64_t at = (int64_t)bx * kPackCols + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
+    for (int i = 0; i < kWarps; ++i) all += part[i][threadIdx.x];
+    const int64_t at = c0 + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
     if (at < g.cols) g.sums[by * g.cols + at] = all;
 }
 
+// The sums of the blocks of rows: 32 columns of a block of threads, each warp an eighth of the sums.
 __global__ void __launch_bounds__(kThreads) k_bias_grad(const float* sums, int64_t blocks, int64_t cols, void* out, int32_t type, int32_t accumulate,
                                                         const int32_t* status)
 {
     wait_for_kernel_before();
     if (has_error(status)) return;
-    const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (c >= cols) return;
+    __shared__ float part[kThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float sum = 0.f;
-    for (int64_t i = 0; i < blocks; ++i) sum += sums[i * cols + c];
+    if (c < cols) {
+#pragma unroll 4
+        for (int64_t i = warp; i < blocks; i += kThreads / 32) sum += sums[i * cols + c];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp > 0 || c >= cols) return;
+#pragma unroll
+    for (int i = 1; i < kThreads / 32; ++i) sum += part[i][lane];
     if (accumulate) sum += load_any(out, type, c);
     store_any(out, type, c, sum);
 }
@@ -443,17 +508,17 @@ Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t co
         f.packs = true;
     }
     f.packs = f.packs || want_sums;
-    // Blocks of rows: eight blocks an SM in all, of 32 rows at least.
+    // Blocks of rows: eight blocks an SM in all, of eight rows, one a warp, at least.
     const int64_t across = ceil_div(cols, kPackCols);
     int64_t down = ceil_div((int64_t)sms * 8, across);
-    if (down > ceil_div(rows, 32)) down = ceil_div(rows, 32);
+    if (down > ceil_div(rows, 8)) down = ceil_div(rows, 8);
     if (down > 65535) down = 65535;
     f.pack.each = ceil_div(rows, down);
     if (want_sums) f.pack.sums = (float*)w.take(ceil_div(rows, f.pack.each) * cols * 4);
     auto vectors = [&](const void* p, int type, int64_t stride) {
         return ((uintptr_t)p & 15) == 0 && (stride * type_bytes(type) & 15) == 0;
     };
-    f.pack.vectors = vectors(u.up, u.up_type, u.up_stride) && (u.act == TT_ACT_NONE || vectors(u.pre, u.pre_type, u.pre_stride));
+    f.pack.vectors = (cols & 7) == 0 && vectors(u.up, u.up_type, u.up_stride) && (u.act == TT_ACT_NONE || vectors(u.pre, u.pre_type, u.pre_stride));
     return f;
 }
 Forms forms_of(Space& w, const void* p, int64_t stride, int64_t rows, int64_t cols, int type, bool want_narrow, bool want_wide, int sms, int32_t* status)
@@ -635,7 +700,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
     }
     if (a->grad_bias &&
-        launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, kThreads), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
+        launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, 32), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
                      a->grad_bias, a->grad_bias_type, a->accumulate, (const int32_t*)h->d_status) != cudaSuccess)
         return TT_ERR_CUDA;
     return TT_OK;

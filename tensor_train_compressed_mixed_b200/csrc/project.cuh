@@ -39,15 +39,19 @@ __device__ __forceinline__ F2 normal_tail(F2 w, F2& e)
     lo = fma2(s, both(-0.5f * kLog2eRest), lo);
     e = exp2_sum(hi, fma2(s_lost, both(-0.5f * kLog2e), lo));
     const F2 d = fma2(w, both(0.4f * 0.70710678f), both(1.f)), t = {rcp(d.x), rcp(d.y)};
-    F2 p = both(0.050265081f);
-    p = fma2(p, t, both(-0.18291025f));
-    p = fma2(p, t, both(0.16909297f));
-    p = fma2(p, t, both(-0.0056056734f));
-    p = fma2(p, t, both(0.14142445f));
-    p = fma2(p, t, both(0.16854656f));
-    p = fma2(p, t, both(0.20784137f));
-    p = fma2(p, t, both(0.22566977f));
-    p = fma2(p, t, both(0.22567585f));
+    // (constants of single instructions need no register, those of paired ones two)
+    auto poly = [](float t) {
+        float p = 0.050265081f;
+        p = fmaf(p, t, -0.18291025f);
+        p = fmaf(p, t, 0.16909297f);
+        p = fmaf(p, t, -0.0056056734f);
+        p = fmaf(p, t, 0.14142445f);
+        p = fmaf(p, t, 0.16854656f);
+        p = fmaf(p, t, 0.20784137f);
+        p = fmaf(p, t, 0.22566977f);
+        return fmaf(p, t, 0.22567585f);
+    };
+    const F2 p = {poly(t.x), poly(t.y)};
     return mul2(mul2(mul2(e, both(0.5f)), t), p);
 }
 
