@@ -38,6 +38,7 @@ struct NormPlan {
     std::vector<NormList> lists;
     std::vector<int> grids;
     int sms = 148, slots = 0;
+    bool few = false;         // so little that one cluster clips in one launch
     char* mem = nullptr;
     NormResult* result() const { return (NormResult*)mem; }
 };
@@ -47,8 +48,8 @@ cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tens
 void norm_free(NormPlan& p);
 // Sums, the norm (rounded once to *norm, which may be null) and the factor for `bound`.
 cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s);
-// Every gradient times the factor of the preceding norm_launch, in place.
-cudaError_t norm_scale(const NormPlan& p, cudaStream_t s);
+// The same, and every gradient times the factor, in place.
+cudaError_t norm_clip(const NormPlan& p, float bound, float* norm, cudaStream_t s);
 // Whether a list can be taken at all, and whether its buffers are apart.
 bool norm_tensors_ok(int32_t count, const tt_emb_norm_tensor* tensors);
 

@@ -134,20 +134,20 @@ class DenseEmbedding:
         'softcap', which is cap * tanh(z / cap).  residual, out: [..., num_rows]; residual may be out.  pre: a buffer of
         that shape that receives x tableᵀ + bias, which the backward of an activation wants.  All of these may be of any of the
         three types, and their rows may lie any one distance apart; no output may overlap another buffer."""
-        self._check(x, "x", self.dtype)
+        for t, name, kind in ((x, "x", self.dtype), (bias, "bias", None), (residual, "residual", None), (pre, "pre", None),
+                              (out, "out", out_dtype)):
+            if t is not None or name == "x":
+                self._check(t, name, kind)
         if x.dim() == 0 or x.size(-1) != self.dim:
             raise ValueError(f"x must hold rows of {self.dim} values, got {tuple(x.shape)}")
-        for t, name in ((bias, "bias"), (residual, "residual"), (pre, "pre")):
-            if t is not None:
-                self._check(t, name)
         with on_device(self.device):
             if out is None:
                 with on_stream(stream):
                     out = torch.empty(*x.shape[:-1], self.num_rows, dtype=out_dtype or self.dtype, device=self.device)
-            else:
-                self._check(out, "out", out_dtype)
             call = abi.project_call(x, self.num_rows, self.dim, out, bias, residual, pre, activation, cap)
-            self._workspace(abi.tt_emb_dense_project_workspace_size(self.handle, call), stream)
+            nbytes = abi.tt_emb_dense_project_workspace_size(self.handle, call)
+            if nbytes:
+                self._workspace(nbytes, stream)
             abi.tt_emb_dense_project(self.handle, call, abi._stream_on(stream, self.device.index))
         return out
 
@@ -179,7 +179,9 @@ class DenseEmbedding:
                 self._check(grad_x, "grad_x")
             call = abi.project_grad_call(x, self.num_rows, self.dim, grad_out, pre, activation, cap, grad_x, grad_bias, table_grad,
                                          accumulate)
-            self._workspace(abi.tt_emb_dense_project_backward_workspace_size(self.handle, call), stream)
+            nbytes = abi.tt_emb_dense_project_backward_workspace_size(self.handle, call)
+            if nbytes:
+                self._workspace(nbytes, stream)
             abi.tt_emb_dense_project_backward(self.handle, call, abi._stream_on(stream, self.device.index))
         return grad_x
 
