@@ -164,6 +164,8 @@ struct PackArgs {
     void* narrow;         // [rows][ld] of narrow_type; may be null
     uint16_t* wide;       // [parts][rows][ld] bf16 terms; may be null
     float* sums;          // [blocks of rows][cols] sums over a block's rows; may be null
+    void* total;          // with one block of rows: the bias's gradient itself; may be null
+    int32_t total_type, accumulate;
     const int32_t* status;
     int32_t narrow_type, parts;
     int32_t vectors;      // every row begins at a place that vector loads can take, and is a multiple of eight values
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_pack(const __grid_constant__ Pa
             pack_row(g, r, c, x, z, sum);
         }
     }
-    if (!g.sums) return;
+    if (!g.sums && !g.total) return;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[warp][i * 32 + lane] = sum[i];
@@ -338,7 +340,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_pack(const __grid_constant__ Pa
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) all += part[i][threadIdx.x];
     const int64_t at = c0 + (threadIdx.x & 31) * 8 + (threadIdx.x >> 5);
-    if (at < g.cols) g.sums[by * g.cols + at] = all;
+    if (at >= g.cols) return;
+    if (g.total) store_any(g.total, g.total_type, at, g.accumulate ? all + load_any(g.total, g.total_type, at) : all);
+    else g.sums[by * g.cols + at] = all;
 }
 
 // The sums of the blocks of rows: 32 columns of a block of threads, each warp an eighth of the sums.
@@ -469,6 +473,7 @@ struct Space {
 };
 
 // One matrix of a call in the forms that its products want.
+constexpr int64_t kAlone = 32;       // rows whose sums one block of rows makes, which saves the launch that joins several
 struct Forms {
     PackArgs pack = {};
     bool packs = false;       // the pass over the values is needed
@@ -512,9 +517,10 @@ Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t co
     const int64_t across = ceil_div(cols, kPackCols);
     int64_t down = ceil_div((int64_t)sms * 8, across);
     if (down > ceil_div(rows, 8)) down = ceil_div(rows, 8);
+    if (want_sums && rows <= kAlone) down = 1;
     if (down > 65535) down = 65535;
     f.pack.each = ceil_div(rows, down);
-    if (want_sums) f.pack.sums = (float*)w.take(ceil_div(rows, f.pack.each) * cols * 4);
+    if (want_sums && f.pack.each < rows) f.pack.sums = (float*)w.take(ceil_div(rows, f.pack.each) * cols * 4);
     auto vectors = [&](const void* p, int type, int64_t stride) {
         return ((uintptr_t)p & 15) == 0 && (stride * type_bytes(type) & 15) == 0;
     };
@@ -642,7 +648,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     const bool big_x = a->grad_x && !small_x, big_t = a->table_grad && !small_t;
     const bool wide_x = big_x && wide_for(a->grad_x_type), wide_t = big_t && wide_for(h->grad_type);
     Space w(size ? nullptr : h->project_ws);
-    const Forms d = forms_of(w, u, plain, a->n, h->rows, type, (big_x && !wide_x) || (big_t && !wide_t), wide_x || wide_t ? 3 : 0, a->grad_bias != nullptr,
+    Forms d = forms_of(w, u, plain, a->n, h->rows, type, (big_x && !wide_x) || (big_t && !wide_t), wide_x || wide_t ? 3 : 0, a->grad_bias != nullptr,
                              h->num_sms, h->d_status);
     const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, type, big_x && !wide_x, wide_x, h->num_sms, h->d_status);
     const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, type, big_t && !wide_t, wide_t, h->num_sms, h->d_status);
@@ -651,6 +657,11 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         return TT_OK;
     }
     if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
+    if (a->grad_bias && !d.pack.sums) {
+        d.pack.total = a->grad_bias;
+        d.pack.total_type = a->grad_bias_type;
+        d.pack.accumulate = a->accumulate;
+    }
     bool early = false;
     if (const int rc = launch_pack({&d, &t, &x}, h->num_sms, &early, s)) return rc;
     SmallArgs g = {};
@@ -699,7 +710,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         p.e = et;
         if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
     }
-    if (a->grad_bias &&
+    if (d.pack.sums &&
         launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, 32), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
                      a->grad_bias, a->grad_bias_type, a->accumulate, (const int32_t*)h->d_status) != cudaSuccess)
         return TT_ERR_CUDA;
