@@ -370,20 +370,6 @@ __device__ __forceinline__ bool all_agree(int part, bool yes)
 }
 __device__ __forceinline__ void part_sync(int part) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + part) : "memory"); }
 
-// asks for the residual of a tile that comes later: what its rows wait for is then in L2
-template <int BN, int kAll, typename Place>
-__device__ __forceinline__ void prefetch_residual(const Args& g, const Place& place, int tile)
-{
-    if (!g.e.residual) return;
-    int c0, r0;
-    place(tile, c0, r0);
-    const int size = g.e.residual_type == TT_F32 ? 4 : 2, lines = size;       // of 128 bytes, in a row of the tile
-    for (int i = threadIdx.x - 64; i < BN * lines; i += kAll) {
-        const int64_t r = r0 + i / lines, c = c0 + i % lines * (128 / size);
-        if (r < g.rows && c < g.cols) asm volatile("prefetch.global.L2 [%0];" ::"l"((const char*)g.e.residual + (r * g.e.residual_stride + c) * size));
-    }
-}
-
 template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
 __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __grid_constant__ Args g)
 {
@@ -558,10 +544,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             // each part of the tile gives kLoad of the passing rows in turn
             const int row = r0 + mine / kLoad * kPart + mine % kLoad;
             Four res[kRows];
-            if (split == 1) {
-                fetch_rows(g.e, l, row, min(kRows, height - row), res);
-                if (tile + step < tiles) prefetch_residual<BN, kFinish * 32>(g, place, tile + step);
-            }
+            if (split == 1) fetch_rows(g.e, l, row, min(kRows, height - row), res);
             float acc[kLong ? kPart : 1];
             bool ok = true;
             int buf = 0;
