@@ -221,3 +221,13 @@ def test_refusals():
             GradNorm([x]).clip(bound)
         with pytest.raises(TTEmbError):
             AdamW([x.clone()], [x]).step(0.1, max_norm=bound)
+
+
+def test_more_than_32_bits_of_values():
+    x = torch.zeros(2 ** 31 + 77, dtype=BF16, device="cuda")
+    x[-3:] = 4.0
+    x[5] = 3.0
+    o = GradNorm([x])
+    want = math.sqrt(3 * 16 + 9)
+    assert abs(float(o.clip(want / 2)) - want) <= NORM_TOL * want
+    assert x[-3:].tolist() == [2.0] * 3 and float(x[5]) == 1.5 and not x[6:-3].any()

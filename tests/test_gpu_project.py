@@ -8,6 +8,8 @@ A result is rounded once, by half a step of its type.  Where a 16-bit result's p
 is off by half a step of that type.
 """
 import math
+import os
+import subprocess
 
 import pytest
 import torch
@@ -408,3 +410,68 @@ def test_a_training_run_of_a_tied_table():
     clip = GradNorm([grad, gb])
     assert abs(float(clip.clip(0.5 * float(total))) - float(total)) <= 4 * STEP * float(total)
     assert abs(float(clip.norm()) - 0.5 * float(total)) <= 8 * STEP * float(total)
+
+
+@pytest.mark.parametrize("n,rows,dim", [(33000, 66000, 8), (3, 2 ** 21 + 5, 1032)])
+def test_offsets_past_32_bits(n, rows, dim):
+    """Results, or the table and its gradient, of more than 2^31 values: the last rows and columns."""
+    g = torch.Generator(device="cuda").manual_seed(12)
+    w = torch.zeros(rows, dim, dtype=BF16, device="cuda")
+    grad = torch.zeros(rows, dim, dtype=BF16, device="cuda")
+    e = DenseEmbedding(rows, dim, dtype=BF16)
+    e.set_table(w, grad=grad)
+    w[-300:] = _randn(g, 300, dim, dtype=BF16)
+    x = _randn(g, n, dim, dtype=BF16)
+    y = e.project(x)
+    want = x[-3:].double() @ w[-300:].double().t()
+    tol = _sum_tol(x[-3:].double(), w[-300:].double().t(), dim)
+    _inside(y[-3:, -300:], want, tol + _half_step(BF16) * (want.abs() + tol) + _least(BF16))
+    assert not y[-3:, :-300].any() and not y[:3, :-300].any()
+    y.zero_()
+    y[-3:, -300:] = _randn(g, 3, 300, dtype=BF16)
+    gx = e.project_backward(x, y, grad_x=torch.empty(n, dim, device="cuda"))
+    e.sync()
+    d = y[-3:, -300:].double()
+    _inside(gx[-3:], d @ w[-300:].double(), _sum_tol(d, w[-300:].double(), rows if rows < 10 ** 5 else 300 * 64))
+    want = d.t() @ x[-3:].double()
+    tol = _sum_tol(d.t(), x[-3:].double(), n)
+    _inside(grad[-300:], want, tol + _half_step(BF16) * (want.abs() + tol) + _least(BF16))
+    assert not grad[:-300].any()
+
+
+NO_CLUSTERS = """
+import ctypes
+import torch
+from tensor_train_compressed_mixed_b200 import DenseEmbedding, GradNorm
+fake = ctypes.CDLL(None)
+g = torch.Generator(device="cuda").manual_seed(1)
+rand = lambda *s, t=torch.float32: torch.randn(*s, generator=g, device="cuda").to(t)
+for kind, n, rows, dim in ((torch.bfloat16, 3000, 9000, 192), (torch.bfloat16, 9, 700, 4096), (torch.float32, 200, 500, 1000)):
+    w, x, dy = rand(rows, dim, t=kind), rand(n, dim, t=kind), rand(n, rows, t=kind)
+    got = []
+    for none_fits in (1, 0):
+        fake.fake_no_clusters(none_fits)
+        before = fake.fake_cluster_launches()
+        e = DenseEmbedding(rows, dim, dtype=kind)
+        e.set_table(w, grad=torch.empty(rows, dim, device="cuda"))
+        y = e.project(x, out_dtype=torch.float32)
+        gx = e.project_backward(x, dy, grad_x=torch.empty(n, dim, device="cuda"))
+        norm = GradNorm([e.grad])
+        size = norm.clip(1.0).clone()
+        short = GradNorm([rand(100)])
+        short.clip(1.0)
+        e.sync()
+        assert (fake.fake_cluster_launches() > before) == (not none_fits)
+        got.append((y, gx, e.grad, size))
+    for a, b in zip(*got):
+        assert (a - b).abs().max() <= 1e-4 * b.abs().max()
+"""
+
+
+def test_a_device_without_clusters(tmp_path):
+    """Where no cluster of blocks fits the device, single blocks take the tiles and two launches clip."""
+    from test_gpu_fake_runtime import _run
+    so = tmp_path / "libfake.so"
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run(["gcc", "-O1", "-fPIC", "-shared", "-I/usr/local/cuda/include", os.path.join(here, "fake_cudart.c"), "-o", str(so), "-ldl"], check=True)
+    _run(str(so), NO_CLUSTERS)
