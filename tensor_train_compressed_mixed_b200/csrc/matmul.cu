@@ -139,7 +139,7 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// a row's sums from another block's shared memory, as row_sums takes them, added to z
+// a row's sums from another block's shared memory, as row_sums takes them
 __device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, int lane, F2 (&z)[2])
 {
     const uint32_t there = in_block(row, rank);
@@ -150,8 +150,8 @@ __device__ __forceinline__ void peer_four(uint32_t row, int rank, bool vectors, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x[i]) : "r"(there + (lane + 32 * i) * 4) : "memory");
     }
-    z[0] = add2(z[0], {x[0], x[1]});
-    z[1] = add2(z[1], {x[2], x[3]});
+    z[0] = {x[0], x[1]};
+    z[1] = {x[2], x[3]};
 }
 
 // Descriptor of an operand tile with the 128-byte swizzle.  k along the rows of 128 bytes: groups of eight rows 1024 bytes
@@ -621,25 +621,36 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     if (split > 1) {
         cluster_sync();
         if (warp >= 2 && !skip && !gone) {
-            constexpr int kBatch = BN >= 64 ? 2 : 1;
             int c0, r0;
             place(start, c0, r0);
             const Lane l(g.e, c0, g.cols, g.vectors, lane);
-            const int each = BN / split;
-            for (int j = (warp - 2) * kBatch; j < each; j += kFinish * kBatch) {
-                const int r = r0 + rank * each + j, rows = max(0, min(min(kBatch, each - j), (int)g.rows - r));
-                Four res[kBatch];
-                fetch_rows(g.e, l, r, rows, res);
-                F2 z[kBatch][2] = {};
-#pragma unroll 2
-                for (int s = 0; s < split; ++s) {
+            // eight pieces of rows on their way to a warp, of all blocks of the cluster
+            auto join = [&](auto of) {
+                constexpr int kBlocks = decltype(of)::value, kBatch = 8 / kBlocks, kEach = BN / kBlocks;
+#pragma unroll 1
+                for (int j = (warp - 2) * kBatch; j < kEach; j += kFinish * kBatch) {
+                    const int r = r0 + rank * kEach + j, rows = max(0, min(min(kBatch, kEach - j), (int)g.rows - r));
+                    Four res[kBatch];
+                    fetch_rows(g.e, l, r, rows, res);
+                    F2 x[kBatch][kBlocks][2], z[kBatch][2];
 #pragma unroll
-                    for (int i = 0; i < kBatch; ++i) {
-                        peer_four(ring + ((rank * each + j + (i < rows ? i : 0)) * kCols) * 4, s, l.vectors, lane, z[i]);
-                    }
+                    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                        for (int s = 0; s < kBlocks; ++s) peer_four(ring + ((rank * kEach + j + (i < rows ? i : 0)) * kCols) * 4, s, l.vectors, lane, x[i][s]);
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            z[i][h] = x[i][0][h];
+#pragma unroll
+                            for (int s = 1; s < kBlocks; ++s) z[i][h] = add2(z[i][h], x[i][s][h]);
+                        }
+                    finish_rows<kBatch, !kLong>(g.e, l, r, rows, z, res);
                 }
-                finish_rows<kBatch, !kLong>(g.e, l, r, rows, z, res);
-            }
+            };
+            if (split == 2) join(std::integral_constant<int, 2>());
+            else if (split == 4) join(std::integral_constant<int, 4>());
+            else join(std::integral_constant<int, 8>());
         }
         cluster_sync();
     }
