@@ -16,7 +16,8 @@
 // Two blocks on neighbouring SMs make a pair where there are many tiles: one tile of 256 columns, of which each block brings its half of
 // both operands and finishes its half, so that a block reads half of B.
 // Where there are fewer tiles than SMs a cluster of blocks shares one tile's k, and its partial sums are added through
-// distributed shared memory in the order of the blocks.
+// distributed shared memory in the order of the blocks.  Where there are so few tiles and so many k that clusters leave most SMs
+// idle, k is cut into slices whose sums go to the workspace; a second kernel adds them in their order and finishes them.
 #include <cuda.h>
 
 #include <math.h>
@@ -33,6 +34,7 @@ namespace {
 
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
+constexpr double kMostSums = 1 << 26;      // of all slices together
 constexpr int kGroup = 16;           // row tiles that are taken in turn before the next column tile: they stay in L2
 
 struct Args {
@@ -46,6 +48,7 @@ struct Args {
     uint32_t idesc;
     int32_t tiles_c, tiles_r;
     int32_t split;        // blocks of a cluster that share a tile
+    int32_t slices;       // of k, each a tile of its own whose sums go to rows of their own
     int32_t vectors;      // four neighbouring values of a row of the result, residual and pre make one access
 };
 
@@ -421,32 +424,39 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(other) : "r"(in_block(smem_u32((const void*)&gone), rank ^ 1)) : "memory");
         skip |= (int)other;
     }
-    const int first = kPair ? 0 : (int)((int64_t)g.blocks * rank / split), last = kPair ? g.blocks : (int)((int64_t)g.blocks * (rank + 1) / split);
-    const int start = blockIdx.x / share, step = (int)gridDim.x / share, tiles = skip ? 0 : g.tiles_c * g.tiles_r;
+    const int start = blockIdx.x / share, step = (int)gridDim.x / share, slices = kPair ? 1 : g.slices;
+    const int tiles = skip ? 0 : g.tiles_c * g.tiles_r * slices;
     const int group_tiles = kGroup * g.tiles_c;
-    // a tile's place: groups of kGroup row tiles, in each a column tile for all of the group's rows after another
-    auto place = [&](int tile, int& c0, int& r0) {
-        const int group = tile / group_tiles, in = tile - group * group_tiles;
+    // A tile's place: groups of kGroup row tiles, in each a column tile for all of the group's rows after another; and its k.
+    struct Tile { int c0, r0, first, last, shift; };
+    auto place = [&](int tile) {
+        Tile t;
+        const int slice = slices > 1 ? tile % slices : 0, at = slices > 1 ? tile / slices : tile;
+        const int group = at / group_tiles, in = at - group * group_tiles;
         const int here = min(kGroup, g.tiles_r - group * kGroup);
-        c0 = in / here * (kCols * kSide) + (kPair ? rank * kCols : 0);
-        r0 = (group * kGroup + in % here) * BN;
+        t.c0 = in / here * (kCols * kSide) + (kPair ? rank * kCols : 0);
+        t.r0 = (group * kGroup + in % here) * BN;
+        const int of = slices > 1 ? slices : split, which = slices > 1 ? slice : kPair ? 0 : rank;
+        t.first = (int)((int64_t)g.blocks * which / of);
+        t.last = (int)((int64_t)g.blocks * (which + 1) / of);
+        t.shift = slice * (int)g.rows;
+        return t;
     };
 
-    const int chunk = kLong ? g.chunk : last - first;
+    const int chunk = kLong ? g.chunk : g.blocks;      // blocks of k whose sums stay in tensor memory
     if (warp == 0 && elected()) {
         int n = 0;      // stages filled
         bool ok = true;
         for (int tile = start; ok && tile < tiles; tile += step) {
-            int c0, r0;
-            place(tile, c0, r0);
-            for (int k0 = first; ok && k0 < last; k0 += chunk) {
-                const int end = min(k0 + chunk, last);
+            const Tile at = place(tile);
+            const int c0 = at.c0, rb = at.r0 + (kPair ? rank * kOwn : 0);
+            for (int k0 = at.first; ok && k0 < at.last; k0 += chunk) {
+                const int end = min(k0 + chunk, at.last);
                 for (int kb = k0; ok && kb < end; ++kb)
                     for (int t = 0; t < terms; ++t, ++n) {
                         const int s = n % kStages, k = kb * kDeep;
                         if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
                         const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2, bar = kPair ? in_block(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                        const int rb = r0 + (kPair ? rank * kOwn : 0);
                         const bool with_a = !kLong || t < g.a_terms, with_b = !kLong || t < g.b_terms;
                         if (!kPair || rank == 0) expect(&full[s], ((with_a ? kCols : 0) + (with_b ? kOwn : 0)) * kDeep * 2 * kSide);
                         if (with_a) {
@@ -473,9 +483,10 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     } else if (warp == 1 && (!kPair || rank == 0) && elected()) {
         int n = 0, seq = 0;
         bool ok = true;
-        for (int tile = start; ok && tile < tiles; tile += step)
-            for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
-                const int buf = seq & 1, end = min(k0 + chunk, last);
+        for (int tile = start; ok && tile < tiles; tile += step) {
+            const Tile at = place(tile);
+            for (int k0 = at.first; ok && k0 < at.last; k0 += chunk, ++seq) {
+                const int buf = seq & 1, end = min(k0 + chunk, at.last);
                 if (seq >= 2 && !wait_for<kPair>(&sums_empty[buf], (seq / 2 - 1) & 1, &gone)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t sums = tmem + buf * BN;
@@ -525,24 +536,25 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                 }
                 if (ok) commit<kPair>(&sums_full[buf]);
             }
+        }
         if (gone == kTimedOut) {    // products on their way end before tensor memory is given up
             commit<kPair>(&drained);
             mbar_wait(&drained, 0);
         }
     } else if (warp >= 2) {
         const int quarter = warp & 3, part = kFinish == 4 ? 0 : (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + part * kPart;
         float* const passing = (float*)(raw + (ring - smem_u32(raw)) + kStages * kStage);
         constexpr int kLoad = kPass / (kFinish / 4);              // rows that a warp takes from tensor memory at a time
         const int mine = (warp - 2) * kRows;                      // the first of the passing rows that this warp finishes
         const int height = (int)g.rows;
         int seq = 0;
         for (int tile = start; tile < tiles; tile += step) {
-            int c0, r0;
-            place(tile, c0, r0);
-            const Lane l(g.e, c0, g.cols, g.vectors, lane);
+            const Tile at = place(tile);
+            const int first = at.first, last = at.last;
+            const Lane l(g.e, at.c0, g.cols, g.vectors, lane);
             // each part of the tile gives kLoad of the passing rows in turn
-            const int row = r0 + mine / kLoad * kPart + mine % kLoad;
+            const int row = at.r0 + mine / kLoad * kPart + mine % kLoad;
             Four res[kRows];
             if (split == 1) fetch_rows(g.e, l, row, min(kRows, height - row), res);
             float acc[kLong ? kPart : 1];
@@ -557,12 +569,12 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
 #pragma unroll
                     for (int j = 0; j < kPart; j += kLoad) {
                         uint32_t x[kLoad];
-                        load_columns<kLoad>(at + buf * BN + j, x);
+                        load_columns<kLoad>(lanes + buf * BN + j, x);
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                         for (int i = 0; i < kLoad; ++i) acc[j + i] = (k0 == first ? 0.f : acc[j + i]) + __uint_as_float(x[i]);
                         if (terms > 1) {
-                            load_columns<kLoad>(at + 2 * BN + buf * BN + j, x);
+                            load_columns<kLoad>(lanes + 2 * BN + buf * BN + j, x);
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                             for (int i = 0; i < kLoad; ++i) acc[j + i] += __uint_as_float(x[i]);
@@ -591,7 +603,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
 #pragma unroll
                     for (int i = 0; i + kLoad < kPart; ++i) acc[i] = acc[i + kLoad];      // registers have no index
                 } else {
-                    load_columns<kLoad>(at + buf * BN + j, x);
+                    load_columns<kLoad>(lanes + buf * BN + j, x);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     if (j + kLoad == kPart) {
                         tc_fence_before();
@@ -612,7 +624,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                 F2 z[kRows][2];
 #pragma unroll
                 for (int i = 0; i < kRows; ++i) row_sums(passing + (mine + i) * kCols, l.vectors, lane, z[i]);
-                finish_rows<kRows, !kLong>(g.e, l, r, rows, z, res);
+                finish_rows<kRows, !kLong>(g.e, l, r + at.shift, rows, z, res);
                 if (j + kLoad < kPart) fetch_rows(g.e, l, r + kLoad, min(kRows, height - r - kLoad), res);
             }
         }
@@ -621,15 +633,14 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
     if (split > 1) {
         cluster_sync();
         if (warp >= 2 && !skip && !gone) {
-            int c0, r0;
-            place(start, c0, r0);
-            const Lane l(g.e, c0, g.cols, g.vectors, lane);
+            const Tile at = place(start);
+            const Lane l(g.e, at.c0, g.cols, g.vectors, lane);
             // eight pieces of rows on their way to a warp, of all blocks of the cluster
             auto join = [&](auto of) {
                 constexpr int kBlocks = decltype(of)::value, kBatch = 8 / kBlocks, kEach = BN / kBlocks;
 #pragma unroll 1
                 for (int j = (warp - 2) * kBatch; j < kEach; j += kFinish * kBatch) {
-                    const int r = r0 + rank * kEach + j, rows = max(0, min(min(kBatch, kEach - j), (int)g.rows - r));
+                    const int r = at.r0 + rank * kEach + j, rows = max(0, min(min(kBatch, kEach - j), (int)g.rows - r));
                     Four res[kBatch];
                     fetch_rows(g.e, l, r, rows, res);
                     F2 x[kBatch][kBlocks][2], z[kBatch][2];
@@ -663,6 +674,34 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         else tmem_dealloc(tmem, columns);
     }
     if (threadIdx.x == 0 && gone == kTimedOut) raise_error(g.status, TT_ERR_TIMEOUT, (int)blockIdx.x);
+}
+
+// The slices' sums added in their order and finished: 32 columns of a row of a block of threads, each warp an eighth of the slices.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) k_join(const float* sums, int slices, int64_t rows, int64_t cols, const __grid_constant__ Epilogue e,
+                                                       const int32_t* status)
+{
+    wait_for_kernel_before();
+    if (has_error(status)) return;
+    __shared__ float part[kJoinThreads / 32][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t across = ceil_div(cols, 32), r = blockIdx.x / across, c = blockIdx.x % across * 32 + lane;
+    float sum = 0.f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int i = warp; i < slices; i += kJoinThreads / 32) sum += sums[(i * rows + r) * cols + c];
+    }
+    part[warp][lane] = sum;
+    __syncthreads();
+    if (warp > 0 || c >= cols) return;
+#pragma unroll
+    for (int i = 1; i < kJoinThreads / 32; ++i) sum += part[i][lane];
+    float z = r == e.skip_row ? 0.f : sum;
+    if (e.bias) z += load_any(e.bias, e.bias_type, c);
+    if (e.pre) store_any(e.pre, e.pre_type, r * e.pre_stride + c, z);
+    float y = activate(e.act, F2{z, z}, e.cap).x;
+    if (e.residual) y += load_any(e.residual, e.residual_type, r * e.residual_stride + c);
+    store_any(e.out, e.out_type, r * e.out_stride + c, y);
 }
 
 using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -744,7 +783,7 @@ cudaError_t launch(Args& g, const MatmulFits& fits, bool early, cudaStream_t s)
     auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
     const cudaError_t e = allow(kernel, block_bytes<BN, kPair>(), told);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)g.tiles_c * g.tiles_r;
+    const int64_t tiles = (int64_t)g.tiles_c * g.tiles_r * g.slices;
     const int64_t blocks = kPair ? 2 * min64(tiles, fits.one[1]) : g.split > 1 ? tiles * g.split : min64(tiles, (int64_t)fits.sms * fit_of(BN));
     const Launch l(blocks, threads_of(BN), block_bytes<BN, kPair>(), kPair ? 2 : g.split, early, s);
     return cudaLaunchKernelEx(&l.c, kernel, g);
@@ -778,58 +817,88 @@ MatmulFits matmul_fits(int sms)
     return f;
 }
 
-int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s)
+// products of the operands' terms: of terms i and j with i + j < 3
+static int products_of(const Product& p)
+{
+    int n = 0;
+    for (int i = 0; i < p.a.parts; ++i)
+        for (int j = 0; j < p.b.parts && i + j < 3; ++j) ++n;
+    return n;
+}
+
+MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits)
+{
+    MatmulPlan q;
+    const int64_t blocks = ceil_div(p.deep, kDeep);
+    const int products = products_of(p);
+    // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
+    // off by up to 2^-23 of it.
+    q.by_chunks = p.e.out_type == TT_F32 || (p.e.pre_type == TT_F32 && p.has_pre) || products > 1 || blocks > 1024;
+    // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  64 k take what their
+    // products take (half a cycle for each row and 16 k, at 128 columns), or what their bytes take, about 55 a cycle and SM; a tile
+    // a few cycles for each of its rows; what a launch, a cluster and a joining kernel take comes from measurement.
+    double best = 0.0;
+    for (int n = p.b_mn ? 64 : 16; n <= (q.by_chunks ? 128 : 256); n *= 2) {
+        const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n), work = 2.0 * n * products;
+        const double each = std::max(work, (kCols * p.a.parts + n * p.b.parts) * (kDeep * 2 / 55.0));
+        const int fit = fit_of(n);
+        const int(&room)[4] = fit > 1 ? fits.two : fits.one;
+        for (int i = 0; i < 4; ++i) {
+            const int k = 1 << i;
+            if (i > 0 && (tiles > room[i] || blocks < 2 * k)) break;
+            // two blocks on an SM share its bandwidth
+            const double turns = fit > 1 ? std::max(1.0, tiles * k / fits.sms) : ceil(tiles * k / fits.sms);
+            const double t = turns * ((double)blocks / k * each + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
+            if (q.height == 0 || t < best) best = t, q.height = n, q.split = k, q.slices = 1, q.pair = false;
+        }
+        const int k = (int)std::min((double)fits.sms * fit / tiles, blocks / 4.0);
+        if (k > 8 && (double)p.rows * p.cols * k <= kMostSums) {
+            const double t = std::max(1.0, tiles * k / fits.sms) * ((double)blocks / k * each + 8.0 * n) + 1500.0 + 6000.0;
+            if (t < best) best = t, q.height = n, q.split = 1, q.slices = k, q.pair = false;
+        }
+        if (n >= 128 && fits.one[1] > 0) {
+            const double count = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
+            const double two = std::max(work, (kCols * p.a.parts + n / 2 * p.b.parts) * (kDeep * 2 / 55.0));
+            const double t = ceil(count / fits.one[1]) * ((double)blocks * two + 8.0 * n) + 2000.0;
+            if (t < best) best = t, q.height = n, q.split = q.slices = 1, q.pair = true;
+        }
+    }
+    q.scratch = q.slices > 1 ? (size_t)(q.slices * p.rows * p.cols) * sizeof(float) : 0;
+    return q;
+}
+
+int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s)
 {
     Args g = {};
     g.e = p.e;
+    if (q.slices > 1) {
+        g.e = {};
+        g.e.out = scratch;
+        g.e.out_type = TT_F32;
+        g.e.out_stride = p.cols;
+        g.e.skip_row = -1;
+    }
     g.status = status;
     g.rows = p.rows;
     g.cols = p.cols;
     g.a_terms = p.a.parts;
     g.b_terms = p.b.parts;
-    int pairs = 0;
-    for (int i = 0; i < p.a.parts; ++i)
-        for (int j = 0; j < p.b.parts && i + j < 3; ++j) ++pairs;
     const int64_t blocks = ceil_div(p.deep, kDeep);
-    // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
-    // off by up to 2^-23 of it.
-    const bool by_chunks = p.e.out_type == TT_F32 || (p.e.pre && p.e.pre_type == TT_F32) || pairs > 1 || blocks > 1024;
+    const int bn = q.height;
+    const bool pair = q.pair;
     g.chunk = 4;
-    // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  64 k take what their
-    // products take (half a cycle for each row and 16 k, at 128 columns), or what their bytes take, about 55 a cycle and SM.
-    int bn = 0, split = 1;
-    bool pair = false;
-    double best = 0.0;
-    for (int n = p.b_mn ? 64 : 16; n <= (by_chunks ? 128 : 256); n *= 2) {
-        const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n), products = 2.0 * n * pairs;
-        const double each = std::max(products, (kCols * p.a.parts + n * p.b.parts) * (kDeep * 2 / 55.0));
-        const int(&room)[4] = fit_of(n) > 1 ? fits.two : fits.one;
-        for (int i = 0; i < 4; ++i) {
-            const int k = 1 << i;
-            if (i > 0 && (tiles > room[i] || blocks < 2 * k)) break;
-            // two blocks on an SM share its bandwidth
-            const double turns = fit_of(n) > 1 ? std::max(1.0, tiles * k / fits.sms) : ceil(tiles * k / fits.sms);
-            const double t = turns * ((double)blocks / k * each + 8.0 * n) + 1500.0 + (k > 1 ? 1500.0 : 0.0);
-            if (bn == 0 || t < best) best = t, bn = n, split = k, pair = false;
-        }
-        if (n >= 128 && fits.one[1] > 0) {
-            const double count = (double)ceil_div(p.cols, 2 * kCols) * ceil_div(p.rows, n);
-            const double two = std::max(products, (kCols * p.a.parts + n / 2 * p.b.parts) * (kDeep * 2 / 55.0));
-            const double t = ceil(count / fits.one[1]) * ((double)blocks * two + 8.0 * n) + 2000.0;
-            if (t < best) best = t, bn = n, split = 1, pair = true;
-        }
-    }
     const int64_t tiles_c = ceil_div(p.cols, pair ? 2 * kCols : kCols), tiles_r = ceil_div(p.rows, bn);
     if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / 8) return TT_ERR_ARG;   // sizes that no device holds
     g.blocks = (int)blocks;
     g.tiles_c = (int)tiles_c;
     g.tiles_r = (int)tiles_r;
-    g.split = split;
-    auto four = [&](const void* q, int type, int64_t stride) {
-        return !q || (((uintptr_t)q & (4 * type_bytes(type) - 1)) == 0 && (stride & 3) == 0);
+    g.split = q.split;
+    g.slices = q.slices;
+    auto four = [&](const void* x, int type, int64_t stride) {
+        return !x || (((uintptr_t)x & (4 * type_bytes(type) - 1)) == 0 && (stride & 3) == 0);
     };
-    g.vectors = (p.cols & 3) == 0 && four(p.e.out, p.e.out_type, p.e.out_stride) && four(p.e.pre, p.e.pre_type, p.e.pre_stride) &&
-                four(p.e.residual, p.e.residual_type, p.e.residual_stride);
+    g.vectors = (p.cols & 3) == 0 && four(g.e.out, g.e.out_type, g.e.out_stride) && four(g.e.pre, g.e.pre_type, g.e.pre_stride) &&
+                four(g.e.residual, g.e.residual_type, g.e.residual_stride);
     g.idesc = (1u << 4) | (p.a.type == TT_BF16 ? 1u << 7 | 1u << 10 : 0u) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u) |
               (uint32_t)(bn >> 3) << 17 | (uint32_t)((pair ? 2 * kCols : kCols) >> 4) << 24;
     if (!encode(&g.a, p.a, p.a_mn ? kDeep : kCols) || !encode(&g.b, p.b, p.b_mn ? kDeep : pair ? bn / 2 : bn)) return TT_ERR_CUDA;
@@ -850,7 +919,11 @@ int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early
         using No = std::false_type;
         return p.b_mn ? by_height(Yes(), Yes(), chunks) : p.a_mn ? by_height(Yes(), No(), chunks) : by_height(No(), No(), chunks);
     };
-    const cudaError_t e = by_chunks ? by_sides(std::true_type()) : by_sides(std::false_type());
+    cudaError_t e = q.by_chunks ? by_sides(std::true_type()) : by_sides(std::false_type());
+    if (e == cudaSuccess && q.slices > 1) {
+        const int64_t blocks_of_rows = p.rows * ceil_div(p.cols, 32);      // (below kMostSums)
+        e = launch_early(k_join, (unsigned)blocks_of_rows, kJoinThreads, s, (const float*)scratch, (int)q.slices, p.rows, p.cols, p.e, (const int32_t*)status);
+    }
     return e == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 

@@ -30,11 +30,18 @@ MatmulFits matmul_fits(int sms);     // of the current device
 // [deep][cols]; B is [rows][deep], or with b_mn [deep][rows].  Both of one type.
 struct Product {
     Operand a, b;
-    bool a_mn = false, b_mn = false;
+    bool a_mn = false, b_mn = false, has_pre = false;
     int64_t rows = 0, cols = 0, deep = 0;
     Epilogue e = {};
 };
+// How a product of these sizes, types and terms (no pointer of it is looked at) is computed.
+struct MatmulPlan {
+    int height = 0, split = 1, slices = 1;
+    bool pair = false, by_chunks = false;
+    size_t scratch = 0;       // device memory for slices' sums
+};
+MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits);
 // early: a kernel of the same call is before it on the stream.  Returns a tt_status.
-int matmul(const Product& p, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s);
+int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status, const MatmulFits& fits, bool early, cudaStream_t s);
 
 }  // namespace tt

@@ -594,13 +594,6 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     const bool wide = h->table_type == TT_F32;
     const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, h->table_type, !wide, wide, h->num_sms, h->d_status);
     const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, h->table_type, !wide, wide, h->num_sms, h->d_status);
-    if (size) {
-        *size = w.used;
-        return TT_OK;
-    }
-    if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
-    bool packed = false;
-    if (const int rc = launch_pack({&t, &x}, h->num_sms, &packed, s)) return rc;
     Product p;
     p.a = wide ? t.wide : t.narrow;
     p.b = wide ? x.wide : x.narrow;
@@ -608,7 +601,17 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     p.cols = h->rows;
     p.deep = h->dim;
     p.e = e;
-    return matmul(p, h->d_status, h->fits, packed, s);
+    p.has_pre = a->pre != nullptr;
+    const MatmulPlan plan = matmul_plan(p, h->fits);
+    void* const scratch = w.take(plan.scratch);
+    if (size) {
+        *size = w.used;
+        return TT_OK;
+    }
+    if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
+    bool packed = false;
+    if (const int rc = launch_pack({&t, &x}, h->num_sms, &packed, s)) return rc;
+    return matmul(p, plan, scratch, h->d_status, h->fits, packed, s);
 }
 
 int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* size, cudaStream_t s)
@@ -652,6 +655,19 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
                              h->num_sms, h->d_status);
     const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, type, big_x && !wide_x, wide_x, h->num_sms, h->d_status);
     const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, type, big_t && !wide_t, wide_t, h->num_sms, h->d_status);
+    Product px, pt;
+    px.cols = pt.cols = h->dim;
+    px.a_mn = pt.a_mn = pt.b_mn = true;
+    px.rows = pt.deep = a->n;
+    px.deep = pt.rows = h->rows;
+    px.a = wide_x ? t.wide : t.narrow;
+    px.b = wide_x ? d.wide : d.narrow;
+    pt.a = wide_t ? x.wide : x.narrow;
+    pt.b = wide_t ? d.wide : d.narrow;
+    px.e = ex;
+    pt.e = et;
+    const MatmulPlan plan_x = big_x ? matmul_plan(px, h->fits) : MatmulPlan(), plan_t = big_t ? matmul_plan(pt, h->fits) : MatmulPlan();
+    void* const scratch = w.take(plan_x.scratch > plan_t.scratch ? plan_x.scratch : plan_t.scratch);     // one after the other
     if (size) {
         *size = w.used;
         return TT_OK;
@@ -689,27 +705,12 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         g.deep = a->n;
         if (const int rc = launch_product(g, s)) return rc;
     }
-    Product p;
-    p.cols = h->dim;
-    p.a_mn = true;
     if (big_x) {
-        p.a = wide_x ? t.wide : t.narrow;
-        p.b = wide_x ? d.wide : d.narrow;
-        p.rows = a->n;
-        p.deep = h->rows;
-        p.e = ex;
-        if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
+        if (const int rc = matmul(px, plan_x, scratch, h->d_status, h->fits, early, s)) return rc;
         early = true;
     }
-    if (big_t) {
-        p.a = wide_t ? x.wide : x.narrow;
-        p.b = wide_t ? d.wide : d.narrow;
-        p.b_mn = true;
-        p.rows = h->rows;
-        p.deep = a->n;
-        p.e = et;
-        if (const int rc = matmul(p, h->d_status, h->fits, early, s)) return rc;
-    }
+    if (big_t)
+        if (const int rc = matmul(pt, plan_t, scratch, h->d_status, h->fits, early, s)) return rc;
     if (d.pack.sums &&
         launch_early(k_bias_grad, (unsigned)ceil_div(h->rows, 32), kThreads, s, (const float*)d.pack.sums, ceil_div(a->n, d.pack.each), h->rows,
                      a->grad_bias, a->grad_bias_type, a->accumulate, (const int32_t*)h->d_status) != cudaSuccess)

@@ -77,7 +77,7 @@ FORWARD = [
     (700, 3, 900, BF16, BF16, None, True, True, True, 1), (2050, 1030, 520, BF16, BF16, "gelu", True, True, False, 0),
     (8, 5000, 8192, BF16, F32, "softcap", False, False, False, 0), (100, 50, 20000, F16, F32, None, True, False, False, 0),
     (3001, 9000, 200, BF16, BF16, "gelu", True, True, True, 0), (3000, 9002, 136, F16, F32, "silu", True, True, False, 2),
-    (4100, 4360, 72, F32, F32, None, False, False, False, 0), (31, 70000, 128, F16, F16, "relu", True, True, True, 0),
+    (4100, 4360, 72, F32, F32, None, False, False, False, 0), (4, 20, 30000, BF16, BF16, "gelu", True, True, True, 1), (31, 70000, 128, F16, F16, "relu", True, True, True, 0),
 ]
 
 
@@ -122,7 +122,8 @@ BACKWARD = [
     (2050, 1030, 128, BF16, BF16, BF16, F32, None, True, True, 0, 1029), (9, 30000, 64, BF16, BF16, BF16, BF16, None, False, False, 0, None),
     (4000, 40, 24, BF16, BF16, BF16, BF16, "gelu", True, False, 0, None), (500, 257, 520, F32, BF16, BF16, BF16, "gelu", True, False, 0, None),
     (4100, 3000, 1288, BF16, BF16, BF16, BF16, "silu", True, True, 0, 17), (5000, 2600, 1100, F16, F16, F32, F32, None, False, False, 4, None),
-    (30, 9000, 2000, F32, F32, F32, F32, None, True, False, 0, None), (513, 640, 264, F16, F16, F32, F32, None, False, False, 0, None),
+    (2, 40000, 100, BF16, BF16, BF16, BF16, "relu", True, False, 0, None), (20, 50000, 33, F32, F32, F32, F32, None, True, True, 3, 9),
+    (5, 30011, 64, F16, F16, F32, F16, "gelu", True, False, 1, None), (30, 9000, 2000, F32, F32, F32, F32, None, True, False, 0, None), (513, 640, 264, F16, F16, F32, F32, None, False, False, 0, None),
 ]
 
 
