@@ -13,6 +13,13 @@
 // (x = t0 + t1 + t2, each 2^-8 of the one before) bring each term once for all products that it is part of: those of terms i and j
 // with i + j < 3, as the others are below fp32's last bit.  All but the first terms' product are summed in an area of their
 // own, so that few steps are made on a large sum.
+//
+// What bounds it.  Many k: the tensor cores and the power limit (4096 x 32000 x 4096 bf16: 1.58 PFLOP/s cold, 1.38 in a row,
+// as the library's product).  Copies and products are issued by an elected thread: behind a comparison of the thread's number the
+// same instructions took 763 us where they now take 680.  Few k: the finishing, whose instructions fill half of the issue slots
+// (8192 x 4096 x 128 fp16 with gelu, residual and pre: 73 us, 60 without gelu, 31 for the bytes).  Few rows: memory (8 rows of
+// 32000 x 4096 bf16: 50 us, 5.3 TB/s).
+//
 // Two blocks on neighbouring SMs make a pair where there are many tiles: one tile of 256 columns, of which each block brings its half of
 // both operands and finishes its half, so that a block reads half of B.
 // Where there are fewer tiles than SMs a cluster of blocks shares one tile's k, and its partial sums are added through
@@ -32,10 +39,15 @@ using namespace tt;
 
 namespace {
 
+// With kLong, blocks of 64 k whose sum is formed in tensor memory: 16 steps, each of which cuts off up to 2^-23 of it.  With 16 blocks
+// the gradients of 301 x 5003 x 257 fp32 were off by 1.2e-6 of their norm, with 4 by 2.5e-7 (fp32 products: 4.9e-7).
+constexpr int kChunk = 4;
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
 constexpr double kMostSums = 1 << 26;      // of all slices together
-constexpr int kGroup = 16;           // row tiles that are taken in turn before the next column tile: they stay in L2
+// Row tiles that are taken in turn before the next column tile, so that they stay in L2 (4096 x 32000 x 4096 bf16: 671 us, 736 with
+// 4 of them and 880 with one).
+constexpr int kGroup = 16;
 
 struct Args {
     CUtensorMap a, b;
@@ -44,7 +56,6 @@ struct Args {
     int64_t rows, cols;
     int32_t blocks;       // of 64 k
     int32_t a_terms, b_terms;     // of the operands' values, 1 to 3; with kLong only
-    int32_t chunk;        // blocks of k whose sums stay in tensor memory
     uint32_t idesc;
     int32_t tiles_c, tiles_r;
     int32_t split;        // blocks of a cluster that share a tile
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         return t;
     };
 
-    const int chunk = kLong ? g.chunk : g.blocks;      // blocks of k whose sums stay in tensor memory
+    const int chunk = kLong ? kChunk : g.blocks;       // blocks of k whose sums stay in tensor memory
     if (warp == 0 && elected()) {
         int n = 0;      // stages filled
         bool ok = true;
@@ -886,7 +897,6 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
     const int64_t blocks = ceil_div(p.deep, kDeep);
     const int bn = q.height;
     const bool pair = q.pair;
-    g.chunk = 4;
     const int64_t tiles_c = ceil_div(p.cols, pair ? 2 * kCols : kCols), tiles_r = ceil_div(p.rows, bn);
     if (blocks > INT32_MAX / 8 || tiles_c * tiles_r > INT32_MAX / 8) return TT_ERR_ARG;   // sizes that no device holds
     g.blocks = (int)blocks;
