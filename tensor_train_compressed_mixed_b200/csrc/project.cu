@@ -25,8 +25,7 @@ constexpr int kThreads = 256;
 // ---------------------------------------------------------------------------
 // products on the FP32 pipes: any type, stride and size
 // ---------------------------------------------------------------------------
-constexpr int kSide = 64, kDeep = 32;
-constexpr int kEach = kSide * kDeep / kThreads;     // values of an operand that a thread brings
+constexpr int kDeep = 32;
 
 struct SmallArgs {
     Matrix a, b;          // A(r, k) and B(c, k)
@@ -37,93 +36,101 @@ struct SmallArgs {
     const int32_t* status;
 };
 
-template <typename T>
-__device__ __forceinline__ void bring(const void* p, const int64_t (&at)[kEach], float (&x)[kEach])
+// A thread's N values of a tile, `step` apart from the first one's place on, all on their way before the first is used; the first n
+// of them are in the matrix, the others 0.
+template <typename T, int N>
+__device__ __forceinline__ void bring(const T* p, int64_t step, int n, float (&x)[N])
 {
-    T q[kEach];
+    T q[N];
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) q[i] = at[i] >= 0 ? ((const T*)p)[at[i]] : T(0.f);
+    for (int i = 0; i < N; ++i, p += step) q[i] = i < n ? *p : T(0.f);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) x[i] = to_f32(q[i]);
+    for (int i = 0; i < N; ++i) x[i] = to_f32(q[i]);
 }
-// a thread's values of a tile, all on their way before the first is used; zero where the place is none
-__device__ __forceinline__ void bring(const void* p, int type, const int64_t (&at)[kEach], float (&x)[kEach])
+template <int N>
+__device__ __forceinline__ void bring(const void* p, int type, int64_t at, int64_t step, int n, float (&x)[N])
 {
-    if (type == TT_BF16) bring<__nv_bfloat16>(p, at, x);
-    else if (type == TT_F16) bring<__half>(p, at, x);
-    else bring<float>(p, at, x);
+    if (type == TT_BF16) bring((const __nv_bfloat16*)p + at, step, n, x);
+    else if (type == TT_F16) bring((const __half*)p + at, step, n, x);
+    else bring((const float*)p + at, step, n, x);
 }
+// places o, o + step, .. below `end`
+__device__ __forceinline__ int count_below(int64_t o, int step, int64_t end) { return o >= end ? 0 : (int)min64(64, (end - o + step - 1) / step); }
 
-// A block computes 64 x 64 values, a thread 4 x 4 of them, 32 steps of k at a time through shared memory; the next 32 are
+// A block computes R x C values, a thread 4 x 4 of them, 32 steps of k at a time through shared memory; the next 32 are
 // on their way meanwhile.
+template <int R, int C>
 __global__ void __launch_bounds__(kThreads) k_product(const __grid_constant__ SmallArgs g)
 {
     if (has_error(g.status)) return;
-    __shared__ float As[kDeep][kSide + 4], Bs[kDeep][kSide + 4];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t tiles_c = ceil_div(g.cols, kSide);
-    const int64_t r0 = blockIdx.x / tiles_c * kSide, c0 = blockIdx.x % tiles_c * kSide;
+    static_assert(R * C == 16 * kThreads, "");
+    constexpr int kAcross = C / 4;      // threads side by side
+    constexpr int kA = R * kDeep / kThreads, kB = C * kDeep / kThreads;     // values of the operands that a thread brings
+    __shared__ __align__(16) float As[kDeep][R + 4], Bs[kDeep][C + 1];      // (writes along k fall into different banks)
+    const int tx = threadIdx.x % kAcross, ty = threadIdx.x / kAcross;
+    const int64_t tiles_c = ceil_div(g.cols, C);
+    const int64_t r0 = blockIdx.x / tiles_c * R, c0 = blockIdx.x % tiles_c * C;
+    const bool busy = r0 + ty * 4 < g.rows;
     float acc[4][4] = {};
     // neighbouring threads read neighbouring places: along k, or along r and c where those are the near ones
     const bool a_k = g.a.sk == 1, b_k = g.b.sk == 1;
-    float a[kEach], z[kEach], b[kEach];
+    float a[kA], z[kA], b[kB];
+    // the thread's values: of one k and every eighth r or c, or of one r or c and every kThreads / R-th k
+    const int ka = a_k ? threadIdx.x % kDeep : threadIdx.x / R, kb = b_k ? threadIdx.x % kDeep : threadIdx.x / C;
+    const int64_t ra = r0 + (a_k ? threadIdx.x / kDeep : threadIdx.x % R), cb = c0 + (b_k ? threadIdx.x / kDeep : threadIdx.x % C);
+    constexpr int kEighth = kThreads / kDeep;
+    const int n_r = a_k ? count_below(ra, kEighth, g.rows) : ra < g.rows ? kA : 0, n_c = b_k ? count_below(cb, kEighth, g.cols) : cb < g.cols ? kB : 0;
     auto fetch = [&](int64_t k0) {
-        int64_t at[kEach];
-#pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const int i = threadIdx.x + q * kThreads;
-            const int64_t k = k0 + (b_k ? i % kDeep : i / kSide), c = c0 + (b_k ? i / kDeep : i % kSide);
-            at[q] = c < g.cols && k < g.deep ? c * g.b.si + k * g.b.sk : -1;
-        }
-        bring(g.b.p, g.b.type, at, b);
-        int64_t pre_at[kEach];
-#pragma unroll
-        for (int q = 0; q < kEach; ++q) {
-            const int i = threadIdx.x + q * kThreads;
-            const int64_t k = k0 + (a_k ? i % kDeep : i / kSide), r = r0 + (a_k ? i / kDeep : i % kSide);
-            const bool in = r < g.rows && k < g.deep;
-            at[q] = in ? r * g.a.si + k * g.a.sk : -1;
-            pre_at[q] = in ? r * g.pre_si + k * g.pre_sk : -1;
-        }
-        bring(g.a.p, g.a.type, at, a);
-        if (g.u.act != TT_ACT_NONE) bring(g.u.pre, g.u.pre_type, pre_at, z);
+        const int64_t i = k0 + kb, j = k0 + ka;
+        bring(g.b.p, g.b.type, cb * g.b.si + i * g.b.sk, b_k ? kEighth * g.b.si : kThreads / C * g.b.sk,
+              b_k ? (i < g.deep ? n_c : 0) : min(n_c, count_below(i, kThreads / C, g.deep)), b);
+        const int n = a_k ? (j < g.deep ? n_r : 0) : min(n_r, count_below(j, kThreads / R, g.deep));
+        bring(g.a.p, g.a.type, ra * g.a.si + j * g.a.sk, a_k ? kEighth * g.a.si : kThreads / R * g.a.sk, n, a);
+        if (g.u.act != TT_ACT_NONE) bring(g.u.pre, g.u.pre_type, ra * g.pre_si + j * g.pre_sk, a_k ? kEighth * g.pre_si : kThreads / R * g.pre_sk, n, z);
     };
     fetch(0);
     for (int64_t k0 = 0; k0 < g.deep; k0 += kDeep) {
         if (g.u.act != TT_ACT_NONE) {
 #pragma unroll
-            for (int q = 0; q < kEach; q += 2) {
+            for (int q = 0; q < kA; q += 2) {
                 const F2 d = slope(g.u.act, F2{z[q], z[q + 1]}, g.u.cap);
                 a[q] *= d.x;
                 a[q + 1] *= d.y;
             }
         }
 #pragma unroll
-        for (int q = 0; q < kEach; ++q) {
+        for (int q = 0; q < kA; ++q) {
             const int i = threadIdx.x + q * kThreads;
-            As[a_k ? i % kDeep : i / kSide][a_k ? i / kDeep : i % kSide] = a[q];
-            Bs[b_k ? i % kDeep : i / kSide][b_k ? i / kDeep : i % kSide] = b[q];
+            As[a_k ? i % kDeep : i / R][a_k ? i / kDeep : i % R] = a[q];
+        }
+#pragma unroll
+        for (int q = 0; q < kB; ++q) {
+            const int i = threadIdx.x + q * kThreads;
+            Bs[b_k ? i % kDeep : i / C][b_k ? i / kDeep : i % C] = b[q];
         }
         __syncthreads();
         if (k0 + kDeep < g.deep) fetch(k0 + kDeep);
+        if (busy) {
 #pragma unroll 8
-        for (int k = 0; k < kDeep; ++k) {
-            float x[4], y[4];
+            for (int k = 0; k < kDeep; ++k) {
+                float x[4], y[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = As[k][ty * 4 + i];
+                for (int i = 0; i < 4; ++i) x[i] = As[k][ty * 4 + i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] = Bs[k][tx + 16 * j];
+                for (int j = 0; j < 4; ++j) y[j] = Bs[k][tx + kAcross * j];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+            }
         }
         __syncthreads();
     }
+    if (!busy) return;
     const Epilogue& e = g.e;
 #pragma unroll 1
     for (int j = 0; j < 4; ++j) {
-        const int64_t c = c0 + tx + 16 * j;
+        const int64_t c = c0 + tx + kAcross * j;
         if (c >= g.cols) break;
         const int64_t r = r0 + ty * 4;
         const int rows = (int)min64(4, g.rows - r);
@@ -451,11 +458,12 @@ int check_backward(tt_emb_dense_t h, const tt_emb_project_grad* a)
 // ---------------------------------------------------------------------------
 // calls
 // ---------------------------------------------------------------------------
+template <int R, int C>
 int launch_product(const SmallArgs& g, cudaStream_t s)
 {
-    const int64_t blocks = ceil_div(g.rows, kSide) * ceil_div(g.cols, kSide);
+    const int64_t blocks = ceil_div(g.rows, R) * ceil_div(g.cols, C);
     if (blocks > INT32_MAX) return TT_ERR_ARG;     // sizes that no device holds
-    k_product<<<(unsigned)blocks, kThreads, 0, s>>>(g);
+    k_product<R, C><<<(unsigned)blocks, kThreads, 0, s>>>(g);
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
@@ -558,6 +566,16 @@ int launch_pack(std::initializer_list<const Forms*> forms, int sms, bool* any, c
 // Products small enough for the FP32 pipes, a block of which takes about a microsecond for 64 of k
 bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 64 && rows * cols <= 65536; }
 
+// Few rows by a table that would have to be laid out for the tensor cores: reading it once as it lies costs less than
+// writing and reading that (26 rows by 84712 x 280 fp32: 70 us so, 107 laid out), unless so few of its rows make so long sums that
+// the blocks are few and their steps many.
+constexpr int kFewRows = 32;
+bool is_few(tt_emb_dense_t h, int64_t n)
+{
+    const bool as_it_lies = h->table_type != TT_F32 && mappable(h->table, h->dim, h->rows, h->dim);
+    return !as_it_lies && n <= kFewRows && h->dim <= 4096 && ceil_div(h->rows, 128) * 2 >= h->num_sms;
+}
+
 Matrix matrix(const void* p, int64_t si, int64_t sk, int type) { return {p, si, sk, type}; }
 
 int enter(tt_emb_dense_t h, cudaStream_t s)
@@ -578,7 +596,8 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     if (a->n == 0) return TT_OK;
     const Epilogue e = {a->out, a->residual, a->pre, a->bias, a->out_stride, a->residual_stride, a->pre_stride, -1,
                         a->out_type, a->residual_type, a->pre_type, a->bias_type, a->activation, a->cap};
-    if (is_small(a->n, h->rows, h->dim)) {
+    const bool few = is_few(h, a->n);
+    if (few || is_small(a->n, h->rows, h->dim)) {
         if (size) return TT_OK;
         SmallArgs g = {};
         g.a = matrix(a->x, a->x_stride, 1, h->table_type);
@@ -588,7 +607,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
         g.cols = h->rows;
         g.deep = h->dim;
         g.status = h->d_status;
-        return launch_product(g, s);
+        return few ? launch_product<kFewRows, 128>(g, s) : launch_product<64, 64>(g, s);
     }
     Space w(size ? nullptr : h->project_ws);
     const bool wide = h->table_type == TT_F32;
@@ -692,7 +711,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         g.rows = a->n;
         g.cols = h->dim;
         g.deep = h->rows;
-        if (const int rc = launch_product(g, s)) return rc;
+        if (const int rc = launch_product<64, 64>(g, s)) return rc;
     }
     if (small_t) {
         g.a = matrix(u.up, 1, u.up_stride, u.up_type);
@@ -703,7 +722,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         g.rows = h->rows;
         g.cols = h->dim;
         g.deep = a->n;
-        if (const int rc = launch_product(g, s)) return rc;
+        if (const int rc = launch_product<64, 64>(g, s)) return rc;
     }
     if (big_x) {
         if (const int rc = matmul(px, plan_x, scratch, h->d_status, h->fits, early, s)) return rc;

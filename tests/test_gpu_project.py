@@ -77,7 +77,7 @@ FORWARD = [
     (700, 3, 900, BF16, BF16, None, True, True, True, 1), (2050, 1030, 520, BF16, BF16, "gelu", True, True, False, 0),
     (8, 5000, 8192, BF16, F32, "softcap", False, False, False, 0), (100, 50, 20000, F16, F32, None, True, False, False, 0),
     (3001, 9000, 200, BF16, BF16, "gelu", True, True, True, 0), (3000, 9002, 136, F16, F32, "silu", True, True, False, 2),
-    (4100, 4360, 72, F32, F32, None, False, False, False, 0), (4, 20, 30000, BF16, BF16, "gelu", True, True, True, 1), (31, 70000, 128, F16, F16, "relu", True, True, True, 0),
+    (4100, 4360, 72, F32, F32, None, False, False, False, 0), (32, 30000, 97, F32, F32, "gelu", True, True, True, 3), (7, 20011, 515, BF16, BF16, None, True, True, False, 1), (4, 20, 30000, BF16, BF16, "gelu", True, True, True, 1), (31, 70000, 128, F16, F16, "relu", True, True, True, 0),
 ]
 
 
