@@ -2,7 +2,8 @@
 //
 //   norm = sqrt(sum over all values of g^2),   factor = bound / norm where norm > bound, else 1
 //
-// The sums read every gradient once and memory bounds them.  A thread squares and adds the 32 or 64 values of its
+// The sums read every gradient once and memory bounds them (55 M fp32 values: 46 us, 4.8 TB/s; 403 M bf16 values: 107 to 140), the
+// scaling reads and writes them (80 us, 5.5 TB/s).  A thread squares and adds the 32 or 64 values of its
 // eight vectors in fp32 and goes on in fp64: squares of values beyond 2^63, or all below 2^-45, leave fp32, and such
 // a group is squared again in fp64, so that the norm is right over the whole range of the types.  Each block has a
 // place for its sum, and the last block adds them in their order: the same gradients give the same bits.
