@@ -481,7 +481,9 @@ struct Space {
 };
 
 // One matrix of a call in the forms that its products want.
-constexpr int64_t kAlone = 32;       // rows whose sums one block of rows makes, which saves the launch that joins several
+// Rows whose sums one block of rows makes, which saves the launch that joins several: 2 us of the host's, while the device takes as long
+// (32 rows by 4000 x 256 bf16, all gradients: 17.2 us, 16.9 with it).
+constexpr int64_t kAlone = 32;
 struct Forms {
     PackArgs pack = {};
     bool packs = false;       // the pass over the values is needed
@@ -563,7 +565,9 @@ int launch_pack(std::initializer_list<const Forms*> forms, int sms, bool* any, c
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-// Products small enough for the FP32 pipes, a block of which takes about a microsecond for 64 of k
+// Products small enough for the FP32 pipes, where the tensor cores would want an operand laid out first: one launch instead of two, and as
+// long on the device (64 x 1000 x 64 fp32: 7.4 us either way; 16 x 4000 x 64: 6.7 and 8.9; 256 x 256 x 64: 7.6 and 6.8). Operands that
+// can be read as they lie take the tensor cores at any size (16 x 96 x 48 bf16: 3.9 us, 6.8 by the FP32 pipes).
 bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 64 && rows * cols <= 65536; }
 
 // Few rows by a table that would have to be laid out for the tensor cores: reading it once as it lies costs less than
@@ -597,7 +601,8 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     const Epilogue e = {a->out, a->residual, a->pre, a->bias, a->out_stride, a->residual_stride, a->pre_stride, -1,
                         a->out_type, a->residual_type, a->pre_type, a->bias_type, a->activation, a->cap};
     const bool few = is_few(h, a->n);
-    if (few || is_small(a->n, h->rows, h->dim)) {
+    const bool as_they_lie = h->table_type != TT_F32 && mappable(h->table, h->dim, h->rows, h->dim) && mappable(a->x, a->x_stride, a->n, h->dim);
+    if (few || (!as_they_lie && is_small(a->n, h->rows, h->dim))) {
         if (size) return TT_OK;
         SmallArgs g = {};
         g.a = matrix(a->x, a->x_stride, 1, h->table_type);
@@ -666,7 +671,9 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     const int type = h->table_type;
     const bool plain = type != TT_F32 && a->grad_out_type == type && a->activation == TT_ACT_NONE;
     auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || (type == TT_F16 && a->grad_out_type == TT_F32))); };
-    const bool small_x = a->grad_x && is_small(a->n, h->dim, h->rows), small_t = a->table_grad && is_small(h->rows, h->dim, a->n);
+    const bool dz_lies = plain && mappable(a->grad_out, a->grad_out_stride, a->n, h->rows);
+    const bool small_x = a->grad_x && is_small(a->n, h->dim, h->rows) && !(dz_lies && mappable(h->table, h->dim, h->rows, h->dim));
+    const bool small_t = a->table_grad && is_small(h->rows, h->dim, a->n) && !(dz_lies && mappable(a->x, a->x_stride, a->n, h->dim));
     const bool big_x = a->grad_x && !small_x, big_t = a->table_grad && !small_t;
     const bool wide_x = big_x && wide_for(a->grad_x_type), wide_t = big_t && wide_for(h->grad_type);
     Space w(size ? nullptr : h->project_ws);
