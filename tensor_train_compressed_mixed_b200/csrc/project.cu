@@ -490,8 +490,8 @@ struct Forms {
     Operand narrow, wide;
 };
 
-// forms of u's values [rows][cols], which are 16-bit values as they lie if `plain`
-Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t cols, int table_type, bool want_narrow, int wide_parts, bool want_sums,
+// forms of u's values [rows][cols], which are values of the narrow form's 16 bits as they lie if `plain`
+Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t cols, int narrow_type, bool want_narrow, int wide_parts, bool want_sums,
                int sms, int32_t* status)
 {
     Forms f;
@@ -504,11 +504,11 @@ Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t co
     f.pack.cols = cols;
     f.pack.ld = ld;
     f.pack.status = status;
-    f.pack.narrow_type = table_type;
+    f.pack.narrow_type = narrow_type;
     // one bf16 term is the value itself
     if (wide_parts == 1) want_narrow = true;
     if (want_narrow) {
-        f.narrow.type = table_type;
+        f.narrow.type = narrow_type;
         f.narrow.outer = rows;
         f.narrow.inner = cols;
         f.narrow.stride = direct ? u.up_stride : ld;
@@ -667,18 +667,21 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     }
     // Which operands each product takes.  Where grad_out is of the table's 16 bits and is dz itself, as they lie.  Where dz
     // is computed, a 16-bit result takes it rounded to the table's type: its own rounding is as large.  fp32
-    // results keep fp32's accuracy by terms, and so does what an fp16 table gets from fp32, whose range fp16 has not.
-    const int type = h->table_type;
-    const bool plain = type != TT_F32 && a->grad_out_type == type && a->activation == TT_ACT_NONE;
-    auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || (type == TT_F16 && a->grad_out_type == TT_F32))); };
+    // results keep fp32's accuracy by terms, and so does what an fp16 table gets from fp32 or bf16, whose range fp16 has not.
+    const int type = h->table_type, up = a->grad_out_type;
+    const bool computed = a->activation != TT_ACT_NONE, plain = type != TT_F32 && up == type && !computed;
+    auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || (type == TT_F16 && up != TT_F16))); };
+    // bf16 terms that hold dz: bf16 values are one, as they lie or copied
+    const int terms = computed || up == TT_F32 ? 3 : up == TT_F16 ? 2 : 1;
+    const int dz_type = terms == 1 ? TT_BF16 : type;
     const bool dz_lies = plain && mappable(a->grad_out, a->grad_out_stride, a->n, h->rows);
     const bool small_x = a->grad_x && is_small(a->n, h->dim, h->rows) && !(dz_lies && mappable(h->table, h->dim, h->rows, h->dim));
     const bool small_t = a->table_grad && is_small(h->rows, h->dim, a->n) && !(dz_lies && mappable(a->x, a->x_stride, a->n, h->dim));
     const bool big_x = a->grad_x && !small_x, big_t = a->table_grad && !small_t;
     const bool wide_x = big_x && wide_for(a->grad_x_type), wide_t = big_t && wide_for(h->grad_type);
     Space w(size ? nullptr : h->project_ws);
-    Forms d = forms_of(w, u, plain, a->n, h->rows, type, (big_x && !wide_x) || (big_t && !wide_t), wide_x || wide_t ? 3 : 0, a->grad_bias != nullptr,
-                             h->num_sms, h->d_status);
+    Forms d = forms_of(w, u, !computed && up != TT_F32 && up == dz_type, a->n, h->rows, dz_type, (big_x && !wide_x) || (big_t && !wide_t),
+                       wide_x || wide_t ? terms : 0, a->grad_bias != nullptr, h->num_sms, h->d_status);
     const Forms t = forms_of(w, h->table, h->dim, h->rows, h->dim, type, big_x && !wide_x, wide_x, h->num_sms, h->d_status);
     const Forms x = forms_of(w, a->x, a->x_stride, a->n, h->dim, type, big_t && !wide_t, wide_t, h->num_sms, h->d_status);
     Product px, pt;

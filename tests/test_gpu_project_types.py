@@ -1,0 +1,71 @@
+"""Gradients of the table's projection where dz, the table and the results are of different types: over the whole range of dz's values,
+and with no fewer bits of dz than the result has.
+
+Tolerances are those of test_gpu_project.py: a sum of k products in fp32 is off by k + 2 steps of 2^-23 of the sum of magnitudes and
+2^-22 for operands as terms, dz in fp32 by 32 steps, and a result is rounded once.
+"""
+import pytest
+import torch
+
+from test_gpu_project import BF16, F16, F32, STEP, _act64, _half_step, _inside, _least, _randn, _sum_tol, _table
+
+pytestmark = pytest.mark.gpu
+
+
+def _backward(n, rows, dim, kind, dy, gx, gw, act=None, extra=0, by=1.0, bias=False, seed=1):
+    """One backward pass on a table of values about `by`, compared with 64 bits: results hold dz in full."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    e, w = _table(rows, dim, kind, g, grad=torch.empty(rows, dim, dtype=gw, device="cuda"))
+    w.copy_(_randn(g, rows, dim, dtype=kind, by=by))
+    x = _randn(g, n, dim + extra, dtype=kind, by=by)[:, :dim]
+    pre = _randn(g, n, rows, dtype=kind, by=3.0) if act else None
+    cap = 2.5 if act == "softcap" else None
+    gb = torch.empty(rows, device="cuda") if bias else None
+    got = e.project_backward(x, dy, pre=pre, activation=act, cap=cap, grad_x=torch.empty(n, dim, dtype=gx, device="cuda"), grad_bias=gb)
+    e.sync()
+    d, off = dy.double(), torch.zeros(n, rows, dtype=torch.float64, device="cuda")
+    if act:
+        z = pre.double().requires_grad_()
+        d, = torch.autograd.grad(_act64(act, z, cap), z, d)
+        off = 32 * STEP * dy.double().abs()
+    for got, a, o, b, k in ((got, d, off, w, rows), (e.grad, d.t(), off.t(), x, n)):
+        want = a @ b.double()
+        tol = _sum_tol(a, b.double(), k) + o @ b.double().abs()
+        _inside(got, want, tol + _half_step(got.dtype) * (want.abs() + tol) + _least(got.dtype))
+    if bias:
+        _inside(gb, d.sum(0), d.abs().sum(0) * (n + 4) * STEP + off.sum(0))
+
+
+def _spread(n, rows, dtype, low, high, extra=0, seed=2):
+    """Values of either sign, of magnitudes from 10^low to 10^high."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = 10.0 ** (low + (high - low) * torch.rand(n, rows + extra, generator=g, device="cuda")) * torch.randn(n, rows + extra, generator=g, device="cuda").sign()
+    return x.to(dtype)[:, :rows]
+
+
+# by the tensor cores as they lie and copied, by few tiles and slices of k, and by the FP32 pipes
+SIZES = [(200, 1000, 512, 0), (65, 129, 257, 3), (2050, 1030, 128, 8), (5, 30011, 64, 1), (7, 70, 40, 0), (1, 1, 1, 0), (4100, 3000, 1288, 0)]
+
+
+@pytest.mark.parametrize("n,rows,dim,extra", SIZES)
+@pytest.mark.parametrize("low,high,by", [(-9, 5, 1e-3), (-9, -7, 1.0), (4, 5, 1e-3), (-2, 2, 1.0)])
+@pytest.mark.parametrize("result", [BF16, F16, F32])
+def test_fp16_table_with_bf16_gradients(n, rows, dim, extra, low, high, by, result):
+    """bf16 gradients go far beyond fp16's range on either side; the sums need not."""
+    if result == F16:       # no fp16 result of a table this large leaves the type: sums of up to 4100 values
+        by = min(by, 1.0 / 10.0 ** high)
+    _backward(n, rows, dim, F16, _spread(n, rows, BF16, low, high, extra), result, result, extra=extra, by=by, bias=True)
+
+
+@pytest.mark.parametrize("result", [BF16, F32])
+@pytest.mark.parametrize("act", ["gelu", "softcap"])
+def test_fp16_table_with_bf16_gradients_and_an_activation(act, result):
+    for n, rows, dim, extra in ((200, 1000, 512, 0), (65, 129, 257, 3)):
+        _backward(n, rows, dim, F16, _spread(n, rows, BF16, -9, 5, extra), result, result, act=act, extra=extra, by=1e-3, bias=True)
+
+
+@pytest.mark.parametrize("up", [BF16, F16])
+@pytest.mark.parametrize("kind,result", [(F32, F32), (F32, BF16), (BF16, F32), (F16, F32)])
+def test_gradients_of_fewer_bits_than_the_table_or_the_result(kind, result, up):
+    for n, rows, dim, extra in SIZES[:4]:
+        _backward(n, rows, dim, kind, _spread(n, rows, up, -3, 1, extra), result, result, extra=extra, bias=True)
