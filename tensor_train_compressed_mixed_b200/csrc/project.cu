@@ -667,10 +667,11 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     }
     // Which operands each product takes.  Where grad_out is of the table's 16 bits and is dz itself, as they lie.  Where dz
     // is computed, a 16-bit result takes it rounded to the table's type: its own rounding is as large.  fp32
-    // results keep fp32's accuracy by terms, and so does what an fp16 table gets from fp32 or bf16, whose range fp16 has not.
+    // results keep fp32's accuracy by terms, and so does what an fp16 table gets from anything but fp16 values as they are: fp32 and
+    // bf16 have more range, and products with slopes leave fp16's at both ends.
     const int type = h->table_type, up = a->grad_out_type;
     const bool computed = a->activation != TT_ACT_NONE, plain = type != TT_F32 && up == type && !computed;
-    auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || (type == TT_F16 && up != TT_F16))); };
+    auto wide_for = [&](int result) { return type == TT_F32 || (!plain && (result == TT_F32 || type == TT_F16)); };
     // bf16 terms that hold dz: bf16 values are one, as they lie or copied
     const int terms = computed || up == TT_F32 ? 3 : up == TT_F16 ? 2 : 1;
     const int dz_type = terms == 1 ? TT_BF16 : type;

@@ -69,3 +69,15 @@ def test_fp16_table_with_bf16_gradients_and_an_activation(act, result):
 def test_gradients_of_fewer_bits_than_the_table_or_the_result(kind, result, up):
     for n, rows, dim, extra in SIZES[:4]:
         _backward(n, rows, dim, kind, _spread(n, rows, up, -3, 1, extra), result, result, extra=extra, bias=True)
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "softcap", "relu"])
+@pytest.mark.parametrize("low,high,by", [(-7, -5, 1.0), (4.6, 4.8, 1e-3)])
+@pytest.mark.parametrize("result", [BF16, F16, F32])
+def test_fp16_gradients_times_slopes_at_the_ends_of_the_range(act, low, high, by, result):
+    """Small gradients times small slopes go below fp16's least value, and large ones times gelu's largest, 1.13, beyond its greatest."""
+    if result == F16:
+        by = min(by, 1e-4)
+    for n, rows, dim, extra in SIZES:
+        if (n, rows) != (1, 1):
+            _backward(n, rows, dim, F16, _spread(n, rows, F16, low, high, extra), result, result, act=act, extra=extra, by=by, bias=True)
