@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 
 def _backward(n, rows, dim, kind, dy, gx, gw, act=None, extra=0, by=1.0, bias=False, seed=1):
-    """One backward pass on a table of values about `by`, compared with 64 bits: results hold dz in full."""
+    """One backward pass on a table of values about `by`, compared with 64 bits."""
     g = torch.Generator(device="cuda").manual_seed(seed)
     e, w = _table(rows, dim, kind, g, grad=torch.empty(rows, dim, dtype=gw, device="cuda"))
     w.copy_(_randn(g, rows, dim, dtype=kind, by=by))
@@ -30,6 +30,8 @@ def _backward(n, rows, dim, kind, dy, gx, gw, act=None, extra=0, by=1.0, bias=Fa
         off = 32 * STEP * dy.double().abs()
     for got, a, o, b, k in ((got, d, off, w, rows), (e.grad, d.t(), off.t(), x, n)):
         want = a @ b.double()
+        if kind == got.dtype == BF16 and (act or dy.dtype != BF16):     # dz in as many bits as this result
+            o = o + _half_step(BF16) * (a.abs() + o) + _least(BF16)
         tol = _sum_tol(a, b.double(), k) + o @ b.double().abs()
         _inside(got, want, tol + _half_step(got.dtype) * (want.abs() + tol) + _least(got.dtype))
     if bias:
@@ -81,3 +83,13 @@ def test_fp16_gradients_times_slopes_at_the_ends_of_the_range(act, low, high, by
     for n, rows, dim, extra in SIZES:
         if (n, rows) != (1, 1):
             _backward(n, rows, dim, F16, _spread(n, rows, F16, low, high, extra), result, result, act=act, extra=extra, by=by, bias=True)
+
+
+@pytest.mark.parametrize("act,up", [("gelu", BF16), ("silu", F16), ("softcap", F32), (None, F16), (None, F32)])
+@pytest.mark.parametrize("gx,gw", [(F16, F16), (F16, BF16), (BF16, F16)])
+def test_fp16_results_beside_a_bf16_table(act, up, gx, gw):
+    """dz of eight bits would cost a result of eleven three of them."""
+    for n, rows, dim, extra in SIZES:
+        g = torch.Generator(device="cuda").manual_seed(3)
+        dy = _randn(g, n, rows + extra, dtype=up)[:, :rows]
+        _backward(n, rows, dim, BF16, dy, gx, gw, act=act, extra=extra, by=0.5, bias=True)
