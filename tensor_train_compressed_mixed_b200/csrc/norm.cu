@@ -56,8 +56,9 @@ __device__ __forceinline__ const NormRec& tensor_of(const NormList& L, int64_t t
     return L.r[lo];
 }
 
-// Values of a tensor: `lead` single ones, whole vectors from there on, single ones behind the last.
-template <typename T>
+// Values of a tensor: `lead` single ones, whole vectors from there on, single ones behind the last.  kStay: nothing in this launch
+// writes them, so that they may come by the read-only path.
+template <typename T, bool kStay>
 __device__ __forceinline__ double tile_squares(const NormRec& r, int64_t tile)
 {
     const T* g = (const T*)r.grad;
@@ -66,7 +67,10 @@ __device__ __forceinline__ double tile_squares(const NormRec& r, int64_t tile)
     const int64_t v0 = (tile - r.tile0) * kTile + threadIdx.x;
     uint4 w[kVectors];
 #pragma unroll
-    for (int k = 0; k < kVectors; ++k) w[k] = v0 + k * kThreads < vectors ? __ldg((const uint4*)(body + v0 + k * kThreads)) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kVectors; ++k) {
+        const uint4* p = (const uint4*)(body + v0 + k * kThreads);
+        w[k] = v0 + k * kThreads >= vectors ? make_uint4(0, 0, 0, 0) : kStay ? __ldg(p) : *p;
+    }
     F2 a[4] = {both(0.f), both(0.f), both(0.f), both(0.f)};
     bool some = false;          // gradients of rows that no token touched are all zero
 #pragma unroll
@@ -129,9 +133,9 @@ __global__ void __launch_bounds__(kThreads, kFit) k_norm(const __grid_constant__
     for (int64_t b = blockIdx.x; b < L.tiles; b += gridDim.x) {
         const NormRec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
-        if (r.type == TT_BF16) sum += tile_squares<__nv_bfloat16>(r, b);
-        else if (r.type == TT_F16) sum += tile_squares<__half>(r, b);
-        else sum += tile_squares<float>(r, b);
+        if (r.type == TT_BF16) sum += tile_squares<__nv_bfloat16, true>(r, b);
+        else if (r.type == TT_F16) sum += tile_squares<__half, true>(r, b);
+        else sum += tile_squares<float, true>(r, b);
     }
     NormResult* res = (NormResult*)mem;
     double* part = (double*)(mem + 256);
@@ -212,9 +216,9 @@ __global__ void __launch_bounds__(kThreads) k_clip_few(const __grid_constant__ N
     for (int64_t b = blockIdx.x; b < L.tiles; b += kCluster) {
         const NormRec& r = tensor_of(L, b);
         if (r.guard && has_error(r.guard)) continue;
-        if (r.type == TT_BF16) sum += tile_squares<__nv_bfloat16>(r, b);
-        else if (r.type == TT_F16) sum += tile_squares<__half>(r, b);
-        else sum += tile_squares<float>(r, b);
+        if (r.type == TT_BF16) sum += tile_squares<__nv_bfloat16, false>(r, b);
+        else if (r.type == TT_F16) sum += tile_squares<__half, false>(r, b);
+        else sum += tile_squares<float, false>(r, b);
     }
     sum = block_sum(sum);
     if (threadIdx.x == 0) mine = sum;
