@@ -573,12 +573,14 @@ cudaError_t launch_step(bool k8, const List& L, int sms, float lr, const float* 
 
 }  // namespace
 
+constexpr size_t kTicketBytes = 256;
+
 struct tt_emb_adamw_handle {
     struct Part { int32_t ptype, gtype; List list; };
     std::vector<Part> parts;
     bool k8 = false;
     int device = 0, sms = 148;
-    uint32_t* ticket = nullptr;
+    uint32_t* ticket = nullptr;      // and behind it the norm's device memory
     NormPlan norm;
     std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // of every buffer of the step
 };
@@ -586,7 +588,6 @@ struct tt_emb_adamw_handle {
 static void free_step(tt_emb_adamw_t h)
 {
     if (h->ticket) cudaFree(h->ticket);
-    norm_free(h->norm);
     delete h;
 }
 
@@ -656,18 +657,30 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
     if (!h) return TT_ERR_ARG;
     h->k8 = k8;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
-        cudaMalloc((void**)&h->ticket, 256) != cudaSuccess) {
-        delete h;
-        return TT_ERR_CUDA;
-    }
-    // waited for, as the first step may run on a stream that is not ordered behind this one
-    if (cudaMemset(h->ticket, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
-        cudaFree(h->ticket);
+        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
         delete h;
         return TT_ERR_CUDA;
     }
     try {
+        std::vector<tt_emb_norm_tensor> grads(count);
+        for (int32_t i = 0; i < count; ++i) {
+            const tt_emb_adamw_tensor& x = tensors[i];
+            grads[i] = {const_cast<void*>(x.grad), x.guard, x.size, x.grad_type, 0};
+            auto note = [&](const void* p, int64_t bytes) { if (x.size > 0) h->spans.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
+            note(x.param, x.size * type_bytes(x.param_type));
+            note(x.grad, x.size * type_bytes(x.grad_type));
+            note(x.exp_avg, x.size * sb);
+            note(x.exp_avg_sq, x.size * sb);
+            if (k8) note(x.m_scale, ceil_div(x.size, kBlk) * 4);
+            if (k8) note(x.v_scale, ceil_div(x.size, kBlk) * 4);
+        }
+        h->spans.emplace_back((uintptr_t)steps, (uintptr_t)(steps + 1));
+        norm_plan(h->norm, h->sms, false, count, grads.data());
+        if (cleared((void**)&h->ticket, kTicketBytes + h->norm.bytes()) != cudaSuccess) {
+            delete h;
+            return TT_ERR_CUDA;
+        }
+        h->norm.mem = (char*)h->ticket + kTicketBytes;
         List base;
         memset(&base, 0, sizeof(base));
         base.log_b1 = log(opt->beta1);   // beta = 0: -inf, and 1 - beta^t = 1
@@ -724,23 +737,6 @@ int tt_emb_adamw_create(int32_t count, const tt_emb_adamw_tensor* tensors, const
         }
         if (h->parts.empty()) h->parts.push_back({TT_F32, TT_F32, base});   // still advances the step
         h->parts.back().list.last = 1;
-        std::vector<tt_emb_norm_tensor> grads(count);
-        for (int32_t i = 0; i < count; ++i) {
-            const tt_emb_adamw_tensor& x = tensors[i];
-            grads[i] = {const_cast<void*>(x.grad), x.guard, x.size, x.grad_type, 0};
-            auto note = [&](const void* p, int64_t bytes) { if (x.size > 0) h->spans.emplace_back((uintptr_t)p, (uintptr_t)p + (uintptr_t)bytes); };
-            note(x.param, x.size * type_bytes(x.param_type));
-            note(x.grad, x.size * type_bytes(x.grad_type));
-            note(x.exp_avg, x.size * sb);
-            note(x.exp_avg_sq, x.size * sb);
-            if (k8) note(x.m_scale, ceil_div(x.size, kBlk) * 4);
-            if (k8) note(x.v_scale, ceil_div(x.size, kBlk) * 4);
-        }
-        h->spans.emplace_back((uintptr_t)steps, (uintptr_t)(steps + 1));
-        if (norm_plan(h->norm, count, grads.data()) != cudaSuccess) {
-            free_step(h);
-            return TT_ERR_CUDA;
-        }
     } catch (...) {
         free_step(h);
         return TT_ERR_ARG;

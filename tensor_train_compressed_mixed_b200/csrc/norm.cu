@@ -284,12 +284,8 @@ bool norm_tensors_ok(int32_t count, const tt_emb_norm_tensor* tensors)
     return true;
 }
 
-cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tensors)
+void norm_plan(NormPlan& p, int sms, bool clips, int32_t count, const tt_emb_norm_tensor* tensors)
 {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&p.sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
     NormList empty;
     memset(&empty, 0, sizeof(empty));
     p.lists.push_back(empty);
@@ -305,31 +301,33 @@ cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tens
     }
     for (NormList& L : p.lists) {
         L.first_slot = p.slots;
-        p.grids.push_back((int)std::max<int64_t>(1, min64(L.tiles, (int64_t)p.sms * kFit)));
+        p.grids.push_back((int)std::max<int64_t>(1, min64(L.tiles, (int64_t)sms * kFit)));
         p.slots += p.grids.back();
     }
     // One launch where each block of the cluster takes one tile of 32 KB, or two: 6.5 us for three tensors of 1334 to 42620 values, 9.5
     // by two launches, but 12.5 us for forty tensors of up to 4099, 9.1 by two.
-    if (p.lists.size() == 1 && p.lists[0].tiles <= 2 * kCluster) {
+    if (clips && p.lists.size() == 1 && p.lists[0].tiles <= 2 * kCluster) {
         const FewLaunch l(nullptr);
         int clusters = 0;
         p.few = cudaOccupancyMaxActiveClusters(&clusters, k_clip_few, &l.c) == cudaSuccess && clusters > 0;
         cudaGetLastError();     // a refusal here is an answer, not an error of the next launch
     }
-    const size_t bytes = 256 + (size_t)p.slots * sizeof(double);
-    e = cudaMalloc((void**)&p.mem, bytes);
-    if (e != cudaSuccess) return e;
-    // waited for, as the first call may run on a stream that is not ordered behind this one
-    e = cudaMemset(p.mem, 0, bytes);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(0);
-    if (e != cudaSuccess) norm_free(p);
-    return e;
 }
 
-void norm_free(NormPlan& p)
+cudaError_t cleared(void** mem, size_t bytes)
 {
-    if (p.mem) cudaFree(p.mem);
-    p.mem = nullptr;
+    cudaError_t e = cudaMalloc(mem, bytes);
+    if (e != cudaSuccess) {
+        *mem = nullptr;
+        return e;
+    }
+    e = cudaMemset(*mem, 0, bytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(0);
+    if (e != cudaSuccess) {
+        cudaFree(*mem);
+        *mem = nullptr;
+    }
+    return e;
 }
 
 cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s)
@@ -395,12 +393,17 @@ int tt_emb_norm_create(int32_t count, const tt_emb_norm_tensor* tensors, tt_emb_
                 h->spans.emplace_back((uintptr_t)tensors[i].grad, (uintptr_t)tensors[i].grad + tensors[i].size * type_bytes(tensors[i].grad_type));
         std::sort(h->spans.begin(), h->spans.end());
         for (size_t i = 1; i < h->spans.size(); ++i) h->apart = h->apart && h->spans[i - 1].second <= h->spans[i].first;
-        if (cudaGetDevice(&h->device) != cudaSuccess || norm_plan(h->plan, count, tensors) != cudaSuccess) rc = TT_ERR_CUDA;
+        int sms = 0;
+        if (cudaGetDevice(&h->device) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
+            rc = TT_ERR_CUDA;
+        } else {
+            norm_plan(h->plan, sms, true, count, tensors);
+            if (cleared((void**)&h->plan.mem, h->plan.bytes()) != cudaSuccess) rc = TT_ERR_CUDA;
+        }
     } catch (...) {
         rc = TT_ERR_ARG;
     }
     if (rc != TT_OK) {
-        norm_free(h->plan);
         delete h;
         return rc;
     }
@@ -422,7 +425,7 @@ int tt_emb_norm_clip(tt_emb_norm_t h, float max_norm, float* norm, tt_stream_t s
 void tt_emb_norm_destroy(tt_emb_norm_t h)
 {
     if (!h) return;
-    norm_free(h->plan);
+    cudaFree(h->plan.mem);
     delete h;
 }
 

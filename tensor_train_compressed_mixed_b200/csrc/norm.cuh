@@ -33,19 +33,21 @@ struct NormResult {
     double sum;        // of the squares
 };
 
-// The plan of one list (host) and its device memory: a NormResult, and the partial sums from byte 256 on.
+// The plan of one list (host).
 struct NormPlan {
     std::vector<NormList> lists;
     std::vector<int> grids;
-    int sms = 148, slots = 0;
+    int slots = 0;
     bool few = false;         // so little that one cluster clips in one launch
-    char* mem = nullptr;
+    char* mem = nullptr;      // the owner's device memory: a NormResult, and the partial sums from byte 256 on; cleared before the first call
     NormResult* result() const { return (NormResult*)mem; }
+    size_t bytes() const { return 256 + (size_t)slots * sizeof(double); }
 };
 
-// May throw std::bad_alloc.  The device memory is allocated on the current device and cleared before it returns.
-cudaError_t norm_plan(NormPlan& p, int32_t count, const tt_emb_norm_tensor* tensors);
-void norm_free(NormPlan& p);
+// For a device of `sms` SMs, the current one.  clips: gradients are to be scaled in place, too.  May throw std::bad_alloc.
+void norm_plan(NormPlan& p, int sms, bool clips, int32_t count, const tt_emb_norm_tensor* tensors);
+// Cleared device memory on the current device; waited for, as the first call may run on a stream that is not ordered behind this one.
+cudaError_t cleared(void** mem, size_t bytes);
 // Sums, the norm (rounded once to *norm, which may be null) and the factor for `bound`.
 cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s);
 // The same, and every gradient times the factor, in place.

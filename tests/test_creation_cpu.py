@@ -1,0 +1,61 @@
+"""What making a handle asks of the CUDA runtime: one allocation and one wait, and nothing for calls that may never come."""
+import ctypes
+import os
+import subprocess
+import sys
+
+from tensor_train_compressed_mixed_b200 import abi
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+MB = 1 << 20
+
+PROGRAM = """
+import sys
+sys.path[:0] = [{root!r}, {here!r}]
+import test_creation_cpu as t
+t.{what}()
+"""
+
+
+def _taken():
+    n = (ctypes.c_int * 3)()
+    ctypes.CDLL(None).count_take(n)
+    return list(n)
+
+
+def _run(tmp_path, what):
+    so = tmp_path / "libcount.so"
+    subprocess.run(["gcc", "-O1", "-fPIC", "-shared", "-I/usr/local/cuda/include", os.path.join(HERE, "count_cudart.c"), "-o", str(so)], check=True)
+    p = subprocess.run([sys.executable, "-c", PROGRAM.format(root=os.path.dirname(HERE), here=HERE, what=what)], capture_output=True, text=True, timeout=600,
+                       env=dict(os.environ, LD_PRELOAD=str(so)))
+    assert p.returncode == 0, p.stdout[-2000:] + p.stderr[-4000:]
+
+
+def adamw():
+    L = abi.lib()
+    t = abi.AdamWTensor(param=MB, grad=2 * MB, exp_avg=3 * MB, exp_avg_sq=4 * MB, size=100)
+    o = abi.AdamWOptions(beta1=0.9, beta2=0.999, eps=1e-8, state_bits=32)
+    h = ctypes.c_void_p()
+    _taken()
+    assert L.tt_emb_adamw_create(1, (abi.AdamWTensor * 1)(t), ctypes.byref(o), 5 * MB, ctypes.byref(h)) == abi.TT_OK
+    assert _taken() == [1, 1, 0]
+    assert L.tt_emb_adamw_step_clipped(h, 0.1, None, 1.0, None, None) == abi.TT_ERR_CUDA      # up to the launch
+    assert _taken() == [0, 0, 0]
+    L.tt_emb_adamw_destroy(h)
+
+
+def norm():
+    L = abi.lib()
+    h = ctypes.c_void_p()
+    _taken()
+    assert L.tt_emb_norm_create(1, (abi.NormTensor * 1)(abi.NormTensor(grad=MB, size=100, grad_type=abi.TT_F32)), ctypes.byref(h)) == abi.TT_OK
+    assert _taken() == [1, 1, 1]
+    L.tt_emb_norm_destroy(h)
+
+
+def test_adamw(tmp_path):
+    _run(tmp_path, "adamw")
+
+
+def test_norm(tmp_path):
+    _run(tmp_path, "norm")
