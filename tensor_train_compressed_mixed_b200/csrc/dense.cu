@@ -1063,7 +1063,6 @@ int tt_emb_dense_create(int64_t num_rows, int32_t dim, int32_t table_type, float
         return TT_ERR_CUDA;
     }
     h->clusters = sort_fits();
-    h->fits = matmul_fits(h->num_sms);
     // the memset is waited for, as the first call may run on a stream that is not ordered behind this one
     if (cudaMemset(h->d_status, 0, 256) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess) {
         cudaFree(h->d_status);

@@ -13,7 +13,8 @@ struct tt_emb_dense_handle {
     int64_t ws_n = -1;
     char* project_ws = nullptr;
     size_t project_bytes = 0;
-    tt::MatmulFits fits;
+    tt::MatmulFits fits;         // of the handle's device, asked for by the first call that wants them
+    bool has_fits = false;
     int32_t* d_status = nullptr;
     int device = 0, num_sms = 148;
     bool clusters = false;       // one of k_token_sort fits this device

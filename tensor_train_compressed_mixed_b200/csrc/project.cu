@@ -580,6 +580,22 @@ bool is_few(tt_emb_dense_t h, int64_t n)
     return !as_it_lies && n <= kFewRows && h->dim <= 4096 && ceil_div(h->rows, 128) * 2 >= h->num_sms;
 }
 
+// What the handle's device holds of the product kernels.  Asked for once, when a product is first planned: most tables are never
+// read as a matrix.  Sizes may be asked for while another device is current.
+const MatmulFits& fits_of(tt_emb_dense_t h)
+{
+    if (!h->has_fits) {
+        int current = h->device;
+        const bool elsewhere = cudaGetDevice(&current) == cudaSuccess && current != h->device;
+        if (!elsewhere || cudaSetDevice(h->device) == cudaSuccess) {
+            h->fits = matmul_fits(h->num_sms);
+            h->has_fits = true;
+        }
+        if (elsewhere) cudaSetDevice(current);
+    }
+    return h->fits;
+}
+
 Matrix matrix(const void* p, int64_t si, int64_t sk, int type) { return {p, si, sk, type}; }
 
 int enter(tt_emb_dense_t h, cudaStream_t s)
@@ -626,7 +642,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     p.deep = h->dim;
     p.e = e;
     p.has_pre = a->pre != nullptr;
-    const MatmulPlan plan = matmul_plan(p, h->fits);
+    const MatmulPlan plan = matmul_plan(p, fits_of(h));
     void* const scratch = w.take(plan.scratch);
     if (size) {
         *size = w.used;
@@ -696,7 +712,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     pt.b = wide_t ? d.wide : d.narrow;
     px.e = ex;
     pt.e = et;
-    const MatmulPlan plan_x = big_x ? matmul_plan(px, h->fits) : MatmulPlan(), plan_t = big_t ? matmul_plan(pt, h->fits) : MatmulPlan();
+    const MatmulPlan plan_x = big_x ? matmul_plan(px, fits_of(h)) : MatmulPlan(), plan_t = big_t ? matmul_plan(pt, fits_of(h)) : MatmulPlan();
     void* const scratch = w.take(plan_x.scratch > plan_t.scratch ? plan_x.scratch : plan_t.scratch);     // one after the other
     if (size) {
         *size = w.used;

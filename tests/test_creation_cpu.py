@@ -59,3 +59,27 @@ def test_adamw(tmp_path):
 
 def test_norm(tmp_path):
     _run(tmp_path, "norm")
+
+
+def dense():
+    from test_project_cpu import FORWARD, Project, _handle
+    L = abi.lib()
+    h = ctypes.c_void_p()
+    _taken()
+    assert L.tt_emb_dense_create(10, 6, abi.TT_F32, 1.0, -1, ctypes.byref(h)) == abi.TT_OK
+    assert _taken() == [1, 1, 5]                     # of the kernels that sort tokens
+    L.tt_emb_dense_destroy(h)
+    h = _handle(L, abi.TT_BF16)
+    _taken()
+    size, call = ctypes.c_size_t(), bytes(Project(**FORWARD))
+    for asked in (0, 0):                             # a product this small has no plan
+        assert L.tt_emb_dense_project_workspace_size(h, call, ctypes.byref(size)) == abi.TT_OK and size.value == 0
+        assert _taken() == [0, 0, asked]
+    call = bytes(Project(**{**FORWARD, "n": 70000, "x_stride": 8, "pre": None, "residual": 300 * MB, "out": 400 * MB}))
+    for asked in (6, 0):                             # the product kernels', once
+        assert L.tt_emb_dense_project_workspace_size(h, call, ctypes.byref(size)) == abi.TT_OK and size.value > 0
+        assert _taken() == [0, 0, asked]
+
+
+def test_dense(tmp_path):
+    _run(tmp_path, "dense")
