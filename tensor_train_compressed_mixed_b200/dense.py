@@ -51,7 +51,9 @@ class DenseEmbedding:
         self.grad = None
         self._ws = []           # the workspace in use is the last; captured calls keep using theirs
         self._ws_tokens = -1
-        self._project_ws = []   # likewise
+        self._project_ws, self._project_bytes = None, 0     # the projection's workspace,
+        self._project_ws_at = None                          # the stream that it was allocated on,
+        self._project_kept = []                             # and those that captured calls use
 
     def _check(self, t, name: str, dtype=None):
         if not isinstance(t, torch.Tensor) or t.get_device() != self.device.index:   # -1 on the CPU
@@ -115,14 +117,29 @@ class DenseEmbedding:
             abi.tt_emb_dense_backward(self.handle, tokens, grad_out, self.dim, accumulate, stream)
         return self.grad
 
-    def _workspace(self, nbytes: int, stream):
-        """A workspace of this size for the projection's calls; earlier, smaller ones live on, as reserve's do."""
-        last = self._project_ws[-1].numel() if self._project_ws else 0
+    def _workspace(self, nbytes: int, stream, at: int):
+        """A workspace of this size for a call of the projection on `stream`, whose handle is `at`.
+
+        One that a captured call uses lives as long as the object; another until a larger one takes its place, which is half
+        as large again, or by 64 MB if that is less."""
+        last = self._project_bytes
         if nbytes > last:
+            size = max(nbytes, last + min(last // 2, 64 << 20))
             with on_stream(stream):
-                ws = torch.empty(max(nbytes, last * 3 // 2), dtype=torch.uint8, device=self.device)
+                ws = torch.empty(size, dtype=torch.uint8, device=self.device)
             abi.tt_emb_dense_set_project_workspace(self.handle, ws)
-            self._project_ws.append(ws)
+            self._project_ws, self._project_bytes, self._project_ws_at = ws, size, at
+        if stream is None:
+            captured = torch._C._cuda_isCurrentStreamCapturing()
+        else:
+            with on_stream(stream):
+                captured = torch._C._cuda_isCurrentStreamCapturing()
+        if captured:
+            if not self._project_kept or self._project_kept[-1] is not self._project_ws:
+                self._project_kept.append(self._project_ws)
+        elif at != self._project_ws_at:
+            with on_stream(stream):
+                self._project_ws.record_stream(torch.cuda.current_stream())
 
     def project(self, x: torch.Tensor, bias: torch.Tensor | None = None, activation: str | None = None,
                 cap: float | None = None, residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
@@ -146,9 +163,10 @@ class DenseEmbedding:
                     out = torch.empty(*x.shape[:-1], self.num_rows, dtype=out_dtype or self.dtype, device=self.device)
             call = abi.project_call(x, self.num_rows, self.dim, out, bias, residual, pre, activation, cap)
             nbytes = abi.tt_emb_dense_project_workspace_size(self.handle, call)
+            at = abi._stream_on(stream, self.device.index)
             if nbytes:
-                self._workspace(nbytes, stream)
-            abi.tt_emb_dense_project(self.handle, call, abi._stream_on(stream, self.device.index))
+                self._workspace(nbytes, stream, at)
+            abi.tt_emb_dense_project(self.handle, call, at)
         return out
 
     def project_backward(self, x: torch.Tensor | None, grad_out: torch.Tensor, pre: torch.Tensor | None = None,
@@ -182,9 +200,10 @@ class DenseEmbedding:
             call = abi.project_grad_call(x, self.num_rows, self.dim, grad_out, pre, activation, cap, grad_x, grad_bias, table_grad,
                                          accumulate)
             nbytes = abi.tt_emb_dense_project_backward_workspace_size(self.handle, call)
+            at = abi._stream_on(stream, self.device.index)
             if nbytes:
-                self._workspace(nbytes, stream)
-            abi.tt_emb_dense_project_backward(self.handle, call, abi._stream_on(stream, self.device.index))
+                self._workspace(nbytes, stream, at)
+            abi.tt_emb_dense_project_backward(self.handle, call, at)
         return grad_x
 
     def sync(self):
