@@ -489,7 +489,9 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                     }
             }
         }
-        if (gone == kTimedOut && (!kPair || rank == 0))      // copies on their way land before the block's memory is given up
+        // All copies have landed before the block's memory is given up, also where another role gives up after the last of them was
+        // asked for.  (A pair's arrive at the first block's barriers.)
+        if (!kPair || rank == 0)
             for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
     } else if (warp == 1 && (!kPair || rank == 0) && elected()) {
         int n = 0, seq = 0;
