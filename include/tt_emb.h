@@ -508,8 +508,8 @@ typedef struct {
  * The residual's is grad_out itself.  The table's padding_row receives no gradient.  Sums are formed in
  * fp32 in an order that depends on the sizes, strides and places only: the same call gives the same bits.  Where
  * the table and a result are of bf16, that result's products take dz rounded to bf16; all others take it and the
- * table or x as they are, as bf16 terms that hold all their bits where their types differ or dz is computed, with what the
- * projection says of infinities.
+ * table or x as they are, where their types differ or dz is computed as bf16 terms: of dz to 2^-17 of it for 16-bit results
+ * beside a 16-bit table, else all bits; with what the projection says of infinities.
  */
 typedef struct {
     const void* x;           /* as the forward's; not read without table_grad */

@@ -2,7 +2,9 @@
 and with no fewer bits of dz than the result has.
 
 Tolerances are those of test_gpu_project.py: a sum of k products in fp32 is off by k + 2 steps of 2^-23 of the sum of magnitudes and
-2^-22 for operands as terms, dz in fp32 by 32 steps, and a result is rounded once.
+2^-22 for operands as terms, dz in fp32 by 32 steps, dz as two terms by 2^-17 of it, and a result is rounded once.  The two terms: a bf16
+value of [2^e, 2^(e + 1)) has steps of 2^(e - 7), so the first leaves at most 2^(e - 8), and the second, whose steps are 2^(e - 16) for what is
+below that, at most 2^(e - 17).
 """
 import pytest
 import torch
@@ -30,6 +32,8 @@ def _backward(n, rows, dim, kind, dy, gx, gw, act=None, extra=0, by=1.0, bias=Fa
         off = 32 * STEP * dy.double().abs()
     for got, a, o, b, k in ((got, d, off, w, rows), (e.grad, d.t(), off.t(), x, n)):
         want = a @ b.double()
+        if kind != F32 and got.dtype != F32 and (act or dy.dtype == F32):       # dz as two terms
+            o = o + 2.0 ** -17 * (a.abs() + o)
         if kind == got.dtype == BF16 and (act or dy.dtype != BF16):     # dz in as many bits as this result
             o = o + _half_step(BF16) * (a.abs() + o) + _least(BF16)
         tol = _sum_tol(a, b.double(), k) + o @ b.double().abs()
