@@ -8,8 +8,8 @@
 // sums from tensor memory through shared memory, 64 rows at a time, where rows lie as they do in the result: a warp
 // then works on whole pieces of 128 values of a row, and reads the residual of the next rows ahead.  Two areas of tensor memory
 // take turns, so that products go on meanwhile.
-// Tensor cores cut the last bits of a sum off at each step.  16-bit results round far above that; for others (kLong) the sums
-// of a few blocks of k at a time are formed in tensor memory and added in fp32 registers.  Operands of several terms
+// Tensor cores cut the last bits of a sum off at each step.  Short sums of 16-bit results round far above that; for others (kLong) the
+// sums of some blocks of k at a time are formed in tensor memory and added in fp32 registers.  Operands of several terms
 // (x = t0 + t1 + t2, each 2^-8 of the one before) bring each term once for all products that it is part of: those of terms i and j
 // with i + j < 3, as the others are below fp32's last bit.  All but the first terms' product are summed in an area of their
 // own, so that few steps are made on a large sum.
@@ -39,9 +39,12 @@ using namespace tt;
 
 namespace {
 
-// With kLong, blocks of 64 k whose sum is formed in tensor memory: 16 steps, each of which cuts off up to 2^-23 of it.  With 16 blocks
-// the gradients of 301 x 5003 x 257 fp32 were off by 1.2e-6 of their norm, with 4 by 2.5e-7 (fp32 products: 4.9e-7).
-constexpr int kChunk = 4;
+// Blocks of 64 k whose sum is formed in tensor memory, before it is added in fp32 registers.  Each block is four steps, and a step
+// cuts off up to 2^-22 of the sum, always towards zero (measured on terms of one sign: 2^-23.3 of a growing sum, 2^-22.2 of one that is large
+// from the start).  Results of fp32: with 16 blocks the gradients of 301 x 5003 x 257 were off by 1.2e-6 of their norm, with 4 by
+// 2.5e-7 (fp32 products: 4.9e-7).  16-bit results: an eighth of half a step at most, 2^-14 for fp16 and 2^-11 for bf16.  Whole sums of
+// 32768 terms of one sign were off by up to 3.9e-4 beyond their rounding, more than half a step of fp16, and of 65536 by 7.7e-4.
+constexpr int kChunk = 4, kChunkF16 = 64, kChunkBf16 = 512;
 constexpr int kDeep = 64;            // k of a stage: 128 bytes, one swizzle row
 constexpr int kCols = 128;
 constexpr double kMostSums = 1 << 26;      // of all slices together
@@ -55,6 +58,7 @@ struct Args {
     int32_t* status;
     int64_t rows, cols;
     int32_t blocks;       // of 64 k
+    int32_t chunk;        // of them, with kLong: those whose sum is formed in tensor memory
     int32_t a_terms, b_terms;     // of the operands' values, 1 to 3; with kLong only
     uint32_t idesc;
     int32_t tiles_c, tiles_r;
@@ -384,18 +388,24 @@ __device__ __forceinline__ bool all_agree(int part, bool yes)
 }
 __device__ __forceinline__ void part_sync(int part) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + part) : "memory"); }
 
-template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
+// kSums: whole sums in tensor memory, chunks of single terms, or chunks of operands of several terms.  Lower tiles take the last for
+// single terms too: memory bounds them.  Higher ones are bound by the thread that issues the products, which the loops over terms delay
+// (2048 rows by 32000 x 1024 fp16, x's gradient: 119 us so, 167 by the loops over terms).  The highest spill some sums, which costs
+// 5 us a tile (4096 rows by 32000 x 4096 fp16: 815 us, 795 as whole sums).
+enum { kWhole, kChunks, kTermChunks };
+template <int BN, bool kAmn, bool kBmn, int kSums, bool kPair>
 __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __grid_constant__ Args g)
 {
     constexpr int kFinish = finish_of(BN), kStages = stages_of(BN, kPair), kStage = stage_bytes(BN, kPair), kPart = BN / (kFinish / 4);
     constexpr int kPass = passing_of(BN), kRows = kPass / kFinish;       // rows at a time of a block and of a finishing warp
+    constexpr bool kLong = kSums != kWhole, kTerms = kSums == kTermChunks;
     constexpr int kSide = kPair ? 2 : 1, kOwn = BN / kSide;              // blocks of a pair, rows of B that each brings
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t full[kStages], empty[kStages], sums_full[2], sums_empty[2], drained;
     __shared__ uint32_t tmem_at;
     __shared__ volatile int gone;
     const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
-    const int terms = kLong ? max(g.a_terms, g.b_terms) : 1;
+    const int terms = kTerms ? max(g.a_terms, g.b_terms) : 1;
     const uint32_t area = terms > 1 ? 4 * BN : 2 * BN, columns = area < 32 ? 32 : area;      // of tensor memory: two of sums, and two of the small terms'
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -454,7 +464,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
         return t;
     };
 
-    const int chunk = kLong ? kChunk : g.blocks;       // blocks of k whose sums stay in tensor memory
+    const int chunk = kLong ? g.chunk : g.blocks;      // blocks of k whose sums stay in tensor memory
     if (warp == 0 && elected()) {
         int n = 0;      // stages filled
         bool ok = true;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                         const int s = n % kStages, k = kb * kDeep;
                         if (n >= kStages && !wait_for(&empty[s], (n / kStages - 1) & 1, &gone)) { ok = false; break; }
                         const uint32_t a = ring + s * kStage, b = a + kCols * kDeep * 2, bar = kPair ? in_block(smem_u32(&full[s]), 0) : smem_u32(&full[s]);
-                        const bool with_a = !kLong || t < g.a_terms, with_b = !kLong || t < g.b_terms;
+                        const bool with_a = !kTerms || t < g.a_terms, with_b = !kTerms || t < g.b_terms;
                         if (!kPair || rank == 0) expect(&full[s], ((with_a ? kCols : 0) + (with_b ? kOwn : 0)) * kDeep * 2 * kSide);
                         if (with_a) {
                             if constexpr (kAmn) {
@@ -512,7 +522,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                         db += (kBmn ? 2048 : 32) >> 4;
                     }
                 };
-                if (!kLong || terms == 1) {
+                if (!kTerms || terms == 1) {
                     for (int kb = k0; kb < end; ++kb, ++n) {
                         const int s = n % kStages;
                         if (!wait_for(&full[s], (n / kStages) & 1, &gone)) { ok = false; break; }
@@ -586,7 +596,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                         for (int i = 0; i < kLoad; ++i) acc[j + i] = (k0 == first ? 0.f : acc[j + i]) + __uint_as_float(x[i]);
-                        if (terms > 1) {
+                        if (kTerms && terms > 1) {
                             load_columns<kLoad>(lanes + 2 * BN + buf * BN + j, x);
                             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
@@ -789,11 +799,11 @@ cudaError_t allow(Kernel kernel, int bytes, std::atomic<uint64_t>& told)
     return e;
 }
 
-template <int BN, bool kAmn, bool kBmn, bool kLong, bool kPair>
+template <int BN, bool kAmn, bool kBmn, int kSums, bool kPair>
 cudaError_t launch(Args& g, const MatmulFits& fits, bool early, cudaStream_t s)
 {
     static std::atomic<uint64_t> told{0};
-    auto* kernel = k_matmul<BN, kAmn, kBmn, kLong, kPair>;
+    auto* kernel = k_matmul<BN, kAmn, kBmn, kSums, kPair>;
     const cudaError_t e = allow(kernel, block_bytes<BN, kPair>(), told);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (int64_t)g.tiles_c * g.tiles_r * g.slices;
@@ -806,7 +816,7 @@ cudaError_t launch(Args& g, const MatmulFits& fits, bool early, cudaStream_t s)
 template <int BN, bool kPair>
 void count_clusters(int (&n)[4])
 {
-    auto* kernel = k_matmul<BN, false, false, false, kPair>;
+    auto* kernel = k_matmul<BN, false, false, kWhole, kPair>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, block_bytes<BN, kPair>()) != cudaSuccess) return;
     for (int i = 1; i < 4; ++i) {
         const Launch l(1 << i, threads_of(BN), block_bytes<BN, kPair>(), 1 << i, false, nullptr);
@@ -844,14 +854,16 @@ MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits)
     MatmulPlan q;
     const int64_t blocks = ceil_div(p.deep, kDeep);
     const int products = products_of(p);
-    // Results of fp32, operands of several terms and sums beyond 65536 of k are formed by chunks: 16 steps on the full sum, each
-    // off by up to 2^-23 of it.
-    q.by_chunks = p.e.out_type == TT_F32 || (p.e.pre_type == TT_F32 && p.has_pre) || products > 1 || blocks > 1024;
+    // Results of fp32 and operands of several terms are formed by chunks of kChunk blocks, 16-bit results by as many as their roundings
+    // hide.
+    auto any = [&](int type) { return p.e.out_type == type || (p.has_pre && p.e.pre_type == type); };
+    const bool fine = any(TT_F32) || products > 1;
+    q.chunk = fine ? kChunk : any(TT_F16) ? kChunkF16 : kChunkBf16;
     // The tile's height and the blocks that share a tile: what a model of the time likes best, in cycles.  64 k take what their
     // products take (half a cycle for each row and 16 k, at 128 columns), or what their bytes take, about 55 a cycle and SM; a tile
     // a few cycles for each of its rows; what a launch, a cluster and a joining kernel take comes from measurement.
     double best = 0.0;
-    for (int n = p.b_mn ? 64 : 16; n <= (q.by_chunks ? 128 : 256); n *= 2) {
+    for (int n = p.b_mn ? 64 : 16; n <= (fine ? 128 : 256); n *= 2) {
         const double tiles = (double)ceil_div(p.cols, kCols) * ceil_div(p.rows, n), work = 2.0 * n * products;
         const double each = std::max(work, (kCols * p.a.parts + n * p.b.parts) * (kDeep * 2 / 55.0));
         const int fit = fit_of(n);
@@ -876,6 +888,7 @@ MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits)
             if (t < best) best = t, q.height = n, q.split = q.slices = 1, q.pair = true;
         }
     }
+    q.by_chunks = fine || ceil_div(blocks, q.split * q.slices) > q.chunk;
     q.scratch = q.slices > 1 ? (size_t)(q.slices * p.rows * p.cols) * sizeof(float) : 0;
     return q;
 }
@@ -904,6 +917,7 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
     g.blocks = (int)blocks;
     g.tiles_c = (int)tiles_c;
     g.tiles_r = (int)tiles_r;
+    g.chunk = q.chunk;
     g.split = q.split;
     g.slices = q.slices;
     auto four = [&](const void* x, int type, int64_t stride) {
@@ -914,24 +928,31 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
     g.idesc = (1u << 4) | (p.a.type == TT_BF16 ? 1u << 7 | 1u << 10 : 0u) | (p.a_mn ? 1u << 15 : 0u) | (p.b_mn ? 1u << 16 : 0u) |
               (uint32_t)(bn >> 3) << 17 | (uint32_t)((pair ? 2 * kCols : kCols) >> 4) << 24;
     if (!encode(&g.a, p.a, p.a_mn ? kDeep : kCols) || !encode(&g.b, p.b, p.b_mn ? kDeep : pair ? bn / 2 : bn)) return TT_ERR_CUDA;
-    auto by_height = [&](auto amn, auto bmn, auto chunks) {
-        constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value, L = decltype(chunks)::value;
-        if constexpr (!L) {
-            if (bn == 256) return pair ? launch<256, A, B, L, true>(g, fits, early, s) : launch<256, A, B, L, false>(g, fits, early, s);
+    auto by_height = [&](auto amn, auto bmn, auto sums) {
+        constexpr bool A = decltype(amn)::value, B = decltype(bmn)::value;
+        constexpr int S = decltype(sums)::value;
+        if constexpr (S != kTermChunks) {       // (whose sums of their own leave tensor memory for half that height)
+            if (bn == 256) return pair ? launch<256, A, B, S, true>(g, fits, early, s) : launch<256, A, B, S, false>(g, fits, early, s);
         }
-        if (bn == 128) return pair ? launch<128, A, B, L, true>(g, fits, early, s) : launch<128, A, B, L, false>(g, fits, early, s);
-        if constexpr (!B) {
-            if (bn == 16) return launch<16, A, B, L, false>(g, fits, early, s);
-            if (bn == 32) return launch<32, A, B, L, false>(g, fits, early, s);
+        if (bn == 128) return pair ? launch<128, A, B, S, true>(g, fits, early, s) : launch<128, A, B, S, false>(g, fits, early, s);
+        if constexpr (S == kChunks) {
+            return cudaErrorInvalidValue;       // no such height
+        } else {
+            if constexpr (!B) {
+                if (bn == 16) return launch<16, A, B, S, false>(g, fits, early, s);
+                if (bn == 32) return launch<32, A, B, S, false>(g, fits, early, s);
+            }
+            return launch<64, A, B, S, false>(g, fits, early, s);
         }
-        return launch<64, A, B, L, false>(g, fits, early, s);
     };
-    auto by_sides = [&](auto chunks) {
+    auto by_sides = [&](auto sums) {
         using Yes = std::true_type;
         using No = std::false_type;
-        return p.b_mn ? by_height(Yes(), Yes(), chunks) : p.a_mn ? by_height(Yes(), No(), chunks) : by_height(No(), No(), chunks);
+        return p.b_mn ? by_height(Yes(), Yes(), sums) : p.a_mn ? by_height(Yes(), No(), sums) : by_height(No(), No(), sums);
     };
-    cudaError_t e = q.by_chunks ? by_sides(std::true_type()) : by_sides(std::false_type());
+    cudaError_t e = !q.by_chunks                                     ? by_sides(std::integral_constant<int, kWhole>())
+                    : bn >= 128 && p.a.parts == 1 && p.b.parts == 1 ? by_sides(std::integral_constant<int, kChunks>())
+                                                                     : by_sides(std::integral_constant<int, kTermChunks>());
     if (e == cudaSuccess && q.slices > 1) {
         const int64_t blocks_of_rows = p.rows * ceil_div(p.cols, 32);      // (below kMostSums)
         e = launch_early(k_join, (unsigned)blocks_of_rows, kJoinThreads, s, (const float*)scratch, (int)q.slices, p.rows, p.cols, p.e, (const int32_t*)status);

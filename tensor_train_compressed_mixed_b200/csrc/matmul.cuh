@@ -37,6 +37,7 @@ struct Product {
 // How a product of these sizes, types and terms (no pointer of it is looked at) is computed.
 struct MatmulPlan {
     int height = 0, split = 1, slices = 1;
+    int chunk = 0;            // with by_chunks: blocks of 64 k whose sum is formed in tensor memory
     bool pair = false, by_chunks = false;
     size_t scratch = 0;       // device memory for slices' sums
 };
