@@ -29,8 +29,6 @@ struct NormResult {
     uint32_t ticket;
     int32_t finite;    // whether the norm is a number
     float factor;      // of every gradient: bound / norm where the norm is above the bound, else 1
-    float pad;
-    double sum;        // of the squares
 };
 
 // The plan of one list (host).
@@ -52,7 +50,5 @@ cudaError_t cleared(void** mem, size_t bytes);
 cudaError_t norm_launch(const NormPlan& p, float bound, float* norm, cudaStream_t s);
 // The same, and every gradient times the factor, in place.
 cudaError_t norm_clip(const NormPlan& p, float bound, float* norm, cudaStream_t s);
-// Whether a list can be taken at all, and whether its buffers are apart.
-bool norm_tensors_ok(int32_t count, const tt_emb_norm_tensor* tensors);
 
 }  // namespace tt

@@ -6,8 +6,8 @@
 // Three products of the same kind.  The tensor cores take them (matmul.cu) on 16-bit operands whose rows begin at 16-byte
 // places.  What is not like that is laid out first, in the workspace: rows at other places are copied; fp32
 // values (and dz, where its rounding to 16 bits would show in a result) are written as three bf16 terms
-// x = t0 + t1 + t2 + rest, each the nearest bf16 to what the ones before leave, |rest| <= 2^-27 |x|, fp16 values beside them
-// as two.  dz is formed in the same pass, and the bias's gradient with it.  Small products, whose time is that of their
+// x = t0 + t1 + t2, each the nearest bf16 to what the ones before leave, which hold all bits of a value above 2^-110, fp16 values beside
+// them as two.  dz is formed in the same pass, and the bias's gradient with it.  Small products, whose time is that of their
 // launches, run on the FP32 pipes from where their operands lie, in one launch each.
 #include <math.h>
 
@@ -480,10 +480,10 @@ struct Space {
     }
 };
 
-// One matrix of a call in the forms that its products want.
 // Rows whose sums one block of rows makes, which saves the launch that joins several: 2 us of the host's, while the device takes as long
 // (32 rows by 4000 x 256 bf16, all gradients: 17.2 us, 16.9 with it).
 constexpr int64_t kAlone = 32;
+// One matrix of a call in the forms that its products want.
 struct Forms {
     PackArgs pack = {};
     bool packs = false;       // the pass over the values is needed
