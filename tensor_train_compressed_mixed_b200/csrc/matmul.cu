@@ -388,11 +388,10 @@ __device__ __forceinline__ bool all_agree(int part, bool yes)
 }
 __device__ __forceinline__ void part_sync(int part) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + part) : "memory"); }
 
-// kSums: whole sums in tensor memory, chunks of single terms, or chunks of operands of several terms.  Lower tiles take the last for
-// single terms too: memory bounds them.  Higher ones are bound by the thread that issues the products, which the loops over terms delay
+// Tiles of less than kHigh rows take kTermChunks for single terms too: memory bounds them.  Higher ones are bound by the thread that issues the products, which the loops over terms delay
 // (2048 rows by 32000 x 1024 fp16, x's gradient: 119 us so, 167 by the loops over terms).  The highest spill some sums, which costs
 // 5 us a tile (4096 rows by 32000 x 4096 fp16: 815 us, 795 as whole sums).
-enum { kWhole, kChunks, kTermChunks };
+constexpr int kHigh = 128;
 template <int BN, bool kAmn, bool kBmn, int kSums, bool kPair>
 __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __grid_constant__ Args g)
 {
@@ -888,7 +887,7 @@ MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits)
             if (t < best) best = t, q.height = n, q.split = q.slices = 1, q.pair = true;
         }
     }
-    q.by_chunks = fine || ceil_div(blocks, q.split * q.slices) > q.chunk;
+    if (fine || ceil_div(blocks, q.split * q.slices) > q.chunk) q.sums = q.height >= kHigh && p.a.parts == 1 && p.b.parts == 1 ? kChunks : kTermChunks;
     q.scratch = q.slices > 1 ? (size_t)(q.slices * p.rows * p.cols) * sizeof(float) : 0;
     return q;
 }
@@ -936,7 +935,7 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
         }
         if (bn == 128) return pair ? launch<128, A, B, S, true>(g, fits, early, s) : launch<128, A, B, S, false>(g, fits, early, s);
         if constexpr (S == kChunks) {
-            return cudaErrorInvalidValue;       // no such height
+            return cudaErrorInvalidValue;       // (no plan has it)
         } else {
             if constexpr (!B) {
                 if (bn == 16) return launch<16, A, B, S, false>(g, fits, early, s);
@@ -950,9 +949,9 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
         using No = std::false_type;
         return p.b_mn ? by_height(Yes(), Yes(), sums) : p.a_mn ? by_height(Yes(), No(), sums) : by_height(No(), No(), sums);
     };
-    cudaError_t e = !q.by_chunks                                     ? by_sides(std::integral_constant<int, kWhole>())
-                    : bn >= 128 && p.a.parts == 1 && p.b.parts == 1 ? by_sides(std::integral_constant<int, kChunks>())
-                                                                     : by_sides(std::integral_constant<int, kTermChunks>());
+    cudaError_t e = q.sums == kWhole    ? by_sides(std::integral_constant<int, kWhole>())
+                    : q.sums == kChunks ? by_sides(std::integral_constant<int, kChunks>())
+                                        : by_sides(std::integral_constant<int, kTermChunks>());
     if (e == cudaSuccess && q.slices > 1) {
         const int64_t blocks_of_rows = p.rows * ceil_div(p.cols, 32);      // (below kMostSums)
         e = launch_early(k_join, (unsigned)blocks_of_rows, kJoinThreads, s, (const float*)scratch, (int)q.slices, p.rows, p.cols, p.e, (const int32_t*)status);

@@ -34,11 +34,14 @@ struct Product {
     int64_t rows = 0, cols = 0, deep = 0;
     Epilogue e = {};
 };
+// How a tile's sums are formed: whole ones in tensor memory, chunks of single terms, or chunks of operands of several terms.
+enum { kWhole, kChunks, kTermChunks };
 // How a product of these sizes, types and terms (no pointer of it is looked at) is computed.
 struct MatmulPlan {
     int height = 0, split = 1, slices = 1;
-    int chunk = 0;            // with by_chunks: blocks of 64 k whose sum is formed in tensor memory
-    bool pair = false, by_chunks = false;
+    int sums = kWhole;
+    int chunk = 0;            // blocks of 64 k of a chunk
+    bool pair = false;
     size_t scratch = 0;       // device memory for slices' sums
 };
 MatmulPlan matmul_plan(const Product& p, const MatmulFits& fits);
