@@ -490,14 +490,17 @@ struct Forms {
     Operand narrow, wide;
 };
 
+// How far apart rows of `cols` values are laid out: at 16-byte places, which tensor maps want; at 128-byte places, where a copied row
+// of 64 values is no more cache lines than it has to be, unless rows are that short (515 fp32 columns, three terms: 8.4 us for 24
+// stages at 1040 bytes a row).
+int64_t laid_out(int64_t cols) { return cols >= 64 ? ceil_div(cols, 64) * 64 : ceil_div(cols, 8) * 8; }
+
 // forms of u's values [rows][cols], which are values of the narrow form's 16 bits as they lie if `plain`
 Forms forms_of(Space& w, const Upstream& u, bool plain, int64_t rows, int64_t cols, int narrow_type, bool want_narrow, int wide_parts, bool want_sums,
                int sms, int32_t* status)
 {
     Forms f;
-    // rows at 16-byte places, which tensor maps want; at 128-byte places, where a copied row of 64 values is no more cache lines
-    // than it has to be, unless rows are that short (515 fp32 columns, three terms: 8.4 us for 24 stages at 1040 bytes a row)
-    const int64_t ld = cols >= 64 ? ceil_div(cols, 64) * 64 : ceil_div(cols, 8) * 8;
+    const int64_t ld = laid_out(cols);
     const bool direct = plain && mappable(u.up, u.up_stride, rows, cols);
     f.pack.u = u;
     f.pack.rows = rows;
@@ -565,19 +568,28 @@ int launch_pack(std::initializer_list<const Forms*> forms, int sms, bool* any, c
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-// Products small enough for the FP32 pipes, where the tensor cores would want an operand laid out first: one launch instead of two, and as
-// long on the device (64 x 1000 x 64 fp32: 7.4 us either way; 16 x 4000 x 64: 6.7 and 8.9; 256 x 256 x 64: 7.6 and 6.8). Operands that
-// can be read as they lie take the tensor cores at any size (16 x 96 x 48 bf16: 3.9 us, 6.8 by the FP32 pipes).
+// Products small enough for the FP32 pipes, where the tensor cores would want an operand laid out first: one launch instead of two, which
+// the host feels (256 x 256 x 64 fp32: 9.0 us a call by the pipes, 12.3 by the tensor cores; 16 x 4000 x 64: 9.0 and 12.5) and the device mostly not
+// (in a replayed graph 7.4 and 6.7, 6.4 and 8.9).  Operands that can be read as they lie take the tensor cores at any size (16 x 96
+// x 48 bf16: 3.9 us, 6.8 by the FP32 pipes).
 bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 64 && rows * cols <= 65536; }
 
-// Few rows by a table that would have to be laid out for the tensor cores: reading it once as it lies costs less than
-// writing and reading that (26 rows by 84712 x 280 fp32: 70 us so, 107 laid out), unless so few of its rows make so long sums that
-// the blocks are few and their steps many.
+// Few rows by a table that would have to be laid out for the tensor cores: reading it once as it lies may cost less than writing and
+// reading that.  What is less is told by a model of both times, in us, whose numbers come from 1 to 32 rows by 2000 to 84712 x 65 to
+// 4095: the pipes take so long a step of 32 k for each block of 128 columns on an SM, and no less than one block's steps do; laying out
+// moves the table, its copy or three terms twice.  (26 rows by 84712 x 280 fp32: 66 us by the pipes, 105 laid out; 32 rows by 12000 x 4095:
+// 210 and 179, bf16 290 and 81; 8 rows by 5844 x 280 fp32: 16.8 and 19.0.)  Calls one after another take the host 9 us and 12.5.
 constexpr int kFewRows = 32;
 bool is_few(tt_emb_dense_t h, int64_t n)
 {
-    const bool as_it_lies = h->table_type != TT_F32 && mappable(h->table, h->dim, h->rows, h->dim);
-    return !as_it_lies && n <= kFewRows && h->dim <= 4096 && ceil_div(h->rows, 128) * 2 >= h->num_sms;
+    const bool fp32 = h->table_type == TT_F32, as_it_lies = !fp32 && mappable(h->table, h->dim, h->rows, h->dim);
+    if (as_it_lies || n > kFewRows || h->dim > 4096) return false;
+    const double steps = (double)ceil_div(h->dim, 32), blocks = (double)ceil_div(ceil_div(h->rows, 128), h->num_sms);
+    const double step = fmax(n <= 16 ? 1.13 : 1.55, blocks * (0.65 + 0.022 * (double)n));
+    const double pipes = fp32 ? 6.5 + steps * step : 5.0 + 1.3 * steps * step;
+    const double moved = (double)h->rows * ((fp32 ? 4.0 : 2.0) * h->dim + (fp32 ? 12.0 : 4.0) * laid_out(h->dim));
+    const double laid = fp32 ? 13.0 + moved / 5.3e6 : 9.5 + moved / 4.4e6 + 8.6e-5 * (double)h->rows;
+    return fmax(pipes, 9.0) < fmax(laid, 12.5);
 }
 
 // What the handle's device holds of the product kernels.  Asked for once, when a product is first planned: most tables are never
