@@ -568,11 +568,21 @@ int launch_pack(std::initializer_list<const Forms*> forms, int sms, bool* any, c
     return cudaGetLastError() == cudaSuccess ? TT_OK : TT_ERR_CUDA;
 }
 
-// Products small enough for the FP32 pipes, where the tensor cores would want an operand laid out first: one launch instead of two, which
-// the host feels (256 x 256 x 64 fp32: 9.0 us a call by the pipes, 12.3 by the tensor cores; 16 x 4000 x 64: 9.0 and 12.5) and the device mostly not
-// (in a replayed graph 7.4 and 6.7, 6.4 and 8.9).  Operands that can be read as they lie take the tensor cores at any size (16 x 96
-// x 48 bf16: 3.9 us, 6.8 by the FP32 pipes).
-bool is_small(int64_t rows, int64_t cols, int64_t deep) { return deep <= 64 && rows * cols <= 65536; }
+// Products by the FP32 pipes, where the tensor cores would want an operand laid out first: one launch instead of two, which the host feels (256
+// x 256 x 64 fp32: 9.0 us a call by the pipes, 12.3 by the tensor cores) and the device mostly not (in a replayed graph 7.4 and 6.7), and
+// no row of a few values copied (33000 x 4 x 9: 11.8 and 31.2; 520 x 4100 x 17: 16.0 and 19.2).  What costs less is told by a model of
+// both times, in us, whose numbers come from 4 to 33000 rows and columns by 1 to 257 k of all three products: the pipes take so long a step of
+// 32 k for each tile of 64 x 64 on an SM, and no less than one tile's steps do; the others lay out `short_rows` rows that k runs along, and
+// write whole tiles of 128 columns.  (Its choices cost 1.5 % more than the better ones in the mean.)  Long sums, for which the host counts
+// less, want 3 us more.  Operands that can be read as they lie take the tensor cores at any size (16 x 96 x 48 bf16: 3.9 us, 6.8 by the pipes).
+bool is_small(tt_emb_dense_t h, int64_t rows, int64_t cols, int64_t deep, int64_t short_rows, int result_type)
+{
+    const double steps = (double)ceil_div(deep, 32), tiles = (double)ceil_div(rows, 64) * (double)ceil_div(cols, 64) / h->num_sms;
+    const double pipes = fmax(9.0, 6.5 + steps * fmax(1.6, 1.21 * tiles) + 1.04 * tiles);
+    const double written = (double)rows * (double)(ceil_div(cols, 128) * 128 * type_bytes(result_type));
+    const double laid = fmax(12.3, (h->table_type == TT_F32 ? 12.0 : 11.5) + 0.4e-3 * (double)short_rows + written / 2.3e6);
+    return pipes + (deep > 64 ? 3.0 : 0.0) < laid;
+}
 
 // Few rows by a table that would have to be laid out for the tensor cores: reading it once as it lies may cost less than writing and
 // reading that.  What is less is told by a model of both times, in us, whose numbers come from 1 to 32 rows by 2000 to 84712 x 65 to
@@ -630,7 +640,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
                         a->out_type, a->residual_type, a->pre_type, a->bias_type, a->activation, a->cap};
     const bool few = is_few(h, a->n);
     const bool as_they_lie = h->table_type != TT_F32 && mappable(h->table, h->dim, h->rows, h->dim) && mappable(a->x, a->x_stride, a->n, h->dim);
-    if (few || (!as_they_lie && is_small(a->n, h->rows, h->dim))) {
+    if (few || (!as_they_lie && is_small(h, a->n, h->rows, h->dim, a->n + h->rows, a->out_type))) {
         if (size) return TT_OK;
         SmallArgs g = {};
         g.a = matrix(a->x, a->x_stride, 1, h->table_type);
@@ -707,8 +717,8 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
     auto terms_for = [&](int result) { return type == TT_F32 || result == TT_F32 || terms < 2 ? terms : 2; };
     const int dz_type = terms == 1 ? TT_BF16 : type;
     const bool dz_lies = plain && mappable(a->grad_out, a->grad_out_stride, a->n, h->rows);
-    const bool small_x = a->grad_x && is_small(a->n, h->dim, h->rows) && !(dz_lies && mappable(h->table, h->dim, h->rows, h->dim));
-    const bool small_t = a->table_grad && is_small(h->rows, h->dim, a->n) && !(dz_lies && mappable(a->x, a->x_stride, a->n, h->dim));
+    const bool small_x = a->grad_x && is_small(h, a->n, h->dim, h->rows, a->n, a->grad_x_type) && !(dz_lies && mappable(h->table, h->dim, h->rows, h->dim));
+    const bool small_t = a->table_grad && is_small(h, h->rows, h->dim, a->n, 0, h->grad_type) && !(dz_lies && mappable(a->x, a->x_stride, a->n, h->dim));
     const bool big_x = a->grad_x && !small_x, big_t = a->table_grad && !small_t;
     const bool wide_x = big_x && wide_for(a->grad_x_type), wide_t = big_t && wide_for(h->grad_type);
     const int terms_x = wide_x ? terms_for(a->grad_x_type) : 0, terms_t = wide_t ? terms_for(h->grad_type) : 0;

@@ -75,7 +75,11 @@ def dense():
     for asked in (0, 0):                             # a product this small has no plan
         assert L.tt_emb_dense_project_workspace_size(h, call, ctypes.byref(size)) == abi.TT_OK and size.value == 0
         assert _taken() == [0, 0, asked]
-    call = bytes(Project(**{**FORWARD, "n": 70000, "x_stride": 8, "pre": None, "residual": 300 * MB, "out": 400 * MB}))
+    L.tt_emb_dense_destroy(h)
+    assert L.tt_emb_dense_create(1000, 512, abi.TT_F32, 1.0, -1, ctypes.byref(h)) == abi.TT_OK
+    assert L.tt_emb_dense_set_table(h, 8 * MB, None, abi.TT_F32) == abi.TT_OK
+    _taken()
+    call = bytes(Project(**{**FORWARD, "x_stride": 512, "residual_stride": 1000, "pre_stride": 1000, "out_stride": 1000}))
     for asked in (6, 0):                             # the product kernels', once
         assert L.tt_emb_dense_project_workspace_size(h, call, ctypes.byref(size)) == abi.TT_OK and size.value > 0
         assert _taken() == [0, 0, asked]

@@ -22,83 +22,83 @@ WHOLE, CHUNKS, TERM_CHUNKS = 0, 1, 2
 # and its plan: height, pair, sums, blocks that share a tile, slices of k
 CASES = [
     (0, BF16, None, F16, "relu", 5543, 130, 69, (128, 0, 0, 1, 1)), (0, F16, None, F16, None, 70, 3, 31704, (128, 0, 0, 1, 124)),
-    (0, F16, None, F16, None, 402, 276, 967, (128, 0, 0, 8, 1)), (0, F16, None, F32, None, 5669, 138, 86, (128, 0, 1, 1, 1)),
+    (0, F16, None, F16, None, 402, 276, 967, (128, 0, 0, 8, 1)), (0, F16, None, F32, None, 3538, 266, 88, (128, 0, 1, 1, 1)),
     (0, F16, None, F32, None, 67, 4, 31829, (128, 0, 1, 1, 124)), (0, F16, None, F32, None, 584, 168, 984, (128, 0, 1, 8, 1)),
-    (0, F32, None, BF16, "relu", 4810, 299, 73, (128, 0, 2, 1, 1)), (0, F32, None, BF16, "relu", 69, 7, 28783, (128, 0, 2, 1, 112)),
+    (0, F32, None, F32, None, 4765, 284, 84, (128, 0, 2, 1, 1)), (0, F32, None, BF16, "relu", 65, 4, 29825, (128, 0, 2, 1, 116)),
     (0, F32, None, F32, None, 457, 141, 972, (128, 0, 2, 8, 1)), (0, F16, None, F16, None, 1176, 916, 196, (128, 1, 0, 1, 1)),
-    (0, F16, None, F32, None, 3352, 272, 208, (128, 1, 1, 1, 1)), (0, F32, None, F32, None, 5225, 144, 65, (128, 1, 2, 1, 1)),
+    (0, F16, None, F32, None, 3146, 275, 215, (128, 1, 1, 1, 1)), (0, F32, None, BF16, "relu", 4827, 148, 77, (128, 1, 2, 1, 1)),
     (0, BF16, None, BF16, None, 16, 5, 72, (16, 0, 0, 1, 1)), (0, F16, None, F16, None, 3, 5, 10824, (16, 0, 0, 1, 42)),
     (0, F16, None, F16, None, 4, 3, 520, (16, 0, 0, 4, 1)), (0, F16, None, F32, None, 16, 8, 72, (16, 0, 2, 1, 1)),
     (0, F32, None, F32, None, 33, 4, 71, (16, 0, 2, 1, 1)), (0, F16, None, F32, None, 4, 5, 9152, (16, 0, 2, 1, 35)),
     (0, BF16, None, F16, "relu", 15, 3133, 45400, (16, 0, 2, 1, 11)), (0, F32, None, F32, None, 35, 5, 4439, (16, 0, 2, 1, 17)),
     (0, F16, None, F32, None, 4, 6, 464, (16, 0, 2, 4, 1)), (0, BF16, None, F16, "relu", 8, 4304, 8640, (16, 0, 2, 2, 1)),
-    (0, F32, None, F32, None, 34, 3, 194, (16, 0, 2, 2, 1)), (0, BF16, None, BF16, None, 6160, 536, 80, (256, 0, 0, 1, 1)),
-    (0, F16, None, F16, None, 143, 9, 36757, (256, 0, 0, 1, 143)), (0, BF16, None, F16, "relu", 424, 544, 1744, (256, 0, 0, 8, 1)),
-    (0, BF16, None, F16, "relu", 3136, 1304, 4728, (256, 0, 1, 1, 1)), (0, BF16, None, F16, "relu", 278, 910, 39404, (256, 0, 1, 1, 9)),
-    (0, BF16, None, F16, "relu", 808, 664, 16888, (256, 0, 1, 4, 1)), (0, BF16, None, BF16, None, 6515, 264, 106, (256, 1, 0, 1, 1)),
+    (0, F32, None, F32, None, 34, 3, 194, (16, 0, 2, 2, 1)), (0, F16, None, F16, None, 6262, 514, 82, (256, 0, 0, 1, 1)),
+    (0, BF16, None, BF16, None, 140, 4, 38206, (256, 0, 0, 1, 148)), (0, BF16, None, F16, "relu", 424, 544, 1744, (256, 0, 0, 8, 1)),
+    (0, BF16, None, F16, "relu", 3136, 1304, 4728, (256, 0, 1, 1, 1)), (0, F16, None, F16, None, 266, 817, 42055, (256, 0, 1, 1, 10)),
+    (0, BF16, None, F16, "relu", 808, 664, 16888, (256, 0, 1, 4, 1)), (0, F16, None, F16, None, 4845, 406, 84, (256, 1, 0, 1, 1)),
     (0, F16, None, F16, None, 1515, 1570, 4138, (256, 1, 1, 1, 1)), (0, BF16, None, BF16, None, 3019, 3, 68, (32, 0, 0, 1, 1)),
-    (0, F16, None, F16, None, 18, 3, 25040, (32, 0, 0, 1, 98)), (0, F16, None, F16, None, 265, 132, 514, (32, 0, 0, 4, 1)),
-    (0, F32, None, BF16, "relu", 2829, 9, 69, (32, 0, 2, 1, 1)), (0, F16, None, F32, None, 3136, 7, 67, (32, 0, 2, 1, 1)),
+    (0, F16, None, F16, None, 18, 3, 25040, (32, 0, 0, 1, 98)), (0, BF16, None, BF16, None, 248, 8, 976, (32, 0, 0, 8, 1)),
+    (0, F16, None, F32, None, 3040, 8, 72, (32, 0, 2, 1, 1)), (0, F32, None, F32, None, 2776, 8, 104, (32, 0, 2, 1, 1)),
     (0, F32, None, F32, None, 33, 3, 15488, (32, 0, 2, 1, 60)), (0, BF16, None, F16, "relu", 24, 3136, 47768, (32, 0, 2, 1, 11)),
-    (0, F16, None, F32, None, 36, 5, 16311, (32, 0, 2, 1, 63)), (0, F16, None, F32, None, 246, 6, 982, (32, 0, 2, 8, 1)),
-    (0, BF16, None, F16, "relu", 32, 4824, 8672, (32, 0, 2, 2, 1)), (0, F32, None, F32, None, 1192, 8, 200, (32, 0, 2, 2, 1)),
-    (0, BF16, None, BF16, None, 6815, 4, 70, (64, 0, 0, 1, 1)), (0, BF16, None, BF16, None, 34, 7, 25778, (64, 0, 0, 1, 100)),
-    (0, F16, None, F16, None, 537, 144, 516, (64, 0, 0, 4, 1)), (0, F32, None, F32, None, 6853, 3, 66, (64, 0, 2, 1, 1)),
-    (0, BF16, None, F16, "relu", 407, 2364, 4661, (64, 0, 2, 1, 1)), (0, F16, None, F32, None, 7196, 8, 68, (64, 0, 2, 1, 1)),
+    (0, F16, None, F32, None, 36, 5, 16311, (32, 0, 2, 1, 63)), (0, F32, None, BF16, "relu", 264, 136, 472, (32, 0, 2, 4, 1)),
+    (0, BF16, None, F16, "relu", 32, 4824, 8672, (32, 0, 2, 2, 1)), (0, F16, None, F32, None, 246, 6, 982, (32, 0, 2, 8, 1)),
+    (0, BF16, None, BF16, None, 7379, 4, 72, (64, 0, 0, 1, 1)), (0, BF16, None, BF16, None, 34, 7, 25778, (64, 0, 0, 1, 100)),
+    (0, F16, None, F16, None, 537, 144, 516, (64, 0, 0, 4, 1)), (0, F16, None, F32, None, 7232, 8, 72, (64, 0, 2, 1, 1)),
+    (0, BF16, None, F16, "relu", 514, 2020, 4710, (64, 0, 2, 1, 1)), (0, F32, None, BF16, "relu", 2231, 260, 81, (64, 0, 2, 1, 1)),
     (0, F32, None, BF16, "relu", 35, 4, 23705, (64, 0, 2, 1, 92)), (0, BF16, None, F16, "relu", 40, 1728, 41232, (64, 0, 2, 1, 10)),
     (0, F16, None, F32, None, 35, 3, 25616, (64, 0, 2, 1, 100)), (0, F32, None, BF16, "relu", 244, 136, 975, (64, 0, 2, 8, 1)),
-    (0, BF16, None, F16, "relu", 816, 528, 9976, (64, 0, 2, 2, 1)), (0, F16, None, F32, None, 244, 141, 1032, (64, 0, 2, 8, 1)),
+    (0, BF16, None, F16, "relu", 701, 656, 9079, (64, 0, 2, 2, 1)), (0, F16, None, F32, None, 244, 141, 1032, (64, 0, 2, 8, 1)),
     (1, F16, F16, F16, None, 5828, 74, 154, (128, 0, 0, 1, 1)), (1, BF16, BF16, BF16, "relu", 68, 32637, 6, (128, 0, 0, 1, 127)),
-    (1, F16, F16, F16, None, 637, 993, 138, (128, 0, 0, 8, 1)), (1, F16, F16, F32, None, 5632, 69, 134, (128, 0, 1, 1, 1)),
+    (1, F16, F16, F16, None, 536, 992, 200, (128, 0, 0, 8, 1)), (1, F16, F16, F32, None, 1160, 72, 1040, (128, 0, 1, 1, 1)),
     (1, F16, F16, F32, None, 68, 32489, 6, (128, 0, 1, 1, 127)), (1, F16, F16, F32, None, 517, 1014, 144, (128, 0, 1, 8, 1)),
     (1, F32, BF16, F32, None, 3227, 67, 259, (128, 0, 2, 1, 1)), (1, BF16, BF16, F32, "relu", 4746, 81, 313, (128, 0, 2, 1, 1)),
-    (1, F16, BF16, BF16, None, 5152, 72, 152, (128, 0, 2, 1, 1)), (1, F32, BF16, F32, None, 79, 24849, 6, (128, 0, 2, 1, 97)),
-    (1, BF16, BF16, F32, "relu", 65, 36606, 14, (128, 0, 2, 1, 143)), (1, F16, BF16, BF16, None, 72, 27248, 8, (128, 0, 2, 1, 106)),
-    (1, F16, BF16, BF16, None, 711, 475, 279, (128, 0, 2, 4, 1)), (1, BF16, BF16, F32, "relu", 624, 1000, 152, (128, 0, 2, 8, 1)),
+    (1, F16, BF16, BF16, None, 5152, 72, 152, (128, 0, 2, 1, 1)), (1, F32, BF16, F32, None, 65, 25629, 10, (128, 0, 2, 1, 100)),
+    (1, BF16, BF16, F32, "relu", 72, 34105, 5, (128, 0, 2, 1, 133)), (1, F16, BF16, BF16, None, 72, 26496, 8, (128, 0, 2, 1, 103)),
+    (1, F16, BF16, BF16, None, 711, 475, 279, (128, 0, 2, 4, 1)), (1, BF16, BF16, F32, "relu", 440, 1008, 264, (128, 0, 2, 8, 1)),
     (1, F32, F32, F32, None, 488, 1046, 135, (128, 0, 2, 8, 1)), (1, BF16, BF16, BF16, "relu", 1868, 231, 523, (128, 1, 0, 1, 1)),
-    (1, F16, F16, F32, None, 1888, 216, 516, (128, 1, 1, 1, 1)), (1, F32, F32, F32, None, 4856, 81, 163, (128, 1, 2, 1, 1)),
-    (1, BF16, BF16, F32, "relu", 4024, 72, 280, (128, 1, 2, 1, 1)), (1, F16, F16, F16, "relu", 1013, 136, 1277, (128, 1, 2, 1, 1)),
+    (1, F16, F16, F32, None, 1888, 216, 516, (128, 1, 1, 1, 1)), (1, BF16, BF16, F32, "relu", 5712, 80, 136, (128, 1, 2, 1, 1)),
+    (1, F16, F16, F16, "relu", 1013, 136, 1277, (128, 1, 2, 1, 1)), (1, F32, F32, F32, None, 460, 73, 2343, (128, 1, 2, 1, 1)),
     (1, F16, F16, F16, None, 17, 68, 4, (16, 0, 0, 1, 1)), (1, F16, F16, F16, None, 3, 9727, 3, (16, 0, 0, 1, 38)),
-    (1, F16, F16, F16, None, 4, 526, 3, (16, 0, 0, 4, 1)), (1, F32, BF16, F32, None, 16, 69, 4, (16, 0, 2, 1, 1)),
-    (1, BF16, BF16, F32, "relu", 17, 78, 4, (16, 0, 2, 1, 1)), (1, F16, F16, F32, None, 16, 71, 4, (16, 0, 2, 1, 1)),
+    (1, F16, F16, F16, None, 3, 515, 4, (16, 0, 0, 4, 1)), (1, F16, F16, F32, None, 16, 67, 3, (16, 0, 2, 1, 1)),
+    (1, BF16, BF16, F32, "relu", 17, 78, 4, (16, 0, 2, 1, 1)), (1, F32, BF16, F32, None, 16, 69, 4, (16, 0, 2, 1, 1)),
     (1, F32, BF16, F32, None, 3, 5683, 3, (16, 0, 2, 1, 22)), (1, BF16, BF16, F32, "relu", 3, 7744, 3, (16, 0, 2, 1, 30)),
-    (1, F16, F16, F16, "relu", 4, 5720, 4, (16, 0, 2, 1, 22)), (1, F32, BF16, F32, None, 4, 202, 4, (16, 0, 2, 2, 1)),
+    (1, F16, F16, F16, "relu", 3, 6240, 3, (16, 0, 2, 1, 24)), (1, F32, F32, F32, None, 3, 227, 4, (16, 0, 2, 2, 1)),
     (1, BF16, BF16, F32, "relu", 4, 598, 3, (16, 0, 2, 4, 1)), (1, F16, F16, F16, "relu", 4, 263, 3, (16, 0, 2, 2, 1)),
     (1, F16, F16, F16, None, 6249, 75, 543, (256, 0, 0, 1, 1)), (1, BF16, BF16, BF16, None, 134, 37515, 5, (256, 0, 0, 1, 146)),
-    (1, F16, F16, F16, None, 438, 1829, 527, (256, 0, 0, 8, 1)), (1, F16, F16, F16, None, 5336, 4144, 792, (256, 0, 1, 1, 1)),
-    (1, F16, F16, F16, None, 592, 41352, 528, (256, 0, 1, 1, 9)), (1, F16, F16, F16, None, 792, 17976, 792, (256, 0, 1, 4, 1)),
-    (1, BF16, BF16, BF16, "relu", 6424, 96, 272, (256, 1, 0, 1, 1)), (1, F16, F16, F16, None, 1436, 4393, 1557, (256, 1, 1, 1, 1)),
-    (1, F16, F16, F16, None, 2962, 73, 3, (32, 0, 0, 1, 1)), (1, F16, F16, F16, None, 37, 15204, 3, (32, 0, 0, 1, 59)),
-    (1, F16, F16, F16, None, 544, 466, 4, (32, 0, 0, 4, 1)), (1, F32, BF16, F32, None, 2739, 67, 7, (32, 0, 2, 1, 1)),
-    (1, BF16, BF16, F32, "relu", 3240, 80, 8, (32, 0, 2, 1, 1)), (1, F16, F16, F16, "relu", 2861, 68, 12, (32, 0, 2, 1, 1)),
-    (1, F32, BF16, F32, None, 20, 22496, 3, (32, 0, 2, 1, 88)), (1, BF16, BF16, F32, "relu", 17, 29561, 5, (32, 0, 2, 1, 115)),
+    (1, F16, F16, F16, None, 438, 1829, 527, (256, 0, 0, 8, 1)), (1, F16, F16, F16, None, 1576, 4521, 2604, (256, 0, 1, 1, 1)),
+    (1, F16, F16, F16, None, 592, 41352, 528, (256, 0, 1, 1, 9)), (1, F16, F16, F16, None, 1646, 16681, 279, (256, 0, 1, 4, 1)),
+    (1, BF16, BF16, BF16, "relu", 6491, 71, 262, (256, 1, 0, 1, 1)), (1, F16, F16, F16, None, 1436, 4393, 1557, (256, 1, 1, 1, 1)),
+    (1, F16, F16, F16, None, 2962, 73, 3, (32, 0, 0, 1, 1)), (1, BF16, BF16, BF16, "relu", 17, 22564, 9, (32, 0, 0, 1, 88)),
+    (1, BF16, BF16, BF16, None, 551, 457, 5, (32, 0, 0, 4, 1)), (1, F16, F16, F16, "relu", 2861, 68, 12, (32, 0, 2, 1, 1)),
+    (1, BF16, BF16, F32, "relu", 1637, 65, 132, (32, 0, 2, 1, 1)), (1, F32, BF16, F32, None, 2656, 104, 8, (32, 0, 2, 1, 1)),
+    (1, F32, BF16, F32, None, 18, 21871, 4, (32, 0, 2, 1, 85)), (1, BF16, BF16, F32, "relu", 17, 29561, 5, (32, 0, 2, 1, 115)),
     (1, F16, F16, F32, None, 18, 25395, 3, (32, 0, 2, 1, 99)), (1, F16, F16, F32, None, 243, 962, 7, (32, 0, 2, 8, 1)),
     (1, BF16, BF16, F32, "relu", 568, 454, 4, (32, 0, 2, 4, 1)), (1, F32, F32, F32, None, 242, 968, 7, (32, 0, 2, 8, 1)),
-    (1, BF16, BF16, BF16, None, 6896, 66, 4, (64, 0, 0, 1, 1)), (1, BF16, BF16, BF16, "relu", 34, 26539, 4, (64, 0, 0, 1, 103)),
-    (1, BF16, BF16, BF16, "relu", 237, 1091, 139, (64, 0, 0, 8, 1)), (1, F32, BF16, F32, None, 5680, 80, 8, (64, 0, 2, 1, 1)),
-    (1, BF16, BF16, F32, "relu", 7416, 72, 8, (64, 0, 2, 1, 1)), (1, F16, BF16, BF16, None, 6141, 81, 4, (64, 0, 2, 1, 1)),
+    (1, BF16, BF16, BF16, None, 6720, 72, 8, (64, 0, 0, 1, 1)), (1, BF16, BF16, BF16, "relu", 34, 26539, 4, (64, 0, 0, 1, 103)),
+    (1, BF16, BF16, BF16, "relu", 237, 1091, 139, (64, 0, 0, 8, 1)), (1, F16, F16, F32, None, 7048, 80, 8, (64, 0, 2, 1, 1)),
+    (1, BF16, BF16, F32, "relu", 1907, 85, 391, (64, 0, 2, 1, 1)), (1, F32, BF16, F32, None, 5496, 144, 8, (64, 0, 2, 1, 1)),
     (1, F32, BF16, F32, None, 38, 21812, 3, (64, 0, 2, 1, 85)), (1, BF16, BF16, F32, "relu", 34, 28645, 11, (64, 0, 2, 1, 112)),
-    (1, F16, BF16, BF16, None, 34, 22707, 8, (64, 0, 2, 1, 88)), (1, F16, BF16, BF16, None, 232, 1059, 154, (64, 0, 2, 8, 1)),
-    (1, BF16, BF16, F32, "relu", 326, 974, 134, (64, 0, 2, 8, 1)), (1, F32, F32, F32, None, 200, 452, 545, (64, 0, 2, 4, 1)),
+    (1, F16, BF16, BF16, None, 34, 22707, 8, (64, 0, 2, 1, 88)), (1, F32, F32, F32, None, 592, 464, 144, (64, 0, 2, 4, 1)),
+    (1, BF16, BF16, F32, "relu", 326, 974, 134, (64, 0, 2, 8, 1)), (1, F16, BF16, BF16, None, 232, 1059, 154, (64, 0, 2, 8, 1)),
     (2, BF16, BF16, BF16, "relu", 76, 4861, 132, (128, 0, 0, 1, 1)), (2, F16, F16, F16, None, 31536, 72, 8, (128, 0, 0, 1, 123)),
-    (2, BF16, BF16, BF16, "relu", 480, 528, 416, (128, 0, 0, 4, 1)), (2, F16, F16, F32, None, 75, 5000, 166, (128, 0, 1, 1, 1)),
+    (2, BF16, BF16, BF16, "relu", 480, 528, 416, (128, 0, 0, 4, 1)), (2, F16, F16, F32, None, 70, 5142, 153, (128, 0, 1, 1, 1)),
     (2, F16, F16, F32, None, 33296, 72, 8, (128, 0, 1, 1, 130)), (2, F16, F16, F32, None, 1040, 208, 432, (128, 0, 1, 8, 1)),
     (2, F16, F16, F16, "relu", 71, 4779, 148, (128, 0, 2, 1, 1)), (2, BF16, BF16, F32, "relu", 68, 4766, 264, (128, 0, 2, 1, 1)),
     (2, F32, BF16, F32, None, 72, 4840, 192, (128, 0, 2, 1, 1)), (2, F32, BF16, F32, None, 25336, 72, 8, (128, 0, 2, 1, 99)),
-    (2, BF16, BF16, F32, "relu", 38713, 69, 3, (128, 0, 2, 1, 148)), (2, F16, BF16, BF16, None, 27135, 74, 6, (128, 0, 2, 1, 106)),
-    (2, F32, BF16, F32, None, 456, 528, 416, (128, 0, 2, 4, 1)), (2, BF16, BF16, F32, "relu", 1016, 376, 264, (128, 0, 2, 8, 1)),
-    (2, F16, F16, F16, "relu", 464, 560, 392, (128, 0, 2, 4, 1)), (2, BF16, BF16, BF16, None, 200, 1424, 784, (128, 1, 0, 1, 1)),
-    (2, F16, F16, F32, None, 206, 3408, 267, (128, 1, 1, 1, 1)), (2, F32, F32, F32, None, 95, 4828, 129, (128, 1, 2, 1, 1)),
+    (2, BF16, BF16, F32, "relu", 35577, 75, 3, (128, 0, 2, 1, 139)), (2, F16, BF16, BF16, None, 27135, 74, 6, (128, 0, 2, 1, 106)),
+    (2, F16, BF16, BF16, None, 453, 1031, 144, (128, 0, 2, 4, 1)), (2, BF16, BF16, F32, "relu", 1016, 376, 264, (128, 0, 2, 8, 1)),
+    (2, F32, BF16, F32, None, 456, 528, 416, (128, 0, 2, 4, 1)), (2, BF16, BF16, BF16, None, 227, 2392, 387, (128, 1, 0, 1, 1)),
+    (2, F16, F16, F32, None, 224, 1064, 1056, (128, 1, 1, 1, 1)), (2, F32, F32, F32, None, 95, 4828, 129, (128, 1, 2, 1, 1)),
     (2, BF16, BF16, F32, "relu", 76, 5430, 137, (128, 1, 2, 1, 1)), (2, F16, F16, F16, "relu", 131, 2026, 520, (128, 1, 2, 1, 1)),
-    (2, F16, F16, F16, None, 120, 6152, 520, (256, 0, 0, 1, 1)), (2, BF16, BF16, BF16, None, 37427, 133, 10, (256, 0, 0, 1, 146)),
-    (2, BF16, BF16, BF16, None, 912, 656, 776, (256, 0, 0, 4, 1)), (2, F16, F16, F16, None, 6328, 4669, 775, (256, 0, 1, 1, 1)),
+    (2, F16, F16, F16, None, 66, 588, 6238, (256, 0, 0, 1, 1)), (2, F16, F16, F16, None, 38687, 133, 4, (256, 0, 0, 1, 148)),
+    (2, BF16, BF16, BF16, None, 912, 656, 776, (256, 0, 0, 4, 1)), (2, F16, F16, F16, None, 4537, 2593, 1620, (256, 0, 1, 1, 1)),
     (2, F16, F16, F16, None, 43796, 296, 770, (256, 0, 1, 1, 10)), (2, F16, F16, F16, None, 16600, 1072, 552, (256, 0, 1, 4, 1)),
     (2, BF16, BF16, BF16, "relu", 80, 6488, 280, (256, 1, 0, 1, 1)), (2, F16, F16, F16, None, 4272, 2328, 946, (256, 1, 1, 1, 1)),
     (2, BF16, BF16, BF16, None, 66, 64, 5, (64, 0, 0, 1, 1)), (2, F16, F16, F16, None, 7883, 3, 3, (64, 0, 0, 1, 31)),
     (2, BF16, BF16, BF16, None, 443, 3, 3, (64, 0, 0, 2, 1)), (2, F16, F16, F32, None, 65, 67, 3, (64, 0, 2, 1, 1)),
-    (2, BF16, BF16, F32, "relu", 80, 64, 8, (64, 0, 2, 1, 1)), (2, F32, BF16, F32, None, 72, 64, 8, (64, 0, 2, 1, 1)),
-    (2, F32, F32, F32, None, 3835, 4, 3, (64, 0, 2, 1, 15)), (2, BF16, BF16, F32, "relu", 6845, 3, 3, (64, 0, 2, 1, 26)),
-    (2, F16, BF16, BF16, None, 5877, 4, 3, (64, 0, 2, 1, 23)), (2, F32, F32, F32, None, 200, 3, 3, (64, 0, 2, 2, 1)),
+    (2, BF16, BF16, F32, "relu", 65, 84, 5, (64, 0, 2, 1, 1)), (2, F32, BF16, F32, None, 71, 65, 5, (64, 0, 2, 1, 1)),
+    (2, F32, F32, F32, None, 3927, 3, 3, (64, 0, 2, 1, 15)), (2, BF16, BF16, F32, "relu", 6845, 3, 3, (64, 0, 2, 1, 26)),
+    (2, F16, F16, F16, "relu", 4837, 5, 3, (64, 0, 2, 1, 19)), (2, F32, F32, F32, None, 200, 3, 3, (64, 0, 2, 2, 1)),
     (2, BF16, BF16, F32, "relu", 266, 4, 3, (64, 0, 2, 2, 1)), (2, F16, F16, F16, "relu", 230, 4, 3, (64, 0, 2, 2, 1)),
 ]
 
