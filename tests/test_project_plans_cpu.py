@@ -26,7 +26,7 @@ CASES = [
     (0, F16, None, F32, None, 67, 4, 31829, (128, 0, 1, 1, 124)), (0, F16, None, F32, None, 584, 168, 984, (128, 0, 1, 8, 1)),
     (0, F32, None, F32, None, 4765, 284, 84, (128, 0, 2, 1, 1)), (0, F32, None, BF16, "relu", 65, 4, 29825, (128, 0, 2, 1, 116)),
     (0, F32, None, F32, None, 457, 141, 972, (128, 0, 2, 8, 1)), (0, F16, None, F16, None, 1176, 916, 196, (128, 1, 0, 1, 1)),
-    (0, F16, None, F32, None, 3146, 275, 215, (128, 1, 1, 1, 1)), (0, F32, None, BF16, "relu", 4827, 148, 77, (128, 1, 2, 1, 1)),
+    (0, BF16, None, F16, "relu", 1228, 984, 4284, (128, 1, 1, 1, 1)), (0, F32, None, BF16, "relu", 4827, 148, 77, (128, 1, 2, 1, 1)),
     (0, BF16, None, BF16, None, 16, 5, 72, (16, 0, 0, 1, 1)), (0, F16, None, F16, None, 3, 5, 10824, (16, 0, 0, 1, 42)),
     (0, F16, None, F16, None, 4, 3, 520, (16, 0, 0, 4, 1)), (0, F16, None, F32, None, 16, 8, 72, (16, 0, 2, 1, 1)),
     (0, F32, None, F32, None, 33, 4, 71, (16, 0, 2, 1, 1)), (0, F16, None, F32, None, 4, 5, 9152, (16, 0, 2, 1, 35)),
@@ -56,7 +56,7 @@ CASES = [
     (1, BF16, BF16, F32, "relu", 72, 34105, 5, (128, 0, 2, 1, 133)), (1, F16, BF16, BF16, None, 72, 26496, 8, (128, 0, 2, 1, 103)),
     (1, F16, BF16, BF16, None, 711, 475, 279, (128, 0, 2, 4, 1)), (1, BF16, BF16, F32, "relu", 440, 1008, 264, (128, 0, 2, 8, 1)),
     (1, F32, F32, F32, None, 488, 1046, 135, (128, 0, 2, 8, 1)), (1, BF16, BF16, BF16, "relu", 1868, 231, 523, (128, 1, 0, 1, 1)),
-    (1, F16, F16, F32, None, 1888, 216, 516, (128, 1, 1, 1, 1)), (1, BF16, BF16, F32, "relu", 5712, 80, 136, (128, 1, 2, 1, 1)),
+    (1, F16, F16, F16, None, 1337, 4130, 909, (128, 1, 1, 1, 1)), (1, BF16, BF16, F32, "relu", 5712, 80, 136, (128, 1, 2, 1, 1)),
     (1, F16, F16, F16, "relu", 1013, 136, 1277, (128, 1, 2, 1, 1)), (1, F32, F32, F32, None, 460, 73, 2343, (128, 1, 2, 1, 1)),
     (1, F16, F16, F16, None, 17, 68, 4, (16, 0, 0, 1, 1)), (1, F16, F16, F16, None, 3, 9727, 3, (16, 0, 0, 1, 38)),
     (1, F16, F16, F16, None, 3, 515, 4, (16, 0, 0, 4, 1)), (1, F16, F16, F32, None, 16, 67, 3, (16, 0, 2, 1, 1)),
@@ -88,7 +88,7 @@ CASES = [
     (2, BF16, BF16, F32, "relu", 35577, 75, 3, (128, 0, 2, 1, 139)), (2, F16, BF16, BF16, None, 27135, 74, 6, (128, 0, 2, 1, 106)),
     (2, F16, BF16, BF16, None, 453, 1031, 144, (128, 0, 2, 4, 1)), (2, BF16, BF16, F32, "relu", 1016, 376, 264, (128, 0, 2, 8, 1)),
     (2, F32, BF16, F32, None, 456, 528, 416, (128, 0, 2, 4, 1)), (2, BF16, BF16, BF16, None, 227, 2392, 387, (128, 1, 0, 1, 1)),
-    (2, F16, F16, F32, None, 224, 1064, 1056, (128, 1, 1, 1, 1)), (2, F32, F32, F32, None, 95, 4828, 129, (128, 1, 2, 1, 1)),
+    (2, F16, F16, F16, None, 4136, 1584, 656, (128, 1, 1, 1, 1)), (2, F32, F32, F32, None, 95, 4828, 129, (128, 1, 2, 1, 1)),
     (2, BF16, BF16, F32, "relu", 76, 5430, 137, (128, 1, 2, 1, 1)), (2, F16, F16, F16, "relu", 131, 2026, 520, (128, 1, 2, 1, 1)),
     (2, F16, F16, F16, None, 66, 588, 6238, (256, 0, 0, 1, 1)), (2, F16, F16, F16, None, 38687, 133, 4, (256, 0, 0, 1, 148)),
     (2, BF16, BF16, BF16, None, 912, 656, 776, (256, 0, 0, 4, 1)), (2, F16, F16, F16, None, 4537, 2593, 1620, (256, 0, 1, 1, 1)),
