@@ -179,7 +179,7 @@ class DenseEmbedding:
 
         pre: what ``project`` left there; not needed without an activation.  The residual's gradient is grad_out.
         grad_out, pre, grad_x, grad_bias and the table's gradient may each be of any of the three types.  A bfloat16 result beside a
-        bfloat16 table is formed from grad_out times the slope rounded to bfloat16; buffers of the other types get it in full.
+        bfloat16 table may be formed from grad_out times the slope rounded to bfloat16; buffers of the other types get it in full.
         The table's padding row receives none.  table_grad=False leaves the table's out, and needs no x."""
         self._check(grad_out, "grad_out")
         if grad_out.dim() == 0 or grad_out.size(-1) != self.num_rows:

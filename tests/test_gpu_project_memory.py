@@ -13,14 +13,15 @@ def _need(e, x):
     return abi.tt_emb_dense_project_workspace_size(e.handle, abi.project_call(x, e.num_rows, e.dim, out))
 
 
-@pytest.mark.parametrize("other", [False, True])
+@pytest.mark.parametrize("other", ["current", "another", "a handle"])
 def test_growing_batches_keep_one_workspace(other):
     g = torch.Generator(device="cuda").manual_seed(1)
     e, w = _table(2000, 512, F32, g)
     x = _randn(g, 8192, 512)
     torch.cuda.synchronize()
     before = torch.cuda.memory_allocated()
-    side = torch.cuda.Stream() if other else None
+    keep = torch.cuda.Stream()
+    side = {"current": None, "another": keep, "a handle": keep.cuda_stream}[other]
     n = 64
     while n < 8192:
         e.project(x[:n], stream=side)
