@@ -505,7 +505,7 @@ typedef struct {
  *   grad_x[r][k] = sum over c of dz[r][c] W[c][k]
  *   grad[c][k]   = (accumulate ? grad[c][k] : 0) + sum over r of dz[r][c] x[r][k]      (the table's gradient buffer)
  *   grad_bias[c] = (accumulate ? grad_bias[c] : 0) + sum over r of dz[r][c]
- * The residual's is grad_out itself.  The table's padding_row receives no gradient.  Sums are formed in
+ * The residual's is grad_out itself, and relu's slope at 0 is 0.  The table's padding_row receives no gradient.  Sums are formed in
  * fp32 in an order that depends on the sizes, strides and places only: the same call gives the same bits.  Where
  * the table and a result are of bf16, that result's products may take dz rounded to bf16; all others take it and the
  * table or x as they are, where their types differ or dz is computed as bf16 terms: of dz to 2^-17 of it for 16-bit results
