@@ -389,7 +389,10 @@ typedef enum {
     TT_INJECT_NONE = 0,
     TT_INJECT_POOL_WAIT = 1,
     TT_INJECT_MMA_WAIT_FWD = 2,
-    TT_INJECT_MMA_WAIT_BWD = 3
+    TT_INJECT_MMA_WAIT_BWD = 3,
+    TT_INJECT_COPIES = 4,    /* these three: of tt_emb_dense_debug_inject */
+    TT_INJECT_PRODUCTS = 5,
+    TT_INJECT_SUMS = 6
 } tt_inject;
 
 int tt_emb_debug_inject(tt_emb_t h, int32_t what, int32_t spin_limit);
@@ -542,6 +545,19 @@ int tt_emb_dense_set_project_workspace(tt_emb_dense_t h, void* workspace, size_t
  * TT_ERR_CUDA.  While a device error waits for tt_emb_dense_sync they do nothing. */
 int tt_emb_dense_project(tt_emb_dense_t h, const tt_emb_project* call, tt_stream_t stream);
 int tt_emb_dense_project_backward(tt_emb_dense_t h, const tt_emb_project_grad* call, tt_stream_t stream);
+
+/*
+ * Test hook for failure detection, as tt_emb_debug_inject (no GPU fault is involved).  In the handle's next projection, or gradients of
+ * one, that runs on the tensor cores, one role of every block of its first product gives up after the first chunk of k, as if a wait had
+ * run out:
+ *   TT_INJECT_COPIES         the role that brings the operands, with copies under way
+ *   TT_INJECT_PRODUCTS       the one that multiplies, with products under way
+ *   TT_INJECT_SUMS           those that finish the sums
+ *   TT_INJECT_NONE           disarms
+ * The others notice, or their own waits run out; copies and products end, tensor memory is freed, TT_ERR_TIMEOUT is recorded, and the
+ * call's later kernels do nothing.  Returns TT_OK or TT_ERR_ARG.
+ */
+int tt_emb_dense_debug_inject(tt_emb_dense_t h, int32_t what);
 
 /* As tt_emb_sync, tt_emb_last_error and tt_emb_destroy.  The sync waits for the stream of the last
  * call; a replayed graph's own stream is the caller's to wait for first.  With another device than the

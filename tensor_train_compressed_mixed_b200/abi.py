@@ -26,6 +26,7 @@ TT_SCHED_STATIC, TT_SCHED_STEAL, TT_SCHED_STEAL_L2 = 0, 1, 2
 TT_GROUP_PREFIX, TT_GROUP_UNIQUE_ONLY = 0, 1
 TT_PREC_FP32, TT_PREC_BF16_TC, TT_PREC_FP32_SPLIT_TC = 0, 1, 2
 TT_INJECT_NONE, TT_INJECT_POOL_WAIT, TT_INJECT_MMA_WAIT_FWD, TT_INJECT_MMA_WAIT_BWD = 0, 1, 2, 3
+TT_INJECT_COPIES, TT_INJECT_PRODUCTS, TT_INJECT_SUMS = 4, 5, 6
 TT_F32, TT_BF16, TT_F16 = 0, 1, 2
 TT_ACT_NONE, TT_ACT_RELU, TT_ACT_GELU, TT_ACT_SILU, TT_ACT_SOFTCAP = 0, 1, 2, 3, 4
 MAX_TABLES, MAX_CORES = 64, 4
@@ -120,6 +121,7 @@ _SIGS = {
     "tt_emb_dense_set_project_workspace": ([ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t], ctypes.c_int),
     "tt_emb_dense_project": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_project_backward": ([ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int),
+    "tt_emb_dense_debug_inject": ([ctypes.c_void_p, ctypes.c_int32], ctypes.c_int),
     "tt_emb_dense_sync": ([ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_last_error": ([ctypes.c_void_p], ctypes.c_int),
     "tt_emb_dense_destroy": ([ctypes.c_void_p], None),
@@ -515,6 +517,11 @@ def tt_emb_dense_project_backward(h, call: bytes, stream: int):
     rc = lib().tt_emb_dense_project_backward(h, call, stream)
     if rc:
         raise TTEmbError(rc, "tt_emb_dense_project_backward")
+
+
+def tt_emb_dense_debug_inject(h, what: int):
+    """Test hook: arms one role's giving up in the next product on the tensor cores (TT_INJECT_COPIES, _PRODUCTS, _SUMS)."""
+    _check(lib().tt_emb_dense_debug_inject(h, int(what)), "tt_emb_dense_debug_inject")
 
 
 def tt_emb_dense_sync(h):

@@ -21,6 +21,7 @@ struct tt_emb_dense_handle {
     cudaStream_t last_stream = nullptr;
     bool used_stream = false;
     int last_error = TT_OK;
+    int inject = TT_INJECT_NONE;     // tt_emb_dense_debug_inject, armed until a product on the tensor cores takes it
 };
 
 namespace tt {

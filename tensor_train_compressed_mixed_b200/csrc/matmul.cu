@@ -64,6 +64,7 @@ struct Args {
     int32_t tiles_c, tiles_r;
     int32_t split;        // blocks of a cluster that share a tile
     int32_t slices;       // of k, each a tile of its own whose sums go to rows of their own
+    int32_t fail;         // TT_INJECT_COPIES, _PRODUCTS or _SUMS (tests): the role that gives up after its first chunk
     int32_t vectors;      // four neighbouring values of a row of the result, residual and pre make one access
 };
 
@@ -78,11 +79,12 @@ __host__ __device__ constexpr int fit_of(int bn) { return bn <= 32 ? 2 : 1; }
 
 // waits that end early where another role of the block has given up, and tell it where this one does
 constexpr int kGone = 1, kTimedOut = 2;
+constexpr int kTries = 1 << 18;      // of a wait: about a second
 template <bool kCluster = false>      // whether other blocks of the cluster arrive there
 __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gone)
 {
     const uint32_t a = smem_u32(bar);
-    for (int it = 0; it < kMbarSpin; ++it) {
+    for (int it = 0; it < kTries; ++it) {
         uint32_t done;
         if constexpr (kCluster)
             asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.b32 %0, 1, 0, p;\n\t}"
@@ -496,12 +498,14 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                             }
                         }
                     }
+                if (g.fail == TT_INJECT_COPIES) gone = kTimedOut, ok = false;
             }
         }
         // All copies have landed before the block's memory is given up, also where another role gives up after the last of them was
         // asked for.  (A pair's arrive at the first block's barriers.)
         if (!kPair || rank == 0)
-            for (int i = max(0, n - kStages); i < n; ++i) mbar_wait(&full[i % kStages], (i / kStages) & 1);
+            for (int i = max(0, n - kStages); i < n; ++i)
+                if (!mbar_wait(&full[i % kStages], (i / kStages) & 1, kTries)) break;
     } else if (warp == 1 && (!kPair || rank == 0) && elected()) {
         int n = 0, seq = 0;
         bool ok = true;
@@ -556,12 +560,13 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                             if (ok && t < terms) commit<kPair>(&empty[slot[t]]);
                     }
                 }
+                if (g.fail == TT_INJECT_PRODUCTS) gone = kTimedOut, ok = false;
                 if (ok) commit<kPair>(&sums_full[buf]);
             }
         }
         if (gone == kTimedOut) {    // products on their way end before tensor memory is given up
             commit<kPair>(&drained);
-            mbar_wait(&drained, 0);
+            mbar_wait(&drained, 0, kTries);
         }
     } else if (warp >= 2) {
         const int quarter = warp & 3, part = kFinish == 4 ? 0 : (warp - 2) >> 2;     // a warp reaches the lanes of its quarter of tensor memory
@@ -586,6 +591,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
                 for (int k0 = first; ok && k0 < last; k0 += chunk, ++seq) {
                     buf = seq & 1;
                     ok = wait_for(&sums_full[buf], (seq / 2) & 1, &gone);
+                    if (g.fail == TT_INJECT_SUMS) gone = kTimedOut, ok = false;
                     if (!ok) break;
                     tc_fence_after();
 #pragma unroll
@@ -609,6 +615,7 @@ __global__ void __launch_bounds__(threads_of(BN), fit_of(BN)) k_matmul(const __g
             } else {
                 buf = seq & 1;
                 ok = wait_for(&sums_full[buf], (seq / 2) & 1, &gone);
+                if (g.fail == TT_INJECT_SUMS) gone = kTimedOut, ok = false;
                 tc_fence_after();
                 ++seq;
             }
@@ -921,6 +928,7 @@ int matmul(const Product& p, const MatmulPlan& q, void* scratch, int32_t* status
     g.tiles_c = (int)tiles_c;
     g.tiles_r = (int)tiles_r;
     g.chunk = q.chunk;
+    g.fail = p.fail;
     g.split = q.split;
     g.slices = q.slices;
     auto four = [&](const void* x, int type, int64_t stride) {

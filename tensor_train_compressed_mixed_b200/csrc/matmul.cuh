@@ -33,6 +33,7 @@ struct Product {
     bool a_mn = false, b_mn = false, has_pre = false;
     int64_t rows = 0, cols = 0, deep = 0;
     Epilogue e = {};
+    int fail = TT_INJECT_NONE;       // the role that gives up, in tests
 };
 // How a tile's sums are formed: whole ones in tensor memory, chunks of single terms, or chunks of operands of several terms.
 enum { kWhole, kChunks, kTermChunks };

@@ -618,6 +618,13 @@ const MatmulFits& fits_of(tt_emb_dense_t h)
     return h->fits;
 }
 
+int take_injection(tt_emb_dense_t h)
+{
+    const int what = h->inject;
+    h->inject = TT_INJECT_NONE;
+    return what;
+}
+
 Matrix matrix(const void* p, int64_t si, int64_t sk, int type) { return {p, si, sk, type}; }
 
 int enter(tt_emb_dense_t h, cudaStream_t s)
@@ -673,6 +680,7 @@ int project(tt_emb_dense_t h, const tt_emb_project* a, size_t* size, cudaStream_
     if (w.used > h->project_bytes) return TT_ERR_WORKSPACE;
     bool packed = false;
     if (const int rc = launch_pack({&t, &x}, h->num_sms, &packed, s)) return rc;
+    p.fail = take_injection(h);
     return matmul(p, plan, scratch, h->d_status, h->fits, packed, s);
 }
 
@@ -780,6 +788,7 @@ int project_backward(tt_emb_dense_t h, const tt_emb_project_grad* a, size_t* siz
         g.deep = a->n;
         if (const int rc = launch_product<64, 64>(g, s)) return rc;
     }
+    if (big_x || big_t) (big_x ? px : pt).fail = take_injection(h);
     if (big_x) {
         if (const int rc = matmul(px, plan_x, scratch, h->d_status, h->fits, early, s)) return rc;
         early = true;
@@ -814,6 +823,13 @@ int tt_emb_dense_set_project_workspace(tt_emb_dense_t h, void* workspace, size_t
     if (!h || !workspace || ((uintptr_t)workspace & 255)) return note(h, TT_ERR_ARG);
     h->project_ws = (char*)workspace;
     h->project_bytes = bytes;
+    return TT_OK;
+}
+
+int tt_emb_dense_debug_inject(tt_emb_dense_t h, int32_t what)
+{
+    if (!h || (what != TT_INJECT_NONE && what != TT_INJECT_COPIES && what != TT_INJECT_PRODUCTS && what != TT_INJECT_SUMS)) return note(h, TT_ERR_ARG);
+    h->inject = what;
     return TT_OK;
 }
 

@@ -5,7 +5,7 @@
 
 namespace tt {
 
-constexpr int kMbarSpin = 1 << 20;   // bounded wait for an MMA completion (tens of ms at most)
+constexpr int kMbarSpin = 1 << 20;   // bounded wait for an MMA completion (some 4 s: a try takes about 4 us)
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -73,10 +73,10 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 // bounded wait for the completion of phase `parity`; false when the bound ran out
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, int tries = kMbarSpin)
 {
     const uint32_t a = smem_u32(bar);
-    for (int it = 0; it < kMbarSpin; ++it) {
+    for (int it = 0; it < tries; ++it) {
         uint32_t done;
         asm volatile(
             "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"

@@ -1,4 +1,4 @@
-"""What making a handle asks of the CUDA runtime: one allocation and one wait, and nothing for calls that may never come."""
+"""What making a handle asks of the CUDA runtime: one allocation and one wait, and nothing for calls that may never come; what its test hook refuses."""
 import ctypes
 import os
 import subprocess
@@ -87,3 +87,18 @@ def dense():
 
 def test_dense(tmp_path):
     _run(tmp_path, "dense")
+
+
+def hook():
+    from test_project_cpu import _handle
+    L = abi.lib()
+    h = _handle(L)
+    for what in (abi.TT_INJECT_COPIES, abi.TT_INJECT_PRODUCTS, abi.TT_INJECT_SUMS, abi.TT_INJECT_NONE):
+        assert L.tt_emb_dense_debug_inject(h, what) == abi.TT_OK
+    for what in (-1, abi.TT_INJECT_POOL_WAIT, abi.TT_INJECT_MMA_WAIT_BWD, 7):
+        assert L.tt_emb_dense_debug_inject(h, what) == abi.TT_ERR_ARG
+    assert L.tt_emb_dense_debug_inject(None, abi.TT_INJECT_NONE) == abi.TT_ERR_ARG
+
+
+def test_hook(tmp_path):
+    _run(tmp_path, "hook")
